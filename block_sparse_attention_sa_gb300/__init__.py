@@ -15,12 +15,17 @@ Entry points (same names as the C ABI):
     sa_qk_quantize(q, k, ...)                         -> (q8, k8, q_exp, k_exp)
     sa_route_pooled(q_out, workspace, prefix_len, tau, ...) -> (row_ptr, col_idx)
     sa_forward_host(q_host, k_host, v_host, ...)      -> o_host (+ lse_host)
+Over a paged key-value cache (one new token per sequence and call):
+    sa_cache_append(k, v, k_cache, v_cache, page_table, seq_lens, ...) -> q_out
+    sa_route_pages(q, k_sum, page_table, seq_lens, prefix_len, budget) -> (row_ptr, col_idx)
+    sa_attn_decode(q, k_cache, v_cache, page_table, seq_lens, ...)     -> (o, lse)
 Tensors are [B, S, H, D] bf16 with a contiguous last dimension.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -34,6 +39,10 @@ __all__ = [
     "sa_qk_quantize", "SA_QK_BF16", "SA_QK_FP8", "QK_FORMATS",
     "SA_DEV_CAPACITY", "SA_DEV_TIMEOUT", "SA_DEV_BAD_ROUTE", "SA_DEV_RANGE",
     "SA_ROUTE_THRESHOLD", "SA_ROUTE_DENSE_PREFIX_QUERIES", "SA_ROUTE_TOP_MASS", "ROUTE_MODES",
+    "sa_cache_params", "make_cache_params", "sa_cache_append", "sa_route_pages", "sa_attn_decode",
+    "sa_route_pages_max_nnz", "sa_route_pages_workspace_bytes", "sa_attn_decode_workspace_bytes",
+    "SA_DEV_BAD_CACHE", "SA_CACHE_BF16", "SA_CACHE_FP8", "CACHE_FORMATS", "SA_ROPE_INTERLEAVED",
+    "SA_ROPE_HALF", "ROPE_LAYOUTS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +50,7 @@ _LIB = None
 
 SA_OK, SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_CAPACITY, SA_ERR_CUDA, SA_ERR_TIMEOUT = range(6)
 SA_DEV_CAPACITY, SA_DEV_TIMEOUT, SA_DEV_BAD_ROUTE, SA_DEV_RANGE = 1, 2, 4, 8
+SA_DEV_BAD_CACHE = 16
 # readings of the router rule (sa_params.route_mode)
 SA_ROUTE_THRESHOLD, SA_ROUTE_DENSE_PREFIX_QUERIES, SA_ROUTE_TOP_MASS = 0, 1, 2
 ROUTE_MODES = {"threshold": SA_ROUTE_THRESHOLD,
@@ -49,6 +59,14 @@ ROUTE_MODES = {"threshold": SA_ROUTE_THRESHOLD,
 # arithmetic of the score product (sa_params.qk_format)
 SA_QK_BF16, SA_QK_FP8 = 0, 1
 QK_FORMATS = {"bf16": SA_QK_BF16, "fp8": SA_QK_FP8}
+# storage of a paged cache (sa_cache_params.cache_format), by the tensors' dtype
+SA_CACHE_BF16, SA_CACHE_FP8 = 0, 1
+CACHE_FORMATS = {torch.bfloat16: SA_CACHE_BF16, torch.float8_e4m3fn: SA_CACHE_FP8,
+                 torch.uint8: SA_CACHE_FP8}
+# which elements of a head vector the rotation pairs (sa_cache_params.rope_layout)
+SA_ROPE_INTERLEAVED, SA_ROPE_HALF = 0, 1
+ROPE_LAYOUTS = {"interleaved": SA_ROPE_INTERLEAVED, "half": SA_ROPE_HALF}
+PAGE = 64
 
 # Every function include/sa.h declares.
 EXPORTS = (
@@ -57,6 +75,8 @@ EXPORTS = (
     "sa_attn_dense", "sa_forward_host", "sa_dev_status_decode", "sa_status_string",
     "sa_route_static", "sa_qk_prologue", "sa_route_pooled", "sa_check_wait_timeout",
     "sa_attn_prepare", "sa_attn_run", "sa_qk_quantize",
+    "sa_cache_params_init", "sa_cache_append", "sa_route_pages", "sa_route_pages_max_nnz",
+    "sa_route_pages_workspace_bytes", "sa_attn_decode", "sa_attn_decode_workspace_bytes",
 )
 SA_ROUTE_STATIC_WS_BYTES = 32 << 20
 
@@ -77,6 +97,15 @@ class sa_params(ctypes.Structure):
         ("route_mode", ctypes.c_int32), ("q_block", ctypes.c_int32),
         ("qk_format", ctypes.c_int32),
     ]
+
+
+class sa_cache_params(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "B", "S", "H", "H_kv", "D", "page", "n_pages", "max_pages", "cache_format", "prefix_len",
+        "page_budget", "qk_norm", "rope_layout", "rope_rows")] + [
+        ("eps", ctypes.c_float), ("softmax_scale", ctypes.c_float),
+        ("table_stride", ctypes.c_int64)] + [(name, ctypes.c_int64 * 3) for name in (
+            "q_stride", "k_stride", "v_stride", "o_stride", "kc_stride", "vc_stride")]
 
 
 def library_path() -> str:
@@ -119,6 +148,16 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "sa_qk_quantize": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp]),
         "sa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     }
+    C, i32 = ctypes.POINTER(sa_cache_params), ctypes.c_int32
+    sig.update({
+        "sa_cache_params_init": (None, [C] + [i32] * 6),
+        "sa_cache_append": (ctypes.c_int, [C] + [vp] * 19),
+        "sa_route_pages_max_nnz": (i64, [C]),
+        "sa_route_pages_workspace_bytes": (sz, [C]),
+        "sa_route_pages": (ctypes.c_int, [C] + [vp] * 6 + [i64, vp, sz, vp, vp]),
+        "sa_attn_decode_workspace_bytes": (sz, [C]),
+        "sa_attn_decode": (ctypes.c_int, [C] + [vp] * 9 + [i64, vp, vp, vp, sz, vp, vp]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -421,6 +460,246 @@ def alloc_layer_buffers(B: int, S: int, H: int, D: int, device="cuda", qk_format
     nbytes = max(sa_route_workspace_bytes(p), sa_attn_workspace_bytes(p))
     bufs["ws"] = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return bufs
+
+
+# ------------------------------------------------------ paged key-value cache --
+
+def _on_device(fn):
+    """The call with its first tensor's device current, so that it is enqueued
+    on that device's stream and allocates there."""
+    @functools.wraps(fn)
+    def call(t, *args, **kwargs):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device: there is no CPU path")
+        if t.device.index == torch.cuda.current_device():
+            return fn(t, *args, **kwargs)
+        with torch.cuda.device(t.device):
+            return fn(t, *args, **kwargs)
+    return call
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _need(t: Optional[torch.Tensor], name: str, device, dtype, shape=None) -> None:
+    """A contiguous tensor (or None) of this device, type and shape."""
+    if t is None:
+        return
+    if t.device != device or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _need_tokens(t: torch.Tensor, name: str, device, shape) -> None:
+    if t.device != device or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bf16 tensor on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _need_map(page_table, seq_lens, device) -> None:
+    if (page_table.device != device or page_table.dtype != torch.int32 or page_table.dim() != 2
+            or (page_table.stride(1) != 1 and page_table.shape[1] != 1)):
+        raise ValueError(f"page_table must be int32 [B, max_pages] on {device}, its rows contiguous")
+    if seq_lens is not None:
+        _need(seq_lens, "seq_lens", device, torch.int32, page_table.shape[:1])
+
+
+def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = None,
+                      k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                      o: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                      v_cache: Optional[torch.Tensor] = None,
+                      k_sum: Optional[torch.Tensor] = None, scale: float = 0.0,
+                      prefix_len: int = 0, budget: int = 0) -> sa_cache_params:
+    """The parameters of a paged-cache call on these tensors (those it takes):
+    q, k, v, o [B, S, heads, D]; k_cache, v_cache [n_pages, H_kv, 64, D] in
+    bf16, or e4m3 as float8_e4m3fn or uint8; k_sum [n_pages, H_kv, D]."""
+    p = sa_cache_params()
+    pool = k_cache if k_cache is not None else k_sum
+    if pool is None or pool.dim() != (4 if k_cache is not None else 3):
+        raise ValueError("k_cache must be [n_pages, H_kv, 64, D], k_sum [n_pages, H_kv, D]")
+    p.n_pages, p.H_kv, p.D = pool.shape[0], pool.shape[1], pool.shape[-1]
+    p.B, p.max_pages = page_table.shape
+    p.page, p.table_stride = PAGE, page_table.stride(0)
+    p.prefix_len, p.page_budget, p.softmax_scale = int(prefix_len), int(budget), float(scale)
+    for field, t in (("q_stride", q), ("k_stride", k), ("v_stride", v), ("o_stride", o)):
+        if t is not None:
+            getattr(p, field)[:] = _bshd_strides(t, field[0])
+    tokens = q if q is not None else k
+    p.S = 1 if tokens is None else tokens.shape[1]
+    p.H = p.H_kv if q is None else q.shape[2]
+    if k_cache is not None:
+        for field, t in (("kc_stride", k_cache), ("vc_stride", v_cache)):
+            if (t.shape != k_cache.shape or t.shape[2] != PAGE or t.stride(3) != 1
+                    or t.dtype != k_cache.dtype or t.device != page_table.device):
+                raise ValueError("k_cache, v_cache must be alike, [n_pages, H_kv, 64, D] with a "
+                                 "contiguous last dimension, on the page table's device")
+            st = t.stride()
+            getattr(p, field)[:] = (st[0], st[1], st[2])
+        if k_cache.dtype not in CACHE_FORMATS:
+            raise ValueError("k_cache, v_cache must be bfloat16, float8_e4m3fn or uint8 (e4m3)")
+        p.cache_format = CACHE_FORMATS[k_cache.dtype]
+    return p
+
+
+@_on_device
+def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
+                    q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                    new_lens: Optional[torch.Tensor] = None, qk_norm: bool = False,
+                    gamma_q: Optional[torch.Tensor] = None,
+                    gamma_k: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+                    rope="interleaved", k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, k_sum: Optional[torch.Tensor] = None,
+                    lens_out: Optional[torch.Tensor] = None,
+                    dev_status: Optional[torch.Tensor] = None,
+                    stream=None) -> Optional[torch.Tensor]:
+    """The new tokens' keys and values (bf16 [B, S, H_kv, D]) into the paged
+    cache behind each sequence's ``seq_lens`` tokens, normed (``qk_norm``) and
+    rotated (``cos``, ``sin`` fp32 [rows, D/2] by position; ``rope``
+    "interleaved" or "half") on the way; see sa.h. With ``q`` [B, S, H, D]
+    returns the queries normed and rotated alike (``q_out``, default new with
+    q's strides; pass q_out=q for in place). ``new_lens``: how many of the S
+    tokens each sequence brings. ``k_sum`` gathers the per-page key sums that
+    sa_route_pages reads; ``lens_out`` receives the new lengths."""
+    dev = k.device
+    B, S, Hkv, D = k.shape
+    _need_tokens(v, "v", dev, k.shape)
+    _need_tokens(k, "k", dev, (page_table.shape[0], S, k_cache.shape[1], k_cache.shape[-1]))
+    if q is not None:
+        _need_tokens(q, "q", dev, (B, S, q.shape[2], D))
+        if q_out is None:
+            q_out = _empty((B, S, q.shape[2], D), q.dtype, dev, stream)
+        _need_tokens(q_out, "q_out", dev, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _need_map(page_table, seq_lens, dev)
+    _need(new_lens, "new_lens", dev, torch.int32, (B,))
+    _need(lens_out, "lens_out", dev, torch.int32, (B,))
+    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        _need(t, name, dev, torch.float32, (D,))
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, name, dev, torch.float32, (Hkv,))
+    _need(k_sum, "k_sum", dev, torch.float32, (k_cache.shape[0], Hkv, D))
+    _need(dev_status, "dev_status", dev, torch.int32)
+    p = make_cache_params(page_table, q=q, k=k, v=v, o=q_out, k_cache=k_cache, v_cache=v_cache)
+    if cos is not None:
+        _need(cos, "cos", dev, torch.float32, (cos.shape[0], D // 2))
+        _need(sin, "sin", dev, torch.float32, cos.shape)
+        p.rope_rows = cos.shape[0]
+    p.qk_norm, p.eps = int(bool(qk_norm)), float(eps)
+    p.rope_layout = ROPE_LAYOUTS[rope] if isinstance(rope, str) else int(rope)
+    code = load_library().sa_cache_append(
+        ctypes.byref(p), _ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(gamma_q), _ptr(gamma_k),
+        _ptr(cos), _ptr(sin), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(k_sum), _ptr(page_table), _ptr(seq_lens), _ptr(new_lens), _ptr(lens_out),
+        _ptr(dev_status), _stream(stream))
+    _check(code, "sa_cache_append")
+    return q_out
+
+
+def sa_route_pages_max_nnz(p: sa_cache_params) -> int:
+    return int(load_library().sa_route_pages_max_nnz(ctypes.byref(p)))
+
+
+def sa_route_pages_workspace_bytes(p: sa_cache_params) -> int:
+    return int(load_library().sa_route_pages_workspace_bytes(ctypes.byref(p)))
+
+
+def sa_attn_decode_workspace_bytes(p: sa_cache_params) -> int:
+    return int(load_library().sa_attn_decode_workspace_bytes(ctypes.byref(p)))
+
+
+def _cache_workspace(need: int, device, ws: Optional[torch.Tensor], stream) -> torch.Tensor:
+    if ws is None:
+        return _empty((max(need, 256),), torch.uint8, device, stream)
+    if ws.device != device or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"workspace must be contiguous, on {device} and hold {need} bytes")
+    return ws
+
+
+@_on_device
+def sa_route_pages(q: torch.Tensor, k_sum: torch.Tensor, page_table: torch.Tensor,
+                   seq_lens: torch.Tensor, prefix_len: int, budget: int, *,
+                   row_ptr: Optional[torch.Tensor] = None,
+                   col_idx: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   dev_status: Optional[torch.Tensor] = None,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The pages one new token of each sequence attends (q bf16 [B, 1, H, D],
+    k_sum from sa_cache_append): int32 row_ptr [B*H_kv+1] and col_idx (valid
+    entries are col_idx[:row_ptr[-1]]), for sa_attn_decode. Kept per key-value
+    head: the prefix's pages, the newest one, and the best-scoring others until
+    ``budget`` are."""
+    dev = q.device
+    p = make_cache_params(page_table, q=q, k_sum=k_sum, prefix_len=prefix_len, budget=budget)
+    _need_tokens(q, "q", dev, (p.B, q.shape[1], q.shape[2], p.D))
+    _need(k_sum, "k_sum", dev, torch.float32)
+    _need_map(page_table, seq_lens, dev)
+    _need(dev_status, "dev_status", dev, torch.int32)
+    rows = p.B * p.H_kv
+    if row_ptr is None:
+        row_ptr = _empty((rows + 1,), torch.int32, dev, stream)
+    _need(row_ptr, "row_ptr", dev, torch.int32, (rows + 1,))
+    if col_idx is None:
+        col_idx = _empty((sa_route_pages_max_nnz(p),), torch.int32, dev, stream)
+    _need(col_idx, "col_idx", dev, torch.int32)
+    ws = _cache_workspace(sa_route_pages_workspace_bytes(p), dev, workspace, stream)
+    code = load_library().sa_route_pages(
+        ctypes.byref(p), _ptr(q), _ptr(k_sum), _ptr(page_table), _ptr(seq_lens), _ptr(row_ptr),
+        _ptr(col_idx), col_idx.numel(), _ptr(ws), ws.numel() * ws.element_size(),
+        _ptr(dev_status), _stream(stream))
+    _check(code, "sa_route_pages")
+    return row_ptr, col_idx
+
+
+@_on_device
+def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   page_table: torch.Tensor, seq_lens: torch.Tensor, scale: float = 0.0, *,
+                   row_ptr: Optional[torch.Tensor] = None,
+                   col_idx: Optional[torch.Tensor] = None,
+                   k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                   workspace: Optional[torch.Tensor] = None,
+                   dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of one new token per sequence (q bf16 [B, 1, H, D]) over its
+    ``seq_lens`` cached tokens, or over the pages a route lists (row_ptr,
+    col_idx from sa_route_pages): (o bf16 [B, 1, H, D], lse fp32 [B, H, 1] or
+    None). H is a multiple of the cache's H_kv."""
+    dev = q.device
+    if o is None:
+        o = _empty(q.shape, q.dtype, dev, stream)
+    p = make_cache_params(page_table, q=q, o=o, k_cache=k_cache, v_cache=v_cache, scale=scale)
+    shape = (p.B, q.shape[1], q.shape[2], p.D)
+    _need_tokens(q, "q", dev, shape)
+    _need_tokens(o, "o", dev, shape)
+    if lse is None and want_lse:
+        lse = _empty((p.B, p.H, 1), torch.float32, dev, stream)
+    _need(lse, "lse", dev, torch.float32, (p.B, p.H, 1))
+    _need_map(page_table, seq_lens, dev)
+    _need(row_ptr, "row_ptr", dev, torch.int32, (p.B * p.H_kv + 1,))
+    _need(col_idx, "col_idx", dev, torch.int32)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, name, dev, torch.float32, (p.H_kv,))
+    _need(dev_status, "dev_status", dev, torch.int32)
+    ws = _cache_workspace(sa_attn_decode_workspace_bytes(p), dev, workspace, stream)
+    code = load_library().sa_attn_decode(
+        ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(page_table), _ptr(seq_lens), _ptr(row_ptr), _ptr(col_idx),
+        0 if col_idx is None else col_idx.numel(), _ptr(o), _ptr(lse), _ptr(ws),
+        ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream))
+    _check(code, "sa_attn_decode")
+    return o, lse
 
 
 def check_dev_status(dev_status: torch.Tensor, what: str = "device status") -> None:

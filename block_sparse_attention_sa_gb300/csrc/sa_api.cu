@@ -653,7 +653,7 @@ sa_status sa_forward_host(const sa_params* p, const void* q_host, const void* k_
 
 sa_status sa_dev_status_decode(int32_t d) {
   if (d & SA_DEV_TIMEOUT) return SA_ERR_TIMEOUT;
-  if (d & SA_DEV_BAD_ROUTE) return SA_ERR_INVALID_ARG;
+  if (d & (SA_DEV_BAD_ROUTE | SA_DEV_BAD_CACHE)) return SA_ERR_INVALID_ARG;
   if (d & SA_DEV_CAPACITY) return SA_ERR_CAPACITY;
   if (d & SA_DEV_RANGE) return SA_ERR_UNSUPPORTED;
   return SA_OK;

@@ -58,8 +58,11 @@ enum {
   SA_DEV_BAD_ROUTE = 1 << 2,/* sa_attn_sparse met a CSR that breaks its
                                contract (see sa_attn_sparse for what is then
                                attended)                                      */
-  SA_DEV_RANGE = 1 << 3     /* a V value does not fit fp16 (|v| > 65504); the
+  SA_DEV_RANGE = 1 << 3,    /* a V value does not fit fp16 (|v| > 65504); the
                                P.V product runs in fp16, see sa_attn_sparse    */
+  SA_DEV_BAD_CACHE = 1 << 4 /* a paged-cache call met a sequence length or a
+                               page id outside its range (see sa_cache_params
+                               for what is then done)                         */
 };
 
 /* Arithmetic of the attention's score product Q.K^T (sa_attn_*). */
@@ -391,6 +394,191 @@ sa_status sa_forward_host(const sa_params* p, const void* q_host,
  * stays usable. Nothing faults, traps or hangs. Asynchronous on `stream`.
  */
 sa_status sa_check_wait_timeout(int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The paged key-value cache: keys and values that stay between calls, and the
+ * attention of one new token over them. (The pages attend one whole packed
+ * sequence per call and have no counterpart; the key blocks, the pooled keys,
+ * the sink, the diagonal and the list format are those of the layer above.)
+ *
+ * A cache is a pool of pages of 64 tokens, the library's key block:
+ *   k_cache, v_cache  [n_pages, H_kv, 64, D] bf16 or e4m3, d contiguous, with
+ *                     any strides of page, head and token;
+ *   page_table        int32 [B, max_pages]: token t of sequence b lives in
+ *                     page page_table[b][t / 64], slot t % 64;
+ *   seq_lens          int32 [B], device memory: the tokens of each sequence;
+ *   k_sum             fp32 [n_pages, H_kv, D], contiguous: the sum of a page's
+ *                     keys, which ranks pages as sa_route's block means do
+ *                     (only the router needs it).
+ * H query heads share H_kv key-value heads, H / H_kv consecutive ones each.
+ *
+ * Nothing is read or written outside these extents: a length below 0 counts as
+ * 0, one beyond 64 max_pages as 64 max_pages, and the tokens of a page whose
+ * id is outside [0, n_pages) are left out; each raises SA_DEV_BAD_CACHE.
+ * Entries of page_table behind a sequence's last page are not read. One page
+ * may serve several sequences or places as long as nothing is appended to it;
+ * what a page holds that two sequences append to in one call is undefined.
+ * ---------------------------------------------------------------------- */
+
+/* Storage of the cached keys and values. */
+enum {
+  SA_CACHE_BF16 = 0,
+  SA_CACHE_FP8 = 1   /* e4m3; value = code * scale of its key-value head       */
+};
+
+/* Which two elements of a head vector the rotation turns together. */
+enum {
+  SA_ROPE_INTERLEAVED = 0, /* 2i and 2i + 1, as sa_qk_prologue (the default)  */
+  SA_ROPE_HALF = 1         /* i and i + D/2                                    */
+};
+
+typedef struct sa_cache_params {
+  int32_t B, S, H, H_kv, D; /* S: new tokens per sequence (1 where one new
+                               token attends or is routed); H % H_kv == 0;
+                               D must be 64 or 128                             */
+  int32_t page;             /* must be 64                                      */
+  int32_t n_pages;          /* pages of the pool, >= 1                         */
+  int32_t max_pages;        /* page-table entries of a sequence, >= 1 and
+                               < 2^25                                          */
+  int32_t cache_format;     /* SA_CACHE_*                                      */
+  int32_t prefix_len;       /* sa_route_pages: P >= 0, as sa_params           */
+  int32_t page_budget;      /* sa_route_pages: pages to keep, >= 0            */
+  int32_t qk_norm;          /* sa_cache_append: 0 or 1                         */
+  int32_t rope_layout;      /* sa_cache_append: SA_ROPE_*                      */
+  int32_t rope_rows;        /* sa_cache_append: rows of the rotation tables    */
+  float eps;                /* sa_cache_append: >= 0, added to the mean square */
+  float softmax_scale;      /* sa_attn_decode: 0 => 1/sqrt(D)                  */
+  int64_t table_stride;     /* elements between two sequences of page_table    */
+  int64_t q_stride[3];      /* element strides of b, s, h of the new tokens'   */
+  int64_t k_stride[3];      /* q, k, v and of o (sa_cache_append: of q_out),   */
+  int64_t v_stride[3];      /* multiples of 8 as in sa_params                  */
+  int64_t o_stride[3];
+  int64_t kc_stride[3];     /* element strides of page, head, token of the     */
+  int64_t vc_stride[3];     /* caches: multiples of 16 bytes                   */
+} sa_cache_params;
+
+/* Fills p for contiguous tensors and caches in bf16: page = 64, S = 1,
+ * table_stride = max_pages, eps = 1e-6, the rest 0. */
+void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv, int32_t D,
+                          int32_t n_pages, int32_t max_pages);
+
+/*
+ * sa_cache_append -- the new tokens' keys and values into the cache, with
+ * QK-norm and rotation on the way (the step sa_qk_prologue makes for a whole
+ * packed sequence). Token s < n_b of sequence b (n_b = new_lens[b], S where
+ * new_lens is NULL) takes position t = seq_lens[b] + s. For every head vector
+ * x [D] of k (gamma_k) and, where q is given, of q (gamma_q):
+ *   y = x / sqrt(mean_d(x_d^2) + eps) * gamma    (y = x with qk_norm = 0)
+ *   (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c), c = rope_cos[t][i],
+ *       s = rope_sin[t][i], (a, b) the i-th pair of rope_layout
+ * in fp32, rounded once: q to bf16 into q_out, k to bf16 into k_cache, or with
+ * SA_CACHE_FP8 to the nearest e4m3 code of y / k_scale[h] (ties to even,
+ * |code| at most 448, NaN stays NaN). v goes into v_cache as it is (/ v_scale).
+ * k_sum of the page (where given) gains y before it is rounded; a page's first
+ * slot starts its sum anew.
+ * Tokens that find no place (t >= 64 max_pages, or t >= rope_rows where tables
+ * are given: SA_DEV_CAPACITY; a bad page id: SA_DEV_BAD_CACHE) are left out,
+ * with their q_out. All else of the caches, k_sum and q_out stays as it was.
+ *
+ * k, v         device bf16 [B, S, H_kv, D].
+ * q, q_out     device bf16 [B, S, H, D] (q_stride; o_stride), or both NULL.
+ *              q_out may be q itself with equal strides, else no overlap.
+ * gamma_q,     device fp32 [D], 16-byte aligned, or NULL for all ones (and
+ * gamma_k      NULL without qk_norm).
+ * rope_cos,    device fp32 [rope_rows][D/2], 16-byte aligned; both NULL for
+ * rope_sin     no rotation.
+ * k_scale,     device fp32 [H_kv], > 0, or NULL for ones (and NULL with
+ * v_scale      SA_CACHE_BF16).
+ * seq_lens     the lengths before the call; not modified.
+ * new_lens     device int32 [B] in [0, S] (clamped into it), or NULL.
+ * lens_out     device int32 [B], or NULL: seq_lens[b] + n_b, at most
+ *              64 max_pages; not seq_lens itself.
+ * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED before launch; SA_ERR_CUDA.
+ */
+sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v,
+                          const void* q, void* q_out, const float* gamma_q,
+                          const float* gamma_k, const float* rope_cos, const float* rope_sin,
+                          void* k_cache, void* v_cache, const float* k_scale,
+                          const float* v_scale, float* k_sum, const int32_t* page_table,
+                          const int32_t* seq_lens, const int32_t* new_lens, int32_t* lens_out,
+                          int32_t* dev_status, void* stream);
+
+/* Most entries sa_route_pages can list, B*H_kv*min(max_pages, max(page_budget,
+ * ceil(P/64) + 1)) (0 on bad params). */
+int64_t sa_route_pages_max_nnz(const sa_cache_params* p);
+
+/* Bytes of device workspace sa_route_pages needs (0 on bad params). */
+size_t sa_route_pages_workspace_bytes(const sa_cache_params* p);
+
+/*
+ * sa_route_pages -- the pages one new token of each sequence attends, per
+ * key-value head: the router for a query that is a single token. With
+ * n = seq_lens[b] and Nb = ceil(n / 64), page j < Nb of row (b, g) scores
+ *   s_j = max over the query heads h of g of  q_h . k_sum[page_table[b][j]][g].
+ * Kept are the pages that sa_route always keeps (j < ceil(min(P, n) / 64), and
+ * the newest page Nb - 1) and, while fewer than page_budget are, the others by
+ * s_j descending (equal s_j: lower j first). Pages that compete are full, so
+ * their sums rank as their means do. A score that is not a number ranks last;
+ * so does a page with a bad id. (A budget bounds the attention's cost per
+ * token; sa_route's threshold does not.)
+ * The choice equals that of scores computed in fp64.
+ *
+ * q          device bf16 [B, 1, H, D], rotated as the cached keys are.
+ * row_ptr    device int32 [B*H_kv + 1]; row r = b*H_kv + g.
+ * col_idx    device int32 [col_cap]: page places j, ascending in each row, as
+ *            sa_route lists key blocks. Entries beyond col_cap are dropped and
+ *            SA_DEV_CAPACITY is raised; sa_route_pages_max_nnz(p) is enough.
+ * workspace  device scratch of sa_route_pages_workspace_bytes(p) bytes,
+ *            256-byte aligned; its contents on entry do not matter.
+ * Errors: as sa_route. B*H_kv*max_pages and the most entries must be < 2^31
+ * (SA_ERR_UNSUPPORTED).
+ */
+sa_status sa_route_pages(const sa_cache_params* p, const void* q, const float* k_sum,
+                         const int32_t* page_table, const int32_t* seq_lens, int32_t* row_ptr,
+                         int32_t* col_idx, int64_t col_cap, void* workspace, size_t ws_bytes,
+                         int32_t* dev_status, void* stream);
+
+/* Bytes of device workspace sa_attn_decode needs (0 on bad params). */
+size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p);
+
+/*
+ * sa_attn_decode -- attention of one new token per sequence over its cached
+ * keys: for head h of sequence b, g = h / (H / H_kv), over the tokens
+ * u < seq_lens[b] (the new token's own key among them, once appended)
+ *   l_u = softmax_scale * q_h . k_u,   a_u = exp(l_u - max l) / sum exp(.),
+ *   o_h = sum_u a_u v_u,               lse_h = max l + log sum exp(l - max l)
+ * with k_u, v_u as stored (code * scale). With a route (row_ptr and col_idx)
+ * only tokens in the pages listed for row b*H_kv + g. Nothing to attend gives
+ * o = 0 and lse = -inf. Whatever lies in the slots behind a sequence's last
+ * token, NaN included, has no effect.
+ *
+ * Precision: exact products with fp32 accumulation and an fp32 softmax; P.V
+ * takes P as two bf16 terms (16 bits; with SA_CACHE_FP8 one fp16 term, 11
+ * bits, against V in fp16, which holds every e4m3 value) with fp32
+ * accumulation; o is rounded once to bf16. The sums' order, and so the last
+ * bit, depends on the lengths in the batch, not on timing.
+ *
+ * q          device bf16 [B, 1, H, D], rotated as the cached keys are.
+ * row_ptr,   device int32 CSR as sa_route_pages writes it, or both NULL for
+ * col_idx    every page. One that breaks the contract raises SA_DEV_BAD_ROUTE:
+ *            a row whose span does not lie inside [0, col_cap] or that is
+ *            longer than max_pages is left out whole; an entry outside
+ *            [0, ceil(seq_lens[b] / 64)) or not above the one before it in
+ *            its row is left out. col_cap: the entries col_idx holds.
+ * k_scale,   as sa_cache_append.
+ * v_scale
+ * o          device bf16 [B, 1, H, D] (o_stride).
+ * lse        device fp32 [B, H, 1] (natural log), or NULL.
+ * workspace  device scratch of sa_attn_decode_workspace_bytes(p) bytes,
+ *            256-byte aligned; its contents on entry do not matter.
+ * Errors: as sa_attn_sparse; S must be 1 (SA_ERR_UNSUPPORTED).
+ */
+sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_cache,
+                         const void* v_cache, const float* k_scale, const float* v_scale,
+                         const int32_t* page_table, const int32_t* seq_lens,
+                         const int32_t* row_ptr, const int32_t* col_idx, int64_t col_cap,
+                         void* o, float* lse, void* workspace, size_t ws_bytes,
+                         int32_t* dev_status, void* stream);
 
 /* Decodes *dev_status bits into the most severe sa_status (SA_OK if 0). */
 sa_status sa_dev_status_decode(int32_t dev_status);
