@@ -26,6 +26,7 @@ sa_status check_cache(const sa_cache_params* p) {
   if (p->B > 1 && p->table_stride < p->max_pages) return SA_ERR_INVALID_ARG;
   if (p->D != 64 && p->D != 128) return SA_ERR_UNSUPPORTED;
   if (p->B > 65535 || p->H > 65535) return SA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->B) * p->H > INT32_MAX) return SA_ERR_UNSUPPORTED;
   return SA_OK;
 }
 
@@ -82,6 +83,30 @@ sa_status check_route_pages(const sa_cache_params* p) {
   if (rows * p->max_pages > INT32_MAX || rows * most_pages(p) > INT32_MAX)
     return SA_ERR_UNSUPPORTED;
   return SA_OK;
+}
+
+// [n_pages, Hkv, 64, D] -> 4-D map (D, token, head, page); the box is one
+// head's page, at most 128 bytes of each token, swizzled over as many bytes.
+sa_status encode_cache(CUtensorMap* m, const void* base, const sa_cache_params* p,
+                       const int64_t st[3]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return SA_ERR_CUDA;
+  const bool f8 = p->cache_format == SA_CACHE_FP8;
+  const cuuint64_t elt = f8 ? 1 : 2, D = static_cast<cuuint64_t>(p->D);
+  // the stride of an axis with one entry is never used, but must be encodable
+  auto bytes = [&](int i, int64_t extent) { return extent > 1 ? static_cast<cuuint64_t>(st[i]) * elt : D * elt; };
+  const cuuint64_t dims[4] = {D, kBlock, static_cast<cuuint64_t>(p->H_kv),
+                              static_cast<cuuint64_t>(p->n_pages)};
+  const cuuint64_t strides[3] = {bytes(2, kBlock), bytes(1, p->H_kv), bytes(0, p->n_pages)};
+  const bool wide = D * elt >= 128;
+  const cuuint32_t box[4] = {wide ? static_cast<cuuint32_t>(128 / elt) : 64u, kBlock, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SA_OK : SA_ERR_INVALID_ARG;
 }
 
 sa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
@@ -220,7 +245,7 @@ sa_status sa_route_pages(const sa_cache_params* p, const void* q, const float* k
 
 size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p) {
   if (check_cache(p) != SA_OK || p->S != 1) return 0;
-  return 256;
+  return decode_ws_bytes(p->H, p->H_kv, p->D);
 }
 
 sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_cache,
@@ -232,6 +257,9 @@ sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_
   sa_status s = check_cache(p);
   if (s != SA_OK) return s;
   if (p->S != 1) return SA_ERR_UNSUPPORTED;
+  // the pages of a run are counted in 32 bits
+  if (static_cast<int64_t>(p->B) * p->H * p->max_pages > static_cast<int64_t>(INT32_MAX) * 128)
+    return SA_ERR_UNSUPPORTED;
   if (col_cap < 0) return SA_ERR_INVALID_ARG;
   if (!q || !o || !workspace || (row_ptr == nullptr) != (col_idx == nullptr))
     return SA_ERR_INVALID_ARG;
@@ -265,7 +293,11 @@ sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_
   const double scale = p->softmax_scale > 0.f ? static_cast<double>(p->softmax_scale)
                                               : 1.0 / std::sqrt(static_cast<double>(p->D));
   a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-  return from_cuda(launch_decode(a, p->cache_format == SA_CACHE_FP8,
+  a.ws = static_cast<char*>(workspace);
+  CUtensorMap kmap, vmap;
+  if ((s = encode_cache(&kmap, k_cache, p, p->kc_stride)) != SA_OK) return s;
+  if ((s = encode_cache(&vmap, v_cache, p, p->vc_stride)) != SA_OK) return s;
+  return from_cuda(launch_decode(a, kmap, vmap, p->cache_format == SA_CACHE_FP8,
                                  static_cast<cudaStream_t>(stream)));
 }
 

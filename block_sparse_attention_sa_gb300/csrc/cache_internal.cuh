@@ -54,6 +54,7 @@ struct DecodeArgs {
   int32_t* dev_status;
   int B, H, Hkv, D;
   float scale_log2;          // softmax_scale * log2(e)
+  char* ws;
 };
 
 struct RoutePagesArgs {
@@ -70,7 +71,9 @@ struct RoutePagesArgs {
 };
 
 cudaError_t launch_append(const AppendArgs& a, int D, bool fp8, bool half, cudaStream_t st);
-cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st);
+size_t decode_ws_bytes(int H, int Hkv, int D);
+cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          bool fp8, cudaStream_t st);
 size_t route_pages_ws_bytes(int64_t rows, int max_pages);
 cudaError_t launch_route_pages(const RoutePagesArgs& a, cudaStream_t st);
 

@@ -1,91 +1,794 @@
 // decode.cu -- attention of one new token per sequence over the paged cache.
 //   l_u = scale q.k_u,  a = softmax(l),  o = sum a_u v_u,  lse = log sum exp l
+//
+// One pass over the cached keys and values with the running maximum and sum of
+// the softmax. Every byte of the cache is used for the G = H / H_kv query heads
+// that share a key-value head and for nothing else, 2 G (bf16) or 4 G (e4m3)
+// flops a byte, so up to G of about 100 the kernel is bound by the memory and
+// what matters is that loads never pause:
+//
+// - The pages of all (sequence, key-value head) units are one list, cut into
+//   equal runs, one per CTA, so that any mix of lengths keeps every SM loading
+//   until the end. A CTA finds its run from the lengths (or the route's row
+//   spans) itself: no host plan, nothing to keep between calls.
+// - A producer warp looks the pages up, 32 at a time, and feeds a ring of pages
+//   by TMA (both of its swizzles are those the matrix fragments are read with);
+//   consumer warps take 16 keys each of every page: S = Q K^T on the tensor
+//   cores with the query heads as the 16 rows of mma.m16n8k16 (up to 16, 32 or
+//   64 of them), the softmax in registers, P V with P as the A operand straight
+//   from those registers. tcgen05 has no use here: its smallest tile is 64 rows
+//   of which G are there, and the accumulators would go through tensor memory
+//   for a product that waits for DRAM.
+// - A unit that lies in one run is finished there. One that is cut leaves fp32
+//   partial results (maximum, sum, unnormalised o) in the workspace, which
+//   join_kernel adds in the order of the runs: no atomics, the same bits every
+//   time. join_kernel is launched while the first kernel runs and waits for it.
+//
+// P is taken as two bf16 terms, p = hi + lo (16 bits), so that P V carries no
+// rounding of its own beside the final one to bf16; with an e4m3 cache one fp16
+// term is enough (11 bits against the values' 4), scaled by 2^15 so that weights
+// down to 2^-29 of the largest keep all their bits.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "cache_internal.cuh"
+#include "ptx.cuh"
 
 namespace sa {
 namespace {
 
-template <bool kFp8>
-__device__ __forceinline__ float load(const void* p, int64_t at) {
-  if (kFp8) {
-    __nv_fp8_e4m3 x;
-    x.__x = static_cast<const uint8_t*>(p)[at];
-    return static_cast<float>(x);
-  }
-  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at]) << 16);
+constexpr int kSms = 152;
+constexpr int kMaxRuns = 2 * kSms;
+constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16
+
+// Rows of query heads a CTA holds: RG groups of 16; KW warps share a page's
+// keys, each with every row group's own warp beside it.
+template <int D, bool kFp8, int RG>
+struct Shape {
+  static constexpr int kRows = 16 * RG;
+  static constexpr int kKeyWarps = RG == 4 ? 2 : 4;
+  static constexpr int kWarps = kKeyWarps * RG;         // consumer warps
+  static constexpr int kSlices = 4 / kKeyWarps;         // 16-key slices of a page per warp
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kCtas = RG == 1 ? 2 : 1;         // per SM
+  static constexpr int kRuns = kSms * kCtas;
+  static constexpr int kRowBytes = kFp8 ? D : 2 * D;    // one token of one head
+  static constexpr int kPage = kBlock * kRowBytes;
+  static constexpr int kBox = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kStage = 2 * kPage;
+  static constexpr int kRing = (RG == 1 ? 96 : 160) * 1024;
+  static constexpr int kStages = kRing / kStage < 16 ? kRing / kStage : 16;
+  static constexpr int kChunk = 32;                     // columns joined at a time
+  static constexpr int kPad = kChunk + 8;               // row stride of the join buffer
+  static constexpr int kJoin = kWarps * 16 * kPad * 4;
+  static constexpr int kSmem = kStages * kStage + kJoin + 1024;
+};
+
+struct PageMeta {
+  int live;     // tokens of the page that count
+  int flags;    // 1: first page of a unit's piece, 2: last
+  int unit;
+  int dest;     // -1: the whole unit, else which partial of this run
+};
+
+// The run's pieces of one unit, for join_kernel: unit, and its first and last run.
+struct Cut {
+  int unit, first, last, pad;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// grid (B, H), one warp: one pass over the row's pages with the running
-// maximum and sum of the softmax, lane l holding dims l, l + 32, ...
-template <bool kFp8>
-__global__ void __launch_bounds__(32) decode_kernel(DecodeArgs a) {
-  const int b = blockIdx.x, h = blockIdx.y, g = h / (a.H / a.Hkv), lane = threadIdx.x;
-  const int nd = a.D / 32;
-  bool bad;
-  const int n = clamp_len(a.pm.seq_lens[b], a.pm, &bad), nb = (n + kBlock - 1) / kBlock;
-  int status = bad ? SA_DEV_BAD_CACHE : 0;
-  int beg = 0, end = nb;
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <bool kFp16>
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (kFp16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 codes (low half of x) as two fp16 values; exact.
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float lo_f32(uint32_t bf2) { return __uint_as_float(bf2 << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t bf2) { return __uint_as_float(bf2 & 0xffff0000u); }
+
+// Byte offset of 16-byte piece `piece` of token `row` in a page as TMA lays it
+// out: boxes of at most 128 bytes a token, pieces XORed with the row.
+template <int D, bool kFp8, int RG>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  using S = Shape<D, kFp8, RG>;
+  if (S::kBox == 64) return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+  return (piece >> 3) * (kBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
+// Pages of group `i` of the list: a sequence (every page), or a row of the route.
+__device__ __forceinline__ int group_pages(const DecodeArgs& a, int i, int* status) {
   if (a.row_ptr) {
-    const int r = b * a.Hkv + g;
-    beg = a.row_ptr[r];
-    end = a.row_ptr[r + 1];
+    const int beg = __ldg(a.row_ptr + i), end = __ldg(a.row_ptr + i + 1);
     if (beg < 0 || end < beg || end > a.col_cap || end - beg > a.pm.max_pages) {
-      status |= SA_DEV_BAD_ROUTE;
-      beg = end = 0;
+      *status |= SA_DEV_BAD_ROUTE;
+      return 0;
+    }
+    return end - beg;
+  }
+  bool bad;
+  const int n = clamp_len(__ldg(a.pm.seq_lens + i), a.pm, &bad);
+  if (bad) *status |= SA_DEV_BAD_CACHE;
+  return (n + kBlock - 1) / kBlock;
+}
+
+// Run c of C over T pages: [run_start(c), run_start(c + 1)).
+__device__ __forceinline__ int64_t run_start(int64_t T, int C, int c) {
+  return T / C * c + min(static_cast<int64_t>(c), T % C);
+}
+
+__device__ __forceinline__ int run_of(int64_t T, int C, int64_t page) {
+  const int64_t base = T / C, rem = T % C, big = rem * (base + 1);
+  return static_cast<int>(page < big ? page / (base + 1) : rem + (page - big) / base);
+}
+
+template <int D, bool kFp8, int RG>
+__global__ void __launch_bounds__(Shape<D, kFp8, RG>::kThreads, Shape<D, kFp8, RG>::kCtas)
+decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+              DecodeArgs a, int RT, float* partial, Cut* cuts) {
+  using S = Shape<D, kFp8, RG>;
+  constexpr int NS = S::kStages, W = S::kWarps, NT = S::kThreads;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], joined;
+  __shared__ PageMeta meta[NS];
+  __shared__ float sm_m[W][16], sm_l[W][16];
+  __shared__ int64_t warp_sum[NT / 32 + 1];
+  __shared__ int64_t start_off;
+  __shared__ int start_group;
+  __shared__ volatile int abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  float* join = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + NS * S::kStage);
+  const int G = a.H / a.Hkv, C = gridDim.x, c = blockIdx.x;
+  const bool routed = a.row_ptr != nullptr;
+  const int n_groups = routed ? a.B * a.Hkv : a.B;
+  const int per_group = routed ? RT : a.Hkv * RT;        // units of a group
+  // where join_kernel finds the units that are cut: by unit when they are no
+  // more than the runs, else by the run a unit starts in
+  const bool by_unit = a.B * a.Hkv * RT <= C;
+  const AbortSignal abort{&abort_flag, nullptr};
+  int status = 0;
+
+  // join_kernel may be launched from here on; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), W);
+    }
+    mbar_init(smem_u32(&joined), W);
+    fence_barrier_init();
+    abort_flag = 0;
+    start_group = -1;
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+
+  // this CTA's run of the page list: a scan of the groups' page counts
+  const int per_thread = (n_groups + NT - 1) / NT;
+  const int g0 = min(tid * per_thread, n_groups), g1 = min(g0 + per_thread, n_groups);
+  int64_t mine = 0;
+  for (int i = g0; i < g1; ++i) mine += group_pages(a, i, &status);
+  int64_t incl = mine;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const int64_t T = total * per_group;
+  const int64_t lo = run_start(T, C, c), hi = run_start(T, C, c + 1);
+  const int64_t excl = (before + incl - mine) * per_group;
+  if (lo < hi && lo >= excl && lo < excl + mine * per_group) {
+    int64_t at = excl;
+    int i = g0;
+    for (;; ++i) {
+      const int64_t n = static_cast<int64_t>(group_pages(a, i, &status)) * per_group;
+      if (lo < at + n) break;
+      at += n;
+    }
+    start_group = i;
+    start_off = lo - at;
+  }
+  // groups without a page: nothing to attend
+  for (int i = c + C * warp; i < n_groups; i += C * (NT / 32)) {
+    if (group_pages(a, i, &status) != 0) continue;
+    const int b = routed ? i / a.Hkv : i;
+    const int h0 = routed ? (i % a.Hkv) * G : 0, nh = routed ? G : a.H;
+    for (int e = lane; e < nh * (D / 8); e += 32)
+      *reinterpret_cast<uint4*>(a.o + b * a.os[0] + (h0 + e / (D / 8)) * a.os[2] + e % (D / 8) * 8) =
+          make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse)
+      for (int h = lane; h < nh; h += 32) a.lse[static_cast<int64_t>(b) * a.H + h0 + h] = -INFINITY;
+    if (by_unit)
+      for (int u = lane; u < per_group; u += 32) cuts[i * per_group + u].unit = -1;
+  }
+  __syncthreads();
+
+  if (warp == W) {
+    // ---------------------------------------------------------- producer --
+    int64_t left = hi - lo;
+    int group = start_group;
+    int64_t off = left > 0 ? start_off : 0;     // pages into the group's units
+    int64_t issued = 0;
+    Cut cut{-1, 0, 0, 0};
+    bool ok = true;
+    while (left > 0 && ok) {
+      if (group >= n_groups) break;             // the lengths changed under the call
+      const int cnt = group_pages(a, group, &status);
+      if (off >= static_cast<int64_t>(cnt) * per_group) {
+        ++group;
+        off = 0;
+        continue;
+      }
+      const int sub = static_cast<int>(off / cnt), p0 = static_cast<int>(off % cnt);
+      const int take = static_cast<int>(min(left, static_cast<int64_t>(cnt - p0)));
+      const int bg = routed ? group : group * a.Hkv + sub / RT, rt = sub % RT;
+      const int b = routed ? group / a.Hkv : group, g = bg - b * a.Hkv;
+      const int unit = bg * RT + rt;
+      bool bad;
+      const int n = clamp_len(__ldg(a.pm.seq_lens + b), a.pm, &bad);
+      if (bad) status |= SA_DEV_BAD_CACHE;
+      const int nb = (n + kBlock - 1) / kBlock;
+      const int beg = routed ? __ldg(a.row_ptr + group) : 0;
+      const int dest = take == cnt ? -1 : (p0 == 0 ? 1 : 0);
+      if (dest == 1) {
+        cut.unit = unit;
+        cut.first = c;
+        cut.last = run_of(T, C, hi - left + cnt - 1);
+      }
+      if (by_unit && dest != 0 && lane == 0) cuts[unit] = dest == 1 ? cut : Cut{-1, 0, 0, 0};
+      for (int q0 = 0; q0 < take && ok; q0 += 32) {
+        // 32 pages are looked up at once, then fed one by one
+        const int q = q0 + lane;
+        int page = -1, live = 0;
+        if (q < take) {
+          int j = p0 + q;
+          if (routed) {
+            const int at = beg + j;
+            const int prev = j > 0 ? __ldg(a.col_idx + at - 1) : -1;
+            j = __ldg(a.col_idx + at);
+            if (j < 0 || j >= nb || j <= prev) {
+              status |= SA_DEV_BAD_ROUTE;
+              j = -1;
+            }
+          }
+          if (j >= 0) {
+            page = __ldg(a.pm.table + b * a.pm.table_stride + j);
+            live = min(kBlock, n - j * kBlock);
+            if (page < 0 || page >= a.pm.n_pages) {
+              status |= SA_DEV_BAD_CACHE;
+              live = 0;
+            }
+          }
+        }
+        const int m = min(32, take - q0);
+        for (int x = 0; x < m; ++x) {
+          const int pg = __shfl_sync(0xffffffffu, page, x);
+          const int lv = __shfl_sync(0xffffffffu, live, x);
+          const int s = static_cast<int>(issued % NS);
+          const uint32_t ph = static_cast<uint32_t>(issued / NS) & 1u;
+          if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            meta[s] = PageMeta{lv, (q0 + x == 0 ? 1 : 0) | (q0 + x == take - 1 ? 2 : 0), unit, dest};
+            const uint32_t bar = smem_u32(&full[s]);
+            if (lv > 0) {
+              mbar_arrive_expect_tx(bar, S::kStage);
+              const uint32_t dst = ring + s * S::kStage;
+              constexpr int kElts = kFp8 ? S::kBox : S::kBox / 2;    // elements of a box row
+#pragma unroll
+              for (int i = 0; i < D / kElts; ++i) {
+                tma_load_4d(dst + i * kBlock * S::kBox, &kmap, bar, i * kElts, 0, g, pg);
+                tma_load_4d(dst + S::kPage + i * kBlock * S::kBox, &vmap, bar, i * kElts, 0, g, pg);
+              }
+            } else {
+              mbar_arrive(bar);
+            }
+          }
+          __syncwarp();
+          ++issued;
+        }
+      }
+      off += take;
+      left -= take;
+    }
+    if (lane == 0) {
+      if (!by_unit) cuts[c] = cut;
+      if (!ok) {
+        abort_flag = 1;
+        status |= SA_DEV_TIMEOUT;
+      }
+      // no copy may be in flight when the CTA ends
+      const volatile int never = 0;
+      for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+        mbar_wait(smem_u32(&full[i % NS]), static_cast<uint32_t>(i / NS) & 1u,
+                  AbortSignal{&never, nullptr});
+    }
+  } else {
+    // --------------------------------------------------------- consumers --
+    const int rg = warp / S::kKeyWarps, kw = warp % S::kKeyWarps;
+    const int r = lane >> 2, cq = lane & 3;
+    const int n_pages = static_cast<int>(hi - lo);
+    uint32_t qa[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2], f[2];                  // rows r and r + 8 of the warp's 16
+    uint32_t join_phase = 0;
+    bool ok = true;
+    // all consumer warps meet; false if one of them gave up
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&joined));
+      const bool done = mbar_wait_warp(smem_u32(&joined), join_phase, abort);
+      join_phase ^= 1u;
+      return done;
+    };
+    for (int i = 0; i < n_pages; ++i) {
+      const int s = i % NS;
+      if (!mbar_wait_warp(smem_u32(&full[s]), static_cast<uint32_t>(i / NS) & 1u, abort)) {
+        ok = false;
+        break;
+      }
+      const PageMeta pm = meta[s];
+      const int rt = pm.unit % RT, bg = pm.unit / RT, b = bg / a.Hkv, g = bg % a.Hkv;
+      if (pm.flags & 1) {
+        // the unit's queries as A fragments, rows beyond the group's heads zero
+        const float base = a.scale_log2 * (kFp8 && a.k_scale ? __ldg(a.k_scale + g) : 1.f);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = rt * S::kRows + rg * 16 + r + 8 * x;
+          const bool there = row < G;
+          const uint16_t* q = a.q + b * a.qs[0] + (g * G + (there ? row : 0)) * a.qs[2];
+          f[x] = base;
+          if (!kFp8) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              qa[k][x] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * cq) : 0u;
+              qa[k][2 + x] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * cq + 8) : 0u;
+            }
+          } else {
+            // in fp16, a row scaled by a power of two so that its largest
+            // element is in [2^14, 2^15): bits are lost only below 2^-39 of it
+            uint2 w[D / 16];
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              w[k] = there ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * cq) : make_uint2(0u, 0u);
+              top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_f32(w[k].x)), fabsf(hi_f32(w[k].x))),
+                                     fmaxf(fabsf(lo_f32(w[k].y)), fabsf(hi_f32(w[k].y)))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
+            // 2^e in two steps: 14 - e of a subnormal is beyond one float
+            const float up1 = ldexpf(1.f, e / 2), up2 = ldexpf(1.f, e - e / 2);
+            f[x] = base * ldexpf(1.f, -(e / 2)) * ldexpf(1.f, -(e - e / 2));
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              qa[k][x] = pack_half(lo_f32(w[k].x) * up1 * up2, hi_f32(w[k].x) * up1 * up2);
+              qa[k][2 + x] = pack_half(lo_f32(w[k].y) * up1 * up2, hi_f32(w[k].y) * up1 * up2);
+            }
+          }
+          m[x] = -INFINITY;
+          l[x] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      }
+      const uint32_t kp = ring + s * S::kStage, vp = kp + S::kPage;
+#pragma unroll 1
+      for (int sl = 0; sl < S::kSlices; ++sl) {
+        const int k0 = 16 * (kw * S::kSlices + sl), live = pm.live - k0;   // first key, keys that count
+        if (live <= 0) break;
+        float sc[2][4] = {};
+        if (!kFp8) {
+          const int row = k0 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t kb[4];
+            ldsm4(kb, kp + piece_at<D, kFp8, RG>(row, 2 * k + half));
+            mma<false>(sc[0], qa[k], kb[0], kb[1]);
+            mma<false>(sc[1], qa[k], kb[2], kb[3]);
+          }
+        } else {
+          const int row = k0 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t kb[4];
+            ldsm4(kb, kp + piece_at<D, kFp8, RG>(row, 2 * k + half));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              mma<true>(sc[0], qa[2 * k + x], e4m3x2_half2(kb[x]), e4m3x2_half2(kb[x] >> 16));
+              mma<true>(sc[1], qa[2 * k + x], e4m3x2_half2(kb[2 + x]), e4m3x2_half2(kb[2 + x] >> 16));
+            }
+          }
+        }
+        // lane's scores: rows r (0, 1) and r + 8 (2, 3), keys 8 t + 2 cq + {0, 1}
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            sc[t][x] = 8 * t + 2 * cq + (x & 1) < live ? sc[t][x] * f[x >> 1] : -INFINITY;
+            top[x >> 1] = fmaxf(top[x >> 1], sc[t][x]);
+          }
+        float shift[2];
+        bool grew = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+          grew |= top[x] > m[x];
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+          float corr[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float now = fmaxf(m[x], top[x]);
+            corr[x] = now == -INFINITY ? 1.f : ex2(m[x] - now);
+            m[x] = now;
+            l[x] *= corr[x];
+          }
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][0] *= corr[0];
+            o[j][1] *= corr[0];
+            o[j][2] *= corr[1];
+            o[j][3] *= corr[1];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          shift[x] = (m[x] == -INFINITY ? 0.f : m[x]) - (kFp8 ? kFp16Shift : 0.f);
+        uint32_t hi[4], lw[4];               // P as A fragments
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float p0 = ex2(sc[t][2 * x] - shift[x]), p1 = ex2(sc[t][2 * x + 1] - shift[x]);
+            l[x] += p0 + p1;
+            if (kFp8) {
+              hi[2 * t + x] = pack_half(p0, p1);
+            } else {
+              hi[2 * t + x] = pack_bf16(p0, p1);
+              lw[2 * t + x] = pack_bf16(p0 - lo_f32(hi[2 * t + x]), p1 - hi_f32(hi[2 * t + x]));
+            }
+          }
+        // V: a key that does not count has weight 0, and whatever lies there
+        // (NaN) must not meet it
+        const bool part = live < 16;
+        uint32_t keep[2] = {~0u, ~0u};
+        if (part) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int k = 8 * t + 2 * cq;
+            keep[t] = (k < live ? 0xffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
+          }
+        }
+        const int row = k0 + (lane & 15);
+        if (!kFp8) {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t vb[4];
+            ldsm4_t(vb, vp + piece_at<D, kFp8, RG>(row, 2 * j + (lane >> 4)));
+            if (part)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) vb[x] &= keep[x & 1];
+            mma<false>(o[2 * j], hi, vb[0], vb[1]);
+            mma<false>(o[2 * j + 1], hi, vb[2], vb[3]);
+            mma<false>(o[2 * j], lw, vb[0], vb[1]);
+            mma<false>(o[2 * j + 1], lw, vb[2], vb[3]);
+          }
+        } else {
+          // a transposed 16-bit element is two neighbouring dims: the even ones
+          // make one column tile, the odd ones the next
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            uint32_t vb[4];
+            ldsm4_t(vb, vp + piece_at<D, kFp8, RG>(row, 2 * j + (lane >> 4)));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (part) {
+                vb[2 * x] &= keep[0];
+                vb[2 * x + 1] &= keep[1];
+              }
+              const uint32_t u0 = __byte_perm(vb[2 * x], 0, 0x3120);
+              const uint32_t u1 = __byte_perm(vb[2 * x + 1], 0, 0x3120);
+              mma<true>(o[4 * j + 2 * x], hi, e4m3x2_half2(u0), e4m3x2_half2(u1));
+              mma<true>(o[4 * j + 2 * x + 1], hi, e4m3x2_half2(u0 >> 16), e4m3x2_half2(u1 >> 16));
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
+
+      if (pm.flags & 2) {
+        // the piece ends: the key warps' results are added
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+          l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+          if (cq == 0) {
+            sm_m[warp][r + 8 * x] = m[x];
+            sm_l[warp][r + 8 * x] = l[x];
+          }
+        }
+        if (!meet()) {
+          ok = false;
+          break;
+        }
+        float w[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < S::kKeyWarps; ++k)
+            top = fmaxf(top, sm_m[rg * S::kKeyWarps + k][r + 8 * x]);
+          w[x] = m[x] == -INFINITY ? 0.f : ex2(m[x] - top);
+        }
+        float* part = partial + static_cast<int64_t>(2 * c + max(pm.dest, 0)) * S::kRows * (D + 2);
+        constexpr int kQuads = S::kChunk / 4;
+        constexpr int kElems = S::kRows * kQuads, kIter = (kElems + 32 * W - 1) / (32 * W);
+#pragma unroll 1
+        for (int ch = 0; ch < D / S::kChunk; ++ch) {
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            if (j / (S::kChunk / 8) != ch) continue;
+            // columns of the tile: consecutive, or (e4m3) every second dim of 16
+            float* row0 = join + (warp * 16 + r) * S::kPad;
+            float* row1 = row0 + 8 * S::kPad;
+            if (!kFp8) {
+              const int col = (j % (S::kChunk / 8)) * 8 + 2 * cq;
+              *reinterpret_cast<float2*>(row0 + col) = make_float2(o[j][0] * w[0], o[j][1] * w[0]);
+              *reinterpret_cast<float2*>(row1 + col) = make_float2(o[j][2] * w[1], o[j][3] * w[1]);
+            } else {
+              const int col = (j % (S::kChunk / 8) / 2) * 16 + 4 * cq + (j & 1);
+              row0[col] = o[j][0] * w[0];
+              row0[col + 2] = o[j][1] * w[0];
+              row1[col] = o[j][2] * w[1];
+              row1[col + 2] = o[j][3] * w[1];
+            }
+          }
+          if (!meet()) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int it = 0; it < kIter; ++it) {
+            const int e = it * 32 * W + warp * 32 + lane;
+            if (kElems % (32 * W) != 0 && e >= kElems) break;
+            const int row = e / kQuads, col = e % kQuads * 4, grp = row >> 4, rr = row & 15;
+            const int head = rt * S::kRows + row;
+            if (head >= G) continue;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float top = -INFINITY, tot = 0.f;
+#pragma unroll
+            for (int k = 0; k < S::kKeyWarps; ++k) {
+              const int wp = grp * S::kKeyWarps + k;
+              const float4 v = *reinterpret_cast<const float4*>(join + (wp * 16 + rr) * S::kPad + col);
+              sum.x += v.x;
+              sum.y += v.y;
+              sum.z += v.z;
+              sum.w += v.w;
+              top = fmaxf(top, sm_m[wp][rr]);
+            }
+#pragma unroll
+            for (int k = 0; k < S::kKeyWarps; ++k) {
+              const int wp = grp * S::kKeyWarps + k;
+              // without a maximum the sum is 0, or NaN if only NaN was there
+              tot += sm_m[wp][rr] == -INFINITY ? sm_l[wp][rr] : sm_l[wp][rr] * ex2(sm_m[wp][rr] - top);
+            }
+            const int col_g = ch * S::kChunk + col;
+            if (pm.dest < 0) {
+              const float inv = tot == 0.f ? 0.f : (a.v_scale ? __ldg(a.v_scale + g) : 1.f) / tot;
+              const int h = g * G + head;
+              *reinterpret_cast<uint2*>(a.o + b * a.os[0] + h * a.os[2] + col_g) = make_uint2(
+                  pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+              if (col_g == 0 && a.lse)
+                a.lse[static_cast<int64_t>(b) * a.H + h] =
+                    tot == 0.f ? -INFINITY
+                               : (top - (kFp8 ? kFp16Shift : 0.f) + log2f(tot)) * 0.69314718055994530942f;
+            } else {
+              *reinterpret_cast<float4*>(part + row * D + col_g) = sum;
+              if (col_g == 0) {
+                part[S::kRows * D + row] = top;
+                part[S::kRows * D + S::kRows + row] = tot;
+              }
+            }
+          }
+          // the buffer is written again only after every warp has read it
+          if (!meet()) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      status |= SA_DEV_TIMEOUT;
     }
   }
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-  const float ks = a.k_scale ? a.k_scale[g] : 1.f, vs = a.v_scale ? a.v_scale[g] : 1.f;
-  for (int i = 0; i < nd; ++i)
-    q[i] = load<false>(a.q, b * a.qs[0] + h * a.qs[2] + lane + 32 * i);
-  float m = -INFINITY, l = 0.f;
-  for (int e = beg; e < end; ++e) {
-    const int j = a.row_ptr ? a.col_idx[e] : e;
-    if (j < 0 || j >= nb || (a.row_ptr && e > beg && j <= a.col_idx[e - 1])) {
-      status |= SA_DEV_BAD_ROUTE;
+  if (status && a.dev_status) atomicOr(a.dev_status, status);
+}
+
+// grid (min(units, runs), heads of a unit), 256 threads: adds the pieces of one
+// cut unit for one query head, eight warps taking every eighth piece.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* partial,
+            const Cut* cuts) {
+  __shared__ float sm_o[kJoinWarps][D];
+  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Cut cut = cuts[blockIdx.x];
+  const int units = a.B * a.Hkv * RT;
+  if (cut.unit < 0 || cut.unit >= units || cut.last <= cut.first || cut.last >= runs) return;
+  const int G = a.H / a.Hkv, rt = cut.unit % RT, bg = cut.unit / RT;
+  const int b = bg / a.Hkv, g = bg % a.Hkv, row = blockIdx.y, head = rt * rows + row;
+  if (head >= G) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int V = D / 32;
+  const int64_t stride = static_cast<int64_t>(rows) * (D + 2);
+  // piece 0 is the second partial of its run (the run ends in it), the others the first
+  auto piece = [&](int i) {
+    return partial + stride * (2 * static_cast<int64_t>(cut.first + i) + (i == 0 ? 1 : 0));
+  };
+  const int n = cut.last - cut.first + 1;
+  float o[V] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kJoinWarps) {
+    const float* p = piece(i);
+    const float pm = p[rows * D + row], pl = p[rows * D + rows + row];
+    float v[V];
+#pragma unroll
+    for (int x = 0; x < V; ++x) v[x] = p[row * D + lane + 32 * x];
+    if (pm == -INFINITY) {                   // nothing counted there (a sum of 0, or NaN)
+      l += pl;
       continue;
     }
-    const int page = a.pm.table[b * a.pm.table_stride + j];
-    if (page < 0 || page >= a.pm.n_pages) {
-      status |= SA_DEV_BAD_CACHE;
-      continue;
-    }
-    const int live = min(kBlock, n - j * kBlock);
-    for (int s = 0; s < live; ++s) {
-      float x = 0.f;
-      const int64_t kat = page * a.kcs[0] + g * a.kcs[1] + s * a.kcs[2] + lane;
-      const int64_t vat = page * a.vcs[0] + g * a.vcs[1] + s * a.vcs[2] + lane;
-      for (int i = 0; i < nd; ++i) x = fmaf(q[i], load<kFp8>(a.kc, kat + 32 * i), x);
-      for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-      x *= a.scale_log2 * ks;
-      const float mn = fmaxf(m, x), c = mn == -INFINITY ? 1.f : exp2f(m - mn);
-      const float p = mn == -INFINITY ? 0.f : exp2f(x - mn);
-      m = mn;
-      l = l * c + p;
-      for (int i = 0; i < nd; ++i) o[i] = fmaf(p, load<kFp8>(a.vc, vat + 32 * i), o[i] * c);
-    }
+    const float now = fmaxf(m, pm), c0 = m == -INFINITY ? 0.f : ex2(m - now), c1 = ex2(pm - now);
+    l = (m == -INFINITY ? l : l * c0) + pl * c1;
+    m = now;
+#pragma unroll
+    for (int x = 0; x < V; ++x) o[x] = o[x] * c0 + v[x] * c1;
   }
-  const float inv = l > 0.f ? vs / l : (l == 0.f ? 0.f : l);
-  for (int i = 0; i < nd; ++i)
-    a.o[b * a.os[0] + h * a.os[2] + lane + 32 * i] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-  if (lane == 0 && a.lse)
-    a.lse[b * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-  if (status && lane == 0 && a.dev_status) atomicOr(a.dev_status, status);
+#pragma unroll
+  for (int x = 0; x < V; ++x) sm_o[warp][lane + 32 * x] = o[x];
+  if (lane == 0) {
+    sm_m[warp] = m;
+    sm_l[warp] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float top = -INFINITY, tot = 0.f, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sm_m[w]);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (sm_m[w] == -INFINITY) {
+      tot += sm_l[w];
+      continue;
+    }
+    const float c = ex2(sm_m[w] - top);
+    tot += sm_l[w] * c;
+    sum += sm_o[w][threadIdx.x] * c;
+  }
+  const float inv = tot == 0.f ? 0.f : (a.v_scale ? a.v_scale[g] : 1.f) / tot;
+  const int h = g * G + head;
+  a.o[b * a.os[0] + h * a.os[2] + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(sum * inv));
+  if (threadIdx.x == 0 && a.lse)
+    a.lse[static_cast<int64_t>(b) * a.H + h] =
+        tot == 0.f ? -INFINITY : (top - shift + log2f(tot)) * 0.69314718055994530942f;
+}
+
+// Row groups a CTA holds for G query heads per key-value head.
+int row_groups(int G) { return G <= 16 ? 1 : (G <= 32 ? 2 : 4); }
+
+size_t cuts_bytes() { return (sizeof(Cut) * kMaxRuns + 255) & ~static_cast<size_t>(255); }
+
+template <int D, bool kFp8, int RG>
+cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                   cudaStream_t st) {
+  using S = Shape<D, kFp8, RG>;
+  static_assert(S::kCtas * (S::kSmem + 4096) <= 227 * 1024, "the ring does not fit shared memory");
+  const int G = a.H / a.Hkv, RT = (G + S::kRows - 1) / S::kRows;
+  Cut* cuts = reinterpret_cast<Cut*>(a.ws);
+  float* partial = reinterpret_cast<float*>(a.ws + cuts_bytes());
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kFp8, RG>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * RT;
+  decode_kernel<D, kFp8, RG><<<S::kRuns, S::kThreads, S::kSmem, st>>>(kmap, vmap, a, RT, partial, cuts);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(units < S::kRuns ? units : S::kRuns),
+                     static_cast<unsigned>(G < S::kRows ? G : S::kRows));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, RT, S::kRows, S::kRuns,
+                            kFp8 ? kFp16Shift : 0.f, static_cast<const float*>(partial),
+                            static_cast<const Cut*>(cuts));
+}
+
+template <int D, bool kFp8>
+cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                     cudaStream_t st) {
+  switch (row_groups(a.H / a.Hkv)) {
+    case 1: return launch<D, kFp8, 1>(a, kmap, vmap, st);
+    case 2: return launch<D, kFp8, 2>(a, kmap, vmap, st);
+    default: return launch<D, kFp8, 4>(a, kmap, vmap, st);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
-  const dim3 grid(a.B, a.H);
-  if (fp8)
-    decode_kernel<true><<<grid, 32, 0, st>>>(a);
-  else
-    decode_kernel<false><<<grid, 32, 0, st>>>(a);
-  return cudaGetLastError();
+size_t decode_ws_bytes(int H, int Hkv, int D) {
+  const size_t rows = 16 * static_cast<size_t>(row_groups(H / Hkv));
+  return cuts_bytes() + static_cast<size_t>(2 * kMaxRuns) * rows * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          bool fp8, cudaStream_t st) {
+  if (a.D == 64)
+    return fp8 ? launch_d<64, true>(a, kmap, vmap, st) : launch_d<64, false>(a, kmap, vmap, st);
+  return fp8 ? launch_d<128, true>(a, kmap, vmap, st) : launch_d<128, false>(a, kmap, vmap, st);
 }
 
 }  // namespace sa

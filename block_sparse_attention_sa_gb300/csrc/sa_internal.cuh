@@ -14,6 +14,13 @@ constexpr int kBlock = 64;          // query/key block (tokens)
 constexpr int kMaxNbAttn = 4096;    // key blocks the attention tile can list
 constexpr int kScoreTile = 64;      // pooled-score tile (query blocks x key blocks)
 
+// cuTensorMapEncodeTiled, looked up once in the driver (null if it has none).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 inline int num_blocks(int S) { return (S + kBlock - 1) / kBlock; }
 
 // ------------------------------------------------------------ routing ---
