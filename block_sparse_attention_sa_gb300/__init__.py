@@ -27,6 +27,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -463,6 +464,14 @@ def alloc_layer_buffers(B: int, S: int, H: int, D: int, device="cuda", qk_format
 
 
 # ------------------------------------------------------ paged key-value cache --
+#
+# One call of these serves one token, so its own cost counts: the parameters are
+# packed in one step, the raw stream is asked for without building an object,
+# and each tensor's shape and strides are read once.
+
+_CACHE_PACK = struct.Struct("=14i2f19q").pack
+_NO_STRIDES = (0, 0, 0)
+
 
 def _on_device(fn):
     """The call with its first tensor's device current, so that it is enqueued
@@ -471,11 +480,17 @@ def _on_device(fn):
     def call(t, *args, **kwargs):
         if not t.is_cuda:
             raise ValueError("tensors must be on a CUDA device: there is no CPU path")
-        if t.device.index == torch.cuda.current_device():
+        if t.get_device() == torch._C._cuda_getDevice():
             return fn(t, *args, **kwargs)
         with torch.cuda.device(t.device):
             return fn(t, *args, **kwargs)
     return call
+
+
+def _raw_stream(device, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -488,29 +503,27 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _need(t: Optional[torch.Tensor], name: str, device, dtype, shape=None) -> None:
-    """A contiguous tensor (or None) of this device, type and shape."""
-    if t is None:
-        return
+def _need(t: torch.Tensor, name: str, device, dtype, shape=None) -> int:
+    """The address of a contiguous tensor of this device, type and shape."""
     if t.device != device or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _need_tokens(t: torch.Tensor, name: str, device, shape) -> None:
+def _need_tokens(t: torch.Tensor, name: str, device, shape) -> int:
     if t.device != device or t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be a bf16 tensor on {device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _need_map(page_table, seq_lens, device) -> None:
-    if (page_table.device != device or page_table.dtype != torch.int32 or page_table.dim() != 2
-            or (page_table.stride(1) != 1 and page_table.shape[1] != 1)):
-        raise ValueError(f"page_table must be int32 [B, max_pages] on {device}, its rows contiguous")
-    if seq_lens is not None:
-        _need(seq_lens, "seq_lens", device, torch.int32, page_table.shape[:1])
+    if page_table.device != device:
+        raise ValueError(f"page_table must be on {device}")
+    _need(seq_lens, "seq_lens", device, torch.int32, page_table.shape[:1])
 
 
 def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = None,
@@ -518,36 +531,51 @@ def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = N
                       o: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
                       v_cache: Optional[torch.Tensor] = None,
                       k_sum: Optional[torch.Tensor] = None, scale: float = 0.0,
-                      prefix_len: int = 0, budget: int = 0) -> sa_cache_params:
+                      prefix_len: int = 0, budget: int = 0, qk_norm: bool = False,
+                      rope="interleaved", rope_rows: int = 0,
+                      eps: float = 1e-6) -> sa_cache_params:
     """The parameters of a paged-cache call on these tensors (those it takes):
     q, k, v, o [B, S, heads, D]; k_cache, v_cache [n_pages, H_kv, 64, D] in
     bf16, or e4m3 as float8_e4m3fn or uint8; k_sum [n_pages, H_kv, D]."""
-    p = sa_cache_params()
-    pool = k_cache if k_cache is not None else k_sum
-    if pool is None or pool.dim() != (4 if k_cache is not None else 3):
-        raise ValueError("k_cache must be [n_pages, H_kv, 64, D], k_sum [n_pages, H_kv, D]")
-    p.n_pages, p.H_kv, p.D = pool.shape[0], pool.shape[1], pool.shape[-1]
-    p.B, p.max_pages = page_table.shape
-    p.page, p.table_stride = PAGE, page_table.stride(0)
-    p.prefix_len, p.page_budget, p.softmax_scale = int(prefix_len), int(budget), float(scale)
-    for field, t in (("q_stride", q), ("k_stride", k), ("v_stride", v), ("o_stride", o)):
-        if t is not None:
-            getattr(p, field)[:] = _bshd_strides(t, field[0])
-    tokens = q if q is not None else k
-    p.S = 1 if tokens is None else tokens.shape[1]
-    p.H = p.H_kv if q is None else q.shape[2]
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2
+            or (page_table.stride(1) != 1 and page_table.shape[1] != 1)):
+        raise ValueError("page_table must be int32 [B, max_pages], its rows contiguous")
+    kst = vst = _NO_STRIDES
+    fmt = SA_CACHE_BF16
     if k_cache is not None:
-        for field, t in (("kc_stride", k_cache), ("vc_stride", v_cache)):
-            if (t.shape != k_cache.shape or t.shape[2] != PAGE or t.stride(3) != 1
-                    or t.dtype != k_cache.dtype or t.device != page_table.device):
-                raise ValueError("k_cache, v_cache must be alike, [n_pages, H_kv, 64, D] with a "
-                                 "contiguous last dimension, on the page table's device")
-            st = t.stride()
-            getattr(p, field)[:] = (st[0], st[1], st[2])
-        if k_cache.dtype not in CACHE_FORMATS:
+        shape = k_cache.shape
+        fmt = CACHE_FORMATS.get(k_cache.dtype)
+        if fmt is None:
             raise ValueError("k_cache, v_cache must be bfloat16, float8_e4m3fn or uint8 (e4m3)")
-        p.cache_format = CACHE_FORMATS[k_cache.dtype]
-    return p
+        if (len(shape) != 4 or shape[2] != PAGE or v_cache.shape != shape
+                or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device
+                or k_cache.device != page_table.device):
+            raise ValueError("k_cache, v_cache must be alike, [n_pages, H_kv, 64, D], on the page "
+                             "table's device")
+        kst, vst = k_cache.stride(), v_cache.stride()
+        if kst[3] != 1 or vst[3] != 1:
+            raise ValueError("k_cache, v_cache must have a contiguous last dimension")
+    elif k_sum is not None and k_sum.dim() == 3:
+        shape = k_sum.shape
+    else:
+        raise ValueError("k_cache must be [n_pages, H_kv, 64, D], k_sum [n_pages, H_kv, D]")
+    qst = _NO_STRIDES if q is None else _bshd_strides(q, "q")
+    kt = _NO_STRIDES if k is None else _bshd_strides(k, "k")
+    vt = _NO_STRIDES if v is None else _bshd_strides(v, "v")
+    ost = _NO_STRIDES if o is None else _bshd_strides(o, "o")
+    tokens = q if q is not None else k
+    B, max_pages = page_table.shape
+    if isinstance(rope, str):
+        rope = ROPE_LAYOUTS[rope]
+    try:
+        packed = _CACHE_PACK(
+            B, 1 if tokens is None else tokens.shape[1], shape[1] if q is None else q.shape[2],
+            shape[1], shape[-1], PAGE, shape[0], max_pages, fmt, prefix_len, budget,
+            1 if qk_norm else 0, rope, rope_rows, eps, scale, page_table.stride(0), *qst, *kt,
+            *vt, *ost, *kst[:3], *vst[:3])
+    except struct.error as err:
+        raise ValueError(f"a cache parameter is out of range: {err}") from None
+    return sa_cache_params.from_buffer_copy(packed)
 
 
 @_on_device
@@ -567,43 +595,43 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     cache behind each sequence's ``seq_lens`` tokens, normed (``qk_norm``) and
     rotated (``cos``, ``sin`` fp32 [rows, D/2] by position; ``rope``
     "interleaved" or "half") on the way; see sa.h. With ``q`` [B, S, H, D]
-    returns the queries normed and rotated alike (``q_out``, default new with
-    q's strides; pass q_out=q for in place). ``new_lens``: how many of the S
-    tokens each sequence brings. ``k_sum`` gathers the per-page key sums that
-    sa_route_pages reads; ``lens_out`` receives the new lengths."""
-    dev = k.device
-    B, S, Hkv, D = k.shape
-    _need_tokens(v, "v", dev, k.shape)
-    _need_tokens(k, "k", dev, (page_table.shape[0], S, k_cache.shape[1], k_cache.shape[-1]))
-    if q is not None:
-        _need_tokens(q, "q", dev, (B, S, q.shape[2], D))
-        if q_out is None:
-            q_out = _empty((B, S, q.shape[2], D), q.dtype, dev, stream)
-        _need_tokens(q_out, "q_out", dev, q.shape)
-    elif q_out is not None:
+    returns the queries normed and rotated alike (``q_out``, default new; pass
+    q_out=q for in place). ``new_lens``: how many of the S tokens each sequence
+    brings. ``k_sum`` gathers the per-page key sums that sa_route_pages reads;
+    ``lens_out`` receives the new lengths."""
+    dev, f32, i32 = k.device, torch.float32, torch.int32
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, q.dtype, dev, stream)
+    elif q is None and q_out is not None:
         raise ValueError("q_out without q")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    p = make_cache_params(page_table, q=q, k=k, v=v, o=q_out, k_cache=k_cache, v_cache=v_cache,
+                          qk_norm=qk_norm, rope=rope, eps=eps,
+                          rope_rows=0 if cos is None else cos.shape[0])
+    B, S, Hkv, D = shape = (p.B, k.shape[1], p.H_kv, p.D)
     _need_map(page_table, seq_lens, dev)
-    _need(new_lens, "new_lens", dev, torch.int32, (B,))
-    _need(lens_out, "lens_out", dev, torch.int32, (B,))
-    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-        _need(t, name, dev, torch.float32, (D,))
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _need(t, name, dev, torch.float32, (Hkv,))
-    _need(k_sum, "k_sum", dev, torch.float32, (k_cache.shape[0], Hkv, D))
-    _need(dev_status, "dev_status", dev, torch.int32)
-    p = make_cache_params(page_table, q=q, k=k, v=v, o=q_out, k_cache=k_cache, v_cache=v_cache)
-    if cos is not None:
-        _need(cos, "cos", dev, torch.float32, (cos.shape[0], D // 2))
-        _need(sin, "sin", dev, torch.float32, cos.shape)
-        p.rope_rows = cos.shape[0]
-    p.qk_norm, p.eps = int(bool(qk_norm)), float(eps)
-    p.rope_layout = ROPE_LAYOUTS[rope] if isinstance(rope, str) else int(rope)
+    qp = qo = None
+    if q is not None:
+        shape_q = (B, S, p.H, D)
+        qp, qo = _need_tokens(q, "q", dev, shape_q), _need_tokens(q_out, "q_out", dev, shape_q)
     code = load_library().sa_cache_append(
-        ctypes.byref(p), _ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(gamma_q), _ptr(gamma_k),
-        _ptr(cos), _ptr(sin), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(k_sum), _ptr(page_table), _ptr(seq_lens), _ptr(new_lens), _ptr(lens_out),
-        _ptr(dev_status), _stream(stream))
-    _check(code, "sa_cache_append")
+        ctypes.byref(p), _need_tokens(k, "k", dev, shape), _need_tokens(v, "v", dev, shape), qp, qo,
+        None if gamma_q is None else _need(gamma_q, "gamma_q", dev, f32, (D,)),
+        None if gamma_k is None else _need(gamma_k, "gamma_k", dev, f32, (D,)),
+        None if cos is None else _need(cos, "cos", dev, f32, (p.rope_rows, D // 2)),
+        None if sin is None else _need(sin, "sin", dev, f32, (p.rope_rows, D // 2)),
+        k_cache.data_ptr(), v_cache.data_ptr(),
+        None if k_scale is None else _need(k_scale, "k_scale", dev, f32, (Hkv,)),
+        None if v_scale is None else _need(v_scale, "v_scale", dev, f32, (Hkv,)),
+        None if k_sum is None else _need(k_sum, "k_sum", dev, f32, (p.n_pages, Hkv, D)),
+        page_table.data_ptr(), seq_lens.data_ptr(),
+        None if new_lens is None else _need(new_lens, "new_lens", dev, i32, (B,)),
+        None if lens_out is None else _need(lens_out, "lens_out", dev, i32, (B,)),
+        None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
+        _raw_stream(dev, stream))
+    if code:
+        _check(code, "sa_cache_append")
     return q_out
 
 
@@ -619,12 +647,11 @@ def sa_attn_decode_workspace_bytes(p: sa_cache_params) -> int:
     return int(load_library().sa_attn_decode_workspace_bytes(ctypes.byref(p)))
 
 
-def _cache_workspace(need: int, device, ws: Optional[torch.Tensor], stream) -> torch.Tensor:
-    if ws is None:
-        return _empty((max(need, 256),), torch.uint8, device, stream)
-    if ws.device != device or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
-        raise ValueError(f"workspace must be contiguous, on {device} and hold {need} bytes")
-    return ws
+def _cache_workspace(ws: torch.Tensor, device) -> Tuple[int, int]:
+    """(address, bytes) of a caller's workspace; the library checks its size."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 @_on_device
@@ -640,25 +667,25 @@ def sa_route_pages(q: torch.Tensor, k_sum: torch.Tensor, page_table: torch.Tenso
     entries are col_idx[:row_ptr[-1]]), for sa_attn_decode. Kept per key-value
     head: the prefix's pages, the newest one, and the best-scoring others until
     ``budget`` are."""
-    dev = q.device
+    dev, i32 = q.device, torch.int32
     p = make_cache_params(page_table, q=q, k_sum=k_sum, prefix_len=prefix_len, budget=budget)
-    _need_tokens(q, "q", dev, (p.B, q.shape[1], q.shape[2], p.D))
-    _need(k_sum, "k_sum", dev, torch.float32)
     _need_map(page_table, seq_lens, dev)
-    _need(dev_status, "dev_status", dev, torch.int32)
     rows = p.B * p.H_kv
     if row_ptr is None:
-        row_ptr = _empty((rows + 1,), torch.int32, dev, stream)
-    _need(row_ptr, "row_ptr", dev, torch.int32, (rows + 1,))
+        row_ptr = _empty((rows + 1,), i32, dev, stream)
     if col_idx is None:
-        col_idx = _empty((sa_route_pages_max_nnz(p),), torch.int32, dev, stream)
-    _need(col_idx, "col_idx", dev, torch.int32)
-    ws = _cache_workspace(sa_route_pages_workspace_bytes(p), dev, workspace, stream)
+        col_idx = _empty((sa_route_pages_max_nnz(p),), i32, dev, stream)
+    if workspace is None:
+        workspace = _empty((max(256, sa_route_pages_workspace_bytes(p)),), torch.uint8, dev, stream)
     code = load_library().sa_route_pages(
-        ctypes.byref(p), _ptr(q), _ptr(k_sum), _ptr(page_table), _ptr(seq_lens), _ptr(row_ptr),
-        _ptr(col_idx), col_idx.numel(), _ptr(ws), ws.numel() * ws.element_size(),
-        _ptr(dev_status), _stream(stream))
-    _check(code, "sa_route_pages")
+        ctypes.byref(p), _need_tokens(q, "q", dev, (p.B, p.S, p.H, p.D)),
+        _need(k_sum, "k_sum", dev, torch.float32), page_table.data_ptr(), seq_lens.data_ptr(),
+        _need(row_ptr, "row_ptr", dev, i32, (rows + 1,)), _need(col_idx, "col_idx", dev, i32),
+        col_idx.numel(), *_cache_workspace(workspace, dev),
+        None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
+        _raw_stream(dev, stream))
+    if code:
+        _check(code, "sa_route_pages")
     return row_ptr, col_idx
 
 
@@ -676,29 +703,33 @@ def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``seq_lens`` cached tokens, or over the pages a route lists (row_ptr,
     col_idx from sa_route_pages): (o bf16 [B, 1, H, D], lse fp32 [B, H, 1] or
     None). H is a multiple of the cache's H_kv."""
-    dev = q.device
+    dev, f32, i32 = q.device, torch.float32, torch.int32
     if o is None:
         o = _empty(q.shape, q.dtype, dev, stream)
     p = make_cache_params(page_table, q=q, o=o, k_cache=k_cache, v_cache=v_cache, scale=scale)
-    shape = (p.B, q.shape[1], q.shape[2], p.D)
-    _need_tokens(q, "q", dev, shape)
-    _need_tokens(o, "o", dev, shape)
+    B, H = p.B, p.H
+    shape = (B, p.S, H, p.D)
     if lse is None and want_lse:
-        lse = _empty((p.B, p.H, 1), torch.float32, dev, stream)
-    _need(lse, "lse", dev, torch.float32, (p.B, p.H, 1))
+        lse = _empty((B, H, 1), f32, dev, stream)
+    if workspace is None:
+        workspace = _empty((max(256, sa_attn_decode_workspace_bytes(p)),), torch.uint8, dev, stream)
+    if (row_ptr is None) != (col_idx is None):
+        raise ValueError("row_ptr and col_idx go together")
     _need_map(page_table, seq_lens, dev)
-    _need(row_ptr, "row_ptr", dev, torch.int32, (p.B * p.H_kv + 1,))
-    _need(col_idx, "col_idx", dev, torch.int32)
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _need(t, name, dev, torch.float32, (p.H_kv,))
-    _need(dev_status, "dev_status", dev, torch.int32)
-    ws = _cache_workspace(sa_attn_decode_workspace_bytes(p), dev, workspace, stream)
     code = load_library().sa_attn_decode(
-        ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(page_table), _ptr(seq_lens), _ptr(row_ptr), _ptr(col_idx),
-        0 if col_idx is None else col_idx.numel(), _ptr(o), _ptr(lse), _ptr(ws),
-        ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream))
-    _check(code, "sa_attn_decode")
+        ctypes.byref(p), _need_tokens(q, "q", dev, shape), k_cache.data_ptr(), v_cache.data_ptr(),
+        None if k_scale is None else _need(k_scale, "k_scale", dev, f32, (p.H_kv,)),
+        None if v_scale is None else _need(v_scale, "v_scale", dev, f32, (p.H_kv,)),
+        page_table.data_ptr(), seq_lens.data_ptr(),
+        None if row_ptr is None else _need(row_ptr, "row_ptr", dev, i32, (B * p.H_kv + 1,)),
+        None if col_idx is None else _need(col_idx, "col_idx", dev, i32),
+        0 if col_idx is None else col_idx.numel(), _need_tokens(o, "o", dev, shape),
+        None if lse is None else _need(lse, "lse", dev, f32, (B, H, 1)),
+        *_cache_workspace(workspace, dev),
+        None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
+        _raw_stream(dev, stream))
+    if code:
+        _check(code, "sa_attn_decode")
     return o, lse
 
 

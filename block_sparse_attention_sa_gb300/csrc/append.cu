@@ -2,6 +2,16 @@
 // k (and of q, which goes out in bf16), the store of k and v as bf16 or e4m3,
 // and the per-page key sums the page router reads.
 //   y = x / sqrt(mean(x^2) + eps) * gamma,  (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c)
+//
+// Every byte is read and written once, so the kernel is bound by the memory, or
+// for one token by its chain of dependent loads (length, page, angle). D / 8
+// lanes hold a head vector, eight elements each: with the halves of a vector as
+// pairs, four from each half, so that both rotations turn pairs a lane holds.
+//
+// One launch, two kinds of CTAs. Key-value CTAs own whole pages of one head: a
+// page's tokens of this call are summed in a fixed order by the lanes that
+// store them, so its k_sum needs no atomics and is the same every time. Query
+// CTAs own one token: its angles are loaded once for all heads.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -10,117 +20,346 @@
 namespace sa {
 namespace {
 
-__device__ __forceinline__ float bits_f32(uint16_t b) {
-  return __uint_as_float(static_cast<uint32_t>(b) << 16);
+constexpr int kThreads = 128;
+constexpr int kQueryHeads = 8;     // heads a lane group has in flight
+constexpr int kTokens = 4;         // tokens a lane group has in flight
+
+struct Vec {                       // a lane's eight elements
+  float x[8];
+};
+
+// Where a lane's elements lie: [8 l, 8 l + 8), or [4 l, 4 l + 4) of each half.
+template <int D, bool kHalf>
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int l) {
+  if (!kHalf) return *reinterpret_cast<const uint4*>(p + 8 * l);
+  const uint2 a = *reinterpret_cast<const uint2*>(p + 4 * l);
+  const uint2 b = *reinterpret_cast<const uint2*>(p + D / 2 + 4 * l);
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-// One thread per (token, head vector): reads it twice (norm, then values).
-template <int D, bool kFp8, bool kHalf>
-__device__ void turn(const AppendArgs& a, const uint16_t* x, const float* gamma, int t, float* y) {
-  for (int d = 0; d < D; ++d) y[d] = bits_f32(x[d]);
+template <int D, bool kHalf>
+__device__ __forceinline__ void store8(uint16_t* p, int l, uint4 w) {
+  if (!kHalf) {
+    *reinterpret_cast<uint4*>(p + 8 * l) = w;
+  } else {
+    *reinterpret_cast<uint2*>(p + 4 * l) = make_uint2(w.x, w.y);
+    *reinterpret_cast<uint2*>(p + D / 2 + 4 * l) = make_uint2(w.z, w.w);
+  }
+}
+
+template <int D, bool kHalf>
+__device__ __forceinline__ void load8f(const float* p, int l, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p + (kHalf ? 4 * l : 8 * l));
+  const float4 b = *reinterpret_cast<const float4*>(p + (kHalf ? D / 2 + 4 * l : 8 * l + 4));
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+template <int D, bool kHalf>
+__device__ __forceinline__ void store8f(float* p, int l, const float* x) {
+  *reinterpret_cast<float4*>(p + (kHalf ? 4 * l : 8 * l)) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + (kHalf ? D / 2 + 4 * l : 8 * l + 4)) =
+      make_float4(x[4], x[5], x[6], x[7]);
+}
+
+__device__ __forceinline__ Vec unpack(uint4 w) {
+  Vec v;
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.x[2 * i] = __uint_as_float(u[i] << 16);
+    v.x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint4 pack(const Vec& v) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x[2 * i], v.x[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// One rounding to the nearest e4m3 code (ties to even), saturating.
+__device__ __forceinline__ uint2 pack_e4m3(const Vec& v, float inv_scale) {
+  uint32_t u[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(v.x[4 * i] * inv_scale, v.x[4 * i + 1] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(v.x[4 * i + 2] * inv_scale, v.x[4 * i + 3] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+    u[i] = lo | (hi << 16);
+  }
+  return make_uint2(u[0], u[1]);
+}
+
+template <int D, bool kHalf>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, int l, uint2 w) {
+  if (!kHalf) {
+    *reinterpret_cast<uint2*>(p + 8 * l) = w;
+  } else {
+    *reinterpret_cast<uint32_t*>(p + 4 * l) = w.x;
+    *reinterpret_cast<uint32_t*>(p + D / 2 + 4 * l) = w.y;
+  }
+}
+
+// The angles of a lane's four pairs at one position.
+struct Angle {
+  float4 c, s;
+};
+
+template <int D>
+__device__ __forceinline__ Angle angle_at(const AppendArgs& a, int t, int l) {
+  Angle g{make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (a.cos) {
+    const int64_t at = static_cast<int64_t>(t) * (D / 2) + 4 * l;
+    g.c = __ldg(reinterpret_cast<const float4*>(a.cos + at));
+    g.s = __ldg(reinterpret_cast<const float4*>(a.sin + at));
+  }
+  return g;
+}
+
+// Norm and rotation of a vector held by D / 8 lanes of a converged warp.
+template <int D, bool kHalf>
+__device__ __forceinline__ void turn(Vec& v, const AppendArgs& a, const float* gamma, const Angle& g) {
   if (a.norm) {
     float ss = 0.f;
-    for (int d = 0; d < D; ++d) ss = fmaf(y[d], y[d], ss);
-    const float r = rsqrtf(ss / D + a.eps);
-    for (int d = 0; d < D; ++d) y[d] = y[d] * r * (gamma ? gamma[d] : 1.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(v.x[i], v.x[i], ss);
+#pragma unroll
+    for (int off = D / 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const float r = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.x[i] = v.x[i] * r * gamma[i];
   }
   if (a.cos) {
-    for (int i = 0; i < D / 2; ++i) {
-      const int ia = kHalf ? i : 2 * i, ib = kHalf ? i + D / 2 : 2 * i + 1;
-      const float c = a.cos[static_cast<int64_t>(t) * (D / 2) + i];
-      const float s = a.sin[static_cast<int64_t>(t) * (D / 2) + i];
-      const float ya = y[ia], yb = y[ib];
-      y[ia] = fmaf(ya, c, -yb * s);
-      y[ib] = fmaf(ya, s, yb * c);
+    const float c[4] = {g.c.x, g.c.y, g.c.z, g.c.w}, s[4] = {g.s.x, g.s.y, g.s.z, g.s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float& p = v.x[kHalf ? i : 2 * i];
+      float& q = v.x[kHalf ? 4 + i : 2 * i + 1];
+      const float p0 = p, q0 = q;
+      p = fmaf(p0, c[i], -q0 * s[i]);
+      q = fmaf(p0, s[i], q0 * c[i]);
     }
   }
 }
 
-template <bool kFp8>
-__device__ void store(void* cache, int64_t at, float y, float inv_scale) {
-  if (kFp8)
-    static_cast<uint8_t*>(cache)[at] = __nv_cvt_float_to_fp8(y * inv_scale, __NV_SATFINITE, __NV_E4M3);
-  else
-    static_cast<uint16_t*>(cache)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-}
-
-// grid (B, Hkv + H): one thread per token of head blockIdx.y; a key-value
-// head's k_sum is summed token by token by thread 0.
-template <int D, bool kFp8, bool kHalf>
-__global__ void append_kernel(AppendArgs a) {
-  const int b = blockIdx.x, S = a.S;
+// How many of the new tokens of sequence b have a place in its page table.
+__device__ __forceinline__ int tokens_of(const AppendArgs& a, int b, int* base, int* status) {
   bool bad;
-  const int base = clamp_len(a.pm.seq_lens[b], a.pm, &bad);
-  int n = a.new_lens ? min(max(a.new_lens[b], 0), S) : S;
-  const int most = a.pm.max_pages * kBlock;
-  int status = bad ? SA_DEV_BAD_CACHE : 0;
-  if (n > most - base) {
-    n = most - base;
-    status |= SA_DEV_CAPACITY;
+  *base = clamp_len(__ldg(a.pm.seq_lens + b), a.pm, &bad);
+  int n = a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.S) : a.S;
+  const int room = a.pm.max_pages * kBlock - *base;
+  if (bad) *status |= SA_DEV_BAD_CACHE;
+  if (n > room) {
+    n = room;
+    *status |= SA_DEV_CAPACITY;
   }
-  if (blockIdx.y == 0 && threadIdx.x == 0 && a.lens_out) a.lens_out[b] = base + n;
-  const bool is_q = static_cast<int>(blockIdx.y) >= a.Hkv;
-  const int h = is_q ? blockIdx.y - a.Hkv : blockIdx.y;
-  float y[D];
-  const bool sums = !is_q && a.k_sum;
-  for (int s = threadIdx.x; s < n; s += blockDim.x) {
-    const int t = base + s;
-    const int page = a.pm.table[b * a.pm.table_stride + t / kBlock];
-    if (page < 0 || page >= a.pm.n_pages) {
-      status |= SA_DEV_BAD_CACHE;
-      continue;
-    }
-    if (a.cos && t >= a.rope_rows) {
-      status |= SA_DEV_CAPACITY;
-      continue;
-    }
-    if (is_q) {
-      turn<D, kFp8, kHalf>(a, a.q + b * a.qs[0] + s * a.qs[1] + h * a.qs[2], a.gamma_q, t, y);
-      for (int d = 0; d < D; ++d)
-        store<false>(a.q_out, b * a.os[0] + s * a.os[1] + h * a.os[2] + d, y[d], 1.f);
-      continue;
-    }
-    turn<D, kFp8, kHalf>(a, a.k + b * a.ks[0] + s * a.ks[1] + h * a.ks[2], a.gamma_k, t, y);
-    const float ik = a.k_scale ? 1.f / a.k_scale[h] : 1.f, iv = a.v_scale ? 1.f / a.v_scale[h] : 1.f;
-    const int slot = t % kBlock;
-    for (int d = 0; d < D; ++d) {
-      store<kFp8>(a.kc, page * a.kcs[0] + h * a.kcs[1] + slot * a.kcs[2] + d, y[d], ik);
-      store<kFp8>(a.vc, page * a.vcs[0] + h * a.vcs[1] + slot * a.vcs[2] + d,
-                  bits_f32(a.v[b * a.vs[0] + s * a.vs[1] + h * a.vs[2] + d]), iv);
-    }
-    // the first token of a page in this call sums the page's tokens
-    if (sums && (s == 0 || slot == 0)) {
-      float* out = a.k_sum + (static_cast<int64_t>(page) * a.Hkv + h) * D;
-      const int end = min(n, s + kBlock - slot);
-      float z[D];
-      for (int d = 0; d < D; ++d) z[d] = slot == 0 ? 0.f : out[d];
-      for (int u = s; u < end && !(a.cos && base + u >= a.rope_rows); ++u) {
-        if (u > s)
-          turn<D, kFp8, kHalf>(a, a.k + b * a.ks[0] + u * a.ks[1] + h * a.ks[2], a.gamma_k,
-                               base + u, y);
-        for (int d = 0; d < D; ++d) z[d] += y[d];
+  return n;
+}
+
+// The page of position t, or -1 with the reason in *status.
+__device__ __forceinline__ int page_of(const AppendArgs& a, int b, int t, int* status) {
+  const int page = __ldg(a.pm.table + b * a.pm.table_stride + t / kBlock);
+  if (page >= 0 && page < a.pm.n_pages) return page;
+  *status |= SA_DEV_BAD_CACHE;
+  return -1;
+}
+
+// A key-value unit: the tokens of this call in page place `pu` (counted from
+// the first one touched) of sequence b, one head; kGroups lane groups take
+// every kGroups-th token. Returns with the lanes' sums of what they stored.
+template <int D, bool kFp8, bool kHalf, int kGroups>
+__device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int pu, int h, int grp,
+                                               int l, bool there, int* page, int* slot0,
+                                               float* sum, int* status) {
+  // with one new token its address needs no length: the loads go first
+  const uint16_t* k = a.k + b * a.ks[0] + h * a.ks[2];
+  const uint16_t* v = a.v + b * a.vs[0] + h * a.vs[2];
+  uint4 kw[kTokens], vw[kTokens];
+  const bool early = kGroups == 1 && a.S == 1 && there;
+  if (early) {
+    kw[0] = load8<D, kHalf>(k, l);
+    vw[0] = load8<D, kHalf>(v, l);
+  }
+  float gk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) gk[i] = 1.f;
+  if (a.gamma_k) load8f<D, kHalf>(a.gamma_k, l, gk);
+  const float ik = a.k_scale ? 1.f / __ldg(a.k_scale + h) : 1.f;
+  const float iv = a.v_scale ? 1.f / __ldg(a.v_scale + h) : 1.f;
+  int base = 0;
+  const int n = there ? tokens_of(a, b, &base, status) : 0;
+  // tokens [s0, s1) of the page, as far as the rotation tables reach
+  const int64_t edge = (static_cast<int64_t>(base / kBlock) + pu) * kBlock - base;
+  const int s0 = edge > 0 ? static_cast<int>(min(edge, static_cast<int64_t>(n))) : 0;
+  int s1 = static_cast<int>(min(edge + kBlock, static_cast<int64_t>(n)));
+  if (a.cos && s1 > s0 && s1 > a.rope_rows - base) {
+    s1 = max(s0, a.rope_rows - base);
+    *status |= SA_DEV_CAPACITY;
+  }
+  *page = s0 < s1 ? page_of(a, b, base + s0, status) : -1;
+  *slot0 = (base + s0) % kBlock;
+  if (*page < 0) s1 = s0;
+  const int64_t kat = *page * a.kcs[0] + h * a.kcs[1], vat = *page * a.vcs[0] + h * a.vcs[1];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+  // every lane of the warp makes the same number of rounds: turn() shuffles
+  const int rounds = kGroups == 1
+                         ? __reduce_max_sync(0xffffffffu, (s1 - s0 + kTokens - 1) / kTokens)
+                         : (s1 - s0 + kGroups * kTokens - 1) / (kGroups * kTokens);
+  for (int r = 0; r < rounds; ++r) {
+    Angle g[kTokens];
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u) {
+      const int s = s0 + (r * kTokens + u) * kGroups + grp;
+      if (s >= s1) continue;
+      if (!early) {
+        kw[u] = load8<D, kHalf>(k + s * a.ks[1], l);
+        vw[u] = load8<D, kHalf>(v + s * a.vs[1], l);
       }
-      for (int d = 0; d < D; ++d) out[d] = z[d];
+      g[u] = angle_at<D>(a, base + s, l);
+    }
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u) {
+      const int s = s0 + (r * kTokens + u) * kGroups + grp;
+      if (__all_sync(0xffffffffu, s >= s1)) break;
+      const bool on = s < s1;
+      Vec y = unpack(on ? kw[u] : make_uint4(0u, 0u, 0u, 0u));
+      turn<D, kHalf>(y, a, gk, g[u]);
+      if (!on) continue;
+      const int slot = (base + s) % kBlock;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += y.x[i];
+      if (kFp8) {
+        store8_e4m3<D, kHalf>(static_cast<uint8_t*>(a.kc) + kat + slot * a.kcs[2], l, pack_e4m3(y, ik));
+        store8_e4m3<D, kHalf>(static_cast<uint8_t*>(a.vc) + vat + slot * a.vcs[2], l,
+                              pack_e4m3(unpack(vw[u]), iv));
+      } else {
+        store8<D, kHalf>(static_cast<uint16_t*>(a.kc) + kat + slot * a.kcs[2], l, pack(y));
+        store8<D, kHalf>(static_cast<uint16_t*>(a.vc) + vat + slot * a.vcs[2], l, vw[u]);
+      }
+    }
+  }
+}
+
+// kWhole: a CTA takes one key-value unit, else each of its lane groups one.
+template <int D, bool kFp8, bool kHalf, bool kWhole>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int units, int page_units,
+                                                          int kv_ctas) {
+  constexpr int L = D / 8, kGroups = kThreads / L;
+  const int grp = threadIdx.x / L, l = threadIdx.x % L;
+  int status = 0;
+  if (static_cast<int>(blockIdx.x) < kv_ctas) {
+    // ------------------------------------------------------ keys, values --
+    const int u = kWhole ? blockIdx.x : blockIdx.x * kGroups + grp;
+    const bool there = u < units;
+    const int h = u % a.Hkv, bp = u / a.Hkv, pu = bp % page_units, b = there ? bp / page_units : 0;
+    int page, slot0;
+    float sum[8];
+    key_value_unit<D, kFp8, kHalf, kWhole ? kGroups : 1>(a, b, pu, h, kWhole ? grp : 0, l, there,
+                                                         &page, &slot0, sum, &status);
+    if (there && a.lens_out && pu == 0 && h == 0 && l == 0 && (!kWhole || grp == 0)) {
+      int base;
+      const int n = tokens_of(a, b, &base, &status);
+      a.lens_out[b] = base + n;
+    }
+    if (kWhole && a.k_sum) {
+      // the lane groups' sums, added in their order
+      __shared__ float part[kGroups][D];
+      store8f<D, false>(part[grp], l, sum);      // in the lane's own order
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] += part[g][8 * l + i];
+      }
+    }
+    if (a.k_sum && page >= 0 && (!kWhole || grp == 0)) {
+      float* out = a.k_sum + (static_cast<int64_t>(page) * a.Hkv + h) * D;
+      if (slot0 > 0) {
+        float old[8];
+        load8f<D, kHalf>(out, l, old);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += old[i];
+      }
+      store8f<D, kHalf>(out, l, sum);
+    }
+  } else {
+    // ----------------------------------------------------------- queries --
+    const int token = blockIdx.x - kv_ctas, b = token / a.S, s = token % a.S;
+    const uint16_t* q = a.q + b * a.qs[0] + s * a.qs[1];
+    uint16_t* out = a.q_out + b * a.os[0] + s * a.os[1];
+    uint4 w[kQueryHeads];
+    auto load = [&](int h0) {
+#pragma unroll
+      for (int u = 0; u < kQueryHeads; ++u) {
+        const int h = h0 + u * kGroups + grp;
+        w[u] = h < a.H ? load8<D, kHalf>(q + h * a.qs[2], l) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // a token that may not count is not read before that is known
+    const bool early = a.new_lens == nullptr;
+    if (early) load(0);
+    float gq[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gq[i] = 1.f;
+    if (a.gamma_q) load8f<D, kHalf>(a.gamma_q, l, gq);
+    int base, none = 0;             // the key-value CTAs report what is wrong
+    if (s >= tokens_of(a, b, &base, &none)) return;
+    const int t = base + s;
+    if ((a.cos && t >= a.rope_rows) || page_of(a, b, t, &none) < 0) return;
+    const Angle g = angle_at<D>(a, t, l);
+    for (int h0 = 0; h0 < a.H; h0 += kQueryHeads * kGroups) {
+      if (h0 > 0 || !early) load(h0);
+#pragma unroll
+      for (int u = 0; u < kQueryHeads; ++u) {
+        if (h0 + u * kGroups >= a.H) break;
+        const int h = h0 + u * kGroups + grp;
+        Vec y = unpack(w[u]);
+        turn<D, kHalf>(y, a, gq, g);
+        if (h < a.H) store8<D, kHalf>(out + h * a.os[2], l, pack(y));
+      }
     }
   }
   if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
+template <int D, bool kFp8, bool kHalf>
+cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
+  constexpr int kGroups = kThreads / (D / 8);
+  // the pages S tokens can touch, wherever the first of them lies
+  const int64_t page_units = (static_cast<int64_t>(a.S) + kBlock - 2) / kBlock + 1;
+  const int64_t units = a.B * page_units * a.Hkv;
+  const bool whole = a.S > kTokens;
+  const int64_t kv = whole ? units : (units + kGroups - 1) / kGroups;
+  const int64_t grid = kv + (a.q ? static_cast<int64_t>(a.B) * a.S : 0);
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (whole)
+    append_kernel<D, kFp8, kHalf, true><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
+        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv));
+  else
+    append_kernel<D, kFp8, kHalf, false><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
+        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv));
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const AppendArgs& a, bool fp8, bool half, cudaStream_t st) {
+  if (fp8) return half ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
+  return half ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int D, bool fp8, bool half, cudaStream_t st) {
-  const dim3 grid(a.B, a.Hkv + (a.q ? a.H : 0));
-  const int threads = a.S >= 128 ? 128 : 32;
-  auto run = [&](auto kernel) {
-    kernel<<<grid, threads, 0, st>>>(a);
-    return cudaGetLastError();
-  };
-  if (D == 64) {
-    if (fp8) return half ? run(append_kernel<64, true, true>) : run(append_kernel<64, true, false>);
-    return half ? run(append_kernel<64, false, true>) : run(append_kernel<64, false, false>);
-  }
-  if (fp8) return half ? run(append_kernel<128, true, true>) : run(append_kernel<128, true, false>);
-  return half ? run(append_kernel<128, false, true>) : run(append_kernel<128, false, false>);
+  return D == 64 ? launch_d<64>(a, fp8, half, st) : launch_d<128>(a, fp8, half, st);
 }
 
 }  // namespace sa

@@ -167,6 +167,10 @@ sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v
     return SA_ERR_INVALID_ARG;
   if ((rope_cos == nullptr) != (rope_sin == nullptr)) return SA_ERR_INVALID_ARG;
   if (lens_out && lens_out == seq_lens) return SA_ERR_INVALID_ARG;
+  // blocks of the launch, counted in 32 bits
+  const int64_t rows = static_cast<int64_t>(p->B) * (p->S / kBlock + 2) * p->H_kv +
+                       static_cast<int64_t>(p->B) * p->S;
+  if (rows > INT32_MAX) return SA_ERR_UNSUPPORTED;
   AppendArgs a{};
   a.pm = page_map(p, page_table, seq_lens);
   a.k = static_cast<const uint16_t*>(k);
