@@ -473,18 +473,22 @@ _CACHE_PACK = struct.Struct("=14i2f19q").pack
 _NO_STRIDES = (0, 0, 0)
 
 
-def _on_device(fn):
-    """The call with its first tensor's device current, so that it is enqueued
-    on that device's stream and allocates there."""
-    @functools.wraps(fn)
-    def call(t, *args, **kwargs):
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device: there is no CPU path")
-        if t.get_device() == torch._C._cuda_getDevice():
-            return fn(t, *args, **kwargs)
-        with torch.cuda.device(t.device):
-            return fn(t, *args, **kwargs)
-    return call
+def _launch(what: str, fn, device, *args) -> None:
+    """The library call with `device` current (its address and stream checks
+    and its launches are made there)."""
+    if device.index == torch._C._cuda_getDevice():
+        code = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args)
+    if code:
+        _check(code, what)
+
+
+def _cuda_device(t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device: there is no CPU path")
+    return t.device
 
 
 def _raw_stream(device, stream) -> int:
@@ -498,14 +502,14 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _need(t: torch.Tensor, name: str, device, dtype, shape=None) -> int:
     """The address of a contiguous tensor of this device, type and shape."""
-    if t.device != device or t.dtype != dtype or not t.is_contiguous():
+    if t.device != device or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -513,17 +517,20 @@ def _need(t: torch.Tensor, name: str, device, dtype, shape=None) -> int:
 
 
 def _need_tokens(t: torch.Tensor, name: str, device, shape) -> int:
-    if t.device != device or t.dtype != torch.bfloat16:
+    if t.device != device or t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be a bf16 tensor on {device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _need_map(page_table, seq_lens, device) -> None:
-    if page_table.device != device:
-        raise ValueError(f"page_table must be on {device}")
-    _need(seq_lens, "seq_lens", device, torch.int32, page_table.shape[:1])
+def _token_strides(t: Optional[torch.Tensor], name: str):
+    if t is None:
+        return _NO_STRIDES
+    st = t.stride()
+    if len(st) != 4 or st[3] != 1:
+        raise ValueError(f"{name} must be [B, S, H, D] with a contiguous last dimension")
+    return st[:3]
 
 
 def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = None,
@@ -537,9 +544,8 @@ def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = N
     """The parameters of a paged-cache call on these tensors (those it takes):
     q, k, v, o [B, S, heads, D]; k_cache, v_cache [n_pages, H_kv, 64, D] in
     bf16, or e4m3 as float8_e4m3fn or uint8; k_sum [n_pages, H_kv, D]."""
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2
-            or (page_table.stride(1) != 1 and page_table.shape[1] != 1)):
-        raise ValueError("page_table must be int32 [B, max_pages], its rows contiguous")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
     kst = vst = _NO_STRIDES
     fmt = SA_CACHE_BF16
     if k_cache is not None:
@@ -559,26 +565,26 @@ def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = N
         shape = k_sum.shape
     else:
         raise ValueError("k_cache must be [n_pages, H_kv, 64, D], k_sum [n_pages, H_kv, D]")
-    qst = _NO_STRIDES if q is None else _bshd_strides(q, "q")
-    kt = _NO_STRIDES if k is None else _bshd_strides(k, "k")
-    vt = _NO_STRIDES if v is None else _bshd_strides(v, "v")
-    ost = _NO_STRIDES if o is None else _bshd_strides(o, "o")
+    qst, kt = _token_strides(q, "q"), _token_strides(k, "k")
+    vt, ost = _token_strides(v, "v"), _token_strides(o, "o")
     tokens = q if q is not None else k
     B, max_pages = page_table.shape
+    table_stride, one = page_table.stride()
+    if one != 1 and max_pages != 1:
+        raise ValueError("the rows of page_table must be contiguous")
     if isinstance(rope, str):
         rope = ROPE_LAYOUTS[rope]
     try:
         packed = _CACHE_PACK(
             B, 1 if tokens is None else tokens.shape[1], shape[1] if q is None else q.shape[2],
             shape[1], shape[-1], PAGE, shape[0], max_pages, fmt, prefix_len, budget,
-            1 if qk_norm else 0, rope, rope_rows, eps, scale, page_table.stride(0), *qst, *kt,
+            1 if qk_norm else 0, rope, rope_rows, eps, scale, table_stride, *qst, *kt,
             *vt, *ost, *kst[:3], *vst[:3])
     except struct.error as err:
         raise ValueError(f"a cache parameter is out of range: {err}") from None
     return sa_cache_params.from_buffer_copy(packed)
 
 
-@_on_device
 def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                     v_cache: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
                     q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
@@ -599,7 +605,7 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     q_out=q for in place). ``new_lens``: how many of the S tokens each sequence
     brings. ``k_sum`` gathers the per-page key sums that sa_route_pages reads;
     ``lens_out`` receives the new lengths."""
-    dev, f32, i32 = k.device, torch.float32, torch.int32
+    dev, f32, i32 = _cuda_device(k), torch.float32, torch.int32
     if q is not None and q_out is None:
         q_out = _empty(q.shape, q.dtype, dev, stream)
     elif q is None and q_out is not None:
@@ -610,13 +616,15 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                           qk_norm=qk_norm, rope=rope, eps=eps,
                           rope_rows=0 if cos is None else cos.shape[0])
     B, S, Hkv, D = shape = (p.B, k.shape[1], p.H_kv, p.D)
-    _need_map(page_table, seq_lens, dev)
+    if page_table.device != dev:
+        raise ValueError(f"page_table must be on {dev}")
     qp = qo = None
     if q is not None:
         shape_q = (B, S, p.H, D)
         qp, qo = _need_tokens(q, "q", dev, shape_q), _need_tokens(q_out, "q_out", dev, shape_q)
-    code = load_library().sa_cache_append(
-        ctypes.byref(p), _need_tokens(k, "k", dev, shape), _need_tokens(v, "v", dev, shape), qp, qo,
+    _launch(
+        "sa_cache_append", load_library().sa_cache_append, dev, ctypes.byref(p),
+        _need_tokens(k, "k", dev, shape), _need_tokens(v, "v", dev, shape), qp, qo,
         None if gamma_q is None else _need(gamma_q, "gamma_q", dev, f32, (D,)),
         None if gamma_k is None else _need(gamma_k, "gamma_k", dev, f32, (D,)),
         None if cos is None else _need(cos, "cos", dev, f32, (p.rope_rows, D // 2)),
@@ -625,13 +633,11 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
         None if k_scale is None else _need(k_scale, "k_scale", dev, f32, (Hkv,)),
         None if v_scale is None else _need(v_scale, "v_scale", dev, f32, (Hkv,)),
         None if k_sum is None else _need(k_sum, "k_sum", dev, f32, (p.n_pages, Hkv, D)),
-        page_table.data_ptr(), seq_lens.data_ptr(),
+        page_table.data_ptr(), _need(seq_lens, "seq_lens", dev, i32, (p.B,)),
         None if new_lens is None else _need(new_lens, "new_lens", dev, i32, (B,)),
         None if lens_out is None else _need(lens_out, "lens_out", dev, i32, (B,)),
         None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
         _raw_stream(dev, stream))
-    if code:
-        _check(code, "sa_cache_append")
     return q_out
 
 
@@ -654,7 +660,6 @@ def _cache_workspace(ws: torch.Tensor, device) -> Tuple[int, int]:
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-@_on_device
 def sa_route_pages(q: torch.Tensor, k_sum: torch.Tensor, page_table: torch.Tensor,
                    seq_lens: torch.Tensor, prefix_len: int, budget: int, *,
                    row_ptr: Optional[torch.Tensor] = None,
@@ -667,9 +672,10 @@ def sa_route_pages(q: torch.Tensor, k_sum: torch.Tensor, page_table: torch.Tenso
     entries are col_idx[:row_ptr[-1]]), for sa_attn_decode. Kept per key-value
     head: the prefix's pages, the newest one, and the best-scoring others until
     ``budget`` are."""
-    dev, i32 = q.device, torch.int32
+    dev, i32 = _cuda_device(q), torch.int32
     p = make_cache_params(page_table, q=q, k_sum=k_sum, prefix_len=prefix_len, budget=budget)
-    _need_map(page_table, seq_lens, dev)
+    if page_table.device != dev:
+        raise ValueError(f"page_table must be on {dev}")
     rows = p.B * p.H_kv
     if row_ptr is None:
         row_ptr = _empty((rows + 1,), i32, dev, stream)
@@ -677,19 +683,18 @@ def sa_route_pages(q: torch.Tensor, k_sum: torch.Tensor, page_table: torch.Tenso
         col_idx = _empty((sa_route_pages_max_nnz(p),), i32, dev, stream)
     if workspace is None:
         workspace = _empty((max(256, sa_route_pages_workspace_bytes(p)),), torch.uint8, dev, stream)
-    code = load_library().sa_route_pages(
-        ctypes.byref(p), _need_tokens(q, "q", dev, (p.B, p.S, p.H, p.D)),
-        _need(k_sum, "k_sum", dev, torch.float32), page_table.data_ptr(), seq_lens.data_ptr(),
+    _launch(
+        "sa_route_pages", load_library().sa_route_pages, dev, ctypes.byref(p),
+        _need_tokens(q, "q", dev, (p.B, p.S, p.H, p.D)),
+        _need(k_sum, "k_sum", dev, torch.float32), page_table.data_ptr(),
+        _need(seq_lens, "seq_lens", dev, i32, (p.B,)),
         _need(row_ptr, "row_ptr", dev, i32, (rows + 1,)), _need(col_idx, "col_idx", dev, i32),
         col_idx.numel(), *_cache_workspace(workspace, dev),
         None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
         _raw_stream(dev, stream))
-    if code:
-        _check(code, "sa_route_pages")
     return row_ptr, col_idx
 
 
-@_on_device
 def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    page_table: torch.Tensor, seq_lens: torch.Tensor, scale: float = 0.0, *,
                    row_ptr: Optional[torch.Tensor] = None,
@@ -703,7 +708,7 @@ def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``seq_lens`` cached tokens, or over the pages a route lists (row_ptr,
     col_idx from sa_route_pages): (o bf16 [B, 1, H, D], lse fp32 [B, H, 1] or
     None). H is a multiple of the cache's H_kv."""
-    dev, f32, i32 = q.device, torch.float32, torch.int32
+    dev, f32, i32 = _cuda_device(q), torch.float32, torch.int32
     if o is None:
         o = _empty(q.shape, q.dtype, dev, stream)
     p = make_cache_params(page_table, q=q, o=o, k_cache=k_cache, v_cache=v_cache, scale=scale)
@@ -715,12 +720,14 @@ def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         workspace = _empty((max(256, sa_attn_decode_workspace_bytes(p)),), torch.uint8, dev, stream)
     if (row_ptr is None) != (col_idx is None):
         raise ValueError("row_ptr and col_idx go together")
-    _need_map(page_table, seq_lens, dev)
-    code = load_library().sa_attn_decode(
-        ctypes.byref(p), _need_tokens(q, "q", dev, shape), k_cache.data_ptr(), v_cache.data_ptr(),
+    if page_table.device != dev:
+        raise ValueError(f"page_table must be on {dev}")
+    _launch(
+        "sa_attn_decode", load_library().sa_attn_decode, dev, ctypes.byref(p),
+        _need_tokens(q, "q", dev, shape), k_cache.data_ptr(), v_cache.data_ptr(),
         None if k_scale is None else _need(k_scale, "k_scale", dev, f32, (p.H_kv,)),
         None if v_scale is None else _need(v_scale, "v_scale", dev, f32, (p.H_kv,)),
-        page_table.data_ptr(), seq_lens.data_ptr(),
+        page_table.data_ptr(), _need(seq_lens, "seq_lens", dev, i32, (p.B,)),
         None if row_ptr is None else _need(row_ptr, "row_ptr", dev, i32, (B * p.H_kv + 1,)),
         None if col_idx is None else _need(col_idx, "col_idx", dev, i32),
         0 if col_idx is None else col_idx.numel(), _need_tokens(o, "o", dev, shape),
@@ -728,8 +735,6 @@ def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         *_cache_workspace(workspace, dev),
         None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
         _raw_stream(dev, stream))
-    if code:
-        _check(code, "sa_attn_decode")
     return o, lse
 
 

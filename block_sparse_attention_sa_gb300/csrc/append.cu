@@ -22,7 +22,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kQueryHeads = 8;     // heads a lane group has in flight
-constexpr int kTokens = 4;         // tokens a lane group has in flight
+constexpr int kTokens = 2;         // tokens a lane group has in flight
+constexpr int64_t kManyTokens = 1024;
 
 struct Vec {                       // a lane's eight elements
   float x[8];
@@ -250,8 +251,8 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
 
 // kWhole: a CTA takes one key-value unit, else each of its lane groups one.
 template <int D, bool kFp8, bool kHalf, bool kWhole>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int units, int page_units,
-                                                          int kv_ctas) {
+__global__ void __launch_bounds__(kThreads, kWhole ? 8 : 4) append_kernel(AppendArgs a, int units, int page_units,
+                                                          int kv_ctas, int per_log2) {
   constexpr int L = D / 8, kGroups = kThreads / L;
   const int grp = threadIdx.x / L, l = threadIdx.x % L;
   int status = 0;
@@ -293,38 +294,46 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int unit
     }
   } else {
     // ----------------------------------------------------------- queries --
-    const int token = blockIdx.x - kv_ctas, b = token / a.S, s = token % a.S;
+    // `per` lane groups share a token, every per-th head each
+    const int per = 1 << per_log2;
+    const int64_t token = static_cast<int64_t>(blockIdx.x - kv_ctas) * (kGroups >> per_log2) +
+                          (grp >> per_log2);
+    const bool there = token < static_cast<int64_t>(a.B) * a.S;
+    const int b = there ? static_cast<int>(token / a.S) : 0, s = static_cast<int>(token % a.S);
+    const int hg = grp & (per - 1);
     const uint16_t* q = a.q + b * a.qs[0] + s * a.qs[1];
     uint16_t* out = a.q_out + b * a.os[0] + s * a.os[1];
     uint4 w[kQueryHeads];
-    auto load = [&](int h0) {
+    auto load = [&](int h0, bool on) {
 #pragma unroll
       for (int u = 0; u < kQueryHeads; ++u) {
-        const int h = h0 + u * kGroups + grp;
-        w[u] = h < a.H ? load8<D, kHalf>(q + h * a.qs[2], l) : make_uint4(0u, 0u, 0u, 0u);
+        const int h = h0 + u * per + hg;
+        w[u] = on && h < a.H ? load8<D, kHalf>(q + h * a.qs[2], l) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
     // a token that may not count is not read before that is known
     const bool early = a.new_lens == nullptr;
-    if (early) load(0);
+    if (early) load(0, there);
     float gq[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) gq[i] = 1.f;
     if (a.gamma_q) load8f<D, kHalf>(a.gamma_q, l, gq);
-    int base, none = 0;             // the key-value CTAs report what is wrong
-    if (s >= tokens_of(a, b, &base, &none)) return;
-    const int t = base + s;
-    if ((a.cos && t >= a.rope_rows) || page_of(a, b, t, &none) < 0) return;
-    const Angle g = angle_at<D>(a, t, l);
-    for (int h0 = 0; h0 < a.H; h0 += kQueryHeads * kGroups) {
-      if (h0 > 0 || !early) load(h0);
+    int base = 0, none = 0;             // the key-value CTAs report what is wrong
+    bool on = there && s < tokens_of(a, b, &base, &none);
+    const int t = base + (on ? s : 0);
+    on = on && !(a.cos && t >= a.rope_rows) && page_of(a, b, t, &none) >= 0;
+    if (!__any_sync(0xffffffffu, on)) return;
+    Angle g = {};
+    if (on) g = angle_at<D>(a, t, l);
+    for (int h0 = 0; h0 < a.H; h0 += kQueryHeads * per) {
+      if (h0 > 0 || !early) load(h0, on);
 #pragma unroll
       for (int u = 0; u < kQueryHeads; ++u) {
-        if (h0 + u * kGroups >= a.H) break;
-        const int h = h0 + u * kGroups + grp;
+        if (h0 + u * per >= a.H) break;
+        const int h = h0 + u * per + hg;
         Vec y = unpack(w[u]);
         turn<D, kHalf>(y, a, gq, g);
-        if (h < a.H) store8<D, kHalf>(out + h * a.os[2], l, pack(y));
+        if (on && h < a.H) store8<D, kHalf>(out + h * a.os[2], l, pack(y));
       }
     }
   }
@@ -339,14 +348,22 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   const int64_t units = a.B * page_units * a.Hkv;
   const bool whole = a.S > kTokens;
   const int64_t kv = whole ? units : (units + kGroups - 1) / kGroups;
-  const int64_t grid = kv + (a.q ? static_cast<int64_t>(a.B) * a.S : 0);
+  // lane groups per token: as many as it has heads where tokens are few and
+  // the chain of one token counts, else so many that each has all its loads in
+  // flight at once and a token's angles are loaded by few
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.S;
+  const int want = tokens < kManyTokens ? a.H : (a.H + kQueryHeads - 1) / kQueryHeads;
+  int per_log2 = 0;
+  while ((1 << per_log2) < want && (2 << per_log2) <= kGroups) ++per_log2;
+  const int64_t at_once = kGroups >> per_log2;
+  const int64_t grid = kv + (a.q ? (tokens + at_once - 1) / at_once : 0);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (whole)
     append_kernel<D, kFp8, kHalf, true><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
-        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv));
+        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv), per_log2);
   else
     append_kernel<D, kFp8, kHalf, false><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
-        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv));
+        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv), per_log2);
   return cudaGetLastError();
 }
 

@@ -80,7 +80,7 @@ sa_status check_route_pages(const sa_cache_params* p) {
   if (s != SA_OK) return s;
   if (p->S != 1) return SA_ERR_UNSUPPORTED;
   const int64_t rows = static_cast<int64_t>(p->B) * p->H_kv;
-  if (rows * p->max_pages > INT32_MAX || rows * most_pages(p) > INT32_MAX)
+  if (p->max_pages > (1 << 20) || rows * p->max_pages > INT32_MAX || rows * most_pages(p) > INT32_MAX)
     return SA_ERR_UNSUPPORTED;
   return SA_OK;
 }

@@ -84,6 +84,67 @@ __device__ __forceinline__ int clamp_len(int n, const PageMap& pm, bool* bad) {
   *bad = n < 0 || n > most;
   return n < 0 ? 0 : (n > most ? most : n);
 }
+
+// Run c of C over a list of T items: [run_start(c), run_start(c + 1)).
+__device__ __forceinline__ int64_t run_start(int64_t T, int C, int c) {
+  return T / C * c + (c < T % C ? c : T % C);
+}
+
+// The run an item of the list lies in.
+__device__ __forceinline__ int run_of(int64_t T, int C, int64_t item) {
+  const int64_t base = T / C, rem = T % C, big = rem * (base + 1);
+  return static_cast<int>(item < big ? item / (base + 1) : rem + (item - big) / base);
+}
+
+struct Run {
+  int64_t T, lo, hi;       // items of the list, and this CTA's among them
+};
+
+// The list is that of `groups` groups in order, each count(i) * per_group
+// items. Every CTA of the grid finds its run of it by a scan of the counts;
+// *group and *off (shared memory) say where a run that is not empty begins.
+// All NT threads call it; it ends with every thread past a barrier.
+template <int NT, class Count>
+__device__ __forceinline__ Run plan_run(int groups, int64_t per_group, Count count,
+                                        int64_t* warp_sum, int* group, int64_t* off) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_thread = (groups + NT - 1) / NT;
+  const int g0 = tid * per_thread < groups ? tid * per_thread : groups;
+  const int g1 = g0 + per_thread < groups ? g0 + per_thread : groups;
+  int64_t mine = 0;
+  for (int i = g0; i < g1; ++i) mine += count(i);
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  Run r;
+  r.T = total * per_group;
+  r.lo = run_start(r.T, gridDim.x, blockIdx.x);
+  r.hi = run_start(r.T, gridDim.x, blockIdx.x + 1);
+  int64_t at = (before + incl - mine) * per_group;
+  if (r.lo < r.hi && r.lo >= at && r.lo < at + mine * per_group) {
+    int i = g0;
+    for (;; ++i) {
+      const int64_t n = count(i) * per_group;
+      if (r.lo < at + n) break;
+      at += n;
+    }
+    *group = i;
+    *off = r.lo - at;
+  }
+  __syncthreads();
+  return r;
+}
 #endif
 
 }  // namespace sa

@@ -151,16 +151,6 @@ __device__ __forceinline__ int group_pages(const DecodeArgs& a, int i, int* stat
   return (n + kBlock - 1) / kBlock;
 }
 
-// Run c of C over T pages: [run_start(c), run_start(c + 1)).
-__device__ __forceinline__ int64_t run_start(int64_t T, int C, int c) {
-  return T / C * c + min(static_cast<int64_t>(c), T % C);
-}
-
-__device__ __forceinline__ int run_of(int64_t T, int C, int64_t page) {
-  const int64_t base = T / C, rem = T % C, big = rem * (base + 1);
-  return static_cast<int>(page < big ? page / (base + 1) : rem + (page - big) / base);
-}
-
 template <int D, bool kFp8, int RG>
 __global__ void __launch_bounds__(Shape<D, kFp8, RG>::kThreads, Shape<D, kFp8, RG>::kCtas)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -200,42 +190,16 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     mbar_init(smem_u32(&joined), W);
     fence_barrier_init();
     abort_flag = 0;
-    start_group = -1;
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
 
-  // this CTA's run of the page list: a scan of the groups' page counts
-  const int per_thread = (n_groups + NT - 1) / NT;
-  const int g0 = min(tid * per_thread, n_groups), g1 = min(g0 + per_thread, n_groups);
-  int64_t mine = 0;
-  for (int i = g0; i < g1; ++i) mine += group_pages(a, i, &status);
-  int64_t incl = mine;
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += v;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const int64_t T = total * per_group;
-  const int64_t lo = run_start(T, C, c), hi = run_start(T, C, c + 1);
-  const int64_t excl = (before + incl - mine) * per_group;
-  if (lo < hi && lo >= excl && lo < excl + mine * per_group) {
-    int64_t at = excl;
-    int i = g0;
-    for (;; ++i) {
-      const int64_t n = static_cast<int64_t>(group_pages(a, i, &status)) * per_group;
-      if (lo < at + n) break;
-      at += n;
-    }
-    start_group = i;
-    start_off = lo - at;
-  }
+  // this CTA's run of the page list
+  const Run run = plan_run<NT>(
+      n_groups, per_group,
+      [&](int i) { return static_cast<int64_t>(group_pages(a, i, &status)); }, warp_sum,
+      &start_group, &start_off);
+  const int64_t T = run.T, lo = run.lo, hi = run.hi;
   // groups without a page: nothing to attend
   for (int i = c + C * warp; i < n_groups; i += C * (NT / 32)) {
     if (group_pages(a, i, &status) != 0) continue;
@@ -249,7 +213,6 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     if (by_unit)
       for (int u = lane; u < per_group; u += 32) cuts[i * per_group + u].unit = -1;
   }
-  __syncthreads();
 
   if (warp == W) {
     // ---------------------------------------------------------- producer --

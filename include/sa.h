@@ -530,8 +530,8 @@ size_t sa_route_pages_workspace_bytes(const sa_cache_params* p);
  *            SA_DEV_CAPACITY is raised; sa_route_pages_max_nnz(p) is enough.
  * workspace  device scratch of sa_route_pages_workspace_bytes(p) bytes,
  *            256-byte aligned; its contents on entry do not matter.
- * Errors: as sa_route. B*H_kv*max_pages and the most entries must be < 2^31
- * (SA_ERR_UNSUPPORTED).
+ * Errors: as sa_route. max_pages must be <= 2^20, B*H_kv*max_pages and the
+ * most entries < 2^31 (SA_ERR_UNSUPPORTED).
  */
 sa_status sa_route_pages(const sa_cache_params* p, const void* q, const float* k_sum,
                          const int32_t* page_table, const int32_t* seq_lens, int32_t* row_ptr,

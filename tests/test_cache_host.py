@@ -122,6 +122,7 @@ def test_route_and_decode_refusals(sa):
     assert route(sa, p, n=need - 1) == CAPACITY
     big = params(sa, B=60000, H=64, Hkv=64, max_pages=1 << 20)
     assert route(sa, big) == UNSUPPORTED                        # lists beyond int32
+    assert route(sa, params(sa, B=1, max_pages=(1 << 20) + 1)) == UNSUPPORTED
     p = params(sa)
     for name in ("q", "kc", "vc", "table", "lens", "o", "ws"):
         assert decode(sa, p, **{name: None}) == INVALID, name
