@@ -61,7 +61,8 @@ struct Shape {
   static constexpr int kChunk = 32;                     // columns joined at a time
   static constexpr int kPad = kChunk + 8;               // row stride of the join buffer
   static constexpr int kJoin = kWarps * 16 * kPad * 4;
-  static constexpr int kSmem = kStages * kStage + kJoin + 1024;
+  static constexpr int kQueries = RG * (D / 16) * 32 * 16;
+  static constexpr int kSmem = kStages * kStage + kJoin + kQueries + 1024;
 };
 
 struct PageMeta {
@@ -93,17 +94,17 @@ __device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t addr) {
 }
 
 template <bool kFp16>
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
   if (kFp16)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
                  "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
                  "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 // Two e4m3 codes (low half of x) as two fp16 values; exact.
@@ -161,6 +162,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   __shared__ __align__(8) uint64_t full[NS], empty[NS], joined;
   __shared__ PageMeta meta[NS];
   __shared__ float sm_m[W][16], sm_l[W][16];
+  __shared__ int2 sm_unit[W];                // each warp's copy of its unit and dest
   __shared__ int64_t warp_sum[NT / 32 + 1];
   __shared__ int64_t start_off;
   __shared__ int start_group;
@@ -169,6 +171,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* join = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + NS * S::kStage);
+  uint4* sm_q = reinterpret_cast<uint4*>(reinterpret_cast<char*>(join) + S::kJoin);
   const int G = a.H / a.Hkv, C = gridDim.x, c = blockIdx.x;
   const bool routed = a.row_ptr != nullptr;
   const int n_groups = routed ? a.B * a.Hkv : a.B;
@@ -321,7 +324,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int rg = warp / S::kKeyWarps, kw = warp % S::kKeyWarps;
     const int r = lane >> 2, cq = lane & 3;
     const int n_pages = static_cast<int>(hi - lo);
-    uint32_t qa[D / 16][4];
+    uint4* q_frag = sm_q + rg * (D / 16) * 32 + lane;       // A fragment k at [32 k]
     float o[D / 8][4];
     float m[2], l[2], f[2];                  // rows r and r + 8 of the warp's 16
     uint32_t join_phase = 0;
@@ -334,16 +337,20 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       join_phase ^= 1u;
       return done;
     };
+    int s = 0;
+    uint32_t ph = 0;
     for (int i = 0; i < n_pages; ++i) {
-      const int s = i % NS;
-      if (!mbar_wait_warp(smem_u32(&full[s]), static_cast<uint32_t>(i / NS) & 1u, abort)) {
+      if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort)) {
         ok = false;
         break;
       }
-      const PageMeta pm = meta[s];
-      const int rt = pm.unit % RT, bg = pm.unit / RT, b = bg / a.Hkv, g = bg % a.Hkv;
-      if (pm.flags & 1) {
-        // the unit's queries as A fragments, rows beyond the group's heads zero
+      const int flags = meta[s].flags, page_live = meta[s].live;
+      if (flags & 1) {
+        // the unit's queries as A fragments, rows beyond the group's heads
+        // zero: kept in shared memory, every warp of a row group writing some
+        uint32_t qa[D / 16][4];
+        const int unit = meta[s].unit, rt = unit % RT, bg = unit / RT, b = bg / a.Hkv, g = bg % a.Hkv;
+        if (lane == 0) sm_unit[warp] = make_int2(unit, meta[s].dest);
         const float base = a.scale_log2 * (kFp8 && a.k_scale ? __ldg(a.k_scale + g) : 1.f);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -360,75 +367,92 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           } else {
             // in fp16, a row scaled by a power of two so that its largest
             // element is in [2^14, 2^15): bits are lost only below 2^-39 of it
-            uint2 w[D / 16];
             float top = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              w[k] = there ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * cq) : make_uint2(0u, 0u);
-              top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_f32(w[k].x)), fabsf(hi_f32(w[k].x))),
-                                     fmaxf(fabsf(lo_f32(w[k].y)), fabsf(hi_f32(w[k].y)))));
+              const uint2 w = there ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * cq)
+                                    : make_uint2(0u, 0u);
+              qa[k][x] = w.x;
+              qa[k][2 + x] = w.y;
+              top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_f32(w.x)), fabsf(hi_f32(w.x))),
+                                     fmaxf(fabsf(lo_f32(w.y)), fabsf(hi_f32(w.y)))));
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int e = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
-            // 2^e in two steps: 14 - e of a subnormal is beyond one float
+            // 2^e in two steps: that of a subnormal row is beyond one float
             const float up1 = ldexpf(1.f, e / 2), up2 = ldexpf(1.f, e - e / 2);
             f[x] = base * ldexpf(1.f, -(e / 2)) * ldexpf(1.f, -(e - e / 2));
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              qa[k][x] = pack_half(lo_f32(w[k].x) * up1 * up2, hi_f32(w[k].x) * up1 * up2);
-              qa[k][2 + x] = pack_half(lo_f32(w[k].y) * up1 * up2, hi_f32(w[k].y) * up1 * up2);
-            }
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t w = qa[k][2 * y + x];
+                qa[k][2 * y + x] = pack_half(lo_f32(w) * up1 * up2, hi_f32(w) * up1 * up2);
+              }
           }
           m[x] = -INFINITY;
           l[x] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          if (k % S::kKeyWarps == kw) q_frag[32 * k] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
+        if (!meet()) {
+          ok = false;
+          break;
+        }
       }
-      const uint32_t kp = ring + s * S::kStage, vp = kp + S::kPage;
-#pragma unroll 1
-      for (int sl = 0; sl < S::kSlices; ++sl) {
-        const int k0 = 16 * (kw * S::kSlices + sl), live = pm.live - k0;   // first key, keys that count
-        if (live <= 0) break;
-        float sc[2][4] = {};
-        if (!kFp8) {
+      constexpr int SL = S::kSlices;
+      const int k0 = 16 * kw * SL, live = page_live - k0;     // the warp's first key; those that count
+      if (live > 0) {
+        const uint32_t kp = ring + s * S::kStage, vp = kp + S::kPage;
+        float sc[2 * SL][4] = {};
+        {
           const int row = k0 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t kb[4];
-            ldsm4(kb, kp + piece_at<D, kFp8, RG>(row, 2 * k + half));
-            mma<false>(sc[0], qa[k], kb[0], kb[1]);
-            mma<false>(sc[1], qa[k], kb[2], kb[3]);
-          }
-        } else {
-          const int row = k0 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+          for (int k = 0; k < D / (kFp8 ? 32 : 16); ++k) {
+            uint4 qf[kFp8 ? 2 : 1];
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t kb[4];
-            ldsm4(kb, kp + piece_at<D, kFp8, RG>(row, 2 * k + half));
+            for (int x = 0; x < (kFp8 ? 2 : 1); ++x) qf[x] = q_frag[32 * ((kFp8 ? 2 : 1) * k + x)];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              mma<true>(sc[0], qa[2 * k + x], e4m3x2_half2(kb[x]), e4m3x2_half2(kb[x] >> 16));
-              mma<true>(sc[1], qa[2 * k + x], e4m3x2_half2(kb[2 + x]), e4m3x2_half2(kb[2 + x] >> 16));
+            for (int y = 0; y < SL; ++y) {
+              uint32_t kb[4];
+              ldsm4(kb, kp + piece_at<D, kFp8, RG>(row + 16 * y, 2 * k + half));
+              if (!kFp8) {
+                mma<false>(sc[2 * y], qf[0], kb[0], kb[1]);
+                mma<false>(sc[2 * y + 1], qf[0], kb[2], kb[3]);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  mma<true>(sc[2 * y], qf[x], e4m3x2_half2(kb[x]), e4m3x2_half2(kb[x] >> 16));
+                  mma<true>(sc[2 * y + 1], qf[x], e4m3x2_half2(kb[2 + x]),
+                            e4m3x2_half2(kb[2 + x] >> 16));
+                }
+              }
             }
           }
         }
         // lane's scores: rows r (0, 1) and r + 8 (2, 3), keys 8 t + 2 cq + {0, 1}
+        const bool part = live < 16 * SL;
+        if (part) {
+#pragma unroll
+          for (int t = 0; t < 2 * SL; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (8 * t + 2 * cq + (x & 1) >= live) sc[t][x] = -INFINITY;
+        }
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2 * SL; ++t)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            sc[t][x] = 8 * t + 2 * cq + (x & 1) < live ? sc[t][x] * f[x >> 1] : -INFINITY;
-            top[x >> 1] = fmaxf(top[x >> 1], sc[t][x]);
-          }
-        float shift[2];
+          for (int x = 0; x < 4; ++x) top[x >> 1] = fmaxf(top[x >> 1], sc[t][x]);
         bool grew = false;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * f[x];
           grew |= top[x] > m[x];
         }
         if (__any_sync(0xffffffffu, grew)) {
@@ -448,73 +472,73 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             o[j][3] *= corr[1];
           }
         }
+        uint32_t hi_w[SL][4], lw_w[SL][4];   // P as A fragments
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          shift[x] = (m[x] == -INFINITY ? 0.f : m[x]) - (kFp8 ? kFp16Shift : 0.f);
-        uint32_t hi[4], lw[4];               // P as A fragments
+        for (int x = 0; x < 2; ++x) {
+          const float shift = (m[x] == -INFINITY ? 0.f : m[x]) - (kFp8 ? kFp16Shift : 0.f);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float p0 = ex2(sc[t][2 * x] - shift[x]), p1 = ex2(sc[t][2 * x + 1] - shift[x]);
+          for (int t = 0; t < 2 * SL; ++t) {
+            const float p0 = ex2(fmaf(sc[t][2 * x], f[x], -shift));
+            const float p1 = ex2(fmaf(sc[t][2 * x + 1], f[x], -shift));
+            const int at = 2 * (t & 1) + x;
             l[x] += p0 + p1;
             if (kFp8) {
-              hi[2 * t + x] = pack_half(p0, p1);
+              hi_w[t >> 1][at] = pack_half(p0, p1);
             } else {
-              hi[2 * t + x] = pack_bf16(p0, p1);
-              lw[2 * t + x] = pack_bf16(p0 - lo_f32(hi[2 * t + x]), p1 - hi_f32(hi[2 * t + x]));
+              hi_w[t >> 1][at] = pack_bf16(p0, p1);
+              lw_w[t >> 1][at] = pack_bf16(p0 - lo_f32(hi_w[t >> 1][at]), p1 - hi_f32(hi_w[t >> 1][at]));
             }
           }
+        }
         // V: a key that does not count has weight 0, and whatever lies there
         // (NaN) must not meet it
-        const bool part = live < 16;
-        uint32_t keep[2] = {~0u, ~0u};
-        if (part) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int k = 8 * t + 2 * cq;
-            keep[t] = (k < live ? 0xffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
+        for (int y = 0; y < SL; ++y) {
+          uint32_t keep[2] = {~0u, ~0u};
+          if (part) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int k = 16 * y + 8 * t + 2 * cq;
+              keep[t] = (k < live ? 0xffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
+            }
           }
-        }
-        const int row = k0 + (lane & 15);
-        if (!kFp8) {
+          const uint4 hi = make_uint4(hi_w[y][0], hi_w[y][1], hi_w[y][2], hi_w[y][3]);
+          const uint4 lw = make_uint4(lw_w[y][0], lw_w[y][1], lw_w[y][2], lw_w[y][3]);
+          const int row = k0 + 16 * y + (lane & 15);
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
+          for (int j = 0; j < D / (kFp8 ? 32 : 16); ++j) {
             uint32_t vb[4];
             ldsm4_t(vb, vp + piece_at<D, kFp8, RG>(row, 2 * j + (lane >> 4)));
             if (part)
 #pragma unroll
               for (int x = 0; x < 4; ++x) vb[x] &= keep[x & 1];
-            mma<false>(o[2 * j], hi, vb[0], vb[1]);
-            mma<false>(o[2 * j + 1], hi, vb[2], vb[3]);
-            mma<false>(o[2 * j], lw, vb[0], vb[1]);
-            mma<false>(o[2 * j + 1], lw, vb[2], vb[3]);
-          }
-        } else {
-          // a transposed 16-bit element is two neighbouring dims: the even ones
-          // make one column tile, the odd ones the next
+            if (!kFp8) {
+              mma<false>(o[2 * j], hi, vb[0], vb[1]);
+              mma<false>(o[2 * j + 1], hi, vb[2], vb[3]);
+              mma<false>(o[2 * j], lw, vb[0], vb[1]);
+              mma<false>(o[2 * j + 1], lw, vb[2], vb[3]);
+            } else {
+              // a transposed 16-bit element is two neighbouring dims: the even
+              // ones make one column tile, the odd ones the next
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            uint32_t vb[4];
-            ldsm4_t(vb, vp + piece_at<D, kFp8, RG>(row, 2 * j + (lane >> 4)));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (part) {
-                vb[2 * x] &= keep[0];
-                vb[2 * x + 1] &= keep[1];
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t u0 = __byte_perm(vb[2 * x], 0, 0x3120);
+                const uint32_t u1 = __byte_perm(vb[2 * x + 1], 0, 0x3120);
+                mma<true>(o[4 * j + 2 * x], hi, e4m3x2_half2(u0), e4m3x2_half2(u1));
+                mma<true>(o[4 * j + 2 * x + 1], hi, e4m3x2_half2(u0 >> 16), e4m3x2_half2(u1 >> 16));
               }
-              const uint32_t u0 = __byte_perm(vb[2 * x], 0, 0x3120);
-              const uint32_t u1 = __byte_perm(vb[2 * x + 1], 0, 0x3120);
-              mma<true>(o[4 * j + 2 * x], hi, e4m3x2_half2(u0), e4m3x2_half2(u1));
-              mma<true>(o[4 * j + 2 * x + 1], hi, e4m3x2_half2(u0 >> 16), e4m3x2_half2(u1 >> 16));
             }
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
+      if (++s == NS) {
+        s = 0;
+        ph ^= 1u;
+      }
 
-      if (pm.flags & 2) {
+      if (flags & 2) {
         // the piece ends: the key warps' results are added
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -538,7 +562,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             top = fmaxf(top, sm_m[rg * S::kKeyWarps + k][r + 8 * x]);
           w[x] = m[x] == -INFINITY ? 0.f : ex2(m[x] - top);
         }
-        float* part = partial + static_cast<int64_t>(2 * c + max(pm.dest, 0)) * S::kRows * (D + 2);
+        const int2 ud = sm_unit[warp];
+        const int dest = ud.y, rt = ud.x % RT, bg = ud.x / RT, b = bg / a.Hkv, g = bg % a.Hkv;
+        float* part = partial + static_cast<int64_t>(2 * c + max(dest, 0)) * S::kRows * (D + 2);
         constexpr int kQuads = S::kChunk / 4;
         constexpr int kElems = S::kRows * kQuads, kIter = (kElems + 32 * W - 1) / (32 * W);
 #pragma unroll 1
@@ -591,7 +617,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               tot += sm_m[wp][rr] == -INFINITY ? sm_l[wp][rr] : sm_l[wp][rr] * ex2(sm_m[wp][rr] - top);
             }
             const int col_g = ch * S::kChunk + col;
-            if (pm.dest < 0) {
+            if (dest < 0) {
               const float inv = tot == 0.f ? 0.f : (a.v_scale ? __ldg(a.v_scale + g) : 1.f) / tot;
               const int h = g * G + head;
               *reinterpret_cast<uint2*>(a.o + b * a.os[0] + h * a.os[2] + col_g) = make_uint2(
@@ -705,7 +731,8 @@ template <int D, bool kFp8, int RG>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t st) {
   using S = Shape<D, kFp8, RG>;
-  static_assert(S::kCtas * (S::kSmem + 4096) <= 227 * 1024, "the ring does not fit shared memory");
+  // with 2 KB for the static arrays and the 1 KB that every CTA costs beside
+  static_assert(S::kCtas * (S::kSmem + 3072) <= 228 * 1024, "the ring does not fit shared memory");
   const int G = a.H / a.Hkv, RT = (G + S::kRows - 1) / S::kRows;
   Cut* cuts = reinterpret_cast<Cut*>(a.ws);
   float* partial = reinterpret_cast<float*>(a.ws + cuts_bytes());
