@@ -38,7 +38,7 @@ namespace sa {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMaxRuns = 2 * kSms;
+constexpr int kMaxRuns = 3 * kSms;
 constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16
 
 // Rows of query heads a CTA holds: RG groups of 16; KW warps share a page's
@@ -48,15 +48,18 @@ struct Shape {
   static constexpr int kRows = 16 * RG;
   static constexpr int kKeyWarps = RG == 4 ? 2 : 4;
   static constexpr int kWarps = kKeyWarps * RG;         // consumer warps
-  static constexpr int kSlices = 4 / kKeyWarps;         // 16-key slices of a page per warp
+  static constexpr int kSlices = RG == 4 ? 4 : (RG == 2 ? 2 : 1);                // 16-key slices a warp takes at once
+  static constexpr int kParts = 4 / kSlices;            // warps that share a page
+  static constexpr int kPhases = kKeyWarps / kParts;    // pages being worked on
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kCtas = RG == 1 ? 2 : 1;         // per SM
+  // CTAs on an SM: as many as leave each two or more pages in its ring
+  static constexpr int kCtas = RG > 1 ? 1 : (kFp8 || D == 64 ? 3 : 2);
   static constexpr int kRuns = kSms * kCtas;
   static constexpr int kRowBytes = kFp8 ? D : 2 * D;    // one token of one head
   static constexpr int kPage = kBlock * kRowBytes;
   static constexpr int kBox = kRowBytes < 128 ? kRowBytes : 128;
   static constexpr int kStage = 2 * kPage;
-  static constexpr int kRing = (RG == 1 ? 96 : 160) * 1024;
+  static constexpr int kRing = (kCtas == 3 ? 48 : (kCtas == 2 ? 96 : 160)) * 1024;
   static constexpr int kStages = kRing / kStage < 16 ? kRing / kStage : 16;
   static constexpr int kChunk = 32;                     // columns joined at a time
   static constexpr int kPad = kChunk + 8;               // row stride of the join buffer
@@ -96,21 +99,23 @@ __device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t addr) {
 template <bool kFp16>
 __device__ __forceinline__ void mma(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
   if (kFp16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
                  "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
                  "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes (low half of x) as two fp16 values; exact.
-__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+// Four e4m3 codes as two pairs of fp16 values, lower bytes first; exact.
+__device__ __forceinline__ uint2 e4m3x4_half4(uint32_t x) {
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y) : "r"(x));
   return r;
 }
 
@@ -127,13 +132,20 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 __device__ __forceinline__ float lo_f32(uint32_t bf2) { return __uint_as_float(bf2 << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t bf2) { return __uint_as_float(bf2 & 0xffff0000u); }
 
-// Byte offset of 16-byte piece `piece` of token `row` in a page as TMA lays it
-// out: boxes of at most 128 bytes a token, pieces XORed with the row.
-template <int D, bool kFp8, int RG>
-__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
-  using S = Shape<D, kFp8, RG>;
-  if (S::kBox == 64) return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-  return (piece >> 3) * (kBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+// A page as TMA lays it out: boxes of at most 128 bytes a token, their 16-byte
+// pieces XORed with the row (rows 0 .. 7, or every second one in 64-byte boxes).
+// piece_row is where piece `half` (0, 1) of a row lies; next_piece steps from
+// there to piece 2 k + half: one XOR, as nothing below the row is added.
+template <int kBox>
+__device__ __forceinline__ uint32_t piece_row(int row, int half) {
+  if (kBox == 64) return row * 64 + ((half ^ ((row >> 1) & 3)) << 4);
+  return row * 128 + ((half ^ (row & 7)) << 4);
+}
+
+template <int kBox>
+__device__ __forceinline__ uint32_t next_piece(uint32_t at, int k) {
+  constexpr int kPairs = kBox / 32;          // pieces of a box row, in pairs
+  return (at ^ ((k % kPairs) << 5)) + k / kPairs * (kBlock * kBox);
 }
 
 // Pages of group `i` of the list: a sequence (every page), or a row of the route.
@@ -345,6 +357,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         break;
       }
       const int flags = meta[s].flags, page_live = meta[s].live;
+      const bool mine = i % S::kPhases == kw / S::kParts;
       if (flags & 1) {
         // the unit's queries as A fragments, rows beyond the group's heads
         // zero: kept in shared memory, every warp of a row group writing some
@@ -405,35 +418,49 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
       }
       constexpr int SL = S::kSlices;
-      const int k0 = 16 * kw * SL, live = page_live - k0;     // the warp's first key; those that count
-      if (live > 0) {
+      // the warp's first key of the page, and how many from it on count
+      const int k0 = 16 * SL * (kw % S::kParts), live = page_live - k0;
+      if (mine && live > 0) {
         const uint32_t kp = ring + s * S::kStage, vp = kp + S::kPage;
+        // The fragments of a batch of steps are loaded before the first of them
+        // is used, and the first of V before the softmax.
+        constexpr int kSteps = D / (kFp8 ? 32 : 16), kQ = kFp8 ? 2 : 1;
+        constexpr int KB = SL == 4 || kFp8 ? 1 : 4 / SL, VB = kFp8 ? 2 : 4;   // steps of a batch
         float sc[2 * SL][4] = {};
-        {
-          const int row = k0 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+        const uint32_t k_at = kp + piece_row<S::kBox>(k0 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 #pragma unroll
-          for (int k = 0; k < D / (kFp8 ? 32 : 16); ++k) {
-            uint4 qf[kFp8 ? 2 : 1];
+        for (int k = 0; k < kSteps; k += KB) {
+          uint4 qf[KB * kQ];
+          uint32_t kb[KB][SL][4];
 #pragma unroll
-            for (int x = 0; x < (kFp8 ? 2 : 1); ++x) qf[x] = q_frag[32 * ((kFp8 ? 2 : 1) * k + x)];
+          for (int u = 0; u < KB; ++u) {
+#pragma unroll
+            for (int y = 0; y < SL; ++y)
+              ldsm4(kb[u][y], next_piece<S::kBox>(k_at, k + u) + 16 * y * S::kBox);
+#pragma unroll
+            for (int x = 0; x < kQ; ++x) qf[kQ * u + x] = q_frag[32 * (kQ * (k + u) + x)];
+          }
+#pragma unroll
+          for (int u = 0; u < KB; ++u)
 #pragma unroll
             for (int y = 0; y < SL; ++y) {
-              uint32_t kb[4];
-              ldsm4(kb, kp + piece_at<D, kFp8, RG>(row + 16 * y, 2 * k + half));
               if (!kFp8) {
-                mma<false>(sc[2 * y], qf[0], kb[0], kb[1]);
-                mma<false>(sc[2 * y + 1], qf[0], kb[2], kb[3]);
+                mma<false>(sc[2 * y], qf[u], kb[u][y][0], kb[u][y][1]);
+                mma<false>(sc[2 * y + 1], qf[u], kb[u][y][2], kb[u][y][3]);
               } else {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  mma<true>(sc[2 * y], qf[x], e4m3x2_half2(kb[x]), e4m3x2_half2(kb[x] >> 16));
-                  mma<true>(sc[2 * y + 1], qf[x], e4m3x2_half2(kb[2 + x]),
-                            e4m3x2_half2(kb[2 + x] >> 16));
+                  const uint2 k0h = e4m3x4_half4(kb[u][y][x]), k1h = e4m3x4_half4(kb[u][y][2 + x]);
+                  mma<true>(sc[2 * y], qf[2 * u + x], k0h.x, k0h.y);
+                  mma<true>(sc[2 * y + 1], qf[2 * u + x], k1h.x, k1h.y);
                 }
               }
             }
-          }
         }
+        const uint32_t v_at = vp + piece_row<S::kBox>(k0 + (lane & 15), lane >> 4);
+        uint32_t vb[VB][4];
+#pragma unroll
+        for (int u = 0; u < VB; ++u) ldsm4_t(vb[u], next_piece<S::kBox>(v_at, u));
         // lane's scores: rows r (0, 1) and r + 8 (2, 3), keys 8 t + 2 cq + {0, 1}
         const bool part = live < 16 * SL;
         if (part) {
@@ -472,23 +499,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             o[j][3] *= corr[1];
           }
         }
-        uint32_t hi_w[SL][4], lw_w[SL][4];   // P as A fragments
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float shift = (m[x] == -INFINITY ? 0.f : m[x]) - (kFp8 ? kFp16Shift : 0.f);
+          float sum = 0.f;
 #pragma unroll
           for (int t = 0; t < 2 * SL; ++t) {
-            const float p0 = ex2(fmaf(sc[t][2 * x], f[x], -shift));
-            const float p1 = ex2(fmaf(sc[t][2 * x + 1], f[x], -shift));
-            const int at = 2 * (t & 1) + x;
-            l[x] += p0 + p1;
-            if (kFp8) {
-              hi_w[t >> 1][at] = pack_half(p0, p1);
-            } else {
-              hi_w[t >> 1][at] = pack_bf16(p0, p1);
-              lw_w[t >> 1][at] = pack_bf16(p0 - lo_f32(hi_w[t >> 1][at]), p1 - hi_f32(hi_w[t >> 1][at]));
-            }
+            sc[t][2 * x] = ex2(fmaf(sc[t][2 * x], f[x], -shift));
+            sc[t][2 * x + 1] = ex2(fmaf(sc[t][2 * x + 1], f[x], -shift));
+            sum += sc[t][2 * x] + sc[t][2 * x + 1];
           }
+          l[x] += sum;
         }
         // V: a key that does not count has weight 0, and whatever lies there
         // (NaN) must not meet it
@@ -502,31 +523,49 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               keep[t] = (k < live ? 0xffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
             }
           }
-          const uint4 hi = make_uint4(hi_w[y][0], hi_w[y][1], hi_w[y][2], hi_w[y][3]);
-          const uint4 lw = make_uint4(lw_w[y][0], lw_w[y][1], lw_w[y][2], lw_w[y][3]);
-          const int row = k0 + 16 * y + (lane & 15);
+          uint32_t hi_w[4], lw_w[4];           // P as A fragments
 #pragma unroll
-          for (int j = 0; j < D / (kFp8 ? 32 : 16); ++j) {
-            uint32_t vb[4];
-            ldsm4_t(vb, vp + piece_at<D, kFp8, RG>(row, 2 * j + (lane >> 4)));
+          for (int x = 0; x < 4; ++x) {
+            const float p0 = sc[2 * y + (x >> 1)][2 * (x & 1)], p1 = sc[2 * y + (x >> 1)][2 * (x & 1) + 1];
+            hi_w[x] = kFp8 ? pack_half(p0, p1) : pack_bf16(p0, p1);
+            if (!kFp8) lw_w[x] = pack_bf16(p0 - lo_f32(hi_w[x]), p1 - hi_f32(hi_w[x]));
+          }
+          const uint4 hi = make_uint4(hi_w[0], hi_w[1], hi_w[2], hi_w[3]);
+          const uint4 lw = kFp8 ? hi : make_uint4(lw_w[0], lw_w[1], lw_w[2], lw_w[3]);
+#pragma unroll
+          for (int j = 0; j < kSteps; j += VB) {
+            if (y > 0 || j > 0)
+#pragma unroll
+              for (int u = 0; u < VB; ++u)
+                ldsm4_t(vb[u], next_piece<S::kBox>(v_at, j + u) + 16 * y * S::kBox);
             if (part)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) vb[x] &= keep[x & 1];
+              for (int u = 0; u < VB; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) vb[u][x] &= keep[x & 1];
             if (!kFp8) {
-              mma<false>(o[2 * j], hi, vb[0], vb[1]);
-              mma<false>(o[2 * j + 1], hi, vb[2], vb[3]);
-              mma<false>(o[2 * j], lw, vb[0], vb[1]);
-              mma<false>(o[2 * j + 1], lw, vb[2], vb[3]);
+#pragma unroll
+              for (int u = 0; u < VB; ++u) {
+                mma<false>(o[2 * (j + u)], hi, vb[u][0], vb[u][1]);
+                mma<false>(o[2 * (j + u) + 1], hi, vb[u][2], vb[u][3]);
+              }
+#pragma unroll
+              for (int u = 0; u < VB; ++u) {
+                mma<false>(o[2 * (j + u)], lw, vb[u][0], vb[u][1]);
+                mma<false>(o[2 * (j + u) + 1], lw, vb[u][2], vb[u][3]);
+              }
             } else {
               // a transposed 16-bit element is two neighbouring dims: the even
               // ones make one column tile, the odd ones the next
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t u0 = __byte_perm(vb[2 * x], 0, 0x3120);
-                const uint32_t u1 = __byte_perm(vb[2 * x + 1], 0, 0x3120);
-                mma<true>(o[4 * j + 2 * x], hi, e4m3x2_half2(u0), e4m3x2_half2(u1));
-                mma<true>(o[4 * j + 2 * x + 1], hi, e4m3x2_half2(u0 >> 16), e4m3x2_half2(u1 >> 16));
-              }
+              for (int u = 0; u < VB; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint2 u0 = e4m3x4_half4(__byte_perm(vb[u][2 * x], 0, 0x3120));
+                  const uint2 u1 = e4m3x4_half4(__byte_perm(vb[u][2 * x + 1], 0, 0x3120));
+                  mma<true>(o[4 * (j + u) + 2 * x], hi, u0.x, u1.x);
+                  mma<true>(o[4 * (j + u) + 2 * x + 1], hi, u0.y, u1.y);
+                }
             }
           }
         }
@@ -562,6 +601,15 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             top = fmaxf(top, sm_m[rg * S::kKeyWarps + k][r + 8 * x]);
           w[x] = m[x] == -INFINITY ? 0.f : ex2(m[x] - top);
         }
+        // scaled in place: as products inside the loop below they would be kept
+        // beside the sums, 64 more registers and spills in the loop over pages
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][0] *= w[0];
+          o[j][1] *= w[0];
+          o[j][2] *= w[1];
+          o[j][3] *= w[1];
+        }
         const int2 ud = sm_unit[warp];
         const int dest = ud.y, rt = ud.x % RT, bg = ud.x / RT, b = bg / a.Hkv, g = bg % a.Hkv;
         float* part = partial + static_cast<int64_t>(2 * c + max(dest, 0)) * S::kRows * (D + 2);
@@ -577,14 +625,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             float* row1 = row0 + 8 * S::kPad;
             if (!kFp8) {
               const int col = (j % (S::kChunk / 8)) * 8 + 2 * cq;
-              *reinterpret_cast<float2*>(row0 + col) = make_float2(o[j][0] * w[0], o[j][1] * w[0]);
-              *reinterpret_cast<float2*>(row1 + col) = make_float2(o[j][2] * w[1], o[j][3] * w[1]);
+              *reinterpret_cast<float2*>(row0 + col) = make_float2(o[j][0], o[j][1]);
+              *reinterpret_cast<float2*>(row1 + col) = make_float2(o[j][2], o[j][3]);
             } else {
               const int col = (j % (S::kChunk / 8) / 2) * 16 + 4 * cq + (j & 1);
-              row0[col] = o[j][0] * w[0];
-              row0[col + 2] = o[j][1] * w[0];
-              row1[col] = o[j][2] * w[1];
-              row1[col + 2] = o[j][3] * w[1];
+              row0[col] = o[j][0];
+              row0[col + 2] = o[j][1];
+              row1[col] = o[j][2];
+              row1[col + 2] = o[j][3];
             }
           }
           if (!meet()) {
