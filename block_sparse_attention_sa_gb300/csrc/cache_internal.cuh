@@ -98,18 +98,22 @@ __device__ __forceinline__ int run_of(int64_t T, int C, int64_t item) {
 
 struct Run {
   int64_t T, lo, hi;       // items of the list, and this CTA's among them
+  int64_t off;             // where a run that is not empty begins: item `off`
+  int group;               // of group `group`
 };
 
 // The list is that of `groups` groups in order, each count(i) * per_group
-// items. Every CTA of the grid finds its run of it by a scan of the counts;
-// *group and *off (shared memory) say where a run that is not empty begins.
-// All NT threads call it; it ends with every thread past a barrier.
+// items. Every CTA of the grid finds its run of it by a scan of the counts: up
+// to 32 groups by each warp for itself, more by the CTA. All NT threads call it
+// and get the same; it ends with every thread past a barrier.
 template <int NT, class Count>
-__device__ __forceinline__ Run plan_run(int groups, int64_t per_group, Count count,
-                                        int64_t* warp_sum, int* group, int64_t* off) {
+__device__ __forceinline__ Run plan_run(int groups, int64_t per_group, Count count) {
+  __shared__ int64_t warp_sum[NT / 32], start_off;
+  __shared__ int start_group;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per_thread = (groups + NT - 1) / NT;
-  const int g0 = tid * per_thread < groups ? tid * per_thread : groups;
+  const bool few = groups <= 32;
+  const int per_thread = few ? 1 : (groups + NT - 1) / NT, first = few ? lane : tid * per_thread;
+  const int g0 = first < groups ? first : groups;
   const int g1 = g0 + per_thread < groups ? g0 + per_thread : groups;
   int64_t mine = 0;
   for (int i = g0; i < g1; ++i) mine += count(i);
@@ -119,30 +123,52 @@ __device__ __forceinline__ Run plan_run(int groups, int64_t per_group, Count cou
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += v;
   }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
   int64_t before = 0, total = 0;
+  if (few) {
+    total = __shfl_sync(0xffffffffu, incl, 31);
+  } else {
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
   }
   Run r;
   r.T = total * per_group;
   r.lo = run_start(r.T, gridDim.x, blockIdx.x);
   r.hi = run_start(r.T, gridDim.x, blockIdx.x + 1);
+  r.group = 0;
+  r.off = 0;
   int64_t at = (before + incl - mine) * per_group;
-  if (r.lo < r.hi && r.lo >= at && r.lo < at + mine * per_group) {
+  const bool here = r.lo < r.hi && r.lo >= at && r.lo < at + mine * per_group;
+  if (here) {
     int i = g0;
     for (;; ++i) {
       const int64_t n = count(i) * per_group;
       if (r.lo < at + n) break;
       at += n;
     }
-    *group = i;
-    *off = r.lo - at;
+    r.group = i;
+    r.off = r.lo - at;
   }
-  __syncthreads();
+  if (few) {
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    r.group = __shfl_sync(0xffffffffu, r.group, src < 0 ? 0 : src);
+    r.off = __shfl_sync(0xffffffffu, r.off, src < 0 ? 0 : src);
+    __syncthreads();
+  } else {
+    if (here) {
+      start_group = r.group;
+      start_off = r.off;
+    }
+    __syncthreads();
+    if (r.lo < r.hi) {
+      r.group = start_group;
+      r.off = start_off;
+    }
+  }
   return r;
 }
 #endif

@@ -175,9 +175,6 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   __shared__ PageMeta meta[NS];
   __shared__ float sm_m[W][16], sm_l[W][16];
   __shared__ int2 sm_unit[W];                // each warp's copy of its unit and dest
-  __shared__ int64_t warp_sum[NT / 32 + 1];
-  __shared__ int64_t start_off;
-  __shared__ int start_group;
   __shared__ volatile int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -212,8 +209,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // this CTA's run of the page list
   const Run run = plan_run<NT>(
       n_groups, per_group,
-      [&](int i) { return static_cast<int64_t>(group_pages(a, i, &status)); }, warp_sum,
-      &start_group, &start_off);
+      [&](int i) { return static_cast<int64_t>(group_pages(a, i, &status)); });
   const int64_t T = run.T, lo = run.lo, hi = run.hi;
   // groups without a page: nothing to attend
   for (int i = c + C * warp; i < n_groups; i += C * (NT / 32)) {
@@ -232,8 +228,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (warp == W) {
     // ---------------------------------------------------------- producer --
     int64_t left = hi - lo;
-    int group = start_group;
-    int64_t off = left > 0 ? start_off : 0;     // pages into the group's units
+    int group = run.group;
+    int64_t off = run.off;                      // pages into the group's units
     int64_t issued = 0;
     Cut cut{-1, 0, 0, 0};
     bool ok = true;
@@ -349,6 +345,62 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       join_phase ^= 1u;
       return done;
     };
+    // A unit's queries as A fragments, rows beyond the group's heads zero: kept
+    // in shared memory, every warp of a row group writing some of them.
+    auto load_queries = [&](int unit) {
+      uint32_t qa[D / 16][4];
+      const int rt = unit % RT, bg = unit / RT, b = bg / a.Hkv, g = bg % a.Hkv;
+      const float base = a.scale_log2 * (kFp8 && a.k_scale ? __ldg(a.k_scale + g) : 1.f);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = rt * S::kRows + rg * 16 + r + 8 * x;
+        const bool there = row < G;
+        const uint16_t* q = a.q + b * a.qs[0] + (g * G + (there ? row : 0)) * a.qs[2];
+        f[x] = base;
+        if (!kFp8) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            qa[k][x] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * cq) : 0u;
+            qa[k][2 + x] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * cq + 8) : 0u;
+          }
+        } else {
+          // in fp16, a row scaled by a power of two so that its largest
+          // element is in [2^14, 2^15): bits are lost only below 2^-39 of it
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint2 w = there ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * cq)
+                                  : make_uint2(0u, 0u);
+            qa[k][x] = w.x;
+            qa[k][2 + x] = w.y;
+            top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_f32(w.x)), fabsf(hi_f32(w.x))),
+                                   fmaxf(fabsf(lo_f32(w.y)), fabsf(hi_f32(w.y)))));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
+          // 2^e in two steps: that of a subnormal row is beyond one float
+          const float up1 = ldexpf(1.f, e / 2), up2 = ldexpf(1.f, e - e / 2);
+          f[x] = base * ldexpf(1.f, -(e / 2)) * ldexpf(1.f, -(e - e / 2));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t w = qa[k][2 * y + x];
+              qa[k][2 * y + x] = pack_half(lo_f32(w) * up1 * up2, hi_f32(w) * up1 * up2);
+            }
+        }
+                      }
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        if (k % S::kKeyWarps == kw) q_frag[32 * k] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
+    };
+    // those of the first unit need not wait for its first page
+    if (n_pages > 0) {
+      const int cnt = group_pages(a, run.group, &status);
+      const int sub = cnt > 0 ? static_cast<int>(run.off / cnt) : 0;
+      load_queries(min((routed ? run.group : run.group * a.Hkv) * RT + sub, a.B * a.Hkv * RT - 1));
+    }
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < n_pages; ++i) {
@@ -359,59 +411,12 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const int flags = meta[s].flags, page_live = meta[s].live;
       const bool mine = i % S::kPhases == kw / S::kParts;
       if (flags & 1) {
-        // the unit's queries as A fragments, rows beyond the group's heads
-        // zero: kept in shared memory, every warp of a row group writing some
-        uint32_t qa[D / 16][4];
-        const int unit = meta[s].unit, rt = unit % RT, bg = unit / RT, b = bg / a.Hkv, g = bg % a.Hkv;
-        if (lane == 0) sm_unit[warp] = make_int2(unit, meta[s].dest);
-        const float base = a.scale_log2 * (kFp8 && a.k_scale ? __ldg(a.k_scale + g) : 1.f);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int row = rt * S::kRows + rg * 16 + r + 8 * x;
-          const bool there = row < G;
-          const uint16_t* q = a.q + b * a.qs[0] + (g * G + (there ? row : 0)) * a.qs[2];
-          f[x] = base;
-          if (!kFp8) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              qa[k][x] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * cq) : 0u;
-              qa[k][2 + x] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * cq + 8) : 0u;
-            }
-          } else {
-            // in fp16, a row scaled by a power of two so that its largest
-            // element is in [2^14, 2^15): bits are lost only below 2^-39 of it
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint2 w = there ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * cq)
-                                    : make_uint2(0u, 0u);
-              qa[k][x] = w.x;
-              qa[k][2 + x] = w.y;
-              top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_f32(w.x)), fabsf(hi_f32(w.x))),
-                                     fmaxf(fabsf(lo_f32(w.y)), fabsf(hi_f32(w.y)))));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
-            // 2^e in two steps: that of a subnormal row is beyond one float
-            const float up1 = ldexpf(1.f, e / 2), up2 = ldexpf(1.f, e - e / 2);
-            f[x] = base * ldexpf(1.f, -(e / 2)) * ldexpf(1.f, -(e - e / 2));
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t w = qa[k][2 * y + x];
-                qa[k][2 * y + x] = pack_half(lo_f32(w) * up1 * up2, hi_f32(w) * up1 * up2);
-              }
-          }
-          m[x] = -INFINITY;
-          l[x] = 0.f;
-        }
+        if (lane == 0) sm_unit[warp] = make_int2(meta[s].unit, meta[s].dest);
+        if (i > 0) load_queries(meta[s].unit);
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          if (k % S::kKeyWarps == kw) q_frag[32 * k] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
         if (!meet()) {
           ok = false;
           break;
@@ -578,16 +583,20 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
 
       if (flags & 2) {
-        // the piece ends: the key warps' results are added
+        const int2 ud = sm_unit[warp];
+        const int dest = ud.y, rt = ud.x % RT, bg = ud.x / RT, b = bg / a.Hkv, g = bg % a.Hkv;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        }
+        // the piece ends: the key warps' results are added
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
           if (cq == 0) {
             sm_m[warp][r + 8 * x] = m[x];
             sm_l[warp][r + 8 * x] = l[x];
           }
-        }
         if (!meet()) {
           ok = false;
           break;
@@ -610,40 +619,39 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           o[j][2] *= w[1];
           o[j][3] *= w[1];
         }
-        const int2 ud = sm_unit[warp];
-        const int dest = ud.y, rt = ud.x % RT, bg = ud.x / RT, b = bg / a.Hkv, g = bg % a.Hkv;
         float* part = partial + static_cast<int64_t>(2 * c + max(dest, 0)) * S::kRows * (D + 2);
-        constexpr int kQuads = S::kChunk / 4;
-        constexpr int kElems = S::kRows * kQuads, kIter = (kElems + 32 * W - 1) / (32 * W);
+        // through the join buffer 32 columns at a time, or, behind a run's last
+        // page, through the ring all at once: no page will be loaded any more
+        const bool at_once = i == n_pages - 1;
+        float* buf = at_once ? reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))) : join;
+        const int cols = at_once ? D : S::kChunk, pad = cols + 8, quads = cols / 4;
 #pragma unroll 1
-        for (int ch = 0; ch < D / S::kChunk; ++ch) {
+        for (int c0 = 0; c0 < D; c0 += cols) {
+          float* row0 = buf + (warp * 16 + r) * pad - c0;
+          float* row1 = row0 + 8 * pad;
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            if (j / (S::kChunk / 8) != ch) continue;
-            // columns of the tile: consecutive, or (e4m3) every second dim of 16
-            float* row0 = join + (warp * 16 + r) * S::kPad;
-            float* row1 = row0 + 8 * S::kPad;
-            if (!kFp8) {
-              const int col = (j % (S::kChunk / 8)) * 8 + 2 * cq;
-              *reinterpret_cast<float2*>(row0 + col) = make_float2(o[j][0], o[j][1]);
-              *reinterpret_cast<float2*>(row1 + col) = make_float2(o[j][2], o[j][3]);
+          for (int j = 0; j < D / 8; j += 2) {
+            if (8 * j < c0 || 8 * j >= c0 + cols) continue;
+            // columns of a tile: consecutive, or (e4m3) every second dim of 16
+            if (kFp8) {
+              const int col = 8 * j + 4 * cq;
+              *reinterpret_cast<float4*>(row0 + col) = make_float4(o[j][0], o[j + 1][0], o[j][1], o[j + 1][1]);
+              *reinterpret_cast<float4*>(row1 + col) = make_float4(o[j][2], o[j + 1][2], o[j][3], o[j + 1][3]);
             } else {
-              const int col = (j % (S::kChunk / 8) / 2) * 16 + 4 * cq + (j & 1);
-              row0[col] = o[j][0];
-              row0[col + 2] = o[j][1];
-              row1[col] = o[j][2];
-              row1[col + 2] = o[j][3];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int col = 8 * (j + y) + 2 * cq;
+                *reinterpret_cast<float2*>(row0 + col) = make_float2(o[j + y][0], o[j + y][1]);
+                *reinterpret_cast<float2*>(row1 + col) = make_float2(o[j + y][2], o[j + y][3]);
+              }
             }
           }
           if (!meet()) {
             ok = false;
             break;
           }
-#pragma unroll
-          for (int it = 0; it < kIter; ++it) {
-            const int e = it * 32 * W + warp * 32 + lane;
-            if (kElems % (32 * W) != 0 && e >= kElems) break;
-            const int row = e / kQuads, col = e % kQuads * 4, grp = row >> 4, rr = row & 15;
+          for (int e = warp * 32 + lane; e < S::kRows * quads; e += 32 * W) {
+            const int row = e / quads, col = e % quads * 4, grp = row >> 4, rr = row & 15;
             const int head = rt * S::kRows + row;
             if (head >= G) continue;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -651,7 +659,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < S::kKeyWarps; ++k) {
               const int wp = grp * S::kKeyWarps + k;
-              const float4 v = *reinterpret_cast<const float4*>(join + (wp * 16 + rr) * S::kPad + col);
+              const float4 v = *reinterpret_cast<const float4*>(buf + (wp * 16 + rr) * pad + col);
               sum.x += v.x;
               sum.y += v.y;
               sum.z += v.z;
@@ -664,7 +672,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               // without a maximum the sum is 0, or NaN if only NaN was there
               tot += sm_m[wp][rr] == -INFINITY ? sm_l[wp][rr] : sm_l[wp][rr] * ex2(sm_m[wp][rr] - top);
             }
-            const int col_g = ch * S::kChunk + col;
+            const int col_g = c0 + col;
             if (dest < 0) {
               const float inv = tot == 0.f ? 0.f : (a.v_scale ? __ldg(a.v_scale + g) : 1.f) / tot;
               const int h = g * G + head;
@@ -676,14 +684,12 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                                : (top - (kFp8 ? kFp16Shift : 0.f) + log2f(tot)) * 0.69314718055994530942f;
             } else {
               *reinterpret_cast<float4*>(part + row * D + col_g) = sum;
-              if (col_g == 0) {
-                part[S::kRows * D + row] = top;
-                part[S::kRows * D + S::kRows + row] = tot;
-              }
+              if (col_g == 0)
+                *reinterpret_cast<float2*>(part + S::kRows * D + 2 * row) = make_float2(top, tot);
             }
           }
           // the buffer is written again only after every warp has read it
-          if (!meet()) {
+          if (!at_once && !meet()) {
             ok = false;
             break;
           }
@@ -699,7 +705,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
-// grid (min(units, runs), heads of a unit), 256 threads: adds the pieces of one
+// grid (min(units, runs), heads of a unit), 256 threads: adds the partials of one
 // cut unit for one query head, eight warps taking every eighth piece.
 constexpr int kJoinWarps = 8;
 template <int D>
@@ -718,7 +724,8 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int V = D / 32;
   const int64_t stride = static_cast<int64_t>(rows) * (D + 2);
-  // piece 0 is the second partial of its run (the run ends in it), the others the first
+  // the first piece is the second partial of its run (the run ends in it), the
+  // others the first of theirs
   auto piece = [&](int i) {
     return partial + stride * (2 * static_cast<int64_t>(cut.first + i) + (i == 0 ? 1 : 0));
   };
@@ -727,7 +734,8 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* 
 #pragma unroll 4
   for (int i = warp; i < n; i += kJoinWarps) {
     const float* p = piece(i);
-    const float pm = p[rows * D + row], pl = p[rows * D + rows + row];
+    const float2 ml = *reinterpret_cast<const float2*>(p + rows * D + 2 * row);
+    const float pm = ml.x, pl = ml.y;
     float v[V];
 #pragma unroll
     for (int x = 0; x < V; ++x) v[x] = p[row * D + lane + 32 * x];
@@ -779,6 +787,7 @@ template <int D, bool kFp8, int RG>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t st) {
   using S = Shape<D, kFp8, RG>;
+  static_assert(S::kWarps * 16 * (D + 8) * 4 <= S::kStages * S::kStage, "the ring holds a unit's sums");
   // with 2 KB for the static arrays and the 1 KB that every CTA costs beside
   static_assert(S::kCtas * (S::kSmem + 3072) <= 228 * 1024, "the ring does not fit shared memory");
   const int G = a.H / a.Hkv, RT = (G + S::kRows - 1) / S::kRows;
@@ -818,8 +827,10 @@ cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& kmap, const CUtenso
 }  // namespace
 
 size_t decode_ws_bytes(int H, int Hkv, int D) {
-  const size_t rows = 16 * static_cast<size_t>(row_groups(H / Hkv));
-  return cuts_bytes() + static_cast<size_t>(2 * kMaxRuns) * rows * (D + 2) * sizeof(float);
+  // two partials of every run
+  const size_t rows = row_groups(H / Hkv) == 1 ? static_cast<size_t>(kMaxRuns) * 16
+                                               : static_cast<size_t>(kSms) * 16 * row_groups(H / Hkv);
+  return cuts_bytes() + 2 * rows * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,

@@ -115,9 +115,6 @@ __device__ __forceinline__ float load_heads(const RoutePagesArgs& a, int b, int 
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) score_kernel(RoutePagesArgs a) {
-  __shared__ int64_t warp_sum[kWarps];
-  __shared__ int64_t start_off;
-  __shared__ int start_group;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.H / a.Hkv;
   const Layout L = layout(static_cast<int64_t>(a.B) * a.Hkv, a.pm.max_pages);
@@ -132,13 +129,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(RoutePagesArgs a) {
     return (n + kBlock - 1) / kBlock;
   };
   auto tiles = [&](int b) { return static_cast<int64_t>((pages(b) + kTile - 1) / kTile); };
-  const Run run = plan_run<kThreads>(a.B, a.Hkv, tiles, warp_sum, &start_group, &start_off);
+  const Run run = plan_run<kThreads>(a.B, a.Hkv, tiles);
   // the CTA's run, a consecutive part of it for each warp
   const int64_t n_cta = run.hi - run.lo;
   int64_t left = n_cta * (warp + 1) / kWarps - n_cta * warp / kWarps;
   if (left > 0) {
-    int b = start_group;
-    int64_t off = start_off + n_cta * warp / kWarps;
+    int b = run.group;
+    int64_t off = run.off + n_cta * warp / kWarps;
     uint32_t qa[D / 16][4];
     float q2 = 0.f;
     int have = -1;                           // the row whose queries are loaded
