@@ -48,7 +48,7 @@ struct Shape {
   static constexpr int kRows = 16 * RG;
   static constexpr int kKeyWarps = RG == 4 ? 2 : 4;
   static constexpr int kWarps = kKeyWarps * RG;         // consumer warps
-  static constexpr int kSlices = RG == 4 ? 4 : (RG == 2 ? 2 : 1);                // 16-key slices a warp takes at once
+  static constexpr int kSlices = RG == 4 ? 4 : 2;                // 16-key slices a warp takes at once
   static constexpr int kParts = 4 / kSlices;            // warps that share a page
   static constexpr int kPhases = kKeyWarps / kParts;    // pages being worked on
   static constexpr int kThreads = 32 * (kWarps + 1);
