@@ -27,16 +27,18 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 8;               // pages of a score tile
-constexpr int kScoreCtas = 2 * 152;    // two CTAs on each SM
+constexpr int kTile = 16;              // pages of a score tile
+constexpr int kScoreWarps = 4;
+constexpr int kScoreCtas = 3 * 152;    // three CTAs on each SM
+constexpr int kAhead = 2;              // tiles a warp has in flight
 constexpr float kErr = 1.f / 32768.f;  // 2^-15
 constexpr int kItems = 8;              // pages a thread of select_kernel holds at once
 constexpr int kSpan = kThreads * kItems;
 constexpr int kNear = 256;             // undecided pages ranked in shared memory
 constexpr unsigned kFull = 0xffffffffu;
 
-// Workspace: scores, per tile the largest error bound, fp64 scores of pages
-// that are ranked exactly where they are more than kNear.
+// Workspace: per page its score and |q|^2 |k|^2 (what bounds the score's
+// error), and fp64 scores where more than kNear pages are ranked exactly.
 struct Layout {
   size_t score, err, exact, total;
 };
@@ -44,10 +46,9 @@ struct Layout {
 __host__ __device__ inline Layout layout(int64_t rows, int max_pages) {
   const auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const size_t n = static_cast<size_t>(rows) * max_pages;
-  const size_t tiles = static_cast<size_t>(rows) * ((max_pages + kTile - 1) / kTile);
   Layout l{};
   l.err = up(n * sizeof(float));
-  l.exact = l.err + up(tiles * sizeof(float));
+  l.exact = l.err + up(n * sizeof(float));
   l.total = l.exact + up(n * sizeof(double));
   return l;
 }
@@ -73,54 +74,62 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+__device__ __forceinline__ void mma(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
                "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// 16 query heads from h0 on as A fragments (heads beyond the group zero) and
+// 8 query heads from h0 on as B fragments (heads beyond the group zero) and
 // their largest squared norm, in every lane. The 16 dims of a step are taken in
 // the order the key sums' 16-byte loads give: lane quad c holds 4c .. 4c + 3.
 template <int D>
 __device__ __forceinline__ float load_heads(const RoutePagesArgs& a, int b, int g, int G, int h0,
-                                            int lane, uint32_t qa[D / 16][4]) {
-  const int r = lane >> 2, c = lane & 3;
-  float norm = 0.f;
+                                            int lane, uint2 qb[D / 16]) {
+  const int h = h0 + (lane >> 2), c = lane & 3;
+  const bool there = h < G;
+  const uint16_t* q = a.q + b * a.qs[0] + (g * G + (there ? h : 0)) * a.qs[2];
+  float n2 = 0.f;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const bool there = h0 + r + 8 * x < G;
-    const uint16_t* q = a.q + b * a.qs[0] + (g * G + (there ? h0 + r + 8 * x : 0)) * a.qs[2];
-    float n2 = 0.f;
+  for (int k = 0; k < D / 16; ++k) {
+    qb[k] = there ? __ldg(reinterpret_cast<const uint2*>(q + 16 * k + 4 * c)) : make_uint2(0u, 0u);
+    const float f[4] = {bits_f32(qb[k].x), __uint_as_float(qb[k].x & 0xffff0000u), bits_f32(qb[k].y),
+                        __uint_as_float(qb[k].y & 0xffff0000u)};
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint2 w = there ? __ldg(reinterpret_cast<const uint2*>(q + 16 * k + 4 * c))
-                            : make_uint2(0u, 0u);
-      qa[k][x] = w.x;
-      qa[k][2 + x] = w.y;
-      const float f[4] = {bits_f32(w.x), __uint_as_float(w.x & 0xffff0000u), bits_f32(w.y),
-                          __uint_as_float(w.y & 0xffff0000u)};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) n2 = fmaf(f[i], f[i], n2);
-    }
-    n2 += __shfl_xor_sync(kFull, n2, 1);
-    n2 += __shfl_xor_sync(kFull, n2, 2);
-    norm = fmaxf(norm, capped(n2));
+    for (int i = 0; i < 4; ++i) n2 = fmaf(f[i], f[i], n2);
   }
+  n2 += __shfl_xor_sync(kFull, n2, 1);
+  n2 = capped(n2 + __shfl_xor_sync(kFull, n2, 2));
 #pragma unroll
-  for (int off = 4; off <= 16; off <<= 1) norm = fmaxf(norm, __shfl_xor_sync(kFull, norm, off));
-  return norm;
+  for (int off = 4; off <= 16; off <<= 1) n2 = fmaxf(n2, __shfl_xor_sync(kFull, n2, off));
+  return n2;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) score_kernel(RoutePagesArgs a) {
+// A place in the list of items: item `at` of `cnt` of head block `gb` of
+// sequence b. An item is one tile for each warp of a CTA: `heads` warps take
+// neighbouring heads of the same pages, which lie side by side in memory, the
+// others the next tiles.
+struct Cursor {
+  int b, gb, at, cnt, nb;
+};
+
+// kOne: at most eight query heads share a key-value head, so their fragments
+// stay in registers along a row.
+template <int D, bool kOne>
+__global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesArgs a, int heads) {
+  constexpr int kSteps = D / 16;
+  // Every lane keeps the next tiles' pieces that it will use itself in shared
+  // memory, [warp][stage][step][half][lane]: loads in flight that hold no registers.
+  extern __shared__ __align__(16) float4 ring[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.H / a.Hkv;
   const Layout L = layout(static_cast<int64_t>(a.B) * a.Hkv, a.pm.max_pages);
   float* score = reinterpret_cast<float*>(a.ws);
   float* err = reinterpret_cast<float*>(a.ws + L.err);
-  const int row_tiles = (a.pm.max_pages + kTile - 1) / kTile;
+  const int wide = kScoreWarps / heads * kTile;   // pages of an item
+  const int blocks = a.Hkv / heads, wg = warp % heads, wt = warp / heads;
+  float4* mine = ring + warp * kAhead * kSteps * 64 + lane;
   int status = 0;
   auto pages = [&](int b) {
     bool bad;
@@ -128,100 +137,149 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(RoutePagesArgs a) {
     if (bad) status |= SA_DEV_BAD_CACHE;
     return (n + kBlock - 1) / kBlock;
   };
-  auto tiles = [&](int b) { return static_cast<int64_t>((pages(b) + kTile - 1) / kTile); };
-  const Run run = plan_run<kThreads>(a.B, a.Hkv, tiles);
-  // the CTA's run, a consecutive part of it for each warp
-  const int64_t n_cta = run.hi - run.lo;
-  int64_t left = n_cta * (warp + 1) / kWarps - n_cta * warp / kWarps;
-  if (left > 0) {
-    int b = run.group;
-    int64_t off = run.off + n_cta * warp / kWarps;
-    uint32_t qa[D / 16][4];
+  const Run run = plan_run<32 * kScoreWarps>(
+      a.B, blocks, [&](int b) { return static_cast<int64_t>((pages(b) + wide - 1) / wide); });
+  const int n_items = static_cast<int>(run.hi - run.lo);
+  if (n_items > 0) {
+    auto enter = [&](Cursor& c) {            // what follows from c.b
+      c.nb = c.b < a.B ? pages(c.b) : 0;
+      c.cnt = (c.nb + wide - 1) / wide;
+    };
+    auto step = [&](Cursor& c) {             // to the next item
+      if (++c.at < c.cnt) return;
+      c.at = 0;
+      if (++c.gb < blocks) return;
+      c.gb = 0;
+      do {
+        ++c.b;
+        enter(c);
+      } while (c.cnt == 0 && c.b < a.B);
+    };
+    Cursor now{run.group, 0, 0, 0, 0};
+    enter(now);
+    if (now.cnt > 0) {
+      now.gb = static_cast<int>(run.off / now.cnt);
+      now.at = static_cast<int>(run.off % now.cnt);
+    }
+    auto first_page = [&](const Cursor& c) { return c.at * wide + wt * kTile; };
+    auto page_at = [&](const Cursor& c) {    // lane: page lane % 16 of the warp's tile
+      const int j = first_page(c) + (lane & 15);
+      return j < c.nb ? __ldg(a.pm.table + c.b * a.pm.table_stride + j) : -2;
+    };
+    // the tile's sums on their way; which of its pages are there, by bit
+    auto fetch = [&](const Cursor& c, int page, int st) {
+      const bool there = page >= 0 && page < a.pm.n_pages;
+      if (!there && page != -2) status |= SA_DEV_BAD_CACHE;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int pg = __shfl_sync(kFull, there ? page : -1, (lane >> 2) + 8 * x);
+        const float* src = a.k_sum + (static_cast<int64_t>(max(pg, 0)) * a.Hkv + c.gb * heads + wg) * D +
+                           4 * (lane & 3);
+        const int bytes = pg >= 0 ? 16 : 0;  // 0: filled with zeros
+        const uint32_t dst = static_cast<uint32_t>(
+            __cvta_generic_to_shared(mine + (st * kSteps * 2 + x) * 32));
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                       ::"r"(dst + k * 1024), "l"(src + 16 * k), "r"(bytes) : "memory");
+      }
+      return __ballot_sync(kFull, there);
+    };
+    Cursor ahead = now;                      // the item to fetch next
+    int left = n_items;                      // items not yet fetched
+    int page[kAhead + 1];                    // looked up an item before it is fetched
+    unsigned known[kAhead] = {};
+    {
+      Cursor c = now;
+#pragma unroll
+      for (int st = 0; st <= kAhead; ++st) {
+        page[st] = -2;
+        if (st < n_items) {
+          page[st] = page_at(c);
+          step(c);
+        }
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < kAhead; ++st) {
+      if (left > 0) {
+        known[st] = fetch(ahead, page[st], st);
+        step(ahead);
+        --left;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int next = page[kAhead];
+    uint2 qb[kSteps];
     float q2 = 0.f;
-    int have = -1;                           // the row whose queries are loaded
-    while (left > 0 && b < a.B) {
-      const int nb = pages(b), cnt = (nb + kTile - 1) / kTile;
-      if (off >= static_cast<int64_t>(cnt) * a.Hkv) {
-        off -= static_cast<int64_t>(cnt) * a.Hkv;
-        ++b;
-        continue;
+    int64_t have = -1;                       // the row whose queries are loaded
+    int st = 0;
+    for (int i = 0; i < n_items; ++i, step(now)) {
+      const int g = now.gb * heads + wg, j0 = first_page(now);
+      const int64_t row = static_cast<int64_t>(now.b) * a.Hkv + g;
+      if (kOne && have != row) {
+        q2 = load_heads<D>(a, now.b, g, G, 0, lane, qb);
+        have = row;
       }
-      const int g = static_cast<int>(off / cnt);
-      int tile = static_cast<int>(off % cnt);
-      const int take = static_cast<int>(min(left, static_cast<int64_t>(cnt - tile)));
-      const int64_t row = static_cast<int64_t>(b) * a.Hkv + g;
-      auto page_at = [&](int t) {            // lane: page lane / 4 of tile t
-        const int j = t * kTile + (lane >> 2);
-        if (j >= nb) return -1;
-        const int page = __ldg(a.pm.table + b * a.pm.table_stride + j);
-        if (page >= 0 && page < a.pm.n_pages) return page;
-        status |= SA_DEV_BAD_CACHE;
-        return -1;
-      };
-      int page = page_at(tile);
-      for (int i = 0; i < take; ++i, ++tile) {
-        float4 w[D / 16];
-        const float* src = a.k_sum + (static_cast<int64_t>(page) * a.Hkv + g) * D + 4 * (lane & 3);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      const float4* w = mine + st * kSteps * 64;
+      // lane's scores: pages lane / 4 and + 8, over its heads
+      float best[2] = {-INFINITY, -INFINITY}, k2[2];
+      for (int h0 = 0; h0 < (kOne ? 1 : G); h0 += 8) {
+        if (!kOne) q2 = fmaxf(h0 == 0 ? 0.f : q2, load_heads<D>(a, now.b, g, G, h0, lane, qb));
+        float c[4] = {}, d[4] = {};
+        k2[0] = k2[1] = 0.f;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          w[k] = page >= 0 ? __ldg(reinterpret_cast<const float4*>(src + 16 * k))
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-        const bool known = page >= 0;
-        if (i + 1 < take) page = page_at(tile + 1);
-        if (have != row && G <= 16) {
-          q2 = load_heads<D>(a, b, g, G, 0, lane, qa);
-          have = static_cast<int>(row);
-        }
-        // lane's scores: pages 2 (lane % 4) + {0, 1}, heads lane / 4 and + 8
-        float best[2] = {-INFINITY, -INFINITY};
-        for (int h0 = 0; h0 < G; h0 += 16) {
-          if (G > 16) {
-            const float n2 = load_heads<D>(a, b, g, G, h0, lane, qa);
-            q2 = h0 == 0 ? n2 : fmaxf(q2, n2);
+        for (int k = 0; k < kSteps; ++k) {
+          uint4 hi, lo;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float4 v = w[64 * k + 32 * x];
+            k2[x] = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, k2[x]))));
+            const uint32_t h01 = pack_bf16(v.x, v.y), h23 = pack_bf16(v.z, v.w);
+            const uint32_t l01 = pack_bf16(v.x - bits_f32(h01), v.y - __uint_as_float(h01 & 0xffff0000u));
+            const uint32_t l23 = pack_bf16(v.z - bits_f32(h23), v.w - __uint_as_float(h23 & 0xffff0000u));
+            (x ? hi.y : hi.x) = h01;
+            (x ? hi.w : hi.z) = h23;
+            (x ? lo.y : lo.x) = l01;
+            (x ? lo.w : lo.z) = l23;
           }
-          float c[4] = {};
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t hi0 = pack_bf16(w[k].x, w[k].y), hi1 = pack_bf16(w[k].z, w[k].w);
-            const uint32_t lo0 = pack_bf16(w[k].x - bits_f32(hi0), w[k].y - __uint_as_float(hi0 & 0xffff0000u));
-            const uint32_t lo1 = pack_bf16(w[k].z - bits_f32(hi1), w[k].w - __uint_as_float(hi1 & 0xffff0000u));
-            mma(c, qa[k], hi0, hi1);
-            mma(c, qa[k], lo0, lo1);
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x)        // fmaxf passes over NaN
-            if (h0 + (lane >> 2) + 8 * (x >> 1) < G) best[x & 1] = fmaxf(best[x & 1], c[x]);
+          mma(c, hi, qb[k].x, qb[k].y);
+          mma(d, lo, qb[k].x, qb[k].y);
         }
-        float k2 = 0.f;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          k2 = fmaf(w[k].x, w[k].x, k2);
-          k2 = fmaf(w[k].y, w[k].y, k2);
-          k2 = fmaf(w[k].z, w[k].z, k2);
-          k2 = fmaf(w[k].w, w[k].w, k2);
-        }
-        k2 += __shfl_xor_sync(kFull, k2, 1);
-        k2 = capped(k2 + __shfl_xor_sync(kFull, k2, 2));
-#pragma unroll
-        for (int off4 = 4; off4 <= 16; off4 <<= 1) {
-          best[0] = fmaxf(best[0], __shfl_xor_sync(kFull, best[0], off4));
-          best[1] = fmaxf(best[1], __shfl_xor_sync(kFull, best[1], off4));
-          k2 = fmaxf(k2, __shfl_xor_sync(kFull, k2, off4));
-        }
-        const unsigned ok = __ballot_sync(kFull, known);
-        if (lane < 4) {
-          float* to = score + row * a.pm.max_pages + tile * kTile + 2 * lane;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (tile * kTile + 2 * lane + x < nb)
-              to[x] = (ok >> (4 * (2 * lane + x))) & 1u ? best[x] : -INFINITY;
-        }
-        if (lane == 0) err[row * row_tiles + tile] = kErr * sqrtf(q2) * sqrtf(k2);
+        for (int x = 0; x < 4; ++x)          // fmaxf passes over NaN
+          if (h0 + 2 * (lane & 3) + (x & 1) < G) best[x >> 1] = fmaxf(best[x >> 1], c[x] + d[x]);
       }
-      off += take;
-      left -= take;
+      const unsigned there = kAhead == 2 ? (st ? known[1] : known[0]) : known[0];
+      // this stage's pieces have been read: the next tile's take their place
+      if (left > 0) {
+        const unsigned bits = fetch(ahead, next, st);
+        if (st) known[1] = bits;
+        else known[0] = bits;
+        step(ahead);
+        if (--left > 0) next = page_at(ahead);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      st ^= 1;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        best[x] = fmaxf(best[x], __shfl_xor_sync(kFull, best[x], 1));
+        best[x] = fmaxf(best[x], __shfl_xor_sync(kFull, best[x], 2));
+        k2[x] += __shfl_xor_sync(kFull, k2[x], 1);
+        k2[x] = capped(k2[x] + __shfl_xor_sync(kFull, k2[x], 2));
+      }
+      if ((lane & 3) < 2) {                  // one lane a page
+        const int j = (lane >> 2) + 8 * (lane & 1);
+        if (j0 + j < now.nb) {
+          const int64_t at = row * a.pm.max_pages + j0 + j;
+          score[at] = (there >> j) & 1u ? (lane & 1 ? best[1] : best[0]) : -INFINITY;
+          err[at] = q2 * (lane & 1 ? k2[1] : k2[0]);
+        }
+      }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
@@ -294,8 +352,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
 
   const Layout L = layout(rows, a.pm.max_pages);
   const float* score = reinterpret_cast<const float*>(a.ws) + static_cast<int64_t>(row) * a.pm.max_pages;
-  const int row_tiles = (a.pm.max_pages + kTile - 1) / kTile;
-  const float* err = reinterpret_cast<const float*>(a.ws + L.err) + static_cast<int64_t>(row) * row_tiles;
+  const float* err = reinterpret_cast<const float*>(a.ws + L.err) + static_cast<int64_t>(row) * a.pm.max_pages;
   double* exact = reinterpret_cast<double*>(a.ws + L.exact) + static_cast<int64_t>(row) * a.pm.max_pages;
   const int f0 = min(sink, nb), f1 = max(f0, nb - 1);      // the pages that compete
   const int want = keep - (sink < nb ? sink + 1 : nb);
@@ -329,7 +386,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
         hi = fmaxf(hi, v[i]);
       }
     }
-    for (int t = f0 / kTile + tid; t < (f1 + kTile - 1) / kTile; t += kThreads) d = fmaxf(d, err[t]);
+    for (int j = f0 + tid; j < f1; j += kThreads) d = fmaxf(d, err[j]);
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
       lo = fminf(lo, __shfl_xor_sync(kFull, lo, off));
@@ -348,6 +405,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
       hi = fmaxf(hi, ext[1][w]);
       d = fmaxf(d, ext[2][w]);
     }
+    d = kErr * sqrtf(d);
     const bool finite = lo > -1e38f && hi < 1e38f && d < 1e30f;
     if (finite) {
       // the want-th largest score lies in [lo, hi]: at least want are >= lo,
@@ -524,11 +582,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
 size_t route_pages_ws_bytes(int64_t rows, int max_pages) { return layout(rows, max_pages).total; }
 
 cudaError_t launch_route_pages(const RoutePagesArgs& a, cudaStream_t st) {
-  if (a.D == 64)
-    score_kernel<64><<<kScoreCtas, kThreads, 0, st>>>(a);
-  else
-    score_kernel<128><<<kScoreCtas, kThreads, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const size_t smem = static_cast<size_t>(kScoreWarps) * kAhead * (a.D / 16) * 64 * sizeof(float4);
+  const bool one = a.H / a.Hkv <= 8;
+  const auto score = a.D == 64 ? (one ? score_kernel<64, true> : score_kernel<64, false>)
+                               : (one ? score_kernel<128, true> : score_kernel<128, false>);
+  cudaError_t e = cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  // the heads side by side that the warps of a CTA divide between them
+  int heads = 1;
+  while (heads < kScoreWarps && a.Hkv % (2 * heads) == 0) heads *= 2;
+  score<<<kScoreCtas, 32 * kScoreWarps, smem, st>>>(a, heads);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // launched while the scores are made; it waits for them
   cudaLaunchConfig_t cfg{};
