@@ -118,8 +118,8 @@ __device__ __forceinline__ Angle angle_at(const AppendArgs& a, int t, int l) {
   Angle g{make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   if (a.cos) {
     const int64_t at = static_cast<int64_t>(t) * (D / 2) + 4 * l;
-    g.c = __ldg(reinterpret_cast<const float4*>(a.cos + at));
-    g.s = __ldg(reinterpret_cast<const float4*>(a.sin + at));
+    g.c = get(reinterpret_cast<const float4*>(a.cos + at));
+    g.s = get(reinterpret_cast<const float4*>(a.sin + at));
   }
   return g;
 }
@@ -153,8 +153,8 @@ __device__ __forceinline__ void turn(Vec& v, const AppendArgs& a, const float* g
 // How many of the new tokens of sequence b have a place in its page table.
 __device__ __forceinline__ int tokens_of(const AppendArgs& a, int b, int* base, int* status) {
   bool bad;
-  *base = clamp_len(__ldg(a.pm.seq_lens + b), a.pm, &bad);
-  int n = a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.S) : a.S;
+  *base = clamp_len(get(a.pm.seq_lens + b), a.pm, &bad);
+  int n = a.new_lens ? min(max(get(a.new_lens + b), 0), a.S) : a.S;
   const int room = a.pm.max_pages * kBlock - *base;
   if (bad) *status |= SA_DEV_BAD_CACHE;
   if (n > room) {
@@ -166,7 +166,7 @@ __device__ __forceinline__ int tokens_of(const AppendArgs& a, int b, int* base, 
 
 // The page of position t, or -1 with the reason in *status.
 __device__ __forceinline__ int page_of(const AppendArgs& a, int b, int t, int* status) {
-  const int page = __ldg(a.pm.table + b * a.pm.table_stride + t / kBlock);
+  const int page = get(a.pm.table + b * a.pm.table_stride + t / kBlock);
   if (page >= 0 && page < a.pm.n_pages) return page;
   *status |= SA_DEV_BAD_CACHE;
   return -1;
@@ -192,8 +192,8 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
 #pragma unroll
   for (int i = 0; i < 8; ++i) gk[i] = 1.f;
   if (a.gamma_k) load8f<D, kHalf>(a.gamma_k, l, gk);
-  const float ik = a.k_scale ? 1.f / __ldg(a.k_scale + h) : 1.f;
-  const float iv = a.v_scale ? 1.f / __ldg(a.v_scale + h) : 1.f;
+  const float ik = a.k_scale ? 1.f / get(a.k_scale + h) : 1.f;
+  const float iv = a.v_scale ? 1.f / get(a.v_scale + h) : 1.f;
   int base = 0;
   const int n = there ? tokens_of(a, b, &base, status) : 0;
   // tokens [s0, s1) of the page, as far as the rotation tables reach
@@ -358,12 +358,9 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   const int64_t at_once = kGroups >> per_log2;
   const int64_t grid = kv + (a.q ? (tokens + at_once - 1) / at_once : 0);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if (whole)
-    append_kernel<D, kFp8, kHalf, true><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
-        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv), per_log2);
-  else
-    append_kernel<D, kFp8, kHalf, false><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
-        a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv), per_log2);
+  const auto kernel = whole ? append_kernel<D, kFp8, kHalf, true> : append_kernel<D, kFp8, kHalf, false>;
+  kernel<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
+      a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv), per_log2);
   return cudaGetLastError();
 }
 

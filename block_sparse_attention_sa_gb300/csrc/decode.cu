@@ -151,7 +151,7 @@ __device__ __forceinline__ uint32_t next_piece(uint32_t at, int k) {
 // Pages of group `i` of the list: a sequence (every page), or a row of the route.
 __device__ __forceinline__ int group_pages(const DecodeArgs& a, int i, int* status) {
   if (a.row_ptr) {
-    const int beg = __ldg(a.row_ptr + i), end = __ldg(a.row_ptr + i + 1);
+    const int beg = get(a.row_ptr + i), end = get(a.row_ptr + i + 1);
     if (beg < 0 || end < beg || end > a.col_cap || end - beg > a.pm.max_pages) {
       *status |= SA_DEV_BAD_ROUTE;
       return 0;
@@ -159,7 +159,7 @@ __device__ __forceinline__ int group_pages(const DecodeArgs& a, int i, int* stat
     return end - beg;
   }
   bool bad;
-  const int n = clamp_len(__ldg(a.pm.seq_lens + i), a.pm, &bad);
+  const int n = clamp_len(get(a.pm.seq_lens + i), a.pm, &bad);
   if (bad) *status |= SA_DEV_BAD_CACHE;
   return (n + kBlock - 1) / kBlock;
 }
@@ -191,9 +191,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const AbortSignal abort{&abort_flag, nullptr};
   int status = 0;
 
-  // join_kernel may be launched from here on; it waits for this grid's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+  let_next_launch();
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -247,10 +245,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const int b = routed ? group / a.Hkv : group, g = bg - b * a.Hkv;
       const int unit = bg * RT + rt;
       bool bad;
-      const int n = clamp_len(__ldg(a.pm.seq_lens + b), a.pm, &bad);
+      const int n = clamp_len(get(a.pm.seq_lens + b), a.pm, &bad);
       if (bad) status |= SA_DEV_BAD_CACHE;
       const int nb = (n + kBlock - 1) / kBlock;
-      const int beg = routed ? __ldg(a.row_ptr + group) : 0;
+      const int beg = routed ? get(a.row_ptr + group) : 0;
       const int dest = take == cnt ? -1 : (p0 == 0 ? 1 : 0);
       if (dest == 1) {
         cut.unit = unit;
@@ -266,15 +264,15 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           int j = p0 + q;
           if (routed) {
             const int at = beg + j;
-            const int prev = j > 0 ? __ldg(a.col_idx + at - 1) : -1;
-            j = __ldg(a.col_idx + at);
+            const int prev = j > 0 ? get(a.col_idx + at - 1) : -1;
+            j = get(a.col_idx + at);
             if (j < 0 || j >= nb || j <= prev) {
               status |= SA_DEV_BAD_ROUTE;
               j = -1;
             }
           }
           if (j >= 0) {
-            page = __ldg(a.pm.table + b * a.pm.table_stride + j);
+            page = get(a.pm.table + b * a.pm.table_stride + j);
             live = min(kBlock, n - j * kBlock);
             if (page < 0 || page >= a.pm.n_pages) {
               status |= SA_DEV_BAD_CACHE;
@@ -350,7 +348,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     auto load_queries = [&](int unit) {
       uint32_t qa[D / 16][4];
       const int rt = unit % RT, bg = unit / RT, b = bg / a.Hkv, g = bg % a.Hkv;
-      const float base = a.scale_log2 * (kFp8 && a.k_scale ? __ldg(a.k_scale + g) : 1.f);
+      const float base = a.scale_log2 * (kFp8 && a.k_scale ? get(a.k_scale + g) : 1.f);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int row = rt * S::kRows + rg * 16 + r + 8 * x;
@@ -674,7 +672,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
             const int col_g = c0 + col;
             if (dest < 0) {
-              const float inv = tot == 0.f ? 0.f : (a.v_scale ? __ldg(a.v_scale + g) : 1.f) / tot;
+              const float inv = tot == 0.f ? 0.f : (a.v_scale ? get(a.v_scale + g) : 1.f) / tot;
               const int h = g * G + head;
               *reinterpret_cast<uint2*>(a.o + b * a.os[0] + h * a.os[2] + col_g) = make_uint2(
                   pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
@@ -714,7 +712,7 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* 
             const Cut* cuts) {
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_first();
   const Cut cut = cuts[blockIdx.x];
   const int units = a.B * a.Hkv * RT;
   if (cut.unit < 0 || cut.unit >= units || cut.last <= cut.first || cut.last >= runs) return;
@@ -798,20 +796,13 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorM
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * RT;
   decode_kernel<D, kFp8, RG><<<S::kRuns, S::kThreads, S::kSmem, st>>>(kmap, vmap, a, RT, partial, cuts);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units < S::kRuns ? units : S::kRuns),
-                     static_cast<unsigned>(G < S::kRows ? G : S::kRows));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, RT, S::kRows, S::kRuns,
-                            kFp8 ? kFp16Shift : 0.f, static_cast<const float*>(partial),
-                            static_cast<const Cut*>(cuts));
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_close(join_kernel<D>,
+                      dim3(static_cast<unsigned>(units < S::kRuns ? units : S::kRuns),
+                           static_cast<unsigned>(G < S::kRows ? G : S::kRows)),
+                      32 * kJoinWarps, 0, st, a, RT, S::kRows, S::kRuns, kFp8 ? kFp16Shift : 0.f,
+                      partial, cuts);
 }
 
 template <int D, bool kFp8>

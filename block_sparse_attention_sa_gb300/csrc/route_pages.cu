@@ -93,7 +93,7 @@ __device__ __forceinline__ float load_heads(const RoutePagesArgs& a, int b, int 
   float n2 = 0.f;
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
-    qb[k] = there ? __ldg(reinterpret_cast<const uint2*>(q + 16 * k + 4 * c)) : make_uint2(0u, 0u);
+    qb[k] = there ? get(reinterpret_cast<const uint2*>(q + 16 * k + 4 * c)) : make_uint2(0u, 0u);
     const float f[4] = {bits_f32(qb[k].x), __uint_as_float(qb[k].x & 0xffff0000u), bits_f32(qb[k].y),
                         __uint_as_float(qb[k].y & 0xffff0000u)};
 #pragma unroll
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
   // Every lane keeps the next tiles' pieces that it will use itself in shared
   // memory, [warp][stage][step][half][lane]: loads in flight that hold no registers.
   extern __shared__ __align__(16) float4 ring[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.H / a.Hkv;
   const Layout L = layout(static_cast<int64_t>(a.B) * a.Hkv, a.pm.max_pages);
   float* score = reinterpret_cast<float*>(a.ws);
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
   int status = 0;
   auto pages = [&](int b) {
     bool bad;
-    const int n = clamp_len(__ldg(a.pm.seq_lens + b), a.pm, &bad);
+    const int n = clamp_len(get(a.pm.seq_lens + b), a.pm, &bad);
     if (bad) status |= SA_DEV_BAD_CACHE;
     return (n + kBlock - 1) / kBlock;
   };
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
     auto first_page = [&](const Cursor& c) { return c.at * wide + wt * kTile; };
     auto page_at = [&](const Cursor& c) {    // lane: page lane % 16 of the warp's tile
       const int j = first_page(c) + (lane & 15);
-      return j < c.nb ? __ldg(a.pm.table + c.b * a.pm.table_stride + j) : -2;
+      return j < c.nb ? get(a.pm.table + c.b * a.pm.table_stride + j) : -2;
     };
     // the tile's sums on their way; which of its pages are there, by bit
     auto fetch = [&](const Cursor& c, int page, int st) {
@@ -298,7 +298,7 @@ __device__ __forceinline__ int block_sum(int v, int* buf, int turn) {
 
 // fp64 score of one page by a whole warp; NaN heads are passed over.
 __device__ double exact_score(const RoutePagesArgs& a, int b, int g, int j, int lane) {
-  const int page = __ldg(a.pm.table + b * a.pm.table_stride + j), G = a.H / a.Hkv;
+  const int page = get(a.pm.table + b * a.pm.table_stride + j), G = a.H / a.Hkv;
   if (page < 0 || page >= a.pm.n_pages) return -INFINITY;
   const float* k = a.k_sum + (static_cast<int64_t>(page) * a.Hkv + g) * a.D;
   double best = -INFINITY;
@@ -306,7 +306,7 @@ __device__ double exact_score(const RoutePagesArgs& a, int b, int g, int j, int 
     const uint16_t* q = a.q + b * a.qs[0] + static_cast<int64_t>(g * G + h) * a.qs[2];
     double s = 0.0;
     for (int d = lane; d < a.D; d += 32)
-      s = fma(static_cast<double>(bits_f32(__ldg(q + d))), static_cast<double>(__ldg(k + d)), s);
+      s = fma(static_cast<double>(bits_f32(get(q + d))), static_cast<double>(get(k + d)), s);
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
     best = fmax(best, s);
@@ -320,11 +320,11 @@ __device__ double exact_score(const RoutePagesArgs& a, int b, int g, int j, int 
 // 14,700 cycles for three pages in place of MEASURED). For finite scores only.
 template <int D>
 __device__ double paired_score(const RoutePagesArgs& a, int b, int g, int j, int lane) {
-  const int page = __ldg(a.pm.table + b * a.pm.table_stride + j), G = a.H / a.Hkv, c = lane & 3;
+  const int page = get(a.pm.table + b * a.pm.table_stride + j), G = a.H / a.Hkv, c = lane & 3;
   const float* k = a.k_sum + (static_cast<int64_t>(page) * a.Hkv + g) * D + 4 * c;
   float4 kv[D / 16];
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) kv[s] = __ldg(reinterpret_cast<const float4*>(k + 16 * s));
+  for (int s = 0; s < D / 16; ++s) kv[s] = get(reinterpret_cast<const float4*>(k + 16 * s));
   float top = -INFINITY, low = 0.f;
   for (int h0 = 0; h0 < G; h0 += 8) {
     const int h = h0 + (lane >> 2);
@@ -332,7 +332,7 @@ __device__ double paired_score(const RoutePagesArgs& a, int b, int g, int j, int
     float sum = 0.f, rest = 0.f;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + 16 * s));
+      const uint2 w = get(reinterpret_cast<const uint2*>(q + 16 * s));
       const float qv[4] = {bits_f32(w.x), __uint_as_float(w.x & 0xffff0000u), bits_f32(w.y),
                            __uint_as_float(w.y & 0xffff0000u)};
       const float x[4] = {kv[s].x, kv[s].y, kv[s].z, kv[s].w};
@@ -402,21 +402,21 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
   // the row's place in the list: counts follow from the lengths alone
   int nb, sink, keep, before = 0;
   for (int i = tid; i < b; i += kThreads) {
-    row_counts(clamp_len(__ldg(a.pm.seq_lens + i), a.pm, &bad), a.prefix, a.budget, &nb, &sink, &keep);
+    row_counts(clamp_len(get(a.pm.seq_lens + i), a.pm, &bad), a.prefix, a.budget, &nb, &sink, &keep);
     before += keep;
   }
   if (tid == 0) near_n = 0;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) hist[i][tid] = 0;
   before = block_sum(before, sums, turn++);
-  row_counts(clamp_len(__ldg(a.pm.seq_lens + b), a.pm, &bad), a.prefix, a.budget, &nb, &sink, &keep);
+  row_counts(clamp_len(get(a.pm.seq_lens + b), a.pm, &bad), a.prefix, a.budget, &nb, &sink, &keep);
   const int start = before * a.Hkv + g * keep;
   if (tid == 0) {
     a.row_ptr[row] = start;
     if (row == rows - 1) a.row_ptr[rows] = start + keep;
     if (start + keep > a.col_cap) status |= SA_DEV_CAPACITY;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_first();
 
   const Layout L = layout(rows, a.pm.max_pages);
   const int64_t row_at = static_cast<int64_t>(row) * a.pm.max_pages;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int j = span + mine + 32 * i;
-      v[i] = j < f1 ? __ldcg(score + j) : -INFINITY;
+      v[i] = j < f1 ? get(score + j) : -INFINITY;
     }
   };
   // A page scores above `above`: in; below `below`: out; else by its exact
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
     for (int span = f0; span < f1; span += kSpan) {
       float d[kItems];
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) d[i] = span + mine + 32 * i < f1 ? __ldcg(err + span + mine + 32 * i) : 0.f;
+      for (int i = 0; i < kItems; ++i) d[i] = span + mine + 32 * i < f1 ? get(err + span + mine + 32 * i) : 0.f;
       load(span);
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
@@ -699,17 +699,8 @@ cudaError_t launch_route_pages(const RoutePagesArgs& a, cudaStream_t st) {
   score<<<kScoreCtas, 32 * kScoreWarps, smem, st>>>(a, heads);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // launched while the scores are made; it waits for them
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.Hkv));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, a.D == 64 ? select_kernel<64> : select_kernel<128>, a);
+  return launch_close(a.D == 64 ? select_kernel<64> : select_kernel<128>,
+                      dim3(static_cast<unsigned>(a.B * a.Hkv)), kThreads, 0, st, a);
 }
 
 }  // namespace sa
