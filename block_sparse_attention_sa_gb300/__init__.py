@@ -25,9 +25,8 @@ Tensors are [B, S, H, D] bf16 with a contiguous last dimension.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
-import struct
 from typing import Optional, Tuple
 
 import torch
@@ -465,36 +464,46 @@ def alloc_layer_buffers(B: int, S: int, H: int, D: int, device="cuda", qk_format
 
 # ------------------------------------------------------ paged key-value cache --
 #
-# One call of these serves one token, so its own cost counts: the parameters are
-# packed in one step, the raw stream is asked for without building an object,
-# and each tensor's shape and strides are read once.
+# One call of these serves one token, so its own cost counts: tensors are checked
+# and marshalled by the compiled module _sa_bind, which calls the same C ABI.
 
-_CACHE_PACK = struct.Struct("=14i2f19q").pack
-_NO_STRIDES = (0, 0, 0)
+_BIND = None
 
 
-def _launch(what: str, fn, device, *args) -> None:
-    """The library call with `device` current (its address and stream checks
-    and its launches are made there)."""
-    if device.index == torch._C._cuda_getDevice():
-        code = fn(*args)
+def _bind():
+    """The compiled module, attached to the library. Raises if it is missing."""
+    global _BIND
+    if _BIND is None:
+        path = os.path.join(_PKG, "_sa_bind.so")
+        if not os.path.exists(path):
+            raise FileNotFoundError(
+                f"{path} is missing: build it with `python -m block_sparse_attention_sa_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_sa_bind", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        lib = load_library()
+        module.attach(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in
+                        ("sa_cache_append", "sa_route_pages", "sa_attn_decode")))
+        _BIND = module
+    return _BIND
+
+
+def _call(what: str, fn, index: int, stream, *args) -> None:
+    """fn(device, *args, raw stream) with the device of the tensors current."""
+    raw = (torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+    if index == torch._C._cuda_getDevice():
+        code = fn(index, *args, raw)
     else:
-        with torch.cuda.device(device):
-            code = fn(*args)
+        with torch.cuda.device(index):
+            code = fn(index, *args, raw)
     if code:
         _check(code, what)
 
 
-def _cuda_device(t: torch.Tensor) -> torch.device:
+def _cuda_index(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device: there is no CPU path")
-    return t.device
-
-
-def _raw_stream(device, stream) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return _stream(stream)
+    return t.get_device()
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -507,82 +516,41 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _need(t: torch.Tensor, name: str, device, dtype, shape=None) -> int:
-    """The address of a contiguous tensor of this device, type and shape."""
-    if t.device != device or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _need_tokens(t: torch.Tensor, name: str, device, shape) -> int:
-    if t.device != device or t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be a bf16 tensor on {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _token_strides(t: Optional[torch.Tensor], name: str):
-    if t is None:
-        return _NO_STRIDES
-    st = t.stride()
-    if len(st) != 4 or st[3] != 1:
-        raise ValueError(f"{name} must be [B, S, H, D] with a contiguous last dimension")
-    return st[:3]
-
-
 def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = None,
                       k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
                       o: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
                       v_cache: Optional[torch.Tensor] = None,
                       k_sum: Optional[torch.Tensor] = None, scale: float = 0.0,
-                      prefix_len: int = 0, budget: int = 0, qk_norm: bool = False,
-                      rope="interleaved", rope_rows: int = 0,
-                      eps: float = 1e-6) -> sa_cache_params:
+                      prefix_len: int = 0, budget: int = 0) -> sa_cache_params:
     """The parameters of a paged-cache call on these tensors (those it takes):
     q, k, v, o [B, S, heads, D]; k_cache, v_cache [n_pages, H_kv, 64, D] in
     bf16, or e4m3 as float8_e4m3fn or uint8; k_sum [n_pages, H_kv, D]."""
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
-        raise ValueError("page_table must be int32 [B, max_pages]")
-    kst = vst = _NO_STRIDES
-    fmt = SA_CACHE_BF16
-    if k_cache is not None:
-        shape = k_cache.shape
-        fmt = CACHE_FORMATS.get(k_cache.dtype)
-        if fmt is None:
-            raise ValueError("k_cache, v_cache must be bfloat16, float8_e4m3fn or uint8 (e4m3)")
-        if (len(shape) != 4 or shape[2] != PAGE or v_cache.shape != shape
-                or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device
-                or k_cache.device != page_table.device):
-            raise ValueError("k_cache, v_cache must be alike, [n_pages, H_kv, 64, D], on the page "
-                             "table's device")
-        kst, vst = k_cache.stride(), v_cache.stride()
-        if kst[3] != 1 or vst[3] != 1:
-            raise ValueError("k_cache, v_cache must have a contiguous last dimension")
-    elif k_sum is not None and k_sum.dim() == 3:
-        shape = k_sum.shape
-    else:
+    p = sa_cache_params()
+    pool = k_cache if k_cache is not None else k_sum
+    if pool is None or pool.dim() != (4 if k_cache is not None else 3):
         raise ValueError("k_cache must be [n_pages, H_kv, 64, D], k_sum [n_pages, H_kv, D]")
-    qst, kt = _token_strides(q, "q"), _token_strides(k, "k")
-    vt, ost = _token_strides(v, "v"), _token_strides(o, "o")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    p.n_pages, p.H_kv, p.D = pool.shape[0], pool.shape[1], pool.shape[-1]
+    p.B, p.max_pages = page_table.shape
+    p.page, p.table_stride, p.eps = PAGE, page_table.stride(0), 1e-6
+    p.prefix_len, p.page_budget, p.softmax_scale = int(prefix_len), int(budget), float(scale)
+    for field, t in (("q_stride", q), ("k_stride", k), ("v_stride", v), ("o_stride", o)):
+        if t is not None:
+            getattr(p, field)[:] = _bshd_strides(t, field[0])
     tokens = q if q is not None else k
-    B, max_pages = page_table.shape
-    table_stride, one = page_table.stride()
-    if one != 1 and max_pages != 1:
-        raise ValueError("the rows of page_table must be contiguous")
-    if isinstance(rope, str):
-        rope = ROPE_LAYOUTS[rope]
-    try:
-        packed = _CACHE_PACK(
-            B, 1 if tokens is None else tokens.shape[1], shape[1] if q is None else q.shape[2],
-            shape[1], shape[-1], PAGE, shape[0], max_pages, fmt, prefix_len, budget,
-            1 if qk_norm else 0, rope, rope_rows, eps, scale, table_stride, *qst, *kt,
-            *vt, *ost, *kst[:3], *vst[:3])
-    except struct.error as err:
-        raise ValueError(f"a cache parameter is out of range: {err}") from None
-    return sa_cache_params.from_buffer_copy(packed)
+    p.S = 1 if tokens is None else tokens.shape[1]
+    p.H = p.H_kv if q is None else q.shape[2]
+    if k_cache is not None:
+        if (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype
+                or k_cache.shape[2] != PAGE or k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
+            raise ValueError("k_cache, v_cache must be alike, [n_pages, H_kv, 64, D] with a "
+                             "contiguous last dimension")
+        if k_cache.dtype not in CACHE_FORMATS:
+            raise ValueError("k_cache, v_cache must be bfloat16, float8_e4m3fn or uint8 (e4m3)")
+        p.cache_format = CACHE_FORMATS[k_cache.dtype]
+        p.kc_stride[:], p.vc_stride[:] = k_cache.stride()[:3], v_cache.stride()[:3]
+    return p
 
 
 def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -605,39 +573,13 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     q_out=q for in place). ``new_lens``: how many of the S tokens each sequence
     brings. ``k_sum`` gathers the per-page key sums that sa_route_pages reads;
     ``lens_out`` receives the new lengths."""
-    dev, f32, i32 = _cuda_device(k), torch.float32, torch.int32
+    index = _cuda_index(k)
     if q is not None and q_out is None:
-        q_out = _empty(q.shape, q.dtype, dev, stream)
-    elif q is None and q_out is not None:
-        raise ValueError("q_out without q")
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    p = make_cache_params(page_table, q=q, k=k, v=v, o=q_out, k_cache=k_cache, v_cache=v_cache,
-                          qk_norm=qk_norm, rope=rope, eps=eps,
-                          rope_rows=0 if cos is None else cos.shape[0])
-    B, S, Hkv, D = shape = (p.B, k.shape[1], p.H_kv, p.D)
-    if page_table.device != dev:
-        raise ValueError(f"page_table must be on {dev}")
-    qp = qo = None
-    if q is not None:
-        shape_q = (B, S, p.H, D)
-        qp, qo = _need_tokens(q, "q", dev, shape_q), _need_tokens(q_out, "q_out", dev, shape_q)
-    _launch(
-        "sa_cache_append", load_library().sa_cache_append, dev, ctypes.byref(p),
-        _need_tokens(k, "k", dev, shape), _need_tokens(v, "v", dev, shape), qp, qo,
-        None if gamma_q is None else _need(gamma_q, "gamma_q", dev, f32, (D,)),
-        None if gamma_k is None else _need(gamma_k, "gamma_k", dev, f32, (D,)),
-        None if cos is None else _need(cos, "cos", dev, f32, (p.rope_rows, D // 2)),
-        None if sin is None else _need(sin, "sin", dev, f32, (p.rope_rows, D // 2)),
-        k_cache.data_ptr(), v_cache.data_ptr(),
-        None if k_scale is None else _need(k_scale, "k_scale", dev, f32, (Hkv,)),
-        None if v_scale is None else _need(v_scale, "v_scale", dev, f32, (Hkv,)),
-        None if k_sum is None else _need(k_sum, "k_sum", dev, f32, (p.n_pages, Hkv, D)),
-        page_table.data_ptr(), _need(seq_lens, "seq_lens", dev, i32, (p.B,)),
-        None if new_lens is None else _need(new_lens, "new_lens", dev, i32, (B,)),
-        None if lens_out is None else _need(lens_out, "lens_out", dev, i32, (B,)),
-        None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
-        _raw_stream(dev, stream))
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    _call("sa_cache_append", _bind().append, index, stream, k, v, k_cache, v_cache, page_table,
+          seq_lens, q, q_out, new_lens, 1 if qk_norm else 0, gamma_q, gamma_k, eps, cos, sin,
+          ROPE_LAYOUTS[rope] if isinstance(rope, str) else rope, k_scale, v_scale, k_sum,
+          lens_out, dev_status)
     return q_out
 
 
@@ -653,13 +595,6 @@ def sa_attn_decode_workspace_bytes(p: sa_cache_params) -> int:
     return int(load_library().sa_attn_decode_workspace_bytes(ctypes.byref(p)))
 
 
-def _cache_workspace(ws: torch.Tensor, device) -> Tuple[int, int]:
-    """(address, bytes) of a caller's workspace; the library checks its size."""
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
 def sa_route_pages(q: torch.Tensor, k_sum: torch.Tensor, page_table: torch.Tensor,
                    seq_lens: torch.Tensor, prefix_len: int, budget: int, *,
                    row_ptr: Optional[torch.Tensor] = None,
@@ -672,26 +607,18 @@ def sa_route_pages(q: torch.Tensor, k_sum: torch.Tensor, page_table: torch.Tenso
     entries are col_idx[:row_ptr[-1]]), for sa_attn_decode. Kept per key-value
     head: the prefix's pages, the newest one, and the best-scoring others until
     ``budget`` are."""
-    dev, i32 = _cuda_device(q), torch.int32
-    p = make_cache_params(page_table, q=q, k_sum=k_sum, prefix_len=prefix_len, budget=budget)
-    if page_table.device != dev:
-        raise ValueError(f"page_table must be on {dev}")
-    rows = p.B * p.H_kv
-    if row_ptr is None:
-        row_ptr = _empty((rows + 1,), i32, dev, stream)
-    if col_idx is None:
-        col_idx = _empty((sa_route_pages_max_nnz(p),), i32, dev, stream)
-    if workspace is None:
-        workspace = _empty((max(256, sa_route_pages_workspace_bytes(p)),), torch.uint8, dev, stream)
-    _launch(
-        "sa_route_pages", load_library().sa_route_pages, dev, ctypes.byref(p),
-        _need_tokens(q, "q", dev, (p.B, p.S, p.H, p.D)),
-        _need(k_sum, "k_sum", dev, torch.float32), page_table.data_ptr(),
-        _need(seq_lens, "seq_lens", dev, i32, (p.B,)),
-        _need(row_ptr, "row_ptr", dev, i32, (rows + 1,)), _need(col_idx, "col_idx", dev, i32),
-        col_idx.numel(), *_cache_workspace(workspace, dev),
-        None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
-        _raw_stream(dev, stream))
+    index = _cuda_index(q)
+    if row_ptr is None or col_idx is None or workspace is None:
+        p = make_cache_params(page_table, q=q, k_sum=k_sum, prefix_len=prefix_len, budget=budget)
+        if row_ptr is None:
+            row_ptr = _empty((p.B * p.H_kv + 1,), torch.int32, q.device, stream)
+        if col_idx is None:
+            col_idx = _empty((sa_route_pages_max_nnz(p),), torch.int32, q.device, stream)
+        if workspace is None:
+            workspace = _empty((max(256, sa_route_pages_workspace_bytes(p)),), torch.uint8,
+                               q.device, stream)
+    _call("sa_route_pages", _bind().route, index, stream, q, k_sum, page_table, seq_lens,
+          prefix_len, budget, row_ptr, col_idx, workspace, dev_status)
     return row_ptr, col_idx
 
 
@@ -708,33 +635,17 @@ def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``seq_lens`` cached tokens, or over the pages a route lists (row_ptr,
     col_idx from sa_route_pages): (o bf16 [B, 1, H, D], lse fp32 [B, H, 1] or
     None). H is a multiple of the cache's H_kv."""
-    dev, f32, i32 = _cuda_device(q), torch.float32, torch.int32
+    index = _cuda_index(q)
     if o is None:
-        o = _empty(q.shape, q.dtype, dev, stream)
-    p = make_cache_params(page_table, q=q, o=o, k_cache=k_cache, v_cache=v_cache, scale=scale)
-    B, H = p.B, p.H
-    shape = (B, p.S, H, p.D)
+        o = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None and want_lse:
-        lse = _empty((B, H, 1), f32, dev, stream)
+        lse = _empty((q.shape[0], q.shape[2], 1), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = _empty((max(256, sa_attn_decode_workspace_bytes(p)),), torch.uint8, dev, stream)
-    if (row_ptr is None) != (col_idx is None):
-        raise ValueError("row_ptr and col_idx go together")
-    if page_table.device != dev:
-        raise ValueError(f"page_table must be on {dev}")
-    _launch(
-        "sa_attn_decode", load_library().sa_attn_decode, dev, ctypes.byref(p),
-        _need_tokens(q, "q", dev, shape), k_cache.data_ptr(), v_cache.data_ptr(),
-        None if k_scale is None else _need(k_scale, "k_scale", dev, f32, (p.H_kv,)),
-        None if v_scale is None else _need(v_scale, "v_scale", dev, f32, (p.H_kv,)),
-        page_table.data_ptr(), _need(seq_lens, "seq_lens", dev, i32, (p.B,)),
-        None if row_ptr is None else _need(row_ptr, "row_ptr", dev, i32, (B * p.H_kv + 1,)),
-        None if col_idx is None else _need(col_idx, "col_idx", dev, i32),
-        0 if col_idx is None else col_idx.numel(), _need_tokens(o, "o", dev, shape),
-        None if lse is None else _need(lse, "lse", dev, f32, (B, H, 1)),
-        *_cache_workspace(workspace, dev),
-        None if dev_status is None else _need(dev_status, "dev_status", dev, i32),
-        _raw_stream(dev, stream))
+        p = make_cache_params(page_table, q=q, k_cache=k_cache, v_cache=v_cache)
+        workspace = _empty((max(256, sa_attn_decode_workspace_bytes(p)),), torch.uint8, q.device,
+                           stream)
+    _call("sa_attn_decode", _bind().decode, index, stream, q, k_cache, v_cache, page_table,
+          seq_lens, scale, row_ptr, col_idx, k_scale, v_scale, o, lse, workspace, dev_status)
     return o, lse
 
 

@@ -1,10 +1,12 @@
-"""Builds libsa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch).
+"""Builds libsa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch),
+and the small Python module that marshals the paged-cache calls to it.
 
     python -m block_sparse_attention_sa_gb300.build [--verbose-ptxas]
 
 Each .cu is compiled to an object in parallel, then linked into a shared
-library next to this file. Rebuilds only when a source or header is newer
-than the library.
+library next to this file; the module (csrc/bind.cpp, which reads torch's
+tensors directly) is compiled beside them with the host compiler. Rebuilds
+only when a source or header is newer than what was built.
 """
 
 from __future__ import annotations
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsa_gb300.so")
+BIND = os.path.join(PKG, "_sa_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,12 +40,30 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp")) + [
         os.path.join(ROOT, "include", "sa.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _compile_bind() -> None:
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [shutil.which("g++") or "g++", "-shared", "-fPIC", "-O2", "-std=c++17",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", sysconfig.get_path("include"), "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), os.path.join(CSRC, "bind.cpp"),
+           "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath," + os.path.join(root, "lib"), "-o", BIND + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding does not compile:\n{r.stdout}\n{r.stderr}")
+    os.replace(BIND + ".tmp", BIND)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -62,8 +84,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(sources())) as ex:
+    with ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
+        bind = ex.submit(_compile_bind)
         results = list(ex.map(compile_one, sources()))
+        bind.result()
     if verbose_ptxas:
         for _, err in results:
             sys.stderr.write(err)
