@@ -20,7 +20,7 @@
 namespace sa {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kGroups = 8;         // lane groups of a CTA, D / 8 lanes each
 constexpr int kQueryHeads = 8;     // heads a lane group has in flight
 constexpr int kTokens = 2;         // tokens a lane group has in flight
 constexpr int64_t kManyTokens = 1024;
@@ -166,16 +166,16 @@ __device__ __forceinline__ int tokens_of(const AppendArgs& a, int b, int* base, 
 
 // The page of position t, or -1 with the reason in *status.
 __device__ __forceinline__ int page_of(const AppendArgs& a, int b, int t, int* status) {
-  const int page = get(a.pm.table + b * a.pm.table_stride + t / kBlock);
+  const int page = get(a.pm.table + b * a.pm.table_stride + static_cast<unsigned>(t) / kBlock);
   if (page >= 0 && page < a.pm.n_pages) return page;
   *status |= SA_DEV_BAD_CACHE;
   return -1;
 }
 
 // A key-value unit: the tokens of this call in page place `pu` (counted from
-// the first one touched) of sequence b, one head; kGroups lane groups take
-// every kGroups-th token. Returns with the lanes' sums of what they stored.
-template <int D, bool kFp8, bool kHalf, int kGroups>
+// the first one touched) of sequence b, one head; kShare lane groups take
+// every kShare-th token. Returns with the lanes' sums of what they stored.
+template <int D, bool kFp8, bool kHalf, int kShare>
 __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int pu, int h, int grp,
                                                int l, bool there, int* page, int* slot0,
                                                float* sum, int* status) {
@@ -183,7 +183,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
   const uint16_t* k = a.k + b * a.ks[0] + h * a.ks[2];
   const uint16_t* v = a.v + b * a.vs[0] + h * a.vs[2];
   uint4 kw[kTokens], vw[kTokens];
-  const bool early = kGroups == 1 && a.S == 1 && there;
+  const bool early = kShare == 1 && a.S == 1 && there;
   if (early) {
     kw[0] = load8<D, kHalf>(k, l);
     vw[0] = load8<D, kHalf>(v, l);
@@ -204,63 +204,78 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
     s1 = max(s0, a.rope_rows - base);
     *status |= SA_DEV_CAPACITY;
   }
+  // the page is not waited for before the first store
   *page = s0 < s1 ? page_of(a, b, base + s0, status) : -1;
-  *slot0 = (base + s0) % kBlock;
-  if (*page < 0) s1 = s0;
-  const int64_t kat = *page * a.kcs[0] + h * a.kcs[1], vat = *page * a.vcs[0] + h * a.vcs[1];
+  *slot0 = static_cast<unsigned>(base + s0) % kBlock;
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+  // token s0 + grp and every kShare-th one after it: what is left of them, and
+  // where the next one is read and stored
+  int left = (s1 - s0 - grp + kShare - 1) / kShare;
+  int t = base + s0 + grp;
+  k += (s0 + grp) * a.ks[1];
+  v += (s0 + grp) * a.vs[1];
+  const int64_t k_step = kShare * a.ks[1], v_step = kShare * a.vs[1];
+  const int elt = kFp8 ? 1 : 2;
+  char* kc = static_cast<char*>(a.kc) +
+             (*page * a.kcs[0] + h * a.kcs[1] + (*slot0 + grp) * a.kcs[2]) * elt;
+  char* vc = static_cast<char*>(a.vc) +
+             (*page * a.vcs[0] + h * a.vcs[1] + (*slot0 + grp) * a.vcs[2]) * elt;
+  const int64_t kc_step = kShare * a.kcs[2] * elt, vc_step = kShare * a.vcs[2] * elt;
   // every lane of the warp makes the same number of rounds: turn() shuffles
-  const int rounds = kGroups == 1
-                         ? __reduce_max_sync(0xffffffffu, (s1 - s0 + kTokens - 1) / kTokens)
-                         : (s1 - s0 + kGroups * kTokens - 1) / (kGroups * kTokens);
+  int rounds = (max(left, 0) + kTokens - 1) / kTokens;
+  rounds = __reduce_max_sync(0xffffffffu, rounds);
   for (int r = 0; r < rounds; ++r) {
     Angle g[kTokens];
 #pragma unroll
     for (int u = 0; u < kTokens; ++u) {
-      const int s = s0 + (r * kTokens + u) * kGroups + grp;
-      if (s >= s1) continue;
+      if (u >= left) continue;
       if (!early) {
-        kw[u] = load8<D, kHalf>(k + s * a.ks[1], l);
-        vw[u] = load8<D, kHalf>(v + s * a.vs[1], l);
+        kw[u] = load8<D, kHalf>(k, l);
+        vw[u] = load8<D, kHalf>(v, l);
       }
-      g[u] = angle_at<D>(a, base + s, l);
+      g[u] = angle_at<D>(a, t + u * kShare, l);
+      k += k_step;
+      v += v_step;
     }
 #pragma unroll
     for (int u = 0; u < kTokens; ++u) {
-      const int s = s0 + (r * kTokens + u) * kGroups + grp;
-      if (__all_sync(0xffffffffu, s >= s1)) break;
-      const bool on = s < s1;
+      const bool on = u < left;
       Vec y = unpack(on ? kw[u] : make_uint4(0u, 0u, 0u, 0u));
       turn<D, kHalf>(y, a, gk, g[u]);
       if (!on) continue;
-      const int slot = (base + s) % kBlock;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += y.x[i];
+      if (*page < 0) continue;
       if (kFp8) {
-        store8_e4m3<D, kHalf>(static_cast<uint8_t*>(a.kc) + kat + slot * a.kcs[2], l, pack_e4m3(y, ik));
-        store8_e4m3<D, kHalf>(static_cast<uint8_t*>(a.vc) + vat + slot * a.vcs[2], l,
-                              pack_e4m3(unpack(vw[u]), iv));
+        store8_e4m3<D, kHalf>(reinterpret_cast<uint8_t*>(kc), l, pack_e4m3(y, ik));
+        store8_e4m3<D, kHalf>(reinterpret_cast<uint8_t*>(vc), l, pack_e4m3(unpack(vw[u]), iv));
       } else {
-        store8<D, kHalf>(static_cast<uint16_t*>(a.kc) + kat + slot * a.kcs[2], l, pack(y));
-        store8<D, kHalf>(static_cast<uint16_t*>(a.vc) + vat + slot * a.vcs[2], l, vw[u]);
+        store8<D, kHalf>(reinterpret_cast<uint16_t*>(kc), l, pack(y));
+        store8<D, kHalf>(reinterpret_cast<uint16_t*>(vc), l, vw[u]);
       }
+      kc += kc_step;
+      vc += vc_step;
     }
+    left -= kTokens;
+    t += kTokens * kShare;
   }
 }
 
 // kWhole: a CTA takes one key-value unit, else each of its lane groups one.
 template <int D, bool kFp8, bool kHalf, bool kWhole>
-__global__ void __launch_bounds__(kThreads, kWhole ? 8 : 4) append_kernel(AppendArgs a, int units, int page_units,
+__global__ void __launch_bounds__(D, (kWhole ? 7 : 4) * 128 / D) append_kernel(AppendArgs a, int units, int page_units,
                                                           int kv_ctas, int per_log2) {
-  constexpr int L = D / 8, kGroups = kThreads / L;
+  constexpr int L = D / 8;
   const int grp = threadIdx.x / L, l = threadIdx.x % L;
   int status = 0;
   if (static_cast<int>(blockIdx.x) < kv_ctas) {
     // ------------------------------------------------------ keys, values --
-    const int u = kWhole ? blockIdx.x : blockIdx.x * kGroups + grp;
-    const bool there = u < units;
-    const int h = u % a.Hkv, bp = u / a.Hkv, pu = bp % page_units, b = there ? bp / page_units : 0;
+    const unsigned u = kWhole ? blockIdx.x : blockIdx.x * kGroups + grp;
+    const bool there = u < static_cast<unsigned>(units);
+    const unsigned bp = u / static_cast<unsigned>(a.Hkv);
+    const int h = u - bp * a.Hkv, b = there ? bp / static_cast<unsigned>(page_units) : 0;
+    const int pu = there ? bp - b * static_cast<unsigned>(page_units) : 0;
     int page, slot0;
     float sum[8];
     key_value_unit<D, kFp8, kHalf, kWhole ? kGroups : 1>(a, b, pu, h, kWhole ? grp : 0, l, there,
@@ -271,15 +286,19 @@ __global__ void __launch_bounds__(kThreads, kWhole ? 8 : 4) append_kernel(Append
       a.lens_out[b] = base + n;
     }
     if (kWhole && a.k_sum) {
-      // the lane groups' sums, added in their order
-      __shared__ float part[kGroups][D];
-      store8f<D, false>(part[grp], l, sum);      // in the lane's own order
+      // the lane groups' sums: across a warp, then the warps' in their order
+      __shared__ float part[D / 32][D];
+#pragma unroll
+      for (int off = L; off < 32; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
+      if (threadIdx.x % 32 < L) store8f<D, false>(part[threadIdx.x / 32], l, sum);   // in the lane's own order
       __syncthreads();
       if (grp == 0) {
 #pragma unroll
-        for (int g = 1; g < kGroups; ++g)
+        for (int w = 1; w < D / 32; ++w)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] += part[g][8 * l + i];
+          for (int i = 0; i < 8; ++i) sum[i] += part[w][8 * l + i];
       }
     }
     if (a.k_sum && page >= 0 && (!kWhole || grp == 0)) {
@@ -296,10 +315,9 @@ __global__ void __launch_bounds__(kThreads, kWhole ? 8 : 4) append_kernel(Append
     // ----------------------------------------------------------- queries --
     // `per` lane groups share a token, every per-th head each
     const int per = 1 << per_log2;
-    const int64_t token = static_cast<int64_t>(blockIdx.x - kv_ctas) * (kGroups >> per_log2) +
-                          (grp >> per_log2);
-    const bool there = token < static_cast<int64_t>(a.B) * a.S;
-    const int b = there ? static_cast<int>(token / a.S) : 0, s = static_cast<int>(token % a.S);
+    const unsigned token = (blockIdx.x - kv_ctas) * (kGroups >> per_log2) + (grp >> per_log2);
+    const bool there = token < static_cast<unsigned>(a.B) * a.S;
+    const int b = there ? token / static_cast<unsigned>(a.S) : 0, s = token - b * a.S;
     const int hg = grp & (per - 1);
     const uint16_t* q = a.q + b * a.qs[0] + s * a.qs[1];
     uint16_t* out = a.q_out + b * a.os[0] + s * a.os[1];
@@ -321,12 +339,15 @@ __global__ void __launch_bounds__(kThreads, kWhole ? 8 : 4) append_kernel(Append
     int base = 0, none = 0;             // the key-value CTAs report what is wrong
     bool on = there && s < tokens_of(a, b, &base, &none);
     const int t = base + (on ? s : 0);
-    on = on && !(a.cos && t >= a.rope_rows) && page_of(a, b, t, &none) >= 0;
+    on = on && !(a.cos && t >= a.rope_rows);
     if (!__any_sync(0xffffffffu, on)) return;
+    // the queries and their angles are on their way while the page is looked up
+    if (!early) load(0, on);
     Angle g = {};
     if (on) g = angle_at<D>(a, t, l);
+    on = on && page_of(a, b, t, &none) >= 0;
     for (int h0 = 0; h0 < a.H; h0 += kQueryHeads * per) {
-      if (h0 > 0 || !early) load(h0, on);
+      if (h0 > 0) load(h0, on);
 #pragma unroll
       for (int u = 0; u < kQueryHeads; ++u) {
         if (h0 + u * per >= a.H) break;
@@ -342,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, kWhole ? 8 : 4) append_kernel(Append
 
 template <int D, bool kFp8, bool kHalf>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
-  constexpr int kGroups = kThreads / (D / 8);
   // the pages S tokens can touch, wherever the first of them lies
   const int64_t page_units = (static_cast<int64_t>(a.S) + kBlock - 2) / kBlock + 1;
   const int64_t units = a.B * page_units * a.Hkv;
@@ -359,7 +379,7 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   const int64_t grid = kv + (a.q ? (tokens + at_once - 1) / at_once : 0);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   const auto kernel = whole ? append_kernel<D, kFp8, kHalf, true> : append_kernel<D, kFp8, kHalf, false>;
-  kernel<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(
+  kernel<<<static_cast<unsigned>(grid), D, 0, st>>>(
       a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv), per_log2);
   return cudaGetLastError();
 }
