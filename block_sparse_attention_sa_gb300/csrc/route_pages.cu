@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include "cache_internal.cuh"
+#include "ptx.cuh"
 
 namespace sa {
 namespace {
@@ -119,9 +120,13 @@ struct Cursor {
 template <int D, bool kOne>
 __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesArgs a, int heads) {
   constexpr int kSteps = D / 16;
-  // Every lane keeps the next tiles' pieces that it will use itself in shared
-  // memory, [warp][stage][step][half][lane]: loads in flight that hold no registers.
+  // Every warp has the next tiles on their way into its part of shared memory,
+  // [warp][stage][page]: one bulk copy a page, rows 64 bytes further apart than
+  // they are long, so that the two rows a quarter of a warp reads meet no bank twice.
+  constexpr int kRow = D / 4 + 4;            // in 16-byte pieces
   extern __shared__ __align__(16) float4 ring[];
+  __shared__ __align__(8) uint64_t full[kScoreWarps][kAhead];
+  __shared__ volatile int abort_flag;
   let_next_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.H / a.Hkv;
   const Layout L = layout(static_cast<int64_t>(a.B) * a.Hkv, a.pm.max_pages);
@@ -129,8 +134,14 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
   float* err = reinterpret_cast<float*>(a.ws + L.err);
   const int wide = kScoreWarps / heads * kTile;   // pages of an item
   const int blocks = a.Hkv / heads, wg = warp % heads, wt = warp / heads;
-  float4* mine = ring + warp * kAhead * kSteps * 64 + lane;
+  float4* mine = ring + warp * kAhead * kTile * kRow;
   int status = 0;
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kScoreWarps; ++w)
+      for (int s = 0; s < kAhead; ++s) mbar_init(smem_u32(&full[w][s]), 1);
+    fence_barrier_init();
+    abort_flag = 0;
+  }
   auto pages = [&](int b) {
     bool bad;
     const int n = clamp_len(get(a.pm.seq_lens + b), a.pm, &bad);
@@ -170,20 +181,17 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
     auto fetch = [&](const Cursor& c, int page, int st) {
       const bool there = page >= 0 && page < a.pm.n_pages;
       if (!there && page != -2) status |= SA_DEV_BAD_CACHE;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int pg = __shfl_sync(kFull, there ? page : -1, (lane >> 2) + 8 * x);
-        const float* src = a.k_sum + (static_cast<int64_t>(max(pg, 0)) * a.Hkv + c.gb * heads + wg) * D +
-                           4 * (lane & 3);
-        const int bytes = pg >= 0 ? 16 : 0;  // 0: filled with zeros
-        const uint32_t dst = static_cast<uint32_t>(
-            __cvta_generic_to_shared(mine + (st * kSteps * 2 + x) * 32));
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                       ::"r"(dst + k * 1024), "l"(src + 16 * k), "r"(bytes) : "memory");
-      }
-      return __ballot_sync(kFull, there);
+      const unsigned bits = __ballot_sync(kFull, there) & 0xffffu;
+      const uint32_t bar = smem_u32(&full[warp][st]);
+      __syncwarp();                          // every lane has read what lay there
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(bits) * D * 4);
+      __syncwarp();
+      if (there && lane < kTile)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     ::"r"(smem_u32(mine + (st * kTile + lane) * kRow)),
+                       "l"(a.k_sum + (static_cast<int64_t>(page) * a.Hkv + c.gb * heads + wg) * D),
+                       "r"(D * 4), "r"(bar) : "memory");
+      return bits;
     };
     Cursor ahead = now;                      // the item to fetch next
     int left = n_items;                      // items not yet fetched
@@ -207,13 +215,13 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
         step(ahead);
         --left;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     }
     int next = page[kAhead];
     uint2 qb[kSteps];
     float q2 = 0.f;
     int64_t have = -1;                       // the row whose queries are loaded
     int st = 0;
+    uint32_t phase = 0;
     for (int i = 0; i < n_items; ++i, step(now)) {
       const int g = now.gb * heads + wg, j0 = first_page(now);
       const int64_t row = static_cast<int64_t>(now.b) * a.Hkv + g;
@@ -221,8 +229,20 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
         q2 = load_heads<D>(a, now.b, g, G, 0, lane, qb);
         have = row;
       }
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-      const float4* w = mine + st * kSteps * 64;
+      if (!mbar_wait_warp(smem_u32(&full[warp][st]), phase, AbortSignal{&abort_flag, nullptr})) {
+        // give up, but not before the copies still in flight have come in
+        if (lane == 0) {
+          status |= SA_DEV_TIMEOUT;
+          abort_flag = 1;
+          const volatile int never = 0;
+          for (int s = 0; s < kAhead; ++s)
+            if (i + s < n_items)
+              mbar_wait(smem_u32(&full[warp][(st + s) % kAhead]), phase ^ (st + s >= kAhead ? 1u : 0u),
+                        AbortSignal{&never, nullptr});
+        }
+        break;
+      }
+      const float4* w = mine + (st * kTile + (lane >> 2)) * kRow + (lane & 3);
       // lane's scores: pages lane / 4 and + 8, over its heads
       float best[2] = {-INFINITY, -INFINITY}, k2[2];
       for (int h0 = 0; h0 < (kOne ? 1 : G); h0 += 8) {
@@ -234,7 +254,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
           uint4 hi, lo;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float4 v = w[64 * k + 32 * x];
+            const float4 v = w[8 * x * kRow + 4 * k];
             k2[x] = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, k2[x]))));
             const uint32_t h01 = pack_bf16(v.x, v.y), h23 = pack_bf16(v.z, v.w);
             const uint32_t l01 = pack_bf16(v.x - bits_f32(h01), v.y - __uint_as_float(h01 & 0xffff0000u));
@@ -260,8 +280,10 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
         step(ahead);
         if (--left > 0) next = page_at(ahead);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      st ^= 1;
+      if (++st == kAhead) {
+        st = 0;
+        phase ^= 1u;
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         best[x] = fmaxf(best[x], __shfl_xor_sync(kFull, best[x], 1));
@@ -274,12 +296,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
         if (j0 + j < now.nb) {
           const int64_t at = row * a.pm.max_pages + j0 + j;
           score[at] = (there >> j) & 1u ? (lane & 1 ? best[1] : best[0]) : -INFINITY;
-          err[at] = q2 * (lane & 1 ? k2[1] : k2[0]);
+          err[at] = (there >> j) & 1u ? q2 * (lane & 1 ? k2[1] : k2[0]) : 0.f;
         }
       }
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
   if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
@@ -686,7 +707,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
 size_t route_pages_ws_bytes(int64_t rows, int max_pages) { return layout(rows, max_pages).total; }
 
 cudaError_t launch_route_pages(const RoutePagesArgs& a, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(kScoreWarps) * kAhead * (a.D / 16) * 64 * sizeof(float4);
+  const size_t smem = static_cast<size_t>(kScoreWarps) * kAhead * kTile * (a.D / 4 + 4) * sizeof(float4);
   const bool one = a.H / a.Hkv <= 8;
   const auto score = a.D == 64 ? (one ? score_kernel<64, true> : score_kernel<64, false>)
                                : (one ? score_kernel<128, true> : score_kernel<128, false>);
