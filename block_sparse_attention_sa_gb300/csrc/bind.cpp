@@ -175,10 +175,10 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor* sin = a.tensor("sin");
     const float* angles[2] = {};
     if (cos || sin) {
-      if (!cos || !sin || cos->dim() != 2 || cos->size(1) != D / 2 || sin->sizes() != cos->sizes() ||
+      if (!cos || !sin || cos->dim() != 2 || cos->size(0) < 1 || cos->size(1) != D / 2 || sin->sizes() != cos->sizes() ||
           cos->scalar_type() != kF32 || sin->scalar_type() != kF32 || !cos->is_contiguous() ||
           !sin->is_contiguous())
-        refuse("cos and sin go together, both contiguous fp32 [rows, D/2]");
+        refuse("cos and sin go together, both contiguous fp32 [rows, D/2] with rows >= 1");
       p.rope_rows = narrow(cos->size(0), "rope_rows");
       angles[0] = static_cast<const float*>(cos->data_ptr());
       angles[1] = static_cast<const float*>(sin->data_ptr());

@@ -166,7 +166,10 @@ sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v
       !aligned(rope_sin, 16) || !aligned(k_sum, 16))
     return SA_ERR_INVALID_ARG;
   if ((rope_cos == nullptr) != (rope_sin == nullptr)) return SA_ERR_INVALID_ARG;
-  if (lens_out && lens_out == seq_lens) return SA_ERR_INVALID_ARG;
+  if (lens_out && (lens_out == seq_lens || lens_out == new_lens)) return SA_ERR_INVALID_ARG;
+  if (q && q == q_out)
+    for (int i = 0; i < 3; ++i)
+      if (p->q_stride[i] != p->o_stride[i]) return SA_ERR_INVALID_ARG;
   // blocks of the launch, counted in 32 bits
   const int64_t rows = static_cast<int64_t>(p->B) * (p->S / kBlock + 2) * p->H_kv +
                        static_cast<int64_t>(p->B) * p->S;

@@ -46,20 +46,20 @@ constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16
 template <int D, bool kFp8, int RG>
 struct Shape {
   static constexpr int kRows = 16 * RG;
-  static constexpr int kKeyWarps = RG == 4 ? 2 : 4;
+  static constexpr int kKeyWarps = 4 / RG;
   static constexpr int kWarps = kKeyWarps * RG;         // consumer warps
   static constexpr int kSlices = RG == 4 ? 4 : 2;                // 16-key slices a warp takes at once
   static constexpr int kParts = 4 / kSlices;            // warps that share a page
   static constexpr int kPhases = kKeyWarps / kParts;    // pages being worked on
   static constexpr int kThreads = 32 * (kWarps + 1);
   // CTAs on an SM: as many as leave each two or more pages in its ring
-  static constexpr int kCtas = RG > 1 ? 1 : (kFp8 || D == 64 ? 3 : 2);
+  static constexpr int kCtas = (RG == 1 && kFp8) || (RG < 4 && D == 64) ? 3 : 2;
   static constexpr int kRuns = kSms * kCtas;
   static constexpr int kRowBytes = kFp8 ? D : 2 * D;    // one token of one head
   static constexpr int kPage = kBlock * kRowBytes;
   static constexpr int kBox = kRowBytes < 128 ? kRowBytes : 128;
   static constexpr int kStage = 2 * kPage;
-  static constexpr int kRing = (kCtas == 3 ? 48 : (kCtas == 2 ? 96 : 160)) * 1024;
+  static constexpr int kRing = (kCtas == 3 ? 48 : (RG == 1 ? 96 : 64)) * 1024;
   static constexpr int kStages = kRing / kStage < 16 ? kRing / kStage : 16;
   static constexpr int kChunk = 32;                     // columns joined at a time
   static constexpr int kPad = kChunk + 8;               // row stride of the join buffer
@@ -264,8 +264,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           int j = p0 + q;
           if (routed) {
             const int at = beg + j;
-            const int prev = j > 0 ? get(a.col_idx + at - 1) : -1;
-            j = get(a.col_idx + at);
+            const bool there = beg >= 0 && at < a.col_cap;
+            const int prev = there && j > 0 ? get(a.col_idx + at - 1) : -1;
+            j = there ? get(a.col_idx + at) : -1;
             if (j < 0 || j >= nb || j <= prev) {
               status |= SA_DEV_BAD_ROUTE;
               j = -1;
@@ -530,8 +531,15 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float p0 = sc[2 * y + (x >> 1)][2 * (x & 1)], p1 = sc[2 * y + (x >> 1)][2 * (x & 1) + 1];
-            hi_w[x] = kFp8 ? pack_half(p0, p1) : pack_bf16(p0, p1);
-            if (!kFp8) lw_w[x] = pack_bf16(p0 - lo_f32(hi_w[x]), p1 - hi_f32(hi_w[x]));
+            if (kFp8) {
+              hi_w[x] = pack_half(p0, p1);
+            } else {
+              // hi is cut, not rounded, and lo a little above what is left (2^-24
+              // of p), so that both are positive: an infinite value stays one
+              hi_w[x] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+              lw_w[x] = pack_bf16(fmaf(p0, 0x1p-24f, p0 - lo_f32(hi_w[x])),
+                                  fmaf(p1, 0x1p-24f, p1 - hi_f32(hi_w[x])));
+            }
           }
           const uint4 hi = make_uint4(hi_w[0], hi_w[1], hi_w[2], hi_w[3]);
           const uint4 lw = kFp8 ? hi : make_uint4(lw_w[0], lw_w[1], lw_w[2], lw_w[3]);
@@ -715,7 +723,8 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* 
   wait_for_first();
   const Cut cut = cuts[blockIdx.x];
   const int units = a.B * a.Hkv * RT;
-  if (cut.unit < 0 || cut.unit >= units || cut.last <= cut.first || cut.last >= runs) return;
+  if (cut.unit < 0 || cut.unit >= units || cut.first < 0 || cut.last <= cut.first || cut.last >= runs)
+    return;
   const int G = a.H / a.Hkv, rt = cut.unit % RT, bg = cut.unit / RT;
   const int b = bg / a.Hkv, g = bg % a.Hkv, row = blockIdx.y, head = rt * rows + row;
   if (head >= G) return;
@@ -819,8 +828,8 @@ cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& kmap, const CUtenso
 
 size_t decode_ws_bytes(int H, int Hkv, int D) {
   // two partials of every run
-  const size_t rows = row_groups(H / Hkv) == 1 ? static_cast<size_t>(kMaxRuns) * 16
-                                               : static_cast<size_t>(kSms) * 16 * row_groups(H / Hkv);
+  const int groups = row_groups(H / Hkv);
+  const size_t rows = static_cast<size_t>(groups < 4 ? kMaxRuns : 2 * kSms) * 16 * groups;
   return cuts_bytes() + 2 * rows * (D + 2) * sizeof(float);
 }
 

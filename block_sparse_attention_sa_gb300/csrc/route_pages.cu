@@ -224,9 +224,10 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
     uint32_t phase = 0;
     for (int i = 0; i < n_items; ++i, step(now)) {
       const int g = now.gb * heads + wg, j0 = first_page(now);
-      const int64_t row = static_cast<int64_t>(now.b) * a.Hkv + g;
+      const int b = min(now.b, a.B - 1);     // should the lengths change under the call
+      const int64_t row = static_cast<int64_t>(b) * a.Hkv + g;
       if (kOne && have != row) {
-        q2 = load_heads<D>(a, now.b, g, G, 0, lane, qb);
+        q2 = load_heads<D>(a, b, g, G, 0, lane, qb);
         have = row;
       }
       if (!mbar_wait_warp(smem_u32(&full[warp][st]), phase, AbortSignal{&abort_flag, nullptr})) {
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
       // lane's scores: pages lane / 4 and + 8, over its heads
       float best[2] = {-INFINITY, -INFINITY}, k2[2];
       for (int h0 = 0; h0 < (kOne ? 1 : G); h0 += 8) {
-        if (!kOne) q2 = fmaxf(h0 == 0 ? 0.f : q2, load_heads<D>(a, now.b, g, G, h0, lane, qb));
+        if (!kOne) q2 = fmaxf(h0 == 0 ? 0.f : q2, load_heads<D>(a, b, g, G, h0, lane, qb));
         float c[4] = {}, d[4] = {};
         k2[0] = k2[1] = 0.f;
 #pragma unroll
@@ -403,7 +404,6 @@ __device__ __forceinline__ uint64_t order64(double x) {
 }
 
 constexpr int kBins = 256, kPasses = 4;
-static_assert(kBins == kThreads, "a thread clears a bin of each pass");
 
 // grid (B * Hkv): one row.
 template <int D>
@@ -427,8 +427,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
     before += keep;
   }
   if (tid == 0) near_n = 0;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) hist[i][tid] = 0;
+  for (int i = tid; i < kPasses * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   before = block_sum(before, sums, turn++);
   row_counts(clamp_len(get(a.pm.seq_lens + b), a.pm, &bad), a.prefix, a.budget, &nb, &sink, &keep);
   const int start = before * a.Hkv + g * keep;

@@ -417,7 +417,11 @@ sa_status sa_check_wait_timeout(int32_t* dev_status, void* stream);
  * id is outside [0, n_pages) are left out; each raises SA_DEV_BAD_CACHE.
  * Entries of page_table behind a sequence's last page are not read. One page
  * may serve several sequences or places as long as nothing is appended to it;
- * what a page holds that two sequences append to in one call is undefined.
+ * what a page holds that is appended to in two places in one call is undefined.
+ *
+ * Lengths, tables and routes are read when the call runs, so a captured call
+ * serves as they change; they must not change while it runs. Calls that may run
+ * at the same time need workspaces of their own.
  * ---------------------------------------------------------------------- */
 
 /* Storage of the cached keys and values. */
@@ -492,7 +496,7 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * seq_lens     the lengths before the call; not modified.
  * new_lens     device int32 [B] in [0, S] (clamped into it), or NULL.
  * lens_out     device int32 [B], or NULL: seq_lens[b] + n_b, at most
- *              64 max_pages; not seq_lens itself.
+ *              64 max_pages; neither seq_lens nor new_lens itself.
  * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED before launch; SA_ERR_CUDA.
  */
 sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v,
@@ -520,8 +524,9 @@ size_t sa_route_pages_workspace_bytes(const sa_cache_params* p);
  * s_j descending (equal s_j: lower j first). Pages that compete are full, so
  * their sums rank as their means do. A score that is not a number ranks last;
  * so does a page with a bad id. (A budget bounds the attention's cost per
- * token; sa_route's threshold does not.)
- * The choice equals that of scores computed in fp64.
+ * token; sa_route's threshold does not.) Scores are computed in fp32 with an
+ * error bound; those the bound leaves undecided again, to 2^-40 of |q| |k_sum|
+ * (in fp64 where fp32 would overflow), so the choice equals that of fp64 scores.
  *
  * q          device bf16 [B, 1, H, D], rotated as the cached keys are.
  * row_ptr    device int32 [B*H_kv + 1]; row r = b*H_kv + g.
@@ -553,8 +558,8 @@ size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p);
  * token, NaN included, has no effect.
  *
  * Precision: exact products with fp32 accumulation and an fp32 softmax; P.V
- * takes P as two bf16 terms (16 bits; with SA_CACHE_FP8 one fp16 term, 11
- * bits, against V in fp16, which holds every e4m3 value) with fp32
+ * takes P as two bf16 terms (to 2^-15; with SA_CACHE_FP8 one fp16 term, to
+ * 2^-12, against V in fp16, which holds every e4m3 value) with fp32
  * accumulation; o is rounded once to bf16. The sums' order, and so the last
  * bit, depends on the lengths in the batch, not on timing.
  *

@@ -263,6 +263,49 @@ def test_saturation_and_not_a_number(sa):
     assert got[1, 0] == 0 and got[1, 1] == 0
 
 
+def test_pages_beyond_32_bit_offsets(sa):
+    """A pool of 5 GB whose last page takes the tokens."""
+    n_pages, Hkv, D = 40_000, 8, 128
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    kc, vc = (torch.empty((n_pages, Hkv, PAGE, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ksum = torch.empty((n_pages, Hkv, D), device="cuda")
+    gen = torch.Generator().manual_seed(1)
+    k, v = (torch.randn((1, 70, Hkv, D), generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    table = dev([[n_pages - 1, n_pages - 2]])
+    sa.sa_cache_append(k, v, kc, vc, table, dev([0]), k_sum=ksum)
+    torch.cuda.synchronize()
+    for cache, x in ((kc, k), (vc, v)):
+        assert torch.equal(cache[-1].transpose(0, 1), x[0, :64])
+        assert torch.equal(cache[-2, :, :6].transpose(0, 1), x[0, 64:])
+    # 64 fp32 additions: at most 64 roundings of 2^-24 of the magnitudes' sum
+    want, mag = k[0, :64].double().sum(0), k[0, :64].double().abs().sum(0)
+    assert torch.all((ksum[-1].double() - want).abs() <= 64 * 2.0 ** -24 * mag)
+
+
+def test_the_binding_refuses_what_does_not_fit(sa):
+    c = Case(2, 3, 4, 2, 64, "fp8", [5, 64], seed=7)
+    g = lambda t: t.cuda()
+    ok = dict(k=g(c.k), v=g(c.v), k_cache=c.kc, v_cache=c.vc, page_table=dev(c.table),
+              seq_lens=dev(c.lens), q=g(c.q), qk_norm=True, gamma_q=g(c.gq), cos=g(c.cos),
+              sin=g(c.sin), k_scale=g(c.ks), v_scale=g(c.vs), k_sum=c.ksum_d)
+    sa.sa_cache_append(**ok)
+    for bad in (dict(k=ok["k"].float()), dict(k=ok["k"][:, :2]), dict(v=ok["v"][:1]),
+                dict(q=ok["q"][:, :2]), dict(q=None, q_out=ok["q"]), dict(cos=None), dict(sin=None),
+                dict(cos=ok["cos"][:0], sin=ok["sin"][:0]), dict(cos=ok["cos"][:, :16], sin=ok["sin"][:, :16]),
+                dict(gamma_q=ok["gamma_q"][:32]), dict(k_sum=ok["k_sum"][1:]),
+                dict(k_scale=ok["k_scale"].double()), dict(new_lens=dev([1, 2, 3])),
+                dict(lens_out=dev([1])), dict(k_cache=c.kc.view(torch.uint8)), dict(eps=None),
+                dict(rope=1.5), dict(seq_lens=ok["seq_lens"].cpu())):
+        with pytest.raises((ValueError, KeyError)):
+            sa.sa_cache_append(**{**ok, **bad})
+    for bad in (dict(eps=-1.0), dict(rope=7), dict(qk_norm=False), dict(lens_out=ok["seq_lens"])):
+        with pytest.raises(sa.SaError) as e:
+            sa.sa_cache_append(**{**ok, **bad})
+        assert e.value.code == 1
+    torch.cuda.synchronize()
+
+
 def test_captured_and_replayed_on_another_stream(sa):
     c = Case(2, 3, 4, 2, 128, "bf16", [62, 5], sums=False, seed=6)
     e = Case(2, 3, 4, 2, 128, "bf16", [62, 5], sums=False, seed=6)

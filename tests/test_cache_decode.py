@@ -228,6 +228,56 @@ def test_not_a_number_among_valid_keys_stays_in_its_rows(sa):
     assert not torch.isnan(o[0, 0, 2:]).any() and not torch.isnan(o[1]).any()
 
 
+def test_infinite_values_stay_infinite(sa):
+    c = Case([300, 200], 4, 2, 64, "bf16", seed=19)
+    c.vc[int(c.table[0, 1]), 0, 5, 3] = float("inf")
+    c.vc[int(c.table[0, 2]), 0, 9, 40] = float("-inf")
+    o, lse = c.run(sa)
+    for h in (0, 1):
+        assert o[0, 0, h, 3] == float("inf") and o[0, 0, h, 40] == float("-inf")
+        assert torch.isfinite(o[0, 0, h]).sum() == 62
+    assert torch.isfinite(o[0, 0, 2:]).all() and torch.isfinite(o[1]).all()
+    assert torch.isfinite(lse).all()
+
+
+def test_many_routed_rows(sa):
+    """More rows than one warp scans, and than the grid has blocks."""
+    for B, H, Hkv in ((60, 4, 2), (300, 4, 4)):
+        lens = [(71 * i) % 700 for i in range(B)]
+        c = Case(lens, H, Hkv, 64, "bf16", seed=20)
+        rng = np.random.default_rng(B)
+        rows = []
+        for n in lens:
+            nb = (n + PAGE - 1) // PAGE
+            rows += [sorted(rng.choice(nb, size=rng.integers(0, nb + 1), replace=False).tolist())
+                     for _ in range(Hkv)]
+        o, lse = c.run(sa, rows)
+        assert int(c.st.item()) == 0
+        c.check(o, lse, rows)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_pages_beyond_32_bit_offsets(sa, fmt):
+    """A pool of 5 GB whose last pages hold the sequence: bytes and elements
+    past 2^32."""
+    n_pages, D = (320_000, 128) if fmt == "bf16" else (640_000, 128)
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    c = Case([200, 64], 4, 1, D, fmt, seed=21)
+    dt = c.kc.dtype
+    big = [torch.empty((n_pages, 1, PAGE, D), dtype=dt, device="cuda") for _ in range(2)]
+    far = np.array([n_pages - 1 - i for i in range(c.n_pages)])
+    for t, old in zip(big, (c.kc, c.vc)):
+        for i, p in enumerate(far):
+            t.view(torch.uint8)[p] = old.view(torch.uint8)[i]
+    small = (c.kc, c.vc, c.table)
+    c.kc, c.vc = big
+    c.table = np.where(c.table >= 0, far[np.maximum(c.table, 0)], -1).astype(np.int32)
+    o, lse = c.run(sa)
+    c.kc, c.vc, c.table = small
+    c.check(o, lse)
+
+
 def test_shared_pages_and_shared_table_rows(sa):
     """One prefix page in two sequences, and twice in one."""
     c = Case([128, 192], 2, 1, 64, "bf16", seed=15)
@@ -251,6 +301,33 @@ def test_strided_queries_outputs_and_table(sa):
     rest = out.clone()
     rest[:, 1:2, 1:5] = 3.0
     assert torch.all(rest == 3.0)
+
+
+def test_the_binding_refuses_what_does_not_fit(sa):
+    c = Case([70, 64], 4, 2, 64, "bf16", seed=22)
+    q, t, l = c.q.cuda(), dev(c.table), dev(c.lens)
+    ok = dict(q=q, k_cache=c.kc, v_cache=c.vc, page_table=t, seq_lens=l)
+    sa.sa_attn_decode(**ok)
+    rp, ci = dev([0, 1, 2, 3, 4]), dev([0, 0, 0, 0])
+    for bad in (dict(q=q.float()), dict(q=q[:1]), dict(q=q[:, 0]), dict(seq_lens=l[:1]),
+                dict(seq_lens=l.long()), dict(seq_lens=l.cpu()), dict(page_table=t.long()),
+                dict(page_table=t[0]), dict(page_table=t.t().contiguous().t()),
+                dict(k_cache=c.kc[:1]), dict(k_cache=c.kc.transpose(2, 3)),
+                dict(v_cache=c.vc.float()), dict(q=q.transpose(2, 3).contiguous().transpose(2, 3)),
+                dict(row_ptr=rp), dict(row_ptr=rp[:4], col_idx=ci), dict(row_ptr=rp, col_idx=ci.long()),
+                dict(o=q.float()), dict(o=q[:, :, :2]), dict(lse=torch.zeros(3, device="cuda")),
+                dict(k_scale=torch.ones(3, device="cuda")), dict(dev_status=l.long()),
+                dict(scale="x"), dict(workspace=torch.zeros((4, 4), device="cuda").t()[1:])):
+        with pytest.raises(ValueError):
+            sa.sa_attn_decode(**{**ok, **bad})
+    for bad, code in ((dict(k_scale=torch.ones(2, device="cuda")), 1),       # scales of a bf16 cache
+                      (dict(q=q.expand(2, 1, 4, 64)[:, :, :3]), 1),          # 3 heads on 2
+                      (dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")), 3)):
+        with pytest.raises(sa.SaError) as e:
+            sa.sa_attn_decode(**{**ok, **bad})
+        assert e.value.code == code
+    sa.sa_attn_decode(**ok)
+    torch.cuda.synchronize()
 
 
 def test_without_lse_and_with_a_dirty_workspace(sa):

@@ -101,6 +101,12 @@ def test_append_refusals(sa):
     assert append(sa, p, gamma_k=A) == INVALID                  # weights without the norm
     assert append(sa, p, k_scale=A) == INVALID                  # scales of a bf16 cache
     assert append(sa, p, lens_out=A) == INVALID                 # seq_lens itself
+    B = ctypes.c_void_p(8192)
+    assert append(sa, p, lens=B, new=A, lens_out=A) == INVALID  # new_lens itself
+    p.o_stride[1] = 2048                                        # in place, laid out otherwise
+    p.o_stride[0] = 2048
+    assert append(sa, p) == INVALID
+    p = params(sa)
     for field, i in (("q_stride", 1), ("k_stride", 0), ("v_stride", 2), ("o_stride", 2),
                      ("kc_stride", 0), ("vc_stride", 2)):
         for bad in (4, 0, -8):

@@ -138,6 +138,45 @@ def test_long_sequences(sa, n_pages):
     c.check(rp, ci, 951, 300)
 
 
+def test_rows_beyond_32_bit_offsets(sa):
+    """Key sums of a pool of 5 GB, the sequence's pages at its end."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    c = Case([64 * 40 - 3], 8, 8, 128, seed=23)
+    n = 1_250_000
+    big = torch.empty((n, 8, 128), device="cuda")
+    big[n - c.n_pages:] = c.ksum.cuda()
+    table = dev(c.table) + (n - c.n_pages)
+    st = status()
+    rp, ci = sa.sa_route_pages(c.q.cuda(), big, table, dev(c.lens), 64, 9, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    c.check(rp.cpu().numpy(), ci.cpu().numpy(), 64, 9)
+
+
+def test_streams_and_refusals(sa):
+    c = Case([4000, 640], 4, 2, 64, seed=24)
+    q, k, t, l = c.q.cuda(), c.ksum.cuda(), dev(c.table), dev(c.lens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        rp, ci = sa.sa_route_pages(q, k, t, l, 64, 9, stream=stream)
+        torch.cuda.synchronize()
+        c.check(rp.cpu().numpy(), ci.cpu().numpy(), 64, 9)
+    ok = dict(q=q, k_sum=k, page_table=t, seq_lens=l, prefix_len=64, budget=9)
+    for bad in (dict(q=q.float()), dict(k_sum=k.half()), dict(k_sum=k[:, :, :32]), dict(k_sum=k[0]),
+                dict(q=q[:, 0]), dict(seq_lens=l[:1]), dict(budget=1 << 40), dict(budget="x"),
+                dict(row_ptr=dev([0] * 4)), dict(col_idx=torch.zeros(99, device="cuda"))):
+        with pytest.raises((ValueError, TypeError)):
+            sa.sa_route_pages(**{**ok, **bad})
+    for bad, code in ((dict(budget=-1), 1), (dict(prefix_len=-1), 1), (dict(q=q.expand(2, 1, 4, 64)[:, :, :3]), 1)):
+        with pytest.raises(sa.SaError) as e:
+            sa.sa_route_pages(**{**ok, **bad, "row_ptr": dev([0] * 5), "col_idx": dev([0] * 99),
+                                 "workspace": torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")})
+        assert e.value.code == code
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------- run together --
 
 @pytest.mark.parametrize("fmt,rope,D", [("bf16", "interleaved", 128), ("fp8", "half", 64)])
