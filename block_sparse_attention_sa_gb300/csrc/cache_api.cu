@@ -264,8 +264,9 @@ sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_
   sa_status s = check_cache(p);
   if (s != SA_OK) return s;
   if (p->S != 1) return SA_ERR_UNSUPPORTED;
-  // the pages of a run are counted in 32 bits
-  if (static_cast<int64_t>(p->B) * p->H * p->max_pages > static_cast<int64_t>(INT32_MAX) * 128)
+  // the pages of all units are counted in 31 bits
+  if (static_cast<int64_t>(p->B) * p->H_kv * decode_row_tiles(p->H, p->H_kv) >
+      INT32_MAX / static_cast<int64_t>(p->max_pages))
     return SA_ERR_UNSUPPORTED;
   if (col_cap < 0) return SA_ERR_INVALID_ARG;
   if (!q || !o || !workspace || (row_ptr == nullptr) != (col_idx == nullptr))

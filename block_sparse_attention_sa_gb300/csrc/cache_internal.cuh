@@ -72,6 +72,7 @@ struct RoutePagesArgs {
 
 cudaError_t launch_append(const AppendArgs& a, int D, bool fp8, bool half, cudaStream_t st);
 size_t decode_ws_bytes(int H, int Hkv, int D);
+int decode_row_tiles(int H, int Hkv);   // CTAs' worth of query heads on a key-value head
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           bool fp8, cudaStream_t st);
 size_t route_pages_ws_bytes(int64_t rows, int max_pages);
@@ -119,51 +120,44 @@ __device__ __forceinline__ int clamp_len(int n, const PageMap& pm, bool* bad) {
   return n < 0 ? 0 : (n > most ? most : n);
 }
 
-// Run c of C over a list of T items: [run_start(c), run_start(c + 1)).
-__device__ __forceinline__ int64_t run_start(int64_t T, int C, int c) {
-  return T / C * c + (c < T % C ? c : T % C);
-}
-
-// The run an item of the list lies in.
-__device__ __forceinline__ int run_of(int64_t T, int C, int64_t item) {
-  const int64_t base = T / C, rem = T % C, big = rem * (base + 1);
-  return static_cast<int>(item < big ? item / (base + 1) : rem + (item - big) / base);
+// The run of C an item of a list of T items lies in: the first T % C runs hold
+// one item more than the others.
+__device__ __forceinline__ int run_of(unsigned T, unsigned C, unsigned item) {
+  const unsigned base = T / C, rem = T - base * C, big = rem * (base + 1);
+  return item < big ? item / (base + 1) : rem + (item - big) / base;
 }
 
 struct Run {
-  int64_t T, lo, hi;       // items of the list, and this CTA's among them
-  int64_t off;             // where a run that is not empty begins: item `off`
-  int group;               // of group `group`
+  int T, lo, hi;           // items of the list, and this CTA's among them
+  int group, off;          // where a run that is not empty begins: item `off` of a group
 };
 
 // The list is that of `groups` groups in order, each count(i) * per_group
-// items. Every CTA of the grid finds its run of it by a scan of the counts: up
-// to 32 groups by each warp for itself, more by the CTA. All NT threads call it
-// and get the same; it ends with every thread past a barrier.
+// items (the host has checked that 31 bits hold them all). Every CTA of the grid
+// finds its run of it by a scan of the counts: up to 32 groups by each warp for
+// itself, more by the CTA. All NT threads call it and get the same; it ends with
+// every thread past a barrier.
 template <int NT, class Count>
-__device__ __forceinline__ Run plan_run(int groups, int64_t per_group, Count count) {
-  __shared__ int64_t warp_sum[NT / 32], start_off;
-  __shared__ int start_group;
+__device__ __forceinline__ Run plan_run(int groups, int per_group, Count count) {
+  __shared__ int warp_sum[NT / 32], start_off, start_group;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool few = groups <= 32;
   const int per_thread = few ? 1 : (groups + NT - 1) / NT, first = few ? lane : tid * per_thread;
-  const int g0 = first < groups ? first : groups;
-  const int g1 = g0 + per_thread < groups ? g0 + per_thread : groups;
-  int64_t mine = 0;
+  const int g0 = min(first, groups), g1 = min(g0 + per_thread, groups);
+  int mine = 0;
   for (int i = g0; i < g1; ++i) mine += count(i);
-  int64_t incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += v;
   }
-  int64_t before = 0, total = 0;
+  int before = 0, total = 0;
   if (few) {
     total = __shfl_sync(0xffffffffu, incl, 31);
   } else {
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-#pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) before += warp_sum[w];
       total += warp_sum[w];
@@ -171,16 +165,18 @@ __device__ __forceinline__ Run plan_run(int groups, int64_t per_group, Count cou
   }
   Run r;
   r.T = total * per_group;
-  r.lo = run_start(r.T, gridDim.x, blockIdx.x);
-  r.hi = run_start(r.T, gridDim.x, blockIdx.x + 1);
+  const unsigned C = gridDim.x, c = blockIdx.x;
+  const unsigned base = static_cast<unsigned>(r.T) / C, rem = r.T - base * C;
+  r.lo = base * c + min(c, rem);
+  r.hi = r.lo + base + (c < rem ? 1 : 0);
   r.group = 0;
   r.off = 0;
-  int64_t at = (before + incl - mine) * per_group;
+  int at = (before + incl - mine) * per_group;
   const bool here = r.lo < r.hi && r.lo >= at && r.lo < at + mine * per_group;
   if (here) {
     int i = g0;
     for (;; ++i) {
-      const int64_t n = count(i) * per_group;
+      const int n = count(i) * per_group;
       if (r.lo < at + n) break;
       at += n;
     }
@@ -188,20 +184,17 @@ __device__ __forceinline__ Run plan_run(int groups, int64_t per_group, Count cou
     r.off = r.lo - at;
   }
   if (few) {
-    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-    r.group = __shfl_sync(0xffffffffu, r.group, src < 0 ? 0 : src);
-    r.off = __shfl_sync(0xffffffffu, r.off, src < 0 ? 0 : src);
-    __syncthreads();
-  } else {
-    if (here) {
-      start_group = r.group;
-      start_off = r.off;
-    }
-    __syncthreads();
-    if (r.lo < r.hi) {
-      r.group = start_group;
-      r.off = start_off;
-    }
+    const int src = max(__ffs(__ballot_sync(0xffffffffu, here)) - 1, 0);
+    r.group = __shfl_sync(0xffffffffu, r.group, src);
+    r.off = __shfl_sync(0xffffffffu, r.off, src);
+  } else if (here) {
+    start_group = r.group;
+    start_off = r.off;
+  }
+  __syncthreads();
+  if (!few && r.lo < r.hi) {
+    r.group = start_group;
+    r.off = start_off;
   }
   return r;
 }

@@ -76,7 +76,7 @@ struct PageMeta {
 };
 
 // The run's pieces of one unit, for join_kernel: unit, and its first and last run.
-struct Cut {
+struct __align__(16) Cut {
   int unit, first, last, pad;
 };
 
@@ -207,8 +207,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // this CTA's run of the page list
   const Run run = plan_run<NT>(
       n_groups, per_group,
-      [&](int i) { return static_cast<int64_t>(group_pages(a, i, &status)); });
-  const int64_t T = run.T, lo = run.lo, hi = run.hi;
+      [&](int i) { return group_pages(a, i, &status); });
   // groups without a page: nothing to attend
   for (int i = c + C * warp; i < n_groups; i += C * (NT / 32)) {
     if (group_pages(a, i, &status) != 0) continue;
@@ -225,22 +224,21 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
   if (warp == W) {
     // ---------------------------------------------------------- producer --
-    int64_t left = hi - lo;
-    int group = run.group;
-    int64_t off = run.off;                      // pages into the group's units
-    int64_t issued = 0;
+    int left = run.hi - run.lo, group = run.group;
+    int off = run.off;                          // pages into the group's units
+    int s = 0, in_ring = 0;                     // next stage; stages ever used, up to NS
+    uint32_t ph = 0;
     Cut cut{-1, 0, 0, 0};
     bool ok = true;
     while (left > 0 && ok) {
       if (group >= n_groups) break;             // the lengths changed under the call
       const int cnt = group_pages(a, group, &status);
-      if (off >= static_cast<int64_t>(cnt) * per_group) {
+      if (off >= cnt * per_group) {
         ++group;
         off = 0;
         continue;
       }
-      const int sub = static_cast<int>(off / cnt), p0 = static_cast<int>(off % cnt);
-      const int take = static_cast<int>(min(left, static_cast<int64_t>(cnt - p0)));
+      const int sub = off / cnt, p0 = off - sub * cnt, take = min(left, cnt - p0);
       const int bg = routed ? group : group * a.Hkv + sub / RT, rt = sub % RT;
       const int b = routed ? group / a.Hkv : group, g = bg - b * a.Hkv;
       const int unit = bg * RT + rt;
@@ -253,7 +251,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (dest == 1) {
         cut.unit = unit;
         cut.first = c;
-        cut.last = run_of(T, C, hi - left + cnt - 1);
+        cut.last = run_of(run.T, C, run.hi - left + cnt - 1);
       }
       if (by_unit && dest != 0 && lane == 0) cuts[unit] = dest == 1 ? cut : Cut{-1, 0, 0, 0};
       for (int q0 = 0; q0 < take && ok; q0 += 32) {
@@ -285,8 +283,6 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int x = 0; x < m; ++x) {
           const int pg = __shfl_sync(0xffffffffu, page, x);
           const int lv = __shfl_sync(0xffffffffu, live, x);
-          const int s = static_cast<int>(issued % NS);
-          const uint32_t ph = static_cast<uint32_t>(issued / NS) & 1u;
           if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort)) {
             ok = false;
             break;
@@ -308,7 +304,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
           }
           __syncwarp();
-          ++issued;
+          if (++s == NS) {
+            s = 0;
+            ph ^= 1u;
+          }
+          if (in_ring < NS) ++in_ring;
         }
       }
       off += take;
@@ -322,15 +322,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
       // no copy may be in flight when the CTA ends
       const volatile int never = 0;
-      for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
-        mbar_wait(smem_u32(&full[i % NS]), static_cast<uint32_t>(i / NS) & 1u,
-                  AbortSignal{&never, nullptr});
+      for (int i = 0; i < in_ring; ++i) {
+        // from the newest stage back: those below `s` have its phase
+        const int at = s > i ? s - 1 - i : s - 1 - i + NS;
+        mbar_wait(smem_u32(&full[at]), s > i ? ph : ph ^ 1u, AbortSignal{&never, nullptr});
+      }
     }
   } else {
     // --------------------------------------------------------- consumers --
     const int rg = warp / S::kKeyWarps, kw = warp % S::kKeyWarps;
     const int r = lane >> 2, cq = lane & 3;
-    const int n_pages = static_cast<int>(hi - lo);
+    const int n_pages = run.hi - run.lo;
     uint4* q_frag = sm_q + rg * (D / 16) * 32 + lane;       // A fragment k at [32 k]
     float o[D / 8][4];
     float m[2], l[2], f[2];                  // rows r and r + 8 of the warp's 16
@@ -397,7 +399,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // those of the first unit need not wait for its first page
     if (n_pages > 0) {
       const int cnt = group_pages(a, run.group, &status);
-      const int sub = cnt > 0 ? static_cast<int>(run.off / cnt) : 0;
+      const int sub = cnt > 0 ? run.off / cnt : 0;
       load_queries(min((routed ? run.group : run.group * a.Hkv) * RT + sub, a.B * a.Hkv * RT - 1));
     }
     int s = 0;
@@ -721,7 +723,8 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* 
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
   wait_for_first();
-  const Cut cut = cuts[blockIdx.x];
+  const int4 whole = *reinterpret_cast<const int4*>(cuts + blockIdx.x);   // in one load
+  const Cut cut{whole.x, whole.y, whole.z, 0};
   const int units = a.B * a.Hkv * RT;
   if (cut.unit < 0 || cut.unit >= units || cut.first < 0 || cut.last <= cut.first || cut.last >= runs)
     return;
@@ -825,6 +828,11 @@ cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& kmap, const CUtenso
 }
 
 }  // namespace
+
+int decode_row_tiles(int H, int Hkv) {
+  const int G = H / Hkv, rows = 16 * row_groups(G);
+  return (G + rows - 1) / rows;
+}
 
 size_t decode_ws_bytes(int H, int Hkv, int D) {
   // two partials of every run

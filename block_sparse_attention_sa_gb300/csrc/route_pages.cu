@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
     return (n + kBlock - 1) / kBlock;
   };
   const Run run = plan_run<32 * kScoreWarps>(
-      a.B, blocks, [&](int b) { return static_cast<int64_t>((pages(b) + wide - 1) / wide); });
-  const int n_items = static_cast<int>(run.hi - run.lo);
+      a.B, blocks, [&](int b) { return (pages(b) + wide - 1) / wide; });
+  const int n_items = run.hi - run.lo;
   if (n_items > 0) {
     auto enter = [&](Cursor& c) {            // what follows from c.b
       c.nb = c.b < a.B ? pages(c.b) : 0;
@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
     Cursor now{run.group, 0, 0, 0, 0};
     enter(now);
     if (now.cnt > 0) {
-      now.gb = static_cast<int>(run.off / now.cnt);
-      now.at = static_cast<int>(run.off % now.cnt);
+      now.gb = run.off / now.cnt;
+      now.at = run.off - now.gb * now.cnt;
     }
     auto first_page = [&](const Cursor& c) { return c.at * wide + wt * kTile; };
     auto page_at = [&](const Cursor& c) {    // lane: page lane % 16 of the warp's tile

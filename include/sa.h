@@ -576,7 +576,8 @@ size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p);
  * lse        device fp32 [B, H, 1] (natural log), or NULL.
  * workspace  device scratch of sa_attn_decode_workspace_bytes(p) bytes,
  *            256-byte aligned; its contents on entry do not matter.
- * Errors: as sa_attn_sparse; S must be 1 (SA_ERR_UNSUPPORTED).
+ * Errors: as sa_attn_sparse; S must be 1 and B*H_kv*max_pages (times
+ * ceil(G / 64), G = H / H_kv) < 2^31 (SA_ERR_UNSUPPORTED).
  */
 sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_cache,
                          const void* v_cache, const float* k_scale, const float* v_scale,

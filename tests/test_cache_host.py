@@ -129,6 +129,7 @@ def test_route_and_decode_refusals(sa):
     big = params(sa, B=60000, H=64, Hkv=64, max_pages=1 << 20)
     assert route(sa, big) == UNSUPPORTED                        # lists beyond int32
     assert route(sa, params(sa, B=1, max_pages=(1 << 20) + 1)) == UNSUPPORTED
+    assert decode(sa, big) == UNSUPPORTED                       # pages beyond 31 bits
     p = params(sa)
     for name in ("q", "kc", "vc", "table", "lens", "o", "ws"):
         assert decode(sa, p, **{name: None}) == INVALID, name
