@@ -741,23 +741,31 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* 
   };
   const int n = cut.last - cut.first + 1;
   float o[V] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kJoinWarps) {
-    const float* p = piece(i);
-    const float2 ml = *reinterpret_cast<const float2*>(p + rows * D + 2 * row);
-    const float pm = ml.x, pl = ml.y;
-    float v[V];
+  // four pieces on their way at once
+  for (int i0 = warp; i0 < n; i0 += 4 * kJoinWarps) {
+    float2 ml[4];
+    float v[4][V];
 #pragma unroll
-    for (int x = 0; x < V; ++x) v[x] = p[row * D + lane + 32 * x];
-    if (pm == -INFINITY) {                   // nothing counted there (a sum of 0, or NaN)
-      l += pl;
-      continue;
+    for (int u = 0; u < 4; ++u) {
+      const float* p = piece(min(i0 + u * kJoinWarps, n - 1));
+      ml[u] = *reinterpret_cast<const float2*>(p + rows * D + 2 * row);
+#pragma unroll
+      for (int x = 0; x < V; ++x) v[u][x] = p[row * D + lane + 32 * x];
     }
-    const float now = fmaxf(m, pm), c0 = m == -INFINITY ? 0.f : ex2(m - now), c1 = ex2(pm - now);
-    l = (m == -INFINITY ? l : l * c0) + pl * c1;
-    m = now;
 #pragma unroll
-    for (int x = 0; x < V; ++x) o[x] = o[x] * c0 + v[x] * c1;
+    for (int u = 0; u < 4; ++u) {
+      if (i0 + u * kJoinWarps >= n) break;
+      const float pm = ml[u].x, pl = ml[u].y;
+      if (pm == -INFINITY) {                 // nothing counted there (a sum of 0, or NaN)
+        l += pl;
+        continue;
+      }
+      const float now = fmaxf(m, pm), c0 = m == -INFINITY ? 0.f : ex2(m - now), c1 = ex2(pm - now);
+      l = (m == -INFINITY ? l : l * c0) + pl * c1;
+      m = now;
+#pragma unroll
+      for (int x = 0; x < V; ++x) o[x] = o[x] * c0 + v[u][x] * c1;
+    }
   }
 #pragma unroll
   for (int x = 0; x < V; ++x) sm_o[warp][lane + 32 * x] = o[x];
