@@ -11,7 +11,15 @@
 // One launch, two kinds of CTAs. Key-value CTAs own whole pages of one head: a
 // page's tokens of this call are summed in a fixed order by the lanes that
 // store them, so its k_sum needs no atomics and is the same every time. Query
-// CTAs own one token: its angles are loaded once for all heads.
+// CTAs own a few tokens: a token's angles are loaded once for all heads. At most
+// 72 registers a thread, so that seven CTAs of 128 threads share an SM: loads in
+// flight come from many warps, not from deep ones (38,247 tokens, 56/8 heads:
+// 282 us with four CTAs and four tokens in flight a lane group, 219 us now).
+//
+// Measured on GB300 (copy rate 6.79 TB/s): 38,247 tokens, 56/8 heads of 128,
+// bf16, 1.43 GB in 219 us, 6.55 TB/s. 5 x up to 2,047 tokens, 16/16 heads of 64,
+// e4m3, 54 MB in 16.4 us: instructions bound it, 60% of the issue slots. One
+// token 3.5 us, 128 tokens 4.3 us: launch and the chain of loads.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

@@ -3,21 +3,26 @@
 //   s_j = max over the head group of q_h . k_sum_j
 //
 // score_kernel reads every key sum once (4 D bytes a page and head, 1/64 of what
-// the page's keys and values take in bf16) and is bound by that. Eight pages and
-// up to 16 query heads are one tile of mma.m16n8k16: the fp32 sums go in as two
-// bf16 terms, so the products are right to 2^-18, and the tensor cores leave the
-// loads alone. Tiles are cut into equal runs, one per CTA, whatever the lengths.
+// the page's keys and values take in bf16). Sixteen pages and eight query heads
+// are one tile of mma.m16n8k16, the heads as its columns; the fp32 sums go in as
+// two bf16 terms, so the products are right to 2^-17. Sums come into shared
+// memory by bulk copies, two tiles ahead of each warp; tiles are cut into equal
+// runs, one per CTA, whatever the lengths. Measured on GB300: 144 MB (32
+// sequences of up to 112,640 tokens, 32/8 heads of 128) in 30 us, 63% of the
+// DRAM rate, issue slots 42% busy with the splitting; 38 us with select_kernel.
 //
-// select_kernel, one CTA per row, finds the score that the budget ends at by
-// bisection. An order statistic moves by no more than the values do, so a page
+// select_kernel, one CTA per row, narrows down the score that the budget ends at
+// by histograms of 256 bins. An order statistic moves by no more than the values do, so a page
 // whose score is more than twice the error bound above or below that score is
 // decided; the few in between (usually the last page alone) are computed again
-// in fp64 and ranked. Rows with scores that are not finite are ranked in fp64
-// whole.
+// in paired fp32 and ranked. Rows with scores that are not finite, and rows with
+// very many undecided pages, are ranked in fp64. Latency bounds it: 10 us for 8
+// rows of 598 pages with both kernels, about half of it this one.
 //
-// Error of a score against fp64, over sum_d |q_d k_d| <= |q| |k|: 2^-18 from the
-// two terms, and 2 D / 16 tensor-core steps that each add 16 products to the sum
-// with less than 2^-22 of it lost: below 2^-17.9 + 2^-18. kErr doubles that.
+// Error of a score against fp64, over sum_d |q_d k_d| <= |q|_1 max |k|: 2^-18
+// from the two terms; and D / 16 tensor-core steps for each, which add 16 products
+// and the running sum, each cut to 24 bits of the largest or better: 17 2^-24 a
+// step, below 2^-16.9. Together below 2^-16.3; kErr is 2^-16.
 #include <cuda_bf16.h>
 
 #include "cache_internal.cuh"
@@ -32,14 +37,14 @@ constexpr int kTile = 16;              // pages of a score tile
 constexpr int kScoreWarps = 4;
 constexpr int kScoreCtas = 3 * 152;    // three CTAs on each SM
 constexpr int kAhead = 2;              // tiles a warp has in flight
-constexpr float kErr = 1.f / 32768.f;  // 2^-15
+constexpr float kErr = 1.f / 65536.f;  // 2^-16
 constexpr int kItems = 8;              // pages a thread of select_kernel holds at once
 constexpr int kSpan = kThreads * kItems;
 constexpr int kNear = 256;             // undecided pages ranked in shared memory
 constexpr unsigned kFull = 0xffffffffu;
 
-// Workspace: per page its score and |q|^2 |k|^2 (what bounds the score's
-// error), and fp64 scores where more than kNear pages are ranked exactly.
+// Workspace: per page its score and |q|_1 max |k| (what bounds the score's
+// error; a score that is no number or infinite speaks for itself), and fp64 scores where more than kNear pages are ranked exactly.
 struct Layout {
   size_t score, err, exact, total;
 };
@@ -66,9 +71,8 @@ __device__ __forceinline__ void row_counts(int n, int prefix, int budget, int* n
 
 __device__ __forceinline__ float bits_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
-// A squared norm, infinite where the products it bounds might overflow or are
-// no numbers.
-__device__ __forceinline__ float capped(float n2) { return n2 < 1e38f ? n2 : INFINITY; }
+// A sum of magnitudes, infinite where it is no number.
+__device__ __forceinline__ float capped(float n) { return n < 1e38f ? n : INFINITY; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -83,7 +87,7 @@ __device__ __forceinline__ void mma(float* c, const uint4& a, uint32_t b0, uint3
 }
 
 // 8 query heads from h0 on as B fragments (heads beyond the group zero) and
-// their largest squared norm, in every lane. The 16 dims of a step are taken in
+// the largest of their sums of magnitudes, in every lane. The 16 dims of a step are taken in
 // the order the key sums' 16-byte loads give: lane quad c holds 4c .. 4c + 3.
 template <int D>
 __device__ __forceinline__ float load_heads(const RoutePagesArgs& a, int b, int g, int G, int h0,
@@ -91,20 +95,20 @@ __device__ __forceinline__ float load_heads(const RoutePagesArgs& a, int b, int 
   const int h = h0 + (lane >> 2), c = lane & 3;
   const bool there = h < G;
   const uint16_t* q = a.q + b * a.qs[0] + (g * G + (there ? h : 0)) * a.qs[2];
-  float n2 = 0.f;
+  float n1 = 0.f;
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
     qb[k] = there ? get(reinterpret_cast<const uint2*>(q + 16 * k + 4 * c)) : make_uint2(0u, 0u);
     const float f[4] = {bits_f32(qb[k].x), __uint_as_float(qb[k].x & 0xffff0000u), bits_f32(qb[k].y),
                         __uint_as_float(qb[k].y & 0xffff0000u)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n2 = fmaf(f[i], f[i], n2);
+    for (int i = 0; i < 4; ++i) n1 += fabsf(f[i]);
   }
-  n2 += __shfl_xor_sync(kFull, n2, 1);
-  n2 = capped(n2 + __shfl_xor_sync(kFull, n2, 2));
+  n1 += __shfl_xor_sync(kFull, n1, 1);
+  n1 = capped(n1 + __shfl_xor_sync(kFull, n1, 2));
 #pragma unroll
-  for (int off = 4; off <= 16; off <<= 1) n2 = fmaxf(n2, __shfl_xor_sync(kFull, n2, off));
-  return n2;
+  for (int off = 4; off <= 16; off <<= 1) n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, off));
+  return n1;
 }
 
 // A place in the list of items: item `at` of `cnt` of head block `gb` of
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
     }
     int next = page[kAhead];
     uint2 qb[kSteps];
-    float q2 = 0.f;
+    float q1 = 0.f;
     int64_t have = -1;                       // the row whose queries are loaded
     int st = 0;
     uint32_t phase = 0;
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
       const int b = min(now.b, a.B - 1);     // should the lengths change under the call
       const int64_t row = static_cast<int64_t>(b) * a.Hkv + g;
       if (kOne && have != row) {
-        q2 = load_heads<D>(a, b, g, G, 0, lane, qb);
+        q1 = load_heads<D>(a, b, g, G, 0, lane, qb);
         have = row;
       }
       if (!mbar_wait_warp(smem_u32(&full[warp][st]), phase, AbortSignal{&abort_flag, nullptr})) {
@@ -245,18 +249,18 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
       }
       const float4* w = mine + (st * kTile + (lane >> 2)) * kRow + (lane & 3);
       // lane's scores: pages lane / 4 and + 8, over its heads
-      float best[2] = {-INFINITY, -INFINITY}, k2[2];
+      float best[2] = {-INFINITY, -INFINITY}, top[2];
       for (int h0 = 0; h0 < (kOne ? 1 : G); h0 += 8) {
-        if (!kOne) q2 = fmaxf(h0 == 0 ? 0.f : q2, load_heads<D>(a, b, g, G, h0, lane, qb));
+        if (!kOne) q1 = fmaxf(h0 == 0 ? 0.f : q1, load_heads<D>(a, b, g, G, h0, lane, qb));
         float c[4] = {}, d[4] = {};
-        k2[0] = k2[1] = 0.f;
+        top[0] = top[1] = 0.f;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           uint4 hi, lo;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float4 v = w[8 * x * kRow + 4 * k];
-            k2[x] = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, k2[x]))));
+            top[x] = fmaxf(fmaxf(fmaxf(top[x], fabsf(v.x)), fmaxf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
             const uint32_t h01 = pack_bf16(v.x, v.y), h23 = pack_bf16(v.z, v.w);
             const uint32_t l01 = pack_bf16(v.x - bits_f32(h01), v.y - __uint_as_float(h01 & 0xffff0000u));
             const uint32_t l23 = pack_bf16(v.z - bits_f32(h23), v.w - __uint_as_float(h23 & 0xffff0000u));
@@ -289,15 +293,15 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
       for (int x = 0; x < 2; ++x) {
         best[x] = fmaxf(best[x], __shfl_xor_sync(kFull, best[x], 1));
         best[x] = fmaxf(best[x], __shfl_xor_sync(kFull, best[x], 2));
-        k2[x] += __shfl_xor_sync(kFull, k2[x], 1);
-        k2[x] = capped(k2[x] + __shfl_xor_sync(kFull, k2[x], 2));
+        top[x] = fmaxf(top[x], __shfl_xor_sync(kFull, top[x], 1));
+        top[x] = fmaxf(top[x], __shfl_xor_sync(kFull, top[x], 2));
       }
       if ((lane & 3) < 2) {                  // one lane a page
         const int j = (lane >> 2) + 8 * (lane & 1);
         if (j0 + j < now.nb) {
           const int64_t at = row * a.pm.max_pages + j0 + j;
           score[at] = (there >> j) & 1u ? (lane & 1 ? best[1] : best[0]) : -INFINITY;
-          err[at] = (there >> j) & 1u ? q2 * (lane & 1 ? k2[1] : k2[0]) : 0.f;
+          err[at] = (there >> j) & 1u ? q1 * (lane & 1 ? top[1] : top[0]) : 0.f;
         }
       }
     }
@@ -338,8 +342,9 @@ __device__ double exact_score(const RoutePagesArgs& a, int b, int g, int j, int 
 
 // Score of one page by a whole warp as a sum of two floats, each product and
 // sum kept with its rounding error: right to about 2^-40 of |q| |k|. Eight heads
-// at a time, four lanes each (fp64 arithmetic runs at 1/64 of fp32's rate here:
-// 14,700 cycles for three pages in place of MEASURED). For finite scores only.
+// at a time, four lanes each. (In fp64, which runs at 1/64 of fp32's rate here,
+// three pages took 14,700 cycles, more than all else in the kernel.) For finite
+// scores only.
 template <int D>
 __device__ double paired_score(const RoutePagesArgs& a, int b, int g, int j, int lane) {
   const int page = get(a.pm.table + b * a.pm.table_stride + j), G = a.H / a.Hkv, c = lane & 3;
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
       k_d = max(k_d, x.z);
     }
     float lo = unorder32(k_lo), hi = unorder32(k_hi);
-    const float d = kErr * sqrtf(__uint_as_float(k_d));
+    const float d = kErr * __uint_as_float(k_d);
     if (lo > -1e38f && hi < 1e38f && d < 1e30f) {
       // The want-th largest score lies in [lo, hi]. Each pass counts the pages
       // in 256 bins of that range, from the top, and goes on in the bin the

@@ -73,6 +73,16 @@ def test_scores_that_nearly_tie(sa, seed):
     c.check(rp, ci, 64, 20)
 
 
+@pytest.mark.parametrize("scale", [1e-30, 1e-18, 1e15, 1e30])
+def test_near_ties_of_very_small_and_large_sums(sa, scale):
+    """The error bound neither vanishes nor overflows with the sums' size."""
+    c = Case([64 * 300, 64 * 40], 8, 2, 64, seed=7)
+    gen = torch.Generator().manual_seed(7)
+    c.ksum = c.ksum[:1] * (1 + 2.0 ** -22 * torch.randint(-4, 5, c.ksum.shape, generator=gen)) * scale
+    rp, ci = c.run(sa, 64, 20)
+    c.check(rp, ci, 64, 20)
+
+
 def test_equal_scores_go_to_the_lower_page(sa):
     c = Case([64 * 500], 4, 2, 64, seed=1)
     c.ksum[:] = c.ksum[0]
