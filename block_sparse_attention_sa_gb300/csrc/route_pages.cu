@@ -35,6 +35,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;              // pages of a score tile
 constexpr int kScoreWarps = 4;
+static_assert((kScoreWarps & (kScoreWarps - 1)) == 0, "heads, a power of two, divide them");
 constexpr int kScoreCtas = 3 * 152;    // three CTAs on each SM
 constexpr int kAhead = 2;              // tiles a warp has in flight
 constexpr float kErr = 1.f / 65536.f;  // 2^-16
