@@ -394,6 +394,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           // 2^e in two steps: that of a subnormal row is beyond one float
           const float up1 = ldexpf(1.f, e / 2), up2 = ldexpf(1.f, e - e / 2);
           f[x] = base * ldexpf(1.f, -(e / 2)) * ldexpf(1.f, -(e - e / 2));
+          if (f[x] == 0.f) f[x] = 0x1p-149f;   // a masked -inf times 0 would be no number
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -402,7 +403,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               qa[k][2 * y + x] = pack_half(lo_f32(w) * up1 * up2, hi_f32(w) * up1 * up2);
             }
         }
-                      }
+      }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         if (k % S::kKeyWarps == kw) q_frag[32 * k] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);

@@ -154,6 +154,17 @@ def test_peaked_and_flat_softmax(sa, fmt):
         c.check(*c.run(sa))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_next_to_zero(sa, D):
+    """Logits that underflow are zero, in a page with masked keys too."""
+    for q, ks in ((2.0 ** -133, 1e-3), (2.0 ** -126, 1e-20), (-2.0 ** -130, 0.02)):
+        c = Case([65, 1000, 3], 4, 2, D, "fp8", seed=21)
+        c.q.fill_(q)
+        assert float(c.q.float().abs().max()) == abs(q)
+        c.ks.fill_(ks)
+        c.check(*c.run(sa))
+
+
 def test_one_far_key_among_many_small_weights(sa):
     """A key far above the others in one page, the mass spread over the rest."""
     c = Case([6000], 4, 1, 128, "fp8", qmag=0.5, seed=8)
