@@ -346,7 +346,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int n_pages = run.hi - run.lo;
     uint4* q_frag = sm_q + rg * (D / 16) * 32 + lane;       // A fragment k at [32 k]
     float o[D / 8][4];
-    float m[2], l[2], f[2];                  // rows r and r + 8 of the warp's 16
+    // rows r and r + 8 of the warp's 16: largest q.k, sum, and what takes q.k to a
+    // logit (base 2)
+    float m[2], l[2], f[2];
     uint32_t join_phase = 0;
     bool ok = true;
     // all consumer warps meet; false if one of them gave up
@@ -497,7 +499,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * f[x];
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
           grew |= top[x] > m[x];
         }
         if (__any_sync(0xffffffffu, grew)) {
@@ -505,7 +507,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float now = fmaxf(m[x], top[x]);
-            corr[x] = now == -INFINITY ? 1.f : ex2(m[x] - now);
+            corr[x] = now == -INFINITY ? 1.f : ex2((m[x] - now) * f[x]);
             m[x] = now;
             l[x] *= corr[x];
           }
@@ -519,12 +521,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float shift = (m[x] == -INFINITY ? 0.f : m[x]) - (kFp8 ? kFp16Shift : 0.f);
+          // m is subtracted before the scaling: the largest key has weight 1
+          // however coarse fp32 is at its logit's size
+          const float mx = m[x] == -INFINITY ? 0.f : m[x];
           float sum = 0.f;
 #pragma unroll
           for (int t = 0; t < 2 * SL; ++t) {
-            sc[t][2 * x] = ex2(fmaf(sc[t][2 * x], f[x], -shift));
-            sc[t][2 * x + 1] = ex2(fmaf(sc[t][2 * x + 1], f[x], -shift));
+            sc[t][2 * x] = ex2(kFp8 ? fmaf(sc[t][2 * x] - mx, f[x], kFp16Shift) : (sc[t][2 * x] - mx) * f[x]);
+            sc[t][2 * x + 1] = ex2(kFp8 ? fmaf(sc[t][2 * x + 1] - mx, f[x], kFp16Shift) : (sc[t][2 * x + 1] - mx) * f[x]);
             sum += sc[t][2 * x] + sc[t][2 * x + 1];
           }
           l[x] += sum;
@@ -609,6 +613,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int x = 0; x < 2; ++x) {
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+          m[x] *= f[x];
         }
         // the piece ends: the key warps' results are added
 #pragma unroll
@@ -701,7 +706,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               if (col_g == 0 && a.lse)
                 a.lse[static_cast<int64_t>(b) * a.H + h] =
                     tot == 0.f ? -INFINITY
-                               : (top - (kFp8 ? kFp16Shift : 0.f) + log2f(tot)) * 0.69314718055994530942f;
+                               : (top + log2f(kFp8 ? tot * 0x1p-15f : tot)) * 0.69314718055994530942f;
             } else {
               *reinterpret_cast<float4*>(part + row * D + col_g) = sum;
               if (col_g == 0)
@@ -730,7 +735,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* partial,
+join_kernel(DecodeArgs a, int RT, int rows, int runs, float unit, const float* partial,
             const Cut* cuts) {
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
@@ -805,7 +810,7 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float shift, const float* 
   a.o[b * a.os[0] + h * a.os[2] + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(sum * inv));
   if (threadIdx.x == 0 && a.lse)
     a.lse[static_cast<int64_t>(b) * a.H + h] =
-        tot == 0.f ? -INFINITY : (top - shift + log2f(tot)) * 0.69314718055994530942f;
+        tot == 0.f ? -INFINITY : (top + log2f(tot * unit)) * 0.69314718055994530942f;
 }
 
 // Row groups a CTA holds for G query heads per key-value head.
@@ -833,7 +838,7 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorM
   return launch_close(join_kernel<D>,
                       dim3(static_cast<unsigned>(units < S::kRuns ? units : S::kRuns),
                            static_cast<unsigned>(G < S::kRows ? G : S::kRows)),
-                      32 * kJoinWarps, 0, st, a, RT, S::kRows, S::kRuns, kFp8 ? kFp16Shift : 0.f,
+                      32 * kJoinWarps, 0, st, a, RT, S::kRows, S::kRuns, kFp8 ? 0x1p-15f : 1.f,
                       partial, cuts);
 }
 

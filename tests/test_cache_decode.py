@@ -165,6 +165,18 @@ def test_queries_next_to_zero(sa, D):
         c.check(*c.run(sa))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_very_large_logits_stay_finite(sa, fmt):
+    """Logits whose spacing in fp32 is above one: the weights are no better
+    than the logits, but none overflows."""
+    for seed in range(4):
+        for qmag in (1e6, 1e8, 1e12):
+            c = Case([700, 64, 1], 4, 2, 64, fmt, qmag=qmag, seed=seed)
+            o, lse = c.run(sa)
+            assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+            c.check(o, lse)
+
+
 def test_one_far_key_among_many_small_weights(sa):
     """A key far above the others in one page, the mass spread over the rest."""
     c = Case([6000], 4, 1, 128, "fp8", qmag=0.5, seed=8)
