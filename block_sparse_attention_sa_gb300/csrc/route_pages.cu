@@ -15,14 +15,17 @@
 // by histograms of 256 bins. An order statistic moves by no more than the values do, so a page
 // whose score is more than twice the error bound above or below that score is
 // decided; the few in between (usually the last page alone) are computed again
-// in paired fp32 and ranked. Rows with scores that are not finite, and rows with
-// very many undecided pages, are ranked in fp64. Latency bounds it: 10 us for 8
-// rows of 598 pages with both kernels, about half of it this one.
+// in paired fp32 and ranked. Rows with scores that are not finite or so small
+// that fp32 loses their ends, and rows with very many undecided pages, are ranked
+// in fp64. Latency bounds it: 11.6 us for 8 rows of 598 pages with both kernels.
 //
 // Error of a score against fp64, over sum_d |q_d k_d| <= |q|_1 max |k|: 2^-18
 // from the two terms; and D / 16 tensor-core steps for each, which add 16 products
 // and the running sum, each cut to 24 bits of the largest or better: 17 2^-24 a
-// step, below 2^-16.9. Together below 2^-16.3; kErr is 2^-16.
+// step, below 2^-16.9. Together below 2^-16.3; kErr is 2^-16. The second term
+// loses its end where |k| is below 2^-110 or so (bf16 has nothing below 2^-133),
+// so max |k| counts as 2^-100 at least, and |q|_1, unless it is 0, as 2^-40, so
+// that the product is 0 for a row of zeros only.
 #include <cuda_bf16.h>
 
 #include "cache_internal.cuh"
@@ -39,13 +42,18 @@ static_assert((kScoreWarps & (kScoreWarps - 1)) == 0, "heads, a power of two, di
 constexpr int kScoreCtas = 3 * 152;    // three CTAs on each SM
 constexpr int kAhead = 2;              // tiles a warp has in flight
 constexpr float kErr = 1.f / 65536.f;  // 2^-16
+constexpr float kLeastK = 0x1p-100f, kLeastQ = 0x1p-40f;
+// Below these the ends of products are lost in fp32: the error bound of a row,
+// and |q|_1 max |k| of a page that is scored again.
+constexpr float kLeastErr = 0x1p-90f, kLeastSize = 0x1p-60f;
 constexpr int kItems = 8;              // pages a thread of select_kernel holds at once
 constexpr int kSpan = kThreads * kItems;
 constexpr int kNear = 256;             // undecided pages ranked in shared memory
 constexpr unsigned kFull = 0xffffffffu;
 
 // Workspace: per page its score and |q|_1 max |k| (what bounds the score's
-// error; a score that is no number or infinite speaks for itself), and fp64 scores where more than kNear pages are ranked exactly.
+// error; a score that is no number or infinite speaks for itself), and fp64
+// scores where more than kNear pages are ranked exactly.
 struct Layout {
   size_t score, err, exact, total;
 };
@@ -87,9 +95,9 @@ __device__ __forceinline__ void mma(float* c, const uint4& a, uint32_t b0, uint3
                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// 8 query heads from h0 on as B fragments (heads beyond the group zero) and
-// the largest of their sums of magnitudes, in every lane. The 16 dims of a step are taken in
-// the order the key sums' 16-byte loads give: lane quad c holds 4c .. 4c + 3.
+// 8 query heads from h0 on as B fragments (heads beyond the group zero) and the
+// largest of their sums of magnitudes, in every lane. The 16 dims of a step are
+// taken in the order the key sums' 16-byte loads give: lane quad c holds 4c .. 4c + 3.
 template <int D>
 __device__ __forceinline__ float load_heads(const RoutePagesArgs& a, int b, int g, int G, int h0,
                                             int lane, uint2 qb[D / 16]) {
@@ -109,7 +117,7 @@ __device__ __forceinline__ float load_heads(const RoutePagesArgs& a, int b, int 
   n1 = capped(n1 + __shfl_xor_sync(kFull, n1, 2));
 #pragma unroll
   for (int off = 4; off <= 16; off <<= 1) n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, off));
-  return n1;
+  return n1 > 0.f ? fmaxf(n1, kLeastQ) : 0.f;
 }
 
 // A place in the list of items: item `at` of `cnt` of head block `gb` of
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
       for (int h0 = 0; h0 < (kOne ? 1 : G); h0 += 8) {
         if (!kOne) q1 = fmaxf(h0 == 0 ? 0.f : q1, load_heads<D>(a, b, g, G, h0, lane, qb));
         float c[4] = {}, d[4] = {};
-        top[0] = top[1] = 0.f;
+        top[0] = top[1] = kLeastK;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           uint4 hi, lo;
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
     }
     float lo = unorder32(k_lo), hi = unorder32(k_hi);
     const float d = kErr * __uint_as_float(k_d);
-    if (lo > -1e38f && hi < 1e38f && d < 1e30f) {
+    if (lo > -1e38f && hi < 1e38f && d < 1e30f && (k_d == 0u || d > kLeastErr)) {
       // The want-th largest score lies in [lo, hi]. Each pass counts the pages
       // in 256 bins of that range, from the top, and goes on in the bin the
       // count passes `want` in, widened by what its edges may be rounded by.
@@ -583,8 +591,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
       if (n_near <= kNear) {
         by_list = true;
         for (int i = warp; i < n_near; i += kWarps) {
-          const double s = finite ? paired_score<D>(a, b, g, near_j[i], lane)
-                                  : exact_score(a, b, g, near_j[i], lane);
+          const float size = get(err + near_j[i]);
+          double s = finite ? paired_score<D>(a, b, g, near_j[i], lane) : 0.0;
+          if (!finite || (size > 0.f && size < kLeastSize)) s = exact_score(a, b, g, near_j[i], lane);
           if (lane == 0) near_s[i] = s;
         }
         __syncthreads();

@@ -83,6 +83,30 @@ def test_near_ties_of_very_small_and_large_sums(sa, scale):
     c.check(rp, ci, 64, 20)
 
 
+@pytest.mark.parametrize("qmag", [1e-35, 1e-20, 1.0, 1e30])
+@pytest.mark.parametrize("scale", [1e-41, 1e-36, 1e-26])
+def test_near_ties_next_to_the_least_floats(sa, scale, qmag):
+    """Sums, queries and products that fp32 or bf16 hold in part or not at all;
+    a row of 300 pages and one of 40, which are ranked differently."""
+    c = Case([64 * 300, 64 * 40], 8, 2, 64, seed=8, qmag=qmag)
+    gen = torch.Generator().manual_seed(8)
+    c.ksum = c.ksum[:1] * (1 + 2.0 ** -22 * torch.randint(-4, 5, c.ksum.shape, generator=gen)) * scale
+    for budget in (3, 20):
+        rp, ci = c.run(sa, 64, budget)
+        c.check(rp, ci, 64, budget)
+
+
+def test_pages_of_very_unlike_sizes(sa):
+    """Sums between 1e-42 and 1e3 in one row."""
+    for seed, qmag in enumerate((1.0, 1e-10, 1e20)):
+        c = Case([64 * 400], 4, 2, 128, seed=seed, qmag=qmag)
+        gen = torch.Generator().manual_seed(seed)
+        c.ksum = c.ksum * 10.0 ** -(43 * torch.rand((c.n_pages, 1, 1), generator=gen))
+        for budget in (2, 50, 200, 330):
+            rp, ci = c.run(sa, 0, budget)
+            c.check(rp, ci, 0, budget)
+
+
 def test_equal_scores_go_to_the_lower_page(sa):
     c = Case([64 * 500], 4, 2, 64, seed=1)
     c.ksum[:] = c.ksum[0]
