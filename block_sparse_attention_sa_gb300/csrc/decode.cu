@@ -46,7 +46,9 @@ namespace sa {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMaxRuns = 3 * kSms;
+// Runs, of which the workspace holds two partials each, with RG groups of 16 rows.
+constexpr int max_runs(int RG) { return (RG < 4 ? 3 : 2) * kSms; }
+constexpr int kMaxRuns = max_runs(1);
 constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16
 
 // A CTA holds RG groups of 16 rows of query heads. 4 / RG warps divide a page's
@@ -822,6 +824,7 @@ template <int D, bool kFp8, int RG>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t st) {
   using S = Shape<D, kFp8, RG>;
+  static_assert(S::kRuns <= max_runs(RG), "the workspace holds the partials of every run");
   static_assert(S::kWarps * 16 * (D + 8) * 4 <= S::kStages * S::kStage, "the ring holds a unit's sums");
   // with 2 KB for the static arrays and the 1 KB that every CTA costs beside
   static_assert(S::kCtas * (S::kSmem + 3072) <= 228 * 1024, "the ring does not fit shared memory");
@@ -862,7 +865,7 @@ int decode_row_tiles(int H, int Hkv) {
 size_t decode_ws_bytes(int H, int Hkv, int D) {
   // two partials of every run
   const int groups = row_groups(H / Hkv);
-  const size_t rows = static_cast<size_t>(groups < 4 ? kMaxRuns : 2 * kSms) * 16 * groups;
+  const size_t rows = static_cast<size_t>(max_runs(groups)) * 16 * groups;
   return cuts_bytes() + 2 * rows * (D + 2) * sizeof(float);
 }
 
