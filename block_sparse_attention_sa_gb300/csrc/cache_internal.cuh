@@ -129,32 +129,37 @@ __device__ __forceinline__ int run_of(unsigned T, unsigned C, unsigned item) {
 
 struct Run {
   int T, lo, hi;           // items of the list, and this CTA's among them
-  int group, off;          // where a run that is not empty begins: item `off` of a group
+  int group, off;          // where a run that is not empty begins: item `off` of a group,
+  int count, size;         // and what count gave for that group
 };
 
-// The list is that of `groups` groups in order, each count(i) * per_group
-// items (the host has checked that 31 bits hold them all). Every CTA of the grid
+// The list is that of `groups` groups in order, each count(i, size) * per_group
+// items (the host has checked that 31 bits hold them all); `size` is the caller's,
+// given back for the first group, so that nothing is read twice on the way to the
+// first item (a load takes 500 cycles and more here). Every CTA of the grid
 // finds its run of it by a scan of the counts: up to 32 groups by each warp for
 // itself, more by the CTA. All NT threads call it and get the same; it ends with
 // every thread past a barrier.
 template <int NT, class Count>
 __device__ __forceinline__ Run plan_run(int groups, int per_group, Count count) {
-  __shared__ int warp_sum[NT / 32], start_off, start_group;
+  __shared__ int warp_sum[NT / 32], start[4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool few = groups <= 32;
   const int per_thread = few ? 1 : (groups + NT - 1) / NT, first = few ? lane : tid * per_thread;
   const int g0 = min(first, groups), g1 = min(g0 + per_thread, groups);
-  int mine = 0;
-  for (int i = g0; i < g1; ++i) mine += count(i);
+  int mine = 0, size = 0;
+  for (int i = g0; i < g1; ++i) mine += count(i, &size);
   int incl = mine;
+  if (groups > 1) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
   }
   int before = 0, total = 0;
   if (few) {
-    total = __shfl_sync(0xffffffffu, incl, 31);
+    total = __shfl_sync(0xffffffffu, incl, groups - 1);
   } else {
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
@@ -169,33 +174,33 @@ __device__ __forceinline__ Run plan_run(int groups, int per_group, Count count) 
   const unsigned base = static_cast<unsigned>(r.T) / C, rem = r.T - base * C;
   r.lo = base * c + min(c, rem);
   r.hi = r.lo + base + (c < rem ? 1 : 0);
-  r.group = 0;
-  r.off = 0;
   int at = (before + incl - mine) * per_group;
   const bool here = r.lo < r.hi && r.lo >= at && r.lo < at + mine * per_group;
-  if (here) {
-    int i = g0;
-    for (;; ++i) {
-      const int n = count(i) * per_group;
-      if (r.lo < at + n) break;
-      at += n;
-    }
-    r.group = i;
-    r.off = r.lo - at;
+  if (few) {                                 // a lane, a group
+    r.group = max(__ffs(__ballot_sync(0xffffffffu, here)) - 1, 0);
+    r.off = max(r.lo - __shfl_sync(0xffffffffu, at, r.group), 0);
+    r.count = __shfl_sync(0xffffffffu, mine, r.group);
+    r.size = __shfl_sync(0xffffffffu, size, r.group);
+    __syncthreads();
+    return r;
   }
-  if (few) {
-    const int src = max(__ffs(__ballot_sync(0xffffffffu, here)) - 1, 0);
-    r.group = __shfl_sync(0xffffffffu, r.group, src);
-    r.off = __shfl_sync(0xffffffffu, r.off, src);
-  } else if (here) {
-    start_group = r.group;
-    start_off = r.off;
+  if (here) {
+    int i = g0, n;
+    while (r.lo >= at + (n = count(i, &size)) * per_group) {
+      at += n * per_group;
+      ++i;
+    }
+    start[0] = i;
+    start[1] = r.lo - at;
+    start[2] = n;
+    start[3] = size;
   }
   __syncthreads();
-  if (!few && r.lo < r.hi) {
-    r.group = start_group;
-    r.off = start_off;
-  }
+  const bool any = r.lo < r.hi;
+  r.group = any ? start[0] : 0;
+  r.off = any ? start[1] : 0;
+  r.count = any ? start[2] : 0;
+  r.size = any ? start[3] : 0;
   return r;
 }
 #endif

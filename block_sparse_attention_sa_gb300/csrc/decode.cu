@@ -34,8 +34,9 @@
 // TB/s; 24 x 38,247 tokens routed to 96 pages 103 us, 5.9 TB/s. 56 heads of 64
 // on one key-value head, 16 x up to 38,247 tokens: 42 us, 2.3 TB/s, the tensor
 // pipe 47% busy: there 64 rows of products a byte and the latency of each warp's
-// chain bound it. 777 tokens, 32/8 heads: 9.6 us, 2 of them launches, the rest
-// the chain lengths, table, page, product, partial, join.
+// chain bound it. 777 tokens, 32/8 heads: 8.9 us, 3 of them launches, the rest
+// the chain lengths, table, page, product, partial, join, 4.6 us of it in the first
+// kernel: lengths 1 us, table 0.8, page 0.5, its products 1, its partial 0.8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -81,14 +82,20 @@ struct Shape {
   static constexpr int kSmem = kStages * kStage + kJoin + kQueries + 1024;
 };
 
-struct PageMeta {
-  int live;     // tokens of the page that count
-  int flags;    // 1: first page of a unit's piece, 2: last
-  int unit;
-  int dest;     // -1: the whole unit, else which partial of this run
+// A unit: 16 RG query heads (tile rt of those) of one sequence that share a
+// key-value head. dest: -1 if the run holds it whole, else which of the run's
+// partials its piece is.
+struct __align__(16) Unit {
+  int b, g, rt, dest;
 };
 
-// The run's pieces of one unit, for join_kernel: unit, and its first and last run.
+struct __align__(16) PageMeta {
+  Unit unit;
+  int live;     // tokens of the page that count
+  int flags;    // 1: first page of a unit's piece, 2: last
+};
+
+// A unit that is cut, for join_kernel, and its first and last run.
 struct __align__(16) Cut {
   int unit, first, last, pad;
 };
@@ -161,10 +168,12 @@ __device__ __forceinline__ uint32_t next_piece(uint32_t at, int k) {
   return (at ^ ((k % kPairs) << 5)) + k / kPairs * (kBlock * kBox);
 }
 
-// Pages of group `i` of the list: a sequence (every page), or a row of the route.
-__device__ __forceinline__ int group_pages(const DecodeArgs& a, int i, int* status) {
+// Pages of group `i` of the list: a sequence (every page) and its length, or a
+// row of the route and where that begins.
+__device__ __forceinline__ int group_pages(const DecodeArgs& a, int i, int* from, int* status) {
   if (a.row_ptr) {
     const int beg = get(a.row_ptr + i), end = get(a.row_ptr + i + 1);
+    *from = beg;
     if (beg < 0 || end < beg || end > a.col_cap || end - beg > a.pm.max_pages) {
       *status |= SA_DEV_BAD_ROUTE;
       return 0;
@@ -174,7 +183,16 @@ __device__ __forceinline__ int group_pages(const DecodeArgs& a, int i, int* stat
   bool bad;
   const int n = clamp_len(get(a.pm.seq_lens + i), a.pm, &bad);
   if (bad) *status |= SA_DEV_BAD_CACHE;
+  *from = n;
   return (n + kBlock - 1) / kBlock;
+}
+
+// Whether join_kernel finds the units that are cut in a list, by the run that a
+// unit starts in. Where the units are no more than the runs and a warp reads the
+// groups' sizes at once, it works them out by itself (777 tokens: 8.9 us, listed
+// 9.6; 24 x 96 pages, 192 rows: 104.8 us, listed 102.3).
+__host__ __device__ inline bool cuts_listed(const DecodeArgs& a, int RT, int runs) {
+  return a.B * a.Hkv * RT > runs || (a.row_ptr ? a.B * a.Hkv : a.B) > 32;
 }
 
 template <int D, bool kFp8, int RG>
@@ -187,7 +205,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   __shared__ __align__(8) uint64_t full[NS], empty[NS], joined;
   __shared__ PageMeta meta[NS];
   __shared__ float sm_m[W][16], sm_l[W][16];
-  __shared__ int2 sm_unit[W];                // each warp's copy of its unit and dest
+  __shared__ Unit sm_unit[W];                // each warp's copy of its unit
   __shared__ volatile int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,9 +216,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const bool routed = a.row_ptr != nullptr;
   const int n_groups = routed ? a.B * a.Hkv : a.B;
   const int per_group = routed ? RT : a.Hkv * RT;        // units of a group
-  // where join_kernel finds the units that are cut: by unit when they are no
-  // more than the runs, else by the run a unit starts in
-  const bool by_unit = a.B * a.Hkv * RT <= C;
+  const bool listed = cuts_listed(a, RT, C);
   const AbortSignal abort{&abort_flag, nullptr};
   int status = 0;
 
@@ -220,10 +236,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // this CTA's run of the page list
   const Run run = plan_run<NT>(
       n_groups, per_group,
-      [&](int i) { return group_pages(a, i, &status); });
+      [&](int i, int* from) { return group_pages(a, i, from, &status); });
   // groups without a page: nothing to attend
   for (int i = c + C * warp; i < n_groups; i += C * (NT / 32)) {
-    if (group_pages(a, i, &status) != 0) continue;
+    int from;
+    if (group_pages(a, i, &from, &status) != 0) continue;
     const int b = routed ? i / a.Hkv : i;
     const int h0 = routed ? (i % a.Hkv) * G : 0, nh = routed ? G : a.H;
     for (int e = lane; e < nh * (D / 8); e += 32)
@@ -231,42 +248,34 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           make_uint4(0u, 0u, 0u, 0u);
     if (a.lse)
       for (int h = lane; h < nh; h += 32) a.lse[static_cast<int64_t>(b) * a.H + h0 + h] = -INFINITY;
-    if (by_unit)
-      for (int u = lane; u < per_group; u += 32) cuts[i * per_group + u].unit = -1;
   }
 
   if (warp == W) {
     // ---------------------------------------------------------- producer --
     int left = run.hi - run.lo, group = run.group;
     int off = run.off;                          // pages into the group's units
+    int cnt = run.count, from = run.size;       // as group_pages gives them
     int s = 0, in_ring = 0;                     // next stage; stages ever used, up to NS
     uint32_t ph = 0;
     Cut cut{-1, 0, 0, 0};
     bool ok = true;
     while (left > 0 && ok) {
       if (group >= n_groups) break;             // the lengths changed under the call
-      const int cnt = group_pages(a, group, &status);
       if (off >= cnt * per_group) {
-        ++group;
         off = 0;
+        if (++group < n_groups) cnt = group_pages(a, group, &from, &status);
         continue;
       }
-      const int sub = off / cnt, p0 = off - sub * cnt, take = min(left, cnt - p0);
-      const int bg = routed ? group : group * a.Hkv + sub / RT, rt = sub % RT;
-      const int b = routed ? group / a.Hkv : group, g = bg - b * a.Hkv;
-      const int unit = bg * RT + rt;
-      bool bad;
-      const int n = clamp_len(get(a.pm.seq_lens + b), a.pm, &bad);
+      // (divisions, 100 cycles and more each, only where there is something to divide)
+      const int sub = off < cnt ? 0 : off / cnt, p0 = off - sub * cnt, take = min(left, cnt - p0);
+      const int tile = RT == 1 ? sub : sub / RT;
+      const int b = routed ? group / a.Hkv : group, g = routed ? group - b * a.Hkv : tile;
+      const int rt = routed ? sub : sub - tile * RT;
+      bool bad = false;
+      const int n = routed ? clamp_len(get(a.pm.seq_lens + b), a.pm, &bad) : from;
       if (bad) status |= SA_DEV_BAD_CACHE;
       const int nb = (n + kBlock - 1) / kBlock;
-      const int beg = routed ? get(a.row_ptr + group) : 0;
       const int dest = take == cnt ? -1 : (p0 == 0 ? 1 : 0);
-      if (dest == 1) {
-        cut.unit = unit;
-        cut.first = c;
-        cut.last = run_of(run.T, C, run.hi - left + cnt - 1);
-      }
-      if (by_unit && dest != 0 && lane == 0) cuts[unit] = dest == 1 ? cut : Cut{-1, 0, 0, 0};
       for (int q0 = 0; q0 < take && ok; q0 += 32) {
         // 32 pages are looked up at once, then fed one by one
         const int q = q0 + lane;
@@ -274,8 +283,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (q < take) {
           int j = p0 + q;
           if (routed) {
-            const int at = beg + j;
-            const bool there = beg >= 0 && at < a.col_cap;
+            const int at = from + j;
+            const bool there = from >= 0 && at < a.col_cap;
             const int prev = there && j > 0 ? get(a.col_idx + at - 1) : -1;
             j = there ? get(a.col_idx + at) : -1;
             if (j < 0 || j >= nb || j <= prev) {
@@ -301,7 +310,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             break;
           }
           if (lane == 0) {
-            meta[s] = PageMeta{lv, (q0 + x == 0 ? 1 : 0) | (q0 + x == take - 1 ? 2 : 0), unit, dest};
+            meta[s] = PageMeta{Unit{b, g, rt, dest}, lv,
+                               (q0 + x == 0 ? 1 : 0) | (q0 + x == take - 1 ? 2 : 0)};
             const uint32_t bar = smem_u32(&full[s]);
             if (lv > 0) {
               mbar_arrive_expect_tx(bar, S::kStage);
@@ -324,11 +334,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           if (in_ring < NS) ++in_ring;
         }
       }
+      if (dest == 1)
+        cut = Cut{(b * a.Hkv + g) * RT + rt, c, run_of(run.T, C, run.hi - left + cnt - 1), 0};
       off += take;
       left -= take;
     }
     if (lane == 0) {
-      if (!by_unit) cuts[c] = cut;
+      if (listed) cuts[c] = cut;
       if (!ok) {
         abort_flag = 1;
         status |= SA_DEV_TIMEOUT;
@@ -363,9 +375,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     };
     // A unit's queries as A fragments, rows beyond the group's heads zero: kept
     // in shared memory, every warp of a row group writing some of them.
-    auto load_queries = [&](int unit) {
+    auto load_queries = [&](int b, int g, int rt) {
       uint32_t qa[D / 16][4];
-      const int rt = unit % RT, bg = unit / RT, b = bg / a.Hkv, g = bg % a.Hkv;
       const float base = a.scale_log2 * (kFp8 && a.k_scale ? get(a.k_scale + g) : 1.f);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -414,13 +425,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     };
     // those of the first unit need not wait for its first page
     if (n_pages > 0) {
-      const int cnt = group_pages(a, run.group, &status);
-      const int sub = cnt > 0 ? run.off / cnt : 0;
-      load_queries(min((routed ? run.group : run.group * a.Hkv) * RT + sub, a.B * a.Hkv * RT - 1));
+      const int sub = run.off < run.count ? 0 : run.off / run.count;
+      const int b = routed ? run.group / a.Hkv : run.group;
+      load_queries(b, routed ? run.group - b * a.Hkv : sub / RT, routed ? sub : sub % RT);
+      ok = meet();
     }
     int s = 0;
     uint32_t ph = 0;
-    for (int i = 0; i < n_pages; ++i) {
+    for (int i = 0; i < n_pages && ok; ++i) {
       if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort)) {
         ok = false;
         break;
@@ -428,15 +440,18 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const int flags = meta[s].flags, page_live = meta[s].live;
       const bool mine = i % S::kPhases == kw / S::kParts;
       if (flags & 1) {
-        if (lane == 0) sm_unit[warp] = make_int2(meta[s].unit, meta[s].dest);
-        if (i > 0) load_queries(meta[s].unit);
+        const Unit unit = meta[s].unit;
+        if (lane == 0) sm_unit[warp] = unit;
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        if (!meet()) {
-          ok = false;
-          break;
+        if (i > 0) {
+          load_queries(unit.b, unit.g, unit.rt);
+          if (!meet()) {
+            ok = false;
+            break;
+          }
         }
       }
       constexpr int SL = S::kSlices;
@@ -609,8 +624,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
 
       if (flags & 2) {
-        const int2 ud = sm_unit[warp];
-        const int dest = ud.y, rt = ud.x % RT, bg = ud.x / RT, b = bg / a.Hkv, g = bg % a.Hkv;
+        const Unit unit = sm_unit[warp];
+        const int dest = unit.dest, rt = unit.rt, b = unit.b, g = unit.g;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -651,7 +666,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // page, through the ring all at once: no page will be loaded any more
         const bool at_once = i == n_pages - 1;
         float* buf = at_once ? reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))) : join;
-        const int cols = at_once ? D : S::kChunk, pad = cols + 8, quads = cols / 4;
+        const int cols = at_once ? D : S::kChunk, pad = cols + 8;
+        constexpr int kLogD = D == 64 ? 6 : 7;
+        const int quads = at_once ? kLogD - 2 : 3;       // of a row, as a power of two
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += cols) {
           float* row0 = buf + (warp * 16 + r) * pad - c0;
@@ -677,8 +694,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             ok = false;
             break;
           }
-          for (int e = warp * 32 + lane; e < S::kRows * quads; e += 32 * W) {
-            const int row = e / quads, col = e % quads * 4, grp = row >> 4, rr = row & 15;
+          for (int e = warp * 32 + lane; e < S::kRows << quads; e += 32 * W) {
+            const int row = e >> quads, col = (e & ((1 << quads) - 1)) * 4, grp = row >> 4, rr = row & 15;
             const int head = rt * S::kRows + row;
             if (head >= G) continue;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -732,8 +749,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
-// grid (min(units, runs), heads of a unit), 256 threads: adds the partials of one
-// cut unit for one query head, eight warps taking every eighth piece.
+// grid (units, or runs if listed; heads of a unit), 256 threads: adds the partials of one
+// unit that is cut for one query head, eight warps taking every eighth piece.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
@@ -741,16 +758,41 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float unit, const float* p
             const Cut* cuts) {
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
-  wait_for_first();
-  const int4 whole = *reinterpret_cast<const int4*>(cuts + blockIdx.x);   // in one load
-  const Cut cut{whole.x, whole.y, whole.z, 0};
-  const int units = a.B * a.Hkv * RT;
-  if (cut.unit < 0 || cut.unit >= units || cut.first < 0 || cut.last <= cut.first || cut.last >= runs)
-    return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, units = a.B * a.Hkv * RT;
+  // Every CTA passes the wait, whatever it has to do: were this grid to end ahead
+  // of the first, the call's outputs would be taken for finished.
+  Cut cut{static_cast<int>(blockIdx.x), 0, -1, 0};
+  if (cuts_listed(a, RT, runs)) {
+    wait_for_first();
+    const int4 whole = *reinterpret_cast<const int4*>(cuts + blockIdx.x);   // in one load
+    cut = Cut{whole.x, whole.y, whole.z, 0};
+    if (cut.unit < 0 || cut.unit >= units) return;
+  } else {
+    // a unit's place in the list of pages follows from the lengths, which are
+    // there before the first kernel is done
+    const bool routed = a.row_ptr != nullptr;
+    const int n_groups = routed ? a.B * a.Hkv : a.B, per_group = units / n_groups;
+    const int group = cut.unit / per_group;
+    int status = 0, before = 0, total = 0, cnt = 0;
+    if (lane < n_groups) {
+      int from;
+      total = group_pages(a, lane, &from, &status);
+      if (lane < group) before = total;
+      if (lane == group) cnt = total;
+    }
+    total = __reduce_add_sync(0xffffffffu, total) * per_group;
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    before = __reduce_add_sync(0xffffffffu, before) * per_group + (cut.unit - group * per_group) * cnt;
+    if (cnt > 0) {
+      cut.first = run_of(total, runs, before);
+      cut.last = run_of(total, runs, before + cnt - 1);
+    }
+    wait_for_first();
+  }
+  if (cut.first < 0 || cut.last <= cut.first || cut.last >= runs) return;
   const int G = a.H / a.Hkv, rt = cut.unit % RT, bg = cut.unit / RT;
   const int b = bg / a.Hkv, g = bg % a.Hkv, row = blockIdx.y, head = rt * rows + row;
   if (head >= G) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int V = D / 32;
   const int64_t stride = static_cast<int64_t>(rows) * (D + 2);
   // the first piece is the second partial of its run (the run ends in it), the
@@ -839,7 +881,7 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorM
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_close(join_kernel<D>,
-                      dim3(static_cast<unsigned>(units < S::kRuns ? units : S::kRuns),
+                      dim3(static_cast<unsigned>(cuts_listed(a, RT, S::kRuns) ? S::kRuns : units),
                            static_cast<unsigned>(G < S::kRows ? G : S::kRows)),
                       32 * kJoinWarps, 0, st, a, RT, S::kRows, S::kRuns, kFp8 ? 0x1p-15f : 1.f,
                       partial, cuts);

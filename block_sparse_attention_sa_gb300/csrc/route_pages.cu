@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
     return (n + kBlock - 1) / kBlock;
   };
   const Run run = plan_run<32 * kScoreWarps>(
-      a.B, blocks, [&](int b) { return (pages(b) + wide - 1) / wide; });
+      a.B, blocks, [&](int b, int* nb) { return ((*nb = pages(b)) + wide - 1) / wide; });
   const int n_items = run.hi - run.lo;
   if (n_items > 0) {
     auto enter = [&](Cursor& c) {            // what follows from c.b
@@ -179,9 +179,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(RoutePagesAr
         enter(c);
       } while (c.cnt == 0 && c.b < a.B);
     };
-    Cursor now{run.group, 0, 0, 0, 0};
-    enter(now);
-    if (now.cnt > 0) {
+    Cursor now{run.group, 0, run.off, run.count, run.size};
+    if (now.at >= now.cnt) {
       now.gb = run.off / now.cnt;
       now.at = run.off - now.gb * now.cnt;
     }
