@@ -12,12 +12,12 @@
 // DRAM rate, issue slots 42% busy with the splitting; 38 us with select_kernel.
 //
 // select_kernel, one CTA per row, narrows down the score that the budget ends at
-// by histograms of 256 bins. An order statistic moves by no more than the values do, so a page
-// whose score is more than twice the error bound above or below that score is
-// decided; the few in between (usually the last page alone) are computed again
-// in paired fp32 and ranked. Rows with scores that are not finite or so small
-// that fp32 loses their ends, and rows with very many undecided pages, are ranked
-// in fp64. Latency bounds it: 11.6 us for 8 rows of 598 pages with both kernels.
+// by histograms of 256 bins until a few dozen pages are left, and ranks those. An
+// order statistic moves by no more than the values do, so a page whose score is
+// more than twice the error bound above or below that score is decided; the few
+// in between (usually the last page alone) are computed again in paired fp32.
+// Rows with scores that are not finite or so small that fp32 loses their ends,
+// and rows with very many undecided pages, are ranked in fp64. Latency bounds it: 11 us for 8 rows of 598 pages with both kernels.
 //
 // Error of a score against fp64, over sum_d |q_d k_d| <= |q|_1 max |k|: 2^-18
 // from the two terms; and D / 16 tensor-core steps for each, which add 16 products
@@ -48,7 +48,8 @@ constexpr float kLeastK = 0x1p-100f, kLeastQ = 0x1p-40f;
 constexpr float kLeastErr = 0x1p-90f, kLeastSize = 0x1p-60f;
 constexpr int kItems = 8;              // pages a thread of select_kernel holds at once
 constexpr int kSpan = kThreads * kItems;
-constexpr int kNear = 256;             // undecided pages ranked in shared memory
+constexpr int kNear = kThreads;        // undecided pages ranked in shared memory
+constexpr int kFew = 48;               // pages that are ranked rather than counted once more
 constexpr unsigned kFull = 0xffffffffu;
 
 // Workspace: per page its score and |q|_1 max |k| (what bounds the score's
@@ -418,16 +419,18 @@ __device__ __forceinline__ uint64_t order64(double x) {
 
 constexpr int kBins = 256, kPasses = 4;
 
-// grid (B * Hkv): one row.
+// grid (B * Hkv): one row. Three CTAs an SM: with the 128 registers that the
+// compiler takes for two, 12.3 us for 11 (8 rows of 598 pages).
 template <int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
   __shared__ int sums[2 * kWarps];
   __shared__ uint4 ext[kWarps];
   __shared__ __align__(16) int hist[kPasses][kBins];
-  __shared__ int near_j[kNear];
-  __shared__ double near_s[kNear];
-  __shared__ int near_n;
-  __shared__ int warp_n[2][kWarps];
+  __shared__ int near_j[kNear], open_at[kNear], near_n, open_n;
+  __shared__ float near_v[kNear];
+  __shared__ double open_s[kNear];
+  __shared__ unsigned chosen[kSpan / 32];    // of a span's undecided pages, by bit
+  __shared__ int warp_n[2][kWarps], list_n[2][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
   const int row = blockIdx.x, b = row / a.Hkv, g = row % a.Hkv;
@@ -439,7 +442,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
     row_counts(clamp_len(get(a.pm.seq_lens + i), a.pm, &bad), a.prefix, a.budget, &nb, &sink, &keep);
     before += keep;
   }
-  if (tid == 0) near_n = 0;
+  if (tid == 0) near_n = open_n = 0;
+  if (tid < kSpan / 32) chosen[tid] = 0u;
   for (int i = tid; i < kPasses * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   before = block_sum(before, sums, turn++);
   row_counts(clamp_len(get(a.pm.seq_lens + b), a.pm, &bad), a.prefix, a.budget, &nb, &sink, &keep);
@@ -512,7 +516,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
       // The want-th largest score lies in [lo, hi]. Each pass counts the pages
       // in 256 bins of that range, from the top, and goes on in the bin the
       // count passes `want` in, widened by what its edges may be rounded by.
-      for (int pass = 0; pass < kPasses && hi - lo > d; ++pass) {
+      int in_bin = f1 - f0;
+      for (int pass = 0; pass < kPasses && in_bin > kFew && hi - lo > d; ++pass) {
         const float scale = kBins / (hi - lo), width = (hi - lo) / kBins;
         for (int span = f0; span < f1; span += kSpan) {
           if (!held) load(span);
@@ -539,12 +544,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
         int bin = 8 * lane, n = upto - total;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          if (n < want) in_bin = h[i];
           n += h[i];
           bin += n < want;
         }
         // the first lane whose bins reach `want` holds the bin
         const unsigned reached = __ballot_sync(kFull, upto >= want);
         bin = kBins - 1 - __shfl_sync(kFull, bin, __ffs(reached) - 1);
+        in_bin = __shfl_sync(kFull, in_bin, __ffs(reached) - 1);
         const float slack = 0.01f * width + 0x1p-22f * fmaxf(fabsf(lo), fabsf(hi));
         const float new_lo = lo + bin * width - slack, new_hi = lo + (bin + 1) * width + slack;
         if (bin > 0) lo = fmaxf(lo, new_lo);
@@ -567,7 +574,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
         if (!yes && v[i] >= below) {
           ++n_near;
           const int at = atomicAdd(&near_n, 1);
-          if (at < kNear) near_j[at] = j;
+          if (at < kNear) {
+            near_j[at] = j;
+            near_v[at] = v[i];
+          }
         }
       }
     }
@@ -588,24 +598,47 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
     if (need < n_near) {
       const bool finite = below > -INFINITY;
       if (n_near <= kNear) {
+        // A page is in if fewer than `need` others may score as much, out if
+        // `need` do score more; what is left open is decided by exact scores.
         by_list = true;
-        for (int i = warp; i < n_near; i += kWarps) {
-          const float size = get(err + near_j[i]);
-          double s = finite ? paired_score<D>(a, b, g, near_j[i], lane) : 0.0;
-          if (!finite || (size > 0.f && size < kLeastSize)) s = exact_score(a, b, g, near_j[i], lane);
-          if (lane == 0) near_s[i] = s;
+        const int j = tid < n_near ? near_j[tid] : -1;
+        bool yes = false, open = j >= 0;
+        int slot = 0;
+        if (finite && open) {
+          const float mine_v = near_v[tid];
+          int more = 0, reach = 0;
+          for (int i = 0; i < n_near; ++i) {
+            more += near_v[i] > mine_v + 2.f * d;
+            reach += near_v[i] >= mine_v - 2.f * d;
+          }
+          yes = reach <= need;
+          open = !yes && more < need;
         }
-        __syncthreads();
-        // a thread ranks one page; the pages that are out leave the list
-        bool out = false;
-        if (tid < n_near) {
-          int rank = 0;
-          for (int i = 0; i < n_near; ++i)
-            rank += near_s[i] > near_s[tid] || (near_s[i] == near_s[tid] && near_j[i] < near_j[tid]);
-          out = rank >= need;
+        if (open) {
+          slot = atomicAdd(&open_n, 1);
+          open_at[slot] = j;
         }
-        __syncthreads();
-        if (out) near_j[tid] = -1;
+        const int rest = need - block_sum(yes, sums, turn++), n_open = open_n;
+        if (rest > 0 && rest < n_open) {
+          for (int i = warp; i < n_open; i += kWarps) {
+            const int page = open_at[i];
+            const float size = get(err + page);
+            double s = finite ? paired_score<D>(a, b, g, page, lane) : 0.0;
+            if (!finite || (size > 0.f && size < kLeastSize)) s = exact_score(a, b, g, page, lane);
+            if (lane == 0) open_s[i] = s;
+          }
+          __syncthreads();
+          if (open) {
+            int rank = 0;
+            for (int i = 0; i < n_open; ++i)
+              rank += open_s[i] > open_s[slot] || (open_s[i] == open_s[slot] && open_at[i] < j);
+            yes = rank < rest;
+          }
+        } else {
+          yes |= open && rest > 0;
+        }
+        if (yes && j - f0 < kSpan) atomicOr(&chosen[(j - f0) >> 5], 1u << ((j - f0) & 31));
+        if (!yes) near_j[tid] = -1;
         __syncthreads();
       } else {
         by_exact = true;
@@ -644,29 +677,30 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
     if (start + j < a.col_cap) a.col_idx[start + j] = j;
   if (tid == 0 && f0 < nb && start + keep - 1 < a.col_cap) a.col_idx[start + keep - 1] = nb - 1;
   int at = start + f0, tied = 0;
-  if (want > 0) {
-    for (int span = f0; span < f1; span += kSpan) {
-      if (!held) load(span);
-      unsigned take[kItems], equal[kItems];
-      int n_take = 0, n_equal = 0;
+  for (int span = f0, turns = 0; want > 0 && span < f1; span += kSpan, ++turns) {
+    if (!held) load(span);
+    unsigned take[kItems];
+    int n_take = 0;
+    if (!by_exact) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const bool t = all || v[i] > above || (!by_list && v[i] >= below);
+        take[i] = __ballot_sync(kFull, t && span + mine + 32 * i < f1);
+        if (by_list) take[i] |= chosen[warp * kItems + i];
+        n_take += __popc(take[i]);
+      }
+    } else {
+      // of the undecided ones those above the edge, and the first `ties` at it
+      unsigned equal[kItems];
+      int n_equal = 0;
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
         const int j = span + mine + 32 * i;
-        bool t = false, q = false;
-        if (j < f1) {
-          if (all || v[i] > above) {
-            t = true;
-          } else if (v[i] >= below) {
-            if (by_list) {
-              for (int x = 0; x < near_n; ++x) t |= near_j[x] == j;
-            } else if (by_exact) {
-              const uint64_t e = order64(exact[j]);
-              t = e > edge;
-              q = e == edge;
-            } else {
-              t = true;
-            }
-          }
+        bool t = j < f1 && v[i] > above, q = false;
+        if (j < f1 && !t && v[i] >= below) {
+          const uint64_t e = order64(exact[j]);
+          t = e > edge;
+          q = e == edge;
         }
         take[i] = __ballot_sync(kFull, t);
         equal[i] = __ballot_sync(kFull, q);
@@ -674,42 +708,47 @@ __global__ void __launch_bounds__(kThreads) select_kernel(RoutePagesArgs a) {
         n_equal += __popc(equal[i]);
       }
       __syncthreads();                       // warp_n has been read
-      if (by_exact) {
-        // of the equal ones the first `ties` are in
-        if (lane == 0) warp_n[0][warp] = n_equal;
-        __syncthreads();
-        int rank = tied, total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) rank += warp_n[0][w];
-          total += warp_n[0][w];
-        }
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-          const bool q = (equal[i] >> lane) & 1u;
-          const bool t = q && rank + __popc(equal[i] & ((1u << lane) - 1u)) < ties;
-          const unsigned more = __ballot_sync(kFull, t);
-          take[i] |= more;
-          n_take += __popc(more);
-          rank += __popc(equal[i]);
-        }
-        tied += total;
-      }
-      if (lane == 0) warp_n[1][warp] = n_take;
+      if (lane == 0) warp_n[0][warp] = n_equal;
       __syncthreads();
-      int to = at, total = 0;
+      int rank = tied, total = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) to += warp_n[1][w];
-        total += warp_n[1][w];
+        if (w < warp) rank += warp_n[0][w];
+        total += warp_n[0][w];
       }
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
-        const int p = to + __popc(take[i] & ((1u << lane) - 1u));
-        if (((take[i] >> lane) & 1u) && p < a.col_cap) a.col_idx[p] = span + mine + 32 * i;
-        to += __popc(take[i]);
+        const bool q = (equal[i] >> lane) & 1u;
+        const bool t = q && rank + __popc(equal[i] & ((1u << lane) - 1u)) < ties;
+        const unsigned more = __ballot_sync(kFull, t);
+        take[i] |= more;
+        n_take += __popc(more);
+        rank += __popc(equal[i]);
       }
-      at += total;
+      tied += total;
+    }
+    int* count = list_n[turns & 1];          // read for the last time two barriers ago
+    if (lane == 0) count[warp] = n_take;
+    __syncthreads();
+    int to = at, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) to += count[w];
+      total += count[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int p = to + __popc(take[i] & ((1u << lane) - 1u));
+      if (((take[i] >> lane) & 1u) && p < a.col_cap) a.col_idx[p] = span + mine + 32 * i;
+      to += __popc(take[i]);
+    }
+    at += total;
+    if (by_list && span + kSpan < f1) {      // the next span's
+      if (tid < kSpan / 32) chosen[tid] = 0u;
+      __syncthreads();
+      const int j = tid < near_n ? near_j[tid] - (span + kSpan) : -1;
+      if (j >= 0 && j < kSpan) atomicOr(&chosen[j >> 5], 1u << (j & 31));
+      __syncthreads();
     }
   }
   if (status && a.dev_status) atomicOr(a.dev_status, status);
