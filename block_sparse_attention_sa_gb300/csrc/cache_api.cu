@@ -277,6 +277,7 @@ sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_
   if ((s = check_tokens(p, o, p->o_stride, p->H)) != SA_OK) return s;
   if (!aligned(workspace, 256)) return SA_ERR_INVALID_ARG;
   if (ws_bytes < sa_attn_decode_workspace_bytes(p)) return SA_ERR_CAPACITY;
+  if (o == q) return SA_ERR_INVALID_ARG;       // read by CTAs that others' outputs would meet
   DecodeArgs a{};
   a.pm = page_map(p, page_table, seq_lens);
   a.q = static_cast<const uint16_t*>(q);

@@ -476,8 +476,9 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  *   (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c), c = rope_cos[t][i],
  *       s = rope_sin[t][i], (a, b) the i-th pair of rope_layout
  * in fp32, rounded once: q to bf16 into q_out, k to bf16 into k_cache, or with
- * SA_CACHE_FP8 to the nearest e4m3 code of y / k_scale[h] (ties to even,
- * |code| at most 448, NaN stays NaN). v goes into v_cache as it is (/ v_scale).
+ * SA_CACHE_FP8 to the nearest e4m3 code of y times 1 / k_scale[h] (ties to even,
+ * |code| at most 448, NaN stays NaN). v goes into v_cache as it is, or times
+ * 1 / v_scale[h].
  * k_sum of the page (where given) gains y before it is rounded; a page's first
  * slot starts its sum anew.
  * Tokens that find no place (t >= 64 max_pages, or t >= rope_rows where tables
@@ -491,8 +492,8 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * gamma_k      NULL without qk_norm).
  * rope_cos,    device fp32 [rope_rows][D/2], 16-byte aligned; both NULL for
  * rope_sin     no rotation.
- * k_scale,     device fp32 [H_kv], > 0, or NULL for ones (and NULL with
- * v_scale      SA_CACHE_BF16).
+ * k_scale,     device fp32 [H_kv], > 0 with a finite reciprocal, or NULL for ones
+ * v_scale      (and NULL with SA_CACHE_BF16).
  * seq_lens     the lengths before the call; not modified.
  * new_lens     device int32 [B] in [0, S] (clamped into it), or NULL.
  * lens_out     device int32 [B], or NULL: seq_lens[b] + n_b, at most
@@ -572,7 +573,7 @@ size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p);
  *            its row is left out. col_cap: the entries col_idx holds.
  * k_scale,   as sa_cache_append.
  * v_scale
- * o          device bf16 [B, 1, H, D] (o_stride).
+ * o          device bf16 [B, 1, H, D] (o_stride); no overlap with q.
  * lse        device fp32 [B, H, 1] (natural log), or NULL.
  * workspace  device scratch of sa_attn_decode_workspace_bytes(p) bytes,
  *            256-byte aligned; its contents on entry do not matter.

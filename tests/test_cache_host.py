@@ -141,6 +141,12 @@ def test_route_and_decode_refusals(sa):
     assert sa.load_library().sa_dev_status_decode(sa.SA_DEV_BAD_CACHE) == INVALID
 
 
+def test_decode_does_not_write_over_its_queries(sa):
+    p = params(sa)
+    need = sa.load_library().sa_attn_decode_workspace_bytes(ctypes.byref(p))
+    assert decode(sa, p, q=A, o=A, n=need) == INVALID
+
+
 def test_the_binding_refuses_host_tensors(sa):
     z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
     i = torch.zeros((1, 2), dtype=torch.int32)
