@@ -30,13 +30,14 @@
 // down to 2^-29 of the largest keep all their bits.
 //
 // Measured on GB300 (copy rate 6.79 TB/s), 56/8 heads of 128: 64 sequences of up
-// to 8,192 tokens 212 us, 6.34 TB/s; 3 x 112,640 tokens in e4m3 112 us, 6.16
+// to 8,192 tokens 213 us, 6.31 TB/s; 3 x 112,640 tokens in e4m3 112 us, 6.16
 // TB/s; 24 x 38,247 tokens routed to 96 pages 103 us, 5.9 TB/s. 56 heads of 64
-// on one key-value head, 16 x up to 38,247 tokens: 42 us, 2.3 TB/s, the tensor
-// pipe 47% busy: there 64 rows of products a byte and the latency of each warp's
-// chain bound it. 777 tokens, 32/8 heads: 8.9 us, 3 of them launches, the rest
-// the chain lengths, table, page, product, partial, join, 4.6 us of it in the first
-// kernel: lengths 1 us, table 0.8, page 0.5, its products 1, its partial 0.8.
+// on one key-value head, 16 x up to 38,247 tokens: 43 us, 2.3 TB/s:
+// there 64 rows of products a byte, P twice, bind it to the rate of mma.sync, 1.4 us
+// a page of two CTAs an SM, beside 10 us of start and end. 777 tokens, 32/8 heads:
+// 8.9 us, 3 of them launches, the rest the chain lengths, table, page, product,
+// partial, join; of the first kernel's 4.6 us the page takes 0.5, its products 1,
+// its partial 0.9, the way to the page the rest.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -54,7 +55,8 @@ constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16
 
 // A CTA holds RG groups of 16 rows of query heads. 4 / RG warps divide a page's
 // keys for each group, so a CTA has four consumer warps: with eight and one CTA
-// an SM, 56 heads on one key-value head took 48.5 us instead of 43.8.
+// an SM, 56 heads on one key-value head took 48.5 us instead of 43.8 (and two CTAs of eight
+// 47.3 instead of 43.1).
 template <int D, bool kFp8, int RG>
 struct Shape {
   static constexpr int kRows = 16 * RG;
