@@ -194,7 +194,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
   const bool early = kShare == 1 && a.S == 1 && there;
   if (early) {
     kw[0] = load8<D, kHalf>(k, l);
-    vw[0] = load8<D, kHalf>(v, l);
+    vw[0] = load8<D, false>(v, l);
   }
   float gk[8];
 #pragma unroll
@@ -240,7 +240,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
       if (u >= left) continue;
       if (!early) {
         kw[u] = load8<D, kHalf>(k, l);
-        vw[u] = load8<D, kHalf>(v, l);
+        vw[u] = load8<D, false>(v, l);
       }
       g[u] = angle_at<D>(a, t + u * kShare, l);
       k += k_step;
@@ -257,10 +257,10 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
       if (*page < 0) continue;
       if (kFp8) {
         store8_e4m3<D, kHalf>(reinterpret_cast<uint8_t*>(kc), l, pack_e4m3(y, ik));
-        store8_e4m3<D, kHalf>(reinterpret_cast<uint8_t*>(vc), l, pack_e4m3(unpack(vw[u]), iv));
+        store8_e4m3<D, false>(reinterpret_cast<uint8_t*>(vc), l, pack_e4m3(unpack(vw[u]), iv));
       } else {
         store8<D, kHalf>(reinterpret_cast<uint16_t*>(kc), l, pack(y));
-        store8<D, kHalf>(reinterpret_cast<uint16_t*>(vc), l, vw[u]);
+        store8<D, false>(reinterpret_cast<uint16_t*>(vc), l, vw[u]);
       }
       kc += kc_step;
       vc += vc_step;

@@ -871,7 +871,7 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorM
   static_assert(S::kRuns <= max_runs(RG), "the workspace holds the partials of every run");
   static_assert(S::kWarps * 16 * (D + 8) * 4 <= S::kStages * S::kStage, "the ring holds a unit's sums");
   // with 2 KB for the static arrays and the 1 KB that every CTA costs beside
-  static_assert(S::kCtas * (S::kSmem + 3072) <= 228 * 1024, "the ring does not fit shared memory");
+  static_assert(S::kCtas * (S::kSmem + 3 * 1024) <= 228 * 1024, "the ring does not fit shared memory");
   const int G = a.H / a.Hkv, RT = (G + S::kRows - 1) / S::kRows;
   Cut* cuts = reinterpret_cast<Cut*>(a.ws);
   float* partial = reinterpret_cast<float*>(a.ws + cuts_bytes());
