@@ -107,6 +107,19 @@ def test_pages_of_very_unlike_sizes(sa):
             c.check(rp, ci, 0, budget)
 
 
+@pytest.mark.parametrize("n_pages", [40, 250, 2100])
+def test_clusters_of_near_ties(sa, n_pages):
+    """Scores that differ from one part in 16 to the last bits: some pages are
+    decided by the error bound, some by the ranks within it, some exactly."""
+    c = Case([64 * n_pages, 64 * 70], 12, 2, 128, seed=n_pages)
+    gen = torch.Generator().manual_seed(n_pages)
+    step = 2.0 ** -torch.randint(4, 24, (c.n_pages, 1, 1), generator=gen)
+    c.ksum = c.ksum[:1] * (1 + step * torch.randint(-2, 3, (c.n_pages, 1, 1), generator=gen))
+    for budget in (2, 9, 20, 33, 60, n_pages // 2, n_pages - 3):
+        rp, ci = c.run(sa, 64, budget)
+        c.check(rp, ci, 64, budget)
+
+
 def test_equal_scores_go_to_the_lower_page(sa):
     c = Case([64 * 500], 4, 2, 64, seed=1)
     c.ksum[:] = c.ksum[0]
