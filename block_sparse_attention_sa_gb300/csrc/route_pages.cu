@@ -462,7 +462,9 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
   double* exact = reinterpret_cast<double*>(a.ws + L.exact) + row_at;
   const int f0 = min(sink, nb), f1 = max(f0, nb - 1);      // the pages that compete
   const int want = keep - (sink < nb ? sink + 1 : nb);
-  const bool all = want >= f1 - f0, held = f1 - f0 <= kSpan;
+  const bool held = f1 - f0 <= kSpan;
+  bool all = want >= f1 - f0;                // the competing pages below `last` are in
+  int last = f1;
   // thread's pages of a span: span + 256 warp + 32 i + lane, so that a warp's
   // ballots are in the order of the pages; one span is read once and held
   const int mine = warp * 32 * kItems + lane;
@@ -559,6 +561,11 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
       }
       above = hi + 2.f * d;
       below = lo - 2.f * d;
+      if (k_d == 0u) {                       // queries of zeros, as a padded row has them
+        above = below = INFINITY;
+        all = true;
+        last = f0 + want;
+      }
     } else {
       below = -INFINITY;                     // none is decided
     }
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
     if (start + j < a.col_cap) a.col_idx[start + j] = j;
   if (tid == 0 && f0 < nb && start + keep - 1 < a.col_cap) a.col_idx[start + keep - 1] = nb - 1;
   int at = start + f0, tied = 0;
-  for (int span = f0, turns = 0; want > 0 && span < f1; span += kSpan, ++turns) {
+  for (int span = f0, turns = 0; want > 0 && span < last; span += kSpan, ++turns) {
     if (!held) load(span);
     unsigned take[kItems];
     int n_take = 0;
@@ -685,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
         const bool t = all || v[i] > above || (!by_list && v[i] >= below);
-        take[i] = __ballot_sync(kFull, t && span + mine + 32 * i < f1);
+        take[i] = __ballot_sync(kFull, t && span + mine + 32 * i < last);
         if (by_list) take[i] |= chosen[warp * kItems + i];
         n_take += __popc(take[i]);
       }

@@ -120,6 +120,19 @@ def test_clusters_of_near_ties(sa, n_pages):
         c.check(rp, ci, 64, budget)
 
 
+@pytest.mark.parametrize("n_pages", [30, 700, 5000])
+def test_rows_of_zeros_keep_the_first_pages(sa, n_pages):
+    c = Case([64 * n_pages, 64 * 90], 4, 2, 64, seed=9)
+    c.q[0] = 0.0
+    c.q[1, :, 2:] = -0.0
+    for budget in (1, 2, 17, n_pages - 2):
+        rp, ci = c.run(sa, 65, budget)
+        c.check(rp, ci, 65, budget)
+    c.table[0, 3] = -1                                 # one page that is not there
+    rp, ci = c.run(sa, 65, 17)
+    c.check(rp, ci, 65, 17)
+
+
 def test_equal_scores_go_to_the_lower_page(sa):
     c = Case([64 * 500], 4, 2, 64, seed=1)
     c.ksum[:] = c.ksum[0]
