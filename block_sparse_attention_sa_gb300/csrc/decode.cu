@@ -24,17 +24,23 @@
 //   join_kernel adds in the order of the runs: no atomics, the same bits every
 //   time. join_kernel is launched while the first kernel runs and waits for it.
 //
-// P is taken as two bf16 terms, p = hi + lo (16 bits), so that P V carries no
-// rounding of its own beside the final one to bf16; with an e4m3 cache one fp16
-// term is enough (11 bits against the values' 4), scaled by 2^15 so that weights
-// down to 2^-29 of the largest keep all their bits.
+// P keeps what fp32 has of it, but for the last two or three bits, as a sum of
+// terms that an operand holds: three of bf16, 8 bits each, or with an e4m3 cache
+// two of fp16, 11 bits each, scaled by 2^15 so that what is lost of a weight below
+// 2^-18 of the largest is 2^-40 of that. (As two terms and one, an output in a
+// thousand and in a hundred fell on the other side of its rounding to bf16 than
+// with weights in fp32; now no more than between two orders of fp32 sums.) Where at
+// most eight query heads share a key-value head the rows r + 8 of a tile are free
+// and hold the terms that rows r leave: e4m3, 3 x 112,640 tokens of 56/8 heads, 111
+// us so, 121.6 us with a product for each term (one term: 112); 64 x up to 8,192 in
+// bf16, 213 us either way. More heads pay for a product a term: 56/1 of 64 in bf16
+// 49 us (two terms: 43), 56/1 of 128 in e4m3 69 us (one: 58).
 //
 // Measured on GB300 (copy rate 6.79 TB/s), 56/8 heads of 128: 64 sequences of up
-// to 8,192 tokens 213 us, 6.31 TB/s; 3 x 112,640 tokens in e4m3 112 us, 6.16
+// to 8,192 tokens 213 us, 6.31 TB/s; 3 x 112,640 tokens in e4m3 111 us, 6.2
 // TB/s; 24 x 38,247 tokens routed to 96 pages 103 us, 5.9 TB/s. 56 heads of 64
-// on one key-value head, 16 x up to 38,247 tokens: 43 us, 2.3 TB/s:
-// there 64 rows of products a byte, P twice, bind it to the rate of mma.sync, 1.4 us
-// a page of two CTAs an SM, beside 10 us of start and end. 777 tokens, 32/8 heads:
+// on one key-value head, 16 x up to 38,247 tokens: 49 us, 2.0 TB/s: 64 rows of
+// products a byte, P three times. 777 tokens, 32/8 heads:
 // 8.9 us, 3 of them launches, the rest the chain lengths, table, page, product,
 // partial, join; of the first kernel's 4.6 us the page takes 0.5, its products 1,
 // its partial 0.9, the way to the page the rest.
@@ -51,15 +57,18 @@ constexpr int kSms = 152;
 // Runs, of which the workspace holds two partials each, with RG groups of 16 rows.
 constexpr int max_runs(int RG) { return (RG < 4 ? 3 : 2) * kSms; }
 constexpr int kMaxRuns = max_runs(1);
-constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16
+constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16 terms
 
-// A CTA holds RG groups of 16 rows of query heads. 4 / RG warps divide a page's
+// A CTA holds RG groups of 16 rows of query heads (kTwin: 8, each in two rows of a tile). 4 / RG warps divide a page's
 // keys for each group, so a CTA has four consumer warps: with eight and one CTA
 // an SM, 56 heads on one key-value head took 48.5 us instead of 43.8 (and two CTAs of eight
 // 47.3 instead of 43.1).
-template <int D, bool kFp8, int RG>
+template <int D, bool kFp8, int RG, bool kTwin>
 struct Shape {
   static constexpr int kRows = 16 * RG;
+  static constexpr int kX = kTwin ? 1 : 2;  // rows of a lane, r and r + 8, that are heads
+  // products with a page's values for one of P: its terms, two in one where rows are free
+  static constexpr int kTerms = kTwin ? (kFp8 ? 1 : 2) : (kFp8 ? 2 : 3);
   static constexpr int kKeyWarps = 4 / RG;
   static constexpr int kWarps = kKeyWarps * RG;         // consumer warps
   static constexpr int kSlices = RG == 4 ? 4 : 2;   // 16-key slices a warp takes at once (one at
@@ -151,8 +160,33 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The upper 16 bits of two floats: the values cut to bf16.
+__device__ __forceinline__ uint32_t top_bf16(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
 __device__ __forceinline__ float lo_f32(uint32_t bf2) { return __uint_as_float(bf2 << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t bf2) { return __uint_as_float(bf2 & 0xffff0000u); }
+
+// Two weights as sums of terms that an A fragment holds: three of bf16 (2^-22 of the
+// weight is lost), the last times `third`, or two of fp16 (2^-22, and below 2^-14 the last
+// 2^-25). bf16 terms are cut, not rounded, and 2^-24 of the weight is added twice to what
+// is left, so that all are positive: an infinite value stays one (e4m3 has none).
+template <bool kFp8>
+__device__ __forceinline__ void split(float p0, float p1, float third, uint32_t* t) {
+  if (kFp8) {
+    t[0] = pack_half(p0, p1);
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&t[0]));
+    t[1] = pack_half(p0 - h.x, p1 - h.y);
+  } else {
+    t[0] = top_bf16(p0, p1);
+    const float r0 = fmaf(p0, 0x1p-24f, p0 - lo_f32(t[0]));
+    const float r1 = fmaf(p1, 0x1p-24f, p1 - hi_f32(t[0]));
+    t[1] = top_bf16(r0, r1);
+    t[2] = pack_bf16(third * fmaf(p0, 0x1p-24f, r0 - lo_f32(t[1])),
+                     third * fmaf(p1, 0x1p-24f, r1 - hi_f32(t[1])));
+  }
+}
 
 // A page as TMA lays it out: boxes of at most 128 bytes a token, their 16-byte
 // pieces XORed with the row (rows 0 .. 7, or every second one in 64-byte boxes).
@@ -197,11 +231,12 @@ __host__ __device__ inline bool cuts_listed(const DecodeArgs& a, int RT, int run
   return a.B * a.Hkv * RT > runs || (a.row_ptr ? a.B * a.Hkv : a.B) > 32;
 }
 
-template <int D, bool kFp8, int RG>
-__global__ void __launch_bounds__(Shape<D, kFp8, RG>::kThreads, Shape<D, kFp8, RG>::kCtas)
+template <int D, bool kFp8, int RG, bool kTwin>
+__global__ void __launch_bounds__(Shape<D, kFp8, RG, kTwin>::kThreads, Shape<D, kFp8, RG, kTwin>::kCtas)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               DecodeArgs a, int RT, float* partial, Cut* cuts) {
-  using S = Shape<D, kFp8, RG>;
+  using S = Shape<D, kFp8, RG, kTwin>;
+  constexpr int kX = S::kX;
   constexpr int NS = S::kStages, W = S::kWarps, NT = S::kThreads;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[NS], empty[NS], joined;
@@ -383,7 +418,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int row = rt * S::kRows + rg * 16 + r + 8 * x;
-        const bool there = row < G;
+        const bool there = x < kX && row < G;
         const uint16_t* q = a.q + b * a.qs[0] + (g * G + (there ? row : 0)) * a.qs[2];
         f[x] = base;
         if (!kFp8) {
@@ -456,7 +491,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
         }
       }
-      constexpr int SL = S::kSlices;
+      constexpr int SL = S::kSlices, kTerms = S::kTerms;
       // the warp's first key of the page, and how many from it on count
       const int k0 = 16 * SL * (kw % S::kParts), live = page_live - k0;
       if (mine && live > 0) {
@@ -506,17 +541,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
           for (int t = 0; t < 2 * SL; ++t)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 2 * kX; ++x)
               if (8 * t + 2 * cq + (x & 1) >= live) sc[t][x] = -INFINITY;
         }
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int t = 0; t < 2 * SL; ++t)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) top[x >> 1] = fmaxf(top[x >> 1], sc[t][x]);
+          for (int x = 0; x < 2 * kX; ++x) top[x >> 1] = fmaxf(top[x >> 1], sc[t][x]);
         bool grew = false;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kX; ++x) {
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
           grew |= top[x] > m[x];
@@ -524,7 +559,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (__any_sync(0xffffffffu, grew)) {
           float corr[2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < kX; ++x) {
             const float now = fmaxf(m[x], top[x]);
             corr[x] = now == -INFINITY ? 1.f : ex2((m[x] - now) * f[x]);
             m[x] = now;
@@ -534,12 +569,12 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           for (int j = 0; j < D / 8; ++j) {
             o[j][0] *= corr[0];
             o[j][1] *= corr[0];
-            o[j][2] *= corr[1];
-            o[j][3] *= corr[1];
+            o[j][2] *= corr[kX - 1];
+            o[j][3] *= corr[kX - 1];
           }
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kX; ++x) {
           // m is subtracted before the scaling: the largest key has weight 1
           // however coarse fp32 is at its logit's size
           const float mx = m[x] == -INFINITY ? 0.f : m[x];
@@ -564,22 +599,25 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               keep[t] = (k < live ? 0xffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
             }
           }
-          uint32_t hi_w[4], lw_w[4];           // P as A fragments
+          // P as A fragments: registers 0 and 2 are row r, 1 and 3 row r + 8
+          uint32_t pw[kTerms][4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
+            if (x % 2 >= kX) continue;
             const float p0 = sc[2 * y + (x >> 1)][2 * (x & 1)], p1 = sc[2 * y + (x >> 1)][2 * (x & 1) + 1];
-            if (kFp8) {
-              hi_w[x] = pack_half(p0, p1);
+            uint32_t t[3];
+            split<kFp8>(p0, p1, kTwin ? 0.5f : 1.f, t);
+            pw[0][x] = t[0];
+            if (!kTwin) {
+              for (int z = 1; z < kTerms; ++z) pw[z][x] = t[z];
             } else {
-              // hi is cut, not rounded, and lo a little above what is left (2^-24
-              // of p), so that both are positive: an infinite value stays one
-              hi_w[x] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-              lw_w[x] = pack_bf16(fmaf(p0, 0x1p-24f, p0 - lo_f32(hi_w[x])),
-                                  fmaf(p1, 0x1p-24f, p1 - hi_f32(hi_w[x])));
+              pw[0][x + 1] = t[1];
+              if (!kFp8) pw[kTerms - 1][x] = pw[kTerms - 1][x + 1] = t[2];
             }
           }
-          const uint4 hi = make_uint4(hi_w[0], hi_w[1], hi_w[2], hi_w[3]);
-          const uint4 lw = kFp8 ? hi : make_uint4(lw_w[0], lw_w[1], lw_w[2], lw_w[3]);
+          uint4 pt[kTerms];
+#pragma unroll
+          for (int z = 0; z < kTerms; ++z) pt[z] = make_uint4(pw[z][0], pw[z][1], pw[z][2], pw[z][3]);
 #pragma unroll
           for (int j = 0; j < kSteps; j += VB) {
             if (y > 0 || j > 0)
@@ -593,27 +631,31 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 for (int x = 0; x < 4; ++x) vb[u][x] &= keep[x & 1];
             if (!kFp8) {
 #pragma unroll
-              for (int u = 0; u < VB; ++u) {
-                mma<false>(o[2 * (j + u)], hi, vb[u][0], vb[u][1]);
-                mma<false>(o[2 * (j + u) + 1], hi, vb[u][2], vb[u][3]);
-              }
+              for (int z = 0; z < kTerms; ++z)
 #pragma unroll
-              for (int u = 0; u < VB; ++u) {
-                mma<false>(o[2 * (j + u)], lw, vb[u][0], vb[u][1]);
-                mma<false>(o[2 * (j + u) + 1], lw, vb[u][2], vb[u][3]);
-              }
+                for (int u = 0; u < VB; ++u) {
+                  mma<false>(o[2 * (j + u)], pt[z], vb[u][0], vb[u][1]);
+                  mma<false>(o[2 * (j + u) + 1], pt[z], vb[u][2], vb[u][3]);
+                }
             } else {
               // a transposed 16-bit element is two neighbouring dims: the even
               // ones make one column tile, the odd ones the next
 #pragma unroll
-              for (int u = 0; u < VB; ++u)
+              for (int u = 0; u < VB; ++u) {
+                uint2 w[2][2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const uint2 u0 = e4m3x4_half4(__byte_perm(vb[u][2 * x], 0, 0x3120));
-                  const uint2 u1 = e4m3x4_half4(__byte_perm(vb[u][2 * x + 1], 0, 0x3120));
-                  mma<true>(o[4 * (j + u) + 2 * x], hi, u0.x, u1.x);
-                  mma<true>(o[4 * (j + u) + 2 * x + 1], hi, u0.y, u1.y);
+                  w[x][0] = e4m3x4_half4(__byte_perm(vb[u][2 * x], 0, 0x3120));
+                  w[x][1] = e4m3x4_half4(__byte_perm(vb[u][2 * x + 1], 0, 0x3120));
                 }
+#pragma unroll
+                for (int z = 0; z < kTerms; ++z)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    mma<true>(o[4 * (j + u) + 2 * x], pt[z], w[x][0].x, w[x][1].x);
+                    mma<true>(o[4 * (j + u) + 2 * x + 1], pt[z], w[x][0].y, w[x][1].y);
+                  }
+              }
             }
           }
         }
@@ -629,14 +671,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const Unit unit = sm_unit[warp];
         const int dest = unit.dest, rt = unit.rt, b = unit.b, g = unit.g;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kX; ++x) {
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
           m[x] *= f[x];
         }
         // the piece ends: the key warps' results are added
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < kX; ++x)
           if (cq == 0) {
             sm_m[warp][r + 8 * x] = m[x];
             sm_l[warp][r + 8 * x] = l[x];
@@ -647,7 +689,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         float w[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kX; ++x) {
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < S::kKeyWarps; ++k)
@@ -658,10 +700,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // beside the sums, 64 more registers and spills in the loop over pages
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
+          if (kTwin) {                         // the rows of one head's terms
+            o[j][0] += o[j][2];
+            o[j][1] += o[j][3];
+          }
           o[j][0] *= w[0];
           o[j][1] *= w[0];
-          o[j][2] *= w[1];
-          o[j][3] *= w[1];
+          o[j][2] *= w[kX - 1];
+          o[j][3] *= w[kX - 1];
         }
         float* part = partial + static_cast<int64_t>(2 * c + max(dest, 0)) * S::kRows * (D + 2);
         // through the join buffer 32 columns at a time, or, behind a run's last
@@ -864,10 +910,10 @@ int row_groups(int G) { return G <= 16 ? 1 : (G <= 32 ? 2 : 4); }
 
 size_t cuts_bytes() { return (sizeof(Cut) * kMaxRuns + 255) & ~static_cast<size_t>(255); }
 
-template <int D, bool kFp8, int RG>
+template <int D, bool kFp8, int RG, bool kTwin>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t st) {
-  using S = Shape<D, kFp8, RG>;
+  using S = Shape<D, kFp8, RG, kTwin>;
   static_assert(S::kRuns <= max_runs(RG), "the workspace holds the partials of every run");
   static_assert(S::kWarps * 16 * (D + 8) * 4 <= S::kStages * S::kStage, "the ring holds a unit's sums");
   // with 2 KB for the static arrays and the 1 KB that every CTA costs beside
@@ -875,11 +921,11 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorM
   const int G = a.H / a.Hkv, RT = (G + S::kRows - 1) / S::kRows;
   Cut* cuts = reinterpret_cast<Cut*>(a.ws);
   float* partial = reinterpret_cast<float*>(a.ws + cuts_bytes());
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kFp8, RG>,
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kFp8, RG, kTwin>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * RT;
-  decode_kernel<D, kFp8, RG><<<S::kRuns, S::kThreads, S::kSmem, st>>>(kmap, vmap, a, RT, partial, cuts);
+  decode_kernel<D, kFp8, RG, kTwin><<<S::kRuns, S::kThreads, S::kSmem, st>>>(kmap, vmap, a, RT, partial, cuts);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_close(join_kernel<D>,
@@ -893,9 +939,10 @@ template <int D, bool kFp8>
 cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      cudaStream_t st) {
   switch (row_groups(a.H / a.Hkv)) {
-    case 1: return launch<D, kFp8, 1>(a, kmap, vmap, st);
-    case 2: return launch<D, kFp8, 2>(a, kmap, vmap, st);
-    default: return launch<D, kFp8, 4>(a, kmap, vmap, st);
+    case 1: return a.H / a.Hkv <= 8 ? launch<D, kFp8, 1, true>(a, kmap, vmap, st)
+                                    : launch<D, kFp8, 1, false>(a, kmap, vmap, st);
+    case 2: return launch<D, kFp8, 2, false>(a, kmap, vmap, st);
+    default: return launch<D, kFp8, 4, false>(a, kmap, vmap, st);
   }
 }
 

@@ -559,9 +559,9 @@ size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p);
  * token, NaN included, has no effect.
  *
  * Precision: exact products with fp32 accumulation and an fp32 softmax; P.V
- * takes P as two bf16 terms (to 2^-15; with SA_CACHE_FP8 one fp16 term, to
- * 2^-12, against V in fp16, which holds every e4m3 value) with fp32
- * accumulation; o is rounded once to bf16. The sums' order, and so the last
+ * takes P to 2^-21 of itself, as three bf16 terms (with SA_CACHE_FP8 to 2^-21
+ * of itself or 2^-40 of the largest, as two fp16 terms, against V in fp16,
+ * which holds every e4m3 value) with fp32 accumulation; o is rounded once to bf16. The sums' order, and so the last
  * bit, depends on the lengths in the batch, not on timing.
  *
  * q          device bf16 [B, 1, H, D], rotated as the cached keys are.
