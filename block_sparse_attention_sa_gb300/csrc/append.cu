@@ -158,12 +158,14 @@ __device__ __forceinline__ void turn(Vec& v, const AppendArgs& a, const float* g
   }
 }
 
-// How many of the new tokens of sequence b have a place in its page table.
+// How many of the new tokens of sequence b have a place: in its page table, and
+// in the rotation tables where there are some.
 __device__ __forceinline__ int tokens_of(const AppendArgs& a, int b, int* base, int* status) {
   bool bad;
   *base = clamp_len(get(a.pm.seq_lens + b), a.pm, &bad);
   int n = a.new_lens ? min(max(get(a.new_lens + b), 0), a.S) : a.S;
-  const int room = a.pm.max_pages * kBlock - *base;
+  int room = a.pm.max_pages * kBlock - *base;
+  if (a.cos) room = min(room, max(0, a.rope_rows - *base));
   if (bad) *status |= SA_DEV_BAD_CACHE;
   if (n > room) {
     n = room;
@@ -204,14 +206,10 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
   const float iv = a.v_scale ? 1.f / get(a.v_scale + h) : 1.f;
   int base = 0;
   const int n = there ? tokens_of(a, b, &base, status) : 0;
-  // tokens [s0, s1) of the page, as far as the rotation tables reach
+  // tokens [s0, s1) of the page
   const int64_t edge = (static_cast<int64_t>(base / kBlock) + pu) * kBlock - base;
   const int s0 = edge > 0 ? static_cast<int>(min(edge, static_cast<int64_t>(n))) : 0;
-  int s1 = static_cast<int>(min(edge + kBlock, static_cast<int64_t>(n)));
-  if (a.cos && s1 > s0 && s1 > a.rope_rows - base) {
-    s1 = max(s0, a.rope_rows - base);
-    *status |= SA_DEV_CAPACITY;
-  }
+  const int s1 = static_cast<int>(min(edge + kBlock, static_cast<int64_t>(n)));
   // the page is not waited for before the first store
   *page = s0 < s1 ? page_of(a, b, base + s0, status) : -1;
   *slot0 = static_cast<unsigned>(base + s0) % kBlock;
@@ -347,7 +345,6 @@ __global__ void __launch_bounds__(D, (kWhole ? 7 : 4) * 128 / D) append_kernel(A
     int base = 0, none = 0;             // the key-value CTAs report what is wrong
     bool on = there && s < tokens_of(a, b, &base, &none);
     const int t = base + (on ? s : 0);
-    on = on && !(a.cos && t >= a.rope_rows);
     if (!__any_sync(0xffffffffu, on)) return;
     // the queries and their angles are on their way while the page is looked up
     if (!early) load(0, on);

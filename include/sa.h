@@ -483,7 +483,9 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * slot starts its sum anew.
  * Tokens that find no place (t >= 64 max_pages, or t >= rope_rows where tables
  * are given: SA_DEV_CAPACITY; a bad page id: SA_DEV_BAD_CACHE) are left out,
- * with their q_out. All else of the caches, k_sum and q_out stays as it was.
+ * with their q_out. The new length does not count the former, which lie behind
+ * all others; those of a bad page keep their positions in it, and sa_attn_decode
+ * and sa_route_pages leave that page out as well. All else of the caches, k_sum and q_out stays as it was.
  *
  * k, v         device bf16 [B, S, H_kv, D].
  * q, q_out     device bf16 [B, S, H, D] (q_stride; o_stride), or both NULL.
@@ -496,8 +498,9 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * v_scale      (and NULL with SA_CACHE_BF16).
  * seq_lens     the lengths before the call; not modified.
  * new_lens     device int32 [B] in [0, S] (clamped into it), or NULL.
- * lens_out     device int32 [B], or NULL: seq_lens[b] + n_b, at most
- *              64 max_pages; neither seq_lens nor new_lens itself.
+ * lens_out     device int32 [B], or NULL: seq_lens[b] + n_b, at most 64 max_pages
+ *              and, where tables are given, max(seq_lens[b], rope_rows); neither
+ *              seq_lens nor new_lens itself.
  * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED before launch; SA_ERR_CUDA.
  */
 sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v,
