@@ -43,6 +43,12 @@ sa_status check_tokens(const sa_cache_params* p, const void* x, const int64_t s[
   return aligned(x, 16) && strides_fit(s, extent, 8) ? SA_OK : SA_ERR_INVALID_ARG;
 }
 
+// Whether two arrays of n lengths (b may be null) share an entry.
+bool lens_overlap(const int32_t* a, const int32_t* b, int n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return b && (x > y ? x - y : y - x) < static_cast<uintptr_t>(n) * sizeof(int32_t);
+}
+
 // The pool, its scales and the page table.
 sa_status check_pool(const sa_cache_params* p, const void* kc, const void* vc, const float* ks,
                      const float* vs, const int32_t* table, const int32_t* lens) {
@@ -166,7 +172,9 @@ sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v
       !aligned(rope_sin, 16) || !aligned(k_sum, 16))
     return SA_ERR_INVALID_ARG;
   if ((rope_cos == nullptr) != (rope_sin == nullptr)) return SA_ERR_INVALID_ARG;
-  if (lens_out && (lens_out == seq_lens || lens_out == new_lens)) return SA_ERR_INVALID_ARG;
+  // written by some CTAs while others still read those
+  if (lens_out && (lens_overlap(lens_out, seq_lens, p->B) || lens_overlap(lens_out, new_lens, p->B)))
+    return SA_ERR_INVALID_ARG;
   if (q && q == q_out)
     for (int i = 0; i < 3; ++i)
       if (p->q_stride[i] != p->o_stride[i]) return SA_ERR_INVALID_ARG;

@@ -499,8 +499,8 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * seq_lens     the lengths before the call; not modified.
  * new_lens     device int32 [B] in [0, S] (clamped into it), or NULL.
  * lens_out     device int32 [B], or NULL: seq_lens[b] + n_b, at most 64 max_pages
- *              and, where tables are given, max(seq_lens[b], rope_rows); neither
- *              seq_lens nor new_lens itself.
+ *              and, where tables are given, max(seq_lens[b], rope_rows); no overlap
+ *              with seq_lens or new_lens.
  * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED before launch; SA_ERR_CUDA.
  */
 sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v,
