@@ -17,15 +17,17 @@
 // more than twice the error bound above or below that score is decided; the few
 // in between (usually the last page alone) are computed again in paired fp32.
 // Rows with scores that are not finite or so small that fp32 loses their ends,
-// and rows with very many undecided pages, are ranked in fp64. Latency bounds it: 11 us for 8 rows of 598 pages with both kernels.
+// and rows with very many undecided pages, are ranked in fp64. Latency bounds it:
+// 11 us for 8 rows of 598 pages with both kernels.
 //
-// Error of a score against fp64, over sum_d |q_d k_d| <= |q|_1 max |k|: 2^-18
-// from the two terms; and D / 16 tensor-core steps for each, which add 16 products
-// and the running sum, each cut to 24 bits of the largest or better: 17 2^-24 a
-// step, below 2^-16.9. Together below 2^-16.3; kErr is 2^-16. The second term
-// loses its end where |k| is below 2^-110 or so (bf16 has nothing below 2^-133),
-// so max |k| counts as 2^-100 at least, and |q|_1, unless it is 0, as 2^-40, so
-// that the product is 0 for a row of zeros only.
+// Error of a score against fp64, over sum_d |q_d k_d| <= |q|_1 max |k|: 2^-17
+// from the two terms; and D / 16 tensor-core steps for each (the second 2^-8 of the
+// first), which add 16 products and the running sum, each cut to 24 bits of the
+// largest, a unit in the last place each: 17 2^-23 a step, 2^-15.9 at D = 128.
+// Together below kErr = 2^-15.34. The second term loses its end where |k| is below
+// 2^-110 or so (bf16 has nothing below 2^-133), so max |k| counts as 2^-100 at
+// least, and |q|_1, unless it is 0, as 2^-40, so that the product is 0 for a row of
+// zeros only.
 #include <cuda_bf16.h>
 
 #include "cache_internal.cuh"
@@ -41,7 +43,9 @@ constexpr int kScoreWarps = 4;
 static_assert((kScoreWarps & (kScoreWarps - 1)) == 0, "heads, a power of two, divide them");
 constexpr int kScoreCtas = 3 * 152;    // three CTAs on each SM
 constexpr int kAhead = 2;              // tiles a warp has in flight
-constexpr float kErr = 1.f / 65536.f;  // 2^-16
+constexpr float kErr = 0x1.94p-16f;
+static_assert(kErr >= 0x1p-17 + 128 / 16 * 17 * 0x1p-23 * (1 + 0x1p-8) + 0x1p-24,
+              "two terms, the steps of both, and their sum");
 constexpr float kLeastK = 0x1p-100f, kLeastQ = 0x1p-40f;
 // Below these the ends of products are lost in fp32: the error bound of a row,
 // and |q|_1 max |k| of a page that is scored again.
