@@ -15,7 +15,8 @@
 // by histograms of 256 bins until a few dozen pages are left, and ranks those. An
 // order statistic moves by no more than the values do, so a page whose score is
 // more than twice the error bound above or below that score is decided; the few
-// in between (usually the last page alone) are computed again in paired fp32.
+// in between (usually the last page alone) are computed again in paired fp32, and
+// those of them that this leaves within its own error of the edge in fp64.
 // Rows with scores that are not finite or so small that fp32 loses their ends,
 // and rows with very many undecided pages, are ranked in fp64. Latency bounds it:
 // 11 us for 8 rows of 598 pages with both kernels.
@@ -54,6 +55,7 @@ constexpr int kItems = 8;              // pages a thread of select_kernel holds 
 constexpr int kSpan = kThreads * kItems;
 constexpr int kNear = kThreads;        // undecided pages ranked in shared memory
 constexpr int kFew = 48;               // pages that are ranked rather than counted once more
+constexpr double kPairedErr = 0x1p-37;   // of a paired score, over the row's largest |q|_1 max |k|
 constexpr unsigned kFull = 0xffffffffu;
 
 // Workspace: per page its score and |q|_1 max |k| (what bounds the score's
@@ -354,7 +356,9 @@ __device__ double exact_score(const RoutePagesArgs& a, int b, int g, int j, int 
 }
 
 // Score of one page by a whole warp as a sum of two floats, each product and
-// sum kept with its rounding error: right to about 2^-40 of |q| |k|. Eight heads
+// sum kept with its rounding error. A lane's D / 4 steps keep errors of at most
+// 2^-24 (size + |p|) each, size = |q|_1 max |k|, so what is kept stays below 2^-18 size
+// (D = 128) and its own roundings add up to 2^-37 size at most: kPairedErr. Eight heads
 // at a time, four lanes each. (In fp64, which runs at 1/64 of fp32's rate here,
 // three pages took 14,700 cycles, more than all else in the kernel.) For finite
 // scores only.
@@ -433,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
   __shared__ int near_j[kNear], open_at[kNear], near_n, open_n;
   __shared__ float near_v[kNear];
   __shared__ double open_s[kNear];
+  __shared__ bool is_close[kNear];
   __shared__ unsigned chosen[kSpan / 32];    // of a span's undecided pages, by bit
   __shared__ int warp_n[2][kWarps], list_n[2][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -639,11 +644,43 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
             if (lane == 0) open_s[i] = s;
           }
           __syncthreads();
+          // the same once more, with what a paired score may be off by (compared as
+          // integers: fp64 is slow here); the exact scores have the last word
+          bool close = open;
           if (open) {
-            int rank = 0;
-            for (int i = 0; i < n_open; ++i)
-              rank += open_s[i] > open_s[slot] || (open_s[i] == open_s[slot] && open_at[i] < j);
-            yes = rank < rest;
+            if (finite) {
+              const double mine_s = open_s[slot], margin = 2.0 * kPairedErr * __uint_as_float(k_d);
+              const uint64_t hi_u = order64(mine_s + margin), lo_u = order64(mine_s - margin);
+              int more = 0, reach = 0;
+              for (int i = 0; i < n_open; ++i) {
+                const uint64_t u = order64(open_s[i]);
+                more += u > hi_u;
+                reach += u >= lo_u;
+              }
+              yes = reach <= rest;
+              close = !yes && more < rest;
+            }
+            is_close[slot] = close;
+          }
+          if (__syncthreads_or(close)) {
+            const int rest_close = rest - __syncthreads_count(open && yes);
+            if (finite) {
+              for (int i = warp; i < n_open; i += kWarps) {
+                if (!is_close[i]) continue;
+                const double s = exact_score(a, b, g, open_at[i], lane);
+                if (lane == 0) open_s[i] = s;
+              }
+              __syncthreads();
+            }
+            if (close) {
+              const uint64_t mine_u = order64(open_s[slot]);
+              int before = 0;
+              for (int i = 0; i < n_open; ++i) {
+                const uint64_t u = order64(open_s[i]);
+                before += is_close[i] && (u > mine_u || (u == mine_u && open_at[i] < j));
+              }
+              yes = before < rest_close;
+            }
           }
         } else {
           yes |= open && rest > 0;

@@ -529,8 +529,9 @@ size_t sa_route_pages_workspace_bytes(const sa_cache_params* p);
  * their sums rank as their means do. A score that is not a number ranks last;
  * so does a page with a bad id. (A budget bounds the attention's cost per
  * token; sa_route's threshold does not.) Scores are computed in fp32 with an
- * error bound; those the bound leaves undecided again, to 2^-40 of |q| |k_sum|
- * (in fp64 where fp32 would overflow), so the choice equals that of fp64 scores.
+ * error bound; those the bound leaves undecided again, to 2^-37 of
+ * |q|_1 max |k_sum|, and what that leaves undecided (or fp32 would overflow on)
+ * in fp64, so the choice equals that of fp64 scores.
  *
  * q          device bf16 [B, 1, H, D], rotated as the cached keys are.
  * row_ptr    device int32 [B*H_kv + 1]; row r = b*H_kv + g.
