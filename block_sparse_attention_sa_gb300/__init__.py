@@ -571,8 +571,9 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     "interleaved" or "half") on the way; see sa.h. With ``q`` [B, S, H, D]
     returns the queries normed and rotated alike (``q_out``, default new; pass
     q_out=q for in place). ``new_lens``: how many of the S tokens each sequence
-    brings. ``k_sum`` gathers the per-page key sums that sa_route_pages reads;
-    ``lens_out`` receives the new lengths."""
+    brings. ``k_sum`` gathers the per-page key sums that sa_route_pages reads (taking
+    tokens back: keep a copy of the last page's, see sa.h); ``lens_out`` receives the
+    new lengths. Rows of ``q_out`` of tokens that are not stored are not written."""
     index = _cuda_index(k)
     if q is not None and q_out is None:
         q_out = _empty(q.shape, q.dtype, q.device, stream)

@@ -481,6 +481,11 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * 1 / v_scale[h].
  * k_sum of the page (where given) gains y before it is rounded; a page's first
  * slot starts its sum anew.
+ * Taking tokens back (a guess that was rejected) is setting the length back, but
+ * k_sum has gained their keys: before more is appended, the sums of the page that
+ * the sequence then ends in (page_table[b][n / 64], where n % 64 > 0), [H_kv, D]
+ * floats, have to be put back as they were at that length. Those of the pages
+ * behind it start anew.
  * Tokens that find no place (t >= 64 max_pages, or t >= rope_rows where tables
  * are given: SA_DEV_CAPACITY; a bad page id: SA_DEV_BAD_CACHE) are left out,
  * with their q_out. The new length does not count the former, which lie behind
