@@ -531,8 +531,9 @@ size_t sa_route_pages_workspace_bytes(const sa_cache_params* p);
  * Kept are the pages that sa_route always keeps (j < ceil(min(P, n) / 64), and
  * the newest page Nb - 1) and, while fewer than page_budget are, the others by
  * s_j descending (equal s_j: lower j first). Pages that compete are full, so
- * their sums rank as their means do. A score that is not a number ranks last;
- * so does a page with a bad id. (A budget bounds the attention's cost per
+ * their sums rank as their means do. A head whose score is not a number is
+ * passed over; a page without any other head ranks last, as does one with a bad
+ * id. (A budget bounds the attention's cost per
  * token; sa_route's threshold does not.) Scores are computed in fp32 with an
  * error bound; those the bound leaves undecided again, to 2^-37 of
  * |q|_1 max |k_sum|, and what that leaves undecided (or fp32 would overflow on)
