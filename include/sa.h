@@ -476,9 +476,9 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  *   (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c), c = rope_cos[t][i],
  *       s = rope_sin[t][i], (a, b) the i-th pair of rope_layout
  * in fp32, rounded once: q to bf16 into q_out, k to bf16 into k_cache, or with
- * SA_CACHE_FP8 to the nearest e4m3 code of y times 1 / k_scale[h] (ties to even,
- * |code| at most 448, NaN stays NaN). v goes into v_cache as it is, or times
- * 1 / v_scale[h].
+ * SA_CACHE_FP8 to the e4m3 code nearest to the fp32 quotient y / k_scale[h] (ties
+ * to even, |code| at most 448, NaN stays NaN). v goes into v_cache as it is, or as
+ * the code of v / v_scale[h].
  * k_sum of the page (where given) gains y before it is rounded; a page's first
  * slot starts its sum anew.
  * Taking tokens back (a guess that was rejected) is setting the length back, but
