@@ -474,10 +474,13 @@ def _bind():
     """The compiled module, attached to the library. Raises if it is missing."""
     global _BIND
     if _BIND is None:
-        path = os.path.join(_PKG, "_sa_bind.so")
+        from . import build as _build
+
+        path = _build.module_path()
         if not os.path.exists(path):
             raise FileNotFoundError(
-                f"{path} is missing: build it with `python -m block_sparse_attention_sa_gb300.build`")
+                f"{path} is missing (one is built for each torch and Python): build it with "
+                "`python -m block_sparse_attention_sa_gb300.build`")
         spec = importlib.util.spec_from_file_location("_sa_bind", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

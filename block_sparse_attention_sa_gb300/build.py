@@ -1,12 +1,15 @@
-"""Builds libsa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch),
-and the small Python module that marshals the paged-cache calls to it.
+"""Builds libsa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch, no
+Python headers), and the small Python module that marshals the paged-cache calls
+to it.
 
-    python -m block_sparse_attention_sa_gb300.build [--verbose-ptxas]
+    python -m block_sparse_attention_sa_gb300.build [--force] [--verbose-ptxas]
 
 Each .cu is compiled to an object in parallel, then linked into a shared
-library next to this file; the module (csrc/bind.cpp, which reads torch's
-tensors directly) is compiled beside them with the host compiler. Rebuilds
-only when a source or header is newer than what was built.
+library next to this file. The module (csrc/bind.cpp) reads torch's tensors
+directly, so it is compiled against the torch and the Python that run this and
+carries both in its name; where it does not compile, the library and all that
+needs no module stand, and the paged-cache calls from Python say that it is
+missing. Each part is rebuilt only when one of its sources is newer.
 """
 
 from __future__ import annotations
@@ -24,7 +27,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsa_gb300.so")
-BIND = os.path.join(PKG, "_sa_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -39,18 +41,37 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+def module_path() -> str:
+    """Where the module of this torch and this Python lies."""
+    import torch
+
+    return os.path.join(PKG, "_sa_bind.%s.torch-%s.so" % (
+        sysconfig.get_config_var("SOABI"), torch.__version__))
+
+
+def _older(built: str, deps) -> bool:
+    if not os.path.exists(built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp")) + [
-        os.path.join(ROOT, "include", "sa.h"), os.path.abspath(__file__)]
+    t = os.path.getmtime(built)
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def _compile_bind() -> None:
+def _common():
+    return [os.path.join(ROOT, "include", "sa.h"), os.path.abspath(__file__)]
+
+
+def _library_stale() -> bool:
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _common())
+
+
+def _module_stale() -> bool:
+    return _older(module_path(), glob.glob(os.path.join(CSRC, "*.cpp")) + _common())
+
+
+def _compile_module() -> None:
     import torch
 
+    path = module_path()
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [shutil.which("g++") or "g++", "-shared", "-fPIC", "-O2", "-std=c++17",
@@ -59,16 +80,14 @@ def _compile_bind() -> None:
            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I", os.path.join(cuda, "include"), os.path.join(CSRC, "bind.cpp"),
            "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
-           "-Wl,-rpath," + os.path.join(root, "lib"), "-o", BIND + ".tmp"]
+           "-Wl,-rpath," + os.path.join(root, "lib"), "-o", path + ".tmp"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the binding does not compile:\n{r.stdout}\n{r.stderr}")
-    os.replace(BIND + ".tmp", BIND)
+    os.replace(path + ".tmp", path)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+def _compile_library(verbose_ptxas: bool = False) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -84,10 +103,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
-        bind = ex.submit(_compile_bind)
+    with ThreadPoolExecutor(max_workers=len(sources())) as ex:
         results = list(ex.map(compile_one, sources()))
-        bind.result()
     if verbose_ptxas:
         for _, err in results:
             sys.stderr.write(err)
@@ -97,6 +114,18 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(_compile_module) if force or _module_stale() else None
+        if force or _library_stale():
+            _compile_library(verbose_ptxas)
+        if module is not None:
+            try:
+                module.result()
+            except (ImportError, OSError, RuntimeError) as e:
+                sys.stderr.write(f"the module of the paged-cache calls was not built: {e}\n")
     return LIB
 
 
