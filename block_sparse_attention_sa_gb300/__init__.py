@@ -504,7 +504,7 @@ def _call(what: str, fn, index: int, stream, *args) -> None:
 
 
 def _cuda_index(t: torch.Tensor) -> int:
-    if not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device: there is no CPU path")
     return t.get_device()
 
@@ -532,7 +532,7 @@ def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = N
     pool = k_cache if k_cache is not None else k_sum
     if pool is None or pool.dim() != (4 if k_cache is not None else 3):
         raise ValueError("k_cache must be [n_pages, H_kv, 64, D], k_sum [n_pages, H_kv, D]")
-    if page_table.dim() != 2:
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     p.n_pages, p.H_kv, p.D = pool.shape[0], pool.shape[1], pool.shape[-1]
     p.B, p.max_pages = page_table.shape
@@ -545,7 +545,7 @@ def make_cache_params(page_table: torch.Tensor, *, q: Optional[torch.Tensor] = N
     p.S = 1 if tokens is None else tokens.shape[1]
     p.H = p.H_kv if q is None else q.shape[2]
     if k_cache is not None:
-        if (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype
+        if (v_cache is None or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype
                 or k_cache.shape[2] != PAGE or k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
             raise ValueError("k_cache, v_cache must be alike, [n_pages, H_kv, 64, D] with a "
                              "contiguous last dimension")
@@ -640,6 +640,8 @@ def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     col_idx from sa_route_pages): (o bf16 [B, 1, H, D], lse fp32 [B, H, 1] or
     None). H is a multiple of the cache's H_kv."""
     index = _cuda_index(q)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, 1, H, D]")
     if o is None:
         o = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None and want_lse:
