@@ -31,7 +31,6 @@ namespace {
 constexpr int kGroups = 8;         // lane groups of a CTA, D / 8 lanes each
 constexpr int kQueryHeads = 8;     // heads a lane group has in flight
 constexpr int kTokens = 2;         // tokens a lane group has in flight
-constexpr int64_t kManyTokens = 1024;
 
 struct Vec {                       // a lane's eight elements
   float x[8];
@@ -394,11 +393,11 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   const int64_t units = a.B * page_units * a.Hkv;
   const bool whole = a.S > kTokens;
   const int64_t kv = whole ? units : (units + kGroups - 1) / kGroups;
-  // lane groups per token: as many as it has heads where tokens are few and
-  // the chain of one token counts, else so many that each has all its loads in
-  // flight at once and a token's angles are loaded by few
+  // lane groups per token: so many that each has all its heads in flight at once
+  // and a token's angles are loaded by few (a group for each head instead, as far
+  // as they go: the same for 1 to 4,096 tokens)
   const int64_t tokens = static_cast<int64_t>(a.B) * a.S;
-  const int want = tokens < kManyTokens ? a.H : (a.H + kQueryHeads - 1) / kQueryHeads;
+  const int want = (a.H + kQueryHeads - 1) / kQueryHeads;
   int per_log2 = 0;
   while ((1 << per_log2) < want && (2 << per_log2) <= kGroups) ++per_log2;
   const int64_t at_once = kGroups >> per_log2;
