@@ -59,10 +59,10 @@ constexpr int max_runs(int RG) { return (RG < 4 ? 3 : 2) * kSms; }
 constexpr int kMaxRuns = max_runs(1);
 constexpr float kFp16Shift = 15.f;     // P is held as 2^15 p in fp16 terms
 
-// A CTA holds RG groups of 16 rows of query heads (kTwin: 8, each in two rows of a tile). 4 / RG warps divide a page's
-// keys for each group, so a CTA has four consumer warps: with eight and one CTA
-// an SM, 56 heads on one key-value head took 48.5 us instead of 43.8 (and two CTAs of eight
-// 47.3 instead of 43.1).
+// A CTA holds RG groups of 16 rows of query heads (kTwin: 8, each in two rows of a
+// tile). 4 / RG warps divide a page's keys for each group, so a CTA has four consumer
+// warps (eight with one CTA an SM, 56 heads of 64 on one key-value head, P in two terms:
+// 48.5 us for 43.8; two CTAs of eight 47.3 for 43.1).
 template <int D, bool kFp8, int RG, bool kTwin>
 struct Shape {
   static constexpr int kRows = 16 * RG;
@@ -72,13 +72,15 @@ struct Shape {
   static constexpr int kKeyWarps = 4 / RG;
   static constexpr int kWarps = kKeyWarps * RG;         // consumer warps
   static constexpr int kSlices = RG == 4 ? 4 : 2;   // 16-key slices a warp takes at once (one at
-                                               // a time: 215 us for 211, 64 sequences in bf16)
+                                               // a time: 213 us for 210, 64 sequences in bf16)
   static constexpr int kParts = 4 / kSlices;            // warps that share a page
   static constexpr int kPhases = kKeyWarps / kParts;    // pages being worked on
   static constexpr int kThreads = 32 * (kWarps + 1);
   // CTAs on an SM: three where the registers allow it and two pages fit the
-  // ring (e4m3, 3 x 112,640 tokens: 117 us with three, 125 us with two)
-  static constexpr int kCtas = (RG == 1 && kFp8) || (RG < 4 && D == 64) ? 3 : 2;
+  // ring (e4m3, 3 x 112,640 tokens of 56/8 heads: 110 us with three, 112 with two;
+  // 16 sequences of up to 38,247 tokens, 32/1 heads of 64 in bf16: 33.3 and 34.8),
+  // else two (12/1 heads of 128 in e4m3, where three spill: 32.7 and 31.5)
+  static constexpr int kCtas = (kTwin && kFp8) || (RG < 4 && D == 64) ? 3 : 2;
   static constexpr int kRuns = kSms * kCtas;
   static constexpr int kRowBytes = kFp8 ? D : 2 * D;    // one token of one head
   static constexpr int kPage = kBlock * kRowBytes;
@@ -905,7 +907,9 @@ join_kernel(DecodeArgs a, int RT, int rows, int runs, float unit, const float* p
         tot == 0.f ? -INFINITY : (top + log2f(tot * unit)) * 0.69314718055994530942f;
 }
 
-// Row groups a CTA holds for G query heads per key-value head.
+// Row groups a CTA holds for G query heads per key-value head: as few as hold them
+// (16 sequences of up to 38,247 tokens, heads of 128 in bf16: 16 heads in 16 rows 41.7
+// us, in 32 rows 47.3; 17 heads in 32 rows 47.8, in 64 rows 73.9), 64 rows at most.
 int row_groups(int G) { return G <= 16 ? 1 : (G <= 32 ? 2 : 4); }
 
 size_t cuts_bytes() { return (sizeof(Cut) * kMaxRuns + 255) & ~static_cast<size_t>(255); }
