@@ -12,14 +12,15 @@
 // page's tokens of this call are summed in a fixed order by the lanes that
 // store them, so its k_sum needs no atomics and is the same every time. Query
 // CTAs own a few tokens: a token's angles are loaded once for all heads. At most
-// 72 registers a thread, so that seven CTAs of 128 threads share an SM: loads in
-// flight come from many warps, not from deep ones (38,247 tokens, 56/8 heads:
-// 282 us with four CTAs and four tokens in flight a lane group, 219 us now).
+// 72 registers a thread, so that seven CTAs of 128 threads share an SM, which costs 40
+// bytes of spills: loads in flight come from many warps, not from deep ones (38,247
+// tokens, 56/8 heads: 282 us with four CTAs and four tokens in flight a lane group,
+// 227 us with six CTAs without spills, 217 us with seven, 227 us with eight).
 //
 // Measured on GB300 (copy rate 6.79 TB/s): 38,247 tokens, 56/8 heads of 128,
-// bf16, 1.43 GB in 219 us, 6.55 TB/s. 5 x up to 2,047 tokens, 16/16 heads of 64,
-// e4m3, 54 MB in 16.8 us: instructions bound it, 60% of the issue slots. One
-// token 3.5 us, 128 tokens 4.3 us: launch and the chain of loads.
+// bf16, 1.43 GB in 217 us, 6.6 TB/s. 5 x up to 2,047 tokens, 16/16 heads of 64,
+// e4m3, 62 MB in 16.7 us, 3.7 TB/s: instructions bound it, 61% of the issue slots
+// while its CTAs run. One token 3.5 us, 128 tokens 4.1 us: launch and the chain of loads.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

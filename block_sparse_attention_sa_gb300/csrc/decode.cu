@@ -16,9 +16,10 @@
 //   32 or 64 keys of a page at a time: S = Q K^T on the tensor cores with the
 //   query heads as the 16 rows of mma.m16n8k16 (16, 32 or 64 of them in a CTA),
 //   the softmax in registers, P V with P as the A operand straight from those
-//   registers. tcgen05 has no use here: its smallest tile is 64 rows of which G
-//   are there, and the accumulators would go through tensor memory for a
-//   product that waits for DRAM.
+//   registers. With up to 16 heads tcgen05 has nothing to gain: the product
+//   waits for DRAM, and its accumulators would go through tensor memory. For many
+//   heads on one key-value head it (with the keys as the rows, the heads as the
+//   columns) has not been tried.
 // - A unit that lies in one run is finished there. One that is cut leaves fp32
 //   partial results (maximum, sum, unnormalised o) in the workspace, which
 //   join_kernel adds in the order of the runs: no atomics, the same bits every
@@ -37,13 +38,15 @@
 // 49 us (two terms: 43), 56/1 of 128 in e4m3 69 us (one: 58).
 //
 // Measured on GB300 (copy rate 6.79 TB/s), 56/8 heads of 128: 64 sequences of up
-// to 8,192 tokens 213 us, 6.31 TB/s; 3 x 112,640 tokens in e4m3 111 us, 6.2
-// TB/s; 24 x 38,247 tokens routed to 96 pages 103 us, 5.9 TB/s. 56 heads of 64
-// on one key-value head, 16 x up to 38,247 tokens: 49 us, 2.0 TB/s: 64 rows of
-// products a byte, P three times. 777 tokens, 32/8 heads:
-// 8.9 us, 3 of them launches, the rest the chain lengths, table, page, product,
-// partial, join; of the first kernel's 4.6 us the page takes 0.5, its products 1,
-// its partial 0.9, the way to the page the rest.
+// to 8,192 tokens 213 us for 1.37 GB, 6.4 TB/s; 3 x 112,640 tokens in e4m3 111 us,
+// 6.2 TB/s; 24 x 38,247 tokens routed to 96 pages 103 us, 5.9 TB/s. 56 heads of 64 on
+// one key-value head, 16 x up to 38,247 tokens: 49 us for 100 MB, 2.0 TB/s: the
+// latency of each warp's chain bounds it, with two consumer warps a scheduler. Of 6.0
+// warp cycles an instruction a warp waits 1.6 for its own last result, 1.1 for global
+// and 0.4 for shared memory, 0.5 for the tensor pipe, which is busy 51% of the time.
+// 777 tokens, 32/8 heads: 8.9 us, 3 of them launches, the rest the chain lengths,
+// table, page, product, partial, join; of the first kernel's 4.6 us the page takes 0.5,
+// its products 1, its partial 0.9, the way to the page the rest.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -19,7 +19,7 @@
 // those of them that this leaves within its own error of the edge in fp64.
 // Rows with scores that are not finite or so small that fp32 loses their ends,
 // and rows with very many undecided pages, are ranked in fp64. Latency bounds it:
-// 11 us for 8 rows of 598 pages with both kernels.
+// 11.6 us for 8 rows of 598 pages with both kernels.
 //
 // Error of a score against fp64, over sum_d |q_d k_d| <= |q|_1 max |k|: 2^-17
 // from the two terms; and D / 16 tensor-core steps for each (the second 2^-8 of the
@@ -428,7 +428,7 @@ __device__ __forceinline__ uint64_t order64(double x) {
 constexpr int kBins = 256, kPasses = 4;
 
 // grid (B * Hkv): one row. Three CTAs an SM: with the 128 registers that the
-// compiler takes for two, 12.3 us for 11 (8 rows of 598 pages).
+// compiler takes for two, 12.3 us for 11 (8 rows of 598 pages, the error bound at 2^-16).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 3) select_kernel(RoutePagesArgs a) {
   __shared__ int sums[2 * kWarps];
