@@ -19,12 +19,21 @@ Over a paged key-value cache (one new token per sequence and call):
     sa_cache_append(k, v, k_cache, v_cache, page_table, seq_lens, ...) -> q_out
     sa_route_pages(q, k_sum, page_table, seq_lens, prefix_len, budget) -> (row_ptr, col_idx)
     sa_attn_decode(q, k_cache, v_cache, page_table, seq_lens, ...)     -> (o, lse)
+A few drafted tokens per sequence and call:
+    sa_attn_tree(q, k_cache, v_cache, page_table, seq_lens, parents=...) -> (o, lse)
+    sa_cache_accept(k_cache, v_cache, page_table, seq_lens, path, path_lens, ...)
+The pool's pages:
+    sa_pages_fork(page_table, seq_lens, refs, src, ...)  -> the forked table, lengths, refs, moves
+    sa_pages_resize(page_table, refs, seq_lens, more)
+    sa_pages_compact(page_table, refs, ...)              -> table, refs, moves, pages in use
+    sa_cache_copy(k_cache, v_cache, moves, n_moves, ...)
 Tensors are [B, S, H, D] bf16 with a contiguous last dimension.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import importlib.util
 import os
 from typing import Optional, Tuple
@@ -42,7 +51,9 @@ __all__ = [
     "sa_cache_params", "make_cache_params", "sa_cache_append", "sa_route_pages", "sa_attn_decode",
     "sa_route_pages_max_nnz", "sa_route_pages_workspace_bytes", "sa_attn_decode_workspace_bytes",
     "SA_DEV_BAD_CACHE", "SA_CACHE_BF16", "SA_CACHE_FP8", "CACHE_FORMATS", "SA_ROPE_INTERLEAVED",
-    "SA_ROPE_HALF", "ROPE_LAYOUTS",
+    "SA_ROPE_HALF", "ROPE_LAYOUTS", "sa_rope_axes", "sa_attn_tree", "sa_attn_tree_workspace_bytes",
+    "sa_cache_accept", "sa_cache_copy", "sa_pages_fork", "sa_pages_resize", "sa_pages_compact",
+    "sa_pages_workspace_bytes", "SA_DEV_BAD_TREE", "SA_ROPE_STAYS", "SA_TREE_MAX",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -50,7 +61,7 @@ _LIB = None
 
 SA_OK, SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_CAPACITY, SA_ERR_CUDA, SA_ERR_TIMEOUT = range(6)
 SA_DEV_CAPACITY, SA_DEV_TIMEOUT, SA_DEV_BAD_ROUTE, SA_DEV_RANGE = 1, 2, 4, 8
-SA_DEV_BAD_CACHE = 16
+SA_DEV_BAD_CACHE, SA_DEV_BAD_TREE = 16, 32
 # readings of the router rule (sa_params.route_mode)
 SA_ROUTE_THRESHOLD, SA_ROUTE_DENSE_PREFIX_QUERIES, SA_ROUTE_TOP_MASS = 0, 1, 2
 ROUTE_MODES = {"threshold": SA_ROUTE_THRESHOLD,
@@ -66,7 +77,9 @@ CACHE_FORMATS = {torch.bfloat16: SA_CACHE_BF16, torch.float8_e4m3fn: SA_CACHE_FP
 # which elements of a head vector the rotation pairs (sa_cache_params.rope_layout)
 SA_ROPE_INTERLEAVED, SA_ROPE_HALF = 0, 1
 ROPE_LAYOUTS = {"interleaved": SA_ROPE_INTERLEAVED, "half": SA_ROPE_HALF}
+SA_ROPE_STAYS = 255        # a pair that no axis turns
 PAGE = 64
+SA_TREE_MAX = 64           # most new tokens of a sequence in sa_attn_tree
 
 # Every function include/sa.h declares.
 EXPORTS = (
@@ -77,6 +90,9 @@ EXPORTS = (
     "sa_attn_prepare", "sa_attn_run", "sa_qk_quantize",
     "sa_cache_params_init", "sa_cache_append", "sa_route_pages", "sa_route_pages_max_nnz",
     "sa_route_pages_workspace_bytes", "sa_attn_decode", "sa_attn_decode_workspace_bytes",
+    "sa_qk_prologue_axes", "sa_cache_append_axes", "sa_attn_tree", "sa_attn_tree_workspace_bytes",
+    "sa_cache_accept", "sa_cache_copy", "sa_pages_workspace_bytes", "sa_pages_fork",
+    "sa_pages_resize", "sa_pages_compact",
 )
 SA_ROUTE_STATIC_WS_BYTES = 32 << 20
 
@@ -106,6 +122,12 @@ class sa_cache_params(ctypes.Structure):
         ("eps", ctypes.c_float), ("softmax_scale", ctypes.c_float),
         ("table_stride", ctypes.c_int64)] + [(name, ctypes.c_int64 * 3) for name in (
             "q_stride", "k_stride", "v_stride", "o_stride", "kc_stride", "vc_stride")]
+
+
+class sa_rope_axes(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("pos_stride", ctypes.c_int64 * 2),
+                ("n_axes", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("axis_of", ctypes.c_uint8 * 64)]
 
 
 def library_path() -> str:
@@ -157,6 +179,22 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "sa_route_pages": (ctypes.c_int, [C] + [vp] * 6 + [i64, vp, sz, vp, vp]),
         "sa_attn_decode_workspace_bytes": (sz, [C]),
         "sa_attn_decode": (ctypes.c_int, [C] + [vp] * 9 + [i64, vp, vp, vp, sz, vp, vp]),
+    })
+    X, i32 = ctypes.POINTER(sa_rope_axes), ctypes.c_int32
+    sig.update({
+        "sa_qk_prologue_axes": (ctypes.c_int, [P, vp, vp, i32, vp, vp, ctypes.c_float, vp, vp, X,
+                                               vp, vp, vp, sz, vp, vp]),
+        "sa_cache_append_axes": (ctypes.c_int, [C] + [vp] * 8 + [X] + [vp] * 11),
+        "sa_attn_tree_workspace_bytes": (sz, [C]),
+        "sa_attn_tree": (ctypes.c_int, [C] + [vp] * 9 + [i64, vp, vp, i64, vp, vp, vp, sz, vp, vp]),
+        "sa_cache_accept": (ctypes.c_int, [C] + [vp] * 7 + [i64] + [vp] * 4),
+        "sa_cache_copy": (ctypes.c_int, [C] + [vp] * 4 + [i64, vp, vp, vp]),
+        "sa_pages_workspace_bytes": (sz, [i32, i32]),
+        "sa_pages_fork": (ctypes.c_int, [i32] * 4 + [vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp,
+                                                     vp, sz, vp, vp]),
+        "sa_pages_resize": (ctypes.c_int, [i32] * 3 + [vp, i64, vp, vp, vp, i32, vp, sz, vp, vp]),
+        "sa_pages_compact": (ctypes.c_int, [i32] * 3 + [vp, i64, vp, vp, i64, vp, vp, vp, vp, vp,
+                                                        sz, vp, vp]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -269,17 +307,79 @@ def sa_route(q: torch.Tensor, k: torch.Tensor, prefix_len: int, tau: float, scal
     return row_ptr, col_idx
 
 
+@functools.lru_cache(maxsize=64)
+def _axis_bytes(axes: tuple, n_axes: Optional[int], D: int):
+    """The axis of each of the D/2 pairs as bytes, and how many axes there are."""
+    if len(axes) == D // 2 and n_axes != D // 2:
+        of, n = list(axes), max(axes) + 1 if n_axes is None else n_axes
+        if any(a < -1 or a >= n for a in of):
+            raise ValueError(f"axes of the pairs must be -1 or one of {n}")
+        of = [SA_ROPE_STAYS if a < 0 else a for a in of]
+    else:
+        n = len(axes)
+        if any(a < 0 for a in axes) or sum(axes) > D // 2 or (n_axes is not None and n_axes != n):
+            raise ValueError("axes must give the pairs of each axis of positions, at most D/2 "
+                             "in all, or the axis of each of the D/2 pairs")
+        of = [a for a, k in enumerate(axes) for _ in range(k)]
+        of += [SA_ROPE_STAYS] * (D // 2 - len(of))
+    if not 1 <= n <= 8:
+        raise ValueError("positions have 1 to 8 axes")
+    return bytes(of), n
+
+
+def _axes_of(axes, positions: Optional[torch.Tensor], D: int):
+    """((bytes, number of axes), positions [B, S, n_axes] or None) of what a caller gives."""
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dim() not in (2, 3):
+            raise ValueError("positions must be int32 [B, S, n_axes], or [B, S] for one axis")
+        if positions.dim() == 2:
+            positions = positions[..., None]
+    n = None if positions is None else positions.shape[2]
+    if axes is None:
+        if n not in (None, 1):
+            raise ValueError("positions with several axes go with axes")
+        axes = (D // 2,)
+    return _axis_bytes(tuple(int(a) for a in axes), n, D), positions
+
+
+def _rope_axes(of, positions: Optional[torch.Tensor], cos, sin, q: torch.Tensor) -> sa_rope_axes:
+    B, S, _, D = q.shape
+    if (cos is None or sin is None or cos.dim() != 2 or cos.shape[0] < 1
+            or cos.shape[1] != D // 2 or sin.shape != cos.shape):
+        raise ValueError("cos and sin must be fp32 [rows, D/2] with rows >= 1")
+    x = sa_rope_axes()
+    x.axis_of[: D // 2] = of[0]
+    x.n_axes, x.rows = of[1], cos.shape[0]
+    if positions is not None:
+        if (positions.dtype != torch.int32 or positions.shape != (B, S, of[1])
+                or (positions.stride(2) != 1 and of[1] != 1)):
+            raise ValueError(f"positions must be int32 [{B}, {S}, {of[1]}], the axes contiguous")
+        x.positions = positions.data_ptr()
+        x.pos_stride[:] = positions.stride()[:2]
+    return x
+
+
 def sa_qk_prologue(q: torch.Tensor, k: torch.Tensor, gamma_q: Optional[torch.Tensor] = None,
                    gamma_k: Optional[torch.Tensor] = None, eps: float = 1e-6,
                    cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, *,
+                   qk_norm: bool = True, positions: Optional[torch.Tensor] = None, axes=None,
                    q_block: int = 64, q_out: Optional[torch.Tensor] = None,
                    k_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                    dev_status: Optional[torch.Tensor] = None, stream=None):
     """QK-norm + RoPE of q, k (bf16 [B,S,H,D]) with the router's pooling fused
     in: returns (q_out, k_out, workspace); pass the workspace to
     sa_route_pooled. gamma_* fp32 [D] or None; cos, sin fp32 [S, D/2] or None.
-    q_out/k_out default to new tensors with q/k's strides; pass q_out=q for in place."""
-    _require_cuda(q, k, gamma_q, gamma_k, cos, sin)
+    q_out/k_out default to new tensors with q/k's strides; pass q_out=q for in place.
+    Positions with several axes (time, height, width): ``positions`` int32 [B, S, n_axes]
+    (or [B, S] for one axis) pick each pair's row of cos, sin fp32 [rows, D/2]; ``axes``
+    gives the number of pairs of each axis, first axis first (pairs behind the last are
+    not turned), or the axis of each of the D/2 pairs (-1: not turned). Without
+    ``positions`` a token's place counts on every axis. ``qk_norm`` = False leaves the
+    norm out."""
+    _require_cuda(q, k, gamma_q, gamma_k, cos, sin, positions)
+    by_axes = positions is not None or axes is not None or not qk_norm
+    if by_axes:
+        of, pos = _axes_of(axes, positions, q.shape[-1])
     lib = load_library()
     if q_out is None:
         q_out = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
@@ -292,6 +392,16 @@ def sa_qk_prologue(q: torch.Tensor, k: torch.Tensor, gamma_q: Optional[torch.Ten
             raise ValueError(f"{name} must be a contiguous fp32 tensor")
     p = make_params(q, k, q_block=q_block)
     ws = _workspace(sa_route_workspace_bytes(p), q.device, workspace)
+    if by_axes:
+        x = _rope_axes(of, pos, cos, sin, q)
+        with torch.cuda.device(q.device):
+            code = lib.sa_qk_prologue_axes(
+                ctypes.byref(p), _ptr(q), _ptr(k), 1 if qk_norm else 0, _ptr(gamma_q),
+                _ptr(gamma_k), float(eps), _ptr(cos), _ptr(sin), ctypes.byref(x), _ptr(q_out),
+                _ptr(k_out), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status),
+                _stream(stream))
+        _check(code, "sa_qk_prologue")
+        return q_out, k_out, ws
     code = lib.sa_qk_prologue(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
                               float(eps), _ptr(cos), _ptr(sin), _ptr(q_out), _ptr(k_out), _ptr(ws),
                               ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream))
@@ -486,7 +596,10 @@ def _bind():
         spec.loader.exec_module(module)
         lib = load_library()
         module.attach(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in
-                        ("sa_cache_append", "sa_route_pages", "sa_attn_decode")))
+                        ("sa_cache_append", "sa_route_pages", "sa_attn_decode",
+                         "sa_cache_append_axes", "sa_attn_tree", "sa_cache_accept",
+                         "sa_cache_copy", "sa_pages_fork", "sa_pages_resize",
+                         "sa_pages_compact")))
         _BIND = module
     return _BIND
 
@@ -563,7 +676,8 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                     gamma_q: Optional[torch.Tensor] = None,
                     gamma_k: Optional[torch.Tensor] = None, eps: float = 1e-6,
                     cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
-                    rope="interleaved", k_scale: Optional[torch.Tensor] = None,
+                    rope="interleaved", positions: Optional[torch.Tensor] = None, axes=None,
+                    k_scale: Optional[torch.Tensor] = None,
                     v_scale: Optional[torch.Tensor] = None, k_sum: Optional[torch.Tensor] = None,
                     lens_out: Optional[torch.Tensor] = None,
                     dev_status: Optional[torch.Tensor] = None,
@@ -576,14 +690,20 @@ def sa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     q_out=q for in place). ``new_lens``: how many of the S tokens each sequence
     brings. ``k_sum`` gathers the per-page key sums that sa_route_pages reads (taking
     tokens back: keep a copy of the last page's, see sa.h); ``lens_out`` receives the
-    new lengths. Rows of ``q_out`` of tokens that are not stored are not written."""
+    new lengths. Rows of ``q_out`` of tokens that are not stored are not written.
+    ``positions``, ``axes``: as in sa_qk_prologue; a token is rotated by its positions
+    and stored behind its sequence all the same (drafted tokens: their depth; images:
+    time, height, width)."""
     index = _cuda_index(k)
+    of = (None, 0)
+    if positions is not None or axes is not None:
+        of, positions = _axes_of(axes, positions, k.shape[-1])
     if q is not None and q_out is None:
         q_out = _empty(q.shape, q.dtype, q.device, stream)
     _call("sa_cache_append", _bind().append, index, stream, k, v, k_cache, v_cache, page_table,
           seq_lens, q, q_out, new_lens, 1 if qk_norm else 0, gamma_q, gamma_k, eps, cos, sin,
-          ROPE_LAYOUTS[rope] if isinstance(rope, str) else rope, k_scale, v_scale, k_sum,
-          lens_out, dev_status)
+          ROPE_LAYOUTS[rope] if isinstance(rope, str) else rope, positions, of[0], of[1], k_scale,
+          v_scale, k_sum, lens_out, dev_status)
     return q_out
 
 
@@ -653,6 +773,159 @@ def sa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     _call("sa_attn_decode", _bind().decode, index, stream, q, k_cache, v_cache, page_table,
           seq_lens, scale, row_ptr, col_idx, k_scale, v_scale, o, lse, workspace, dev_status)
     return o, lse
+
+
+# ------------------------------------------------------------ drafted tokens --
+
+def sa_attn_tree_workspace_bytes(p: sa_cache_params) -> int:
+    return int(load_library().sa_attn_tree_workspace_bytes(ctypes.byref(p)))
+
+
+def sa_attn_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 page_table: torch.Tensor, seq_lens: torch.Tensor, scale: float = 0.0, *,
+                 parents: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                 row_ptr: Optional[torch.Tensor] = None, col_idx: Optional[torch.Tensor] = None,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 want_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+                 dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of a tree of up to 64 new tokens of each sequence (q bf16 [B, S, H, D],
+    appended behind its ``seq_lens`` tokens) over the cache: (o bf16 [B, S, H, D], lse
+    fp32 [B, H, S] or None). Token s sees what was cached before, and the new tokens it
+    continues: itself, ``parents``[b][s] (int32 [B, S], or [S] for one tree for all; -1:
+    none), that one's parent, and so on; without ``parents`` every new token before it.
+    ``new_lens``: how many of the S tokens each sequence has; rows of o and lse behind
+    those are not written. ``row_ptr``, ``col_idx``: as in sa_attn_decode; pages with
+    new tokens are attended whether listed or not. See sa.h."""
+    index = _cuda_index(q)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, S, H, D]")
+    if o is None:
+        o = _empty(q.shape, q.dtype, q.device, stream)
+    if lse is None and want_lse:
+        lse = _empty((q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device, stream)
+    if workspace is None:
+        p = make_cache_params(page_table, q=q, k_cache=k_cache, v_cache=v_cache)
+        workspace = _empty((max(256, sa_attn_tree_workspace_bytes(p)),), torch.uint8, q.device,
+                           stream)
+    _call("sa_attn_tree", _bind().tree, index, stream, q, k_cache, v_cache, page_table, seq_lens,
+          scale, parents, new_lens, row_ptr, col_idx, k_scale, v_scale, o, lse, workspace,
+          dev_status)
+    return o, lse
+
+
+def sa_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    seq_lens: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor, *,
+                    k_sum: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                    lens_out: Optional[torch.Tensor] = None,
+                    dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The new tokens of an accepted path move together behind each sequence's
+    ``seq_lens`` tokens: token path[b][i] (int32 [B, S], ascending, i < path_lens[b]) to
+    place i, keys and values. ``k_sum`` of the pages touched is made anew from the
+    stored keys (``k_scale``: as in sa_cache_append), so path_lens = 0 takes all new
+    tokens back; ``lens_out`` receives the new lengths."""
+    index = _cuda_index(k_cache)
+    _call("sa_cache_accept", _bind().accept, index, stream, k_cache, v_cache, page_table,
+          seq_lens, path, path_lens, k_sum, k_scale, lens_out, dev_status)
+
+
+# --------------------------------------------------------------------- pages --
+
+def sa_pages_workspace_bytes(n_pages: int, rows: int) -> int:
+    return int(load_library().sa_pages_workspace_bytes(int(n_pages), int(rows)))
+
+
+def _pages_workspace(n_pages: int, rows: int, device, stream, workspace):
+    if workspace is not None:
+        return workspace
+    return _empty((max(256, sa_pages_workspace_bytes(n_pages, rows)),), torch.uint8, device, stream)
+
+
+def sa_pages_fork(page_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
+                  src: torch.Tensor, *, table_out: Optional[torch.Tensor] = None,
+                  lens_out: Optional[torch.Tensor] = None,
+                  refs_out: Optional[torch.Tensor] = None,
+                  moves: Optional[torch.Tensor] = None, n_moves: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  dev_status: Optional[torch.Tensor] = None, stream=None):
+    """A new table whose sequence i continues sequence src[i] (int32 [N]; -1: an empty
+    one) of the old one, which is given up: full pages are shared, the page in progress
+    is copied for all but the first. refs int32 [n_pages] counts the places that hold a
+    page (0: free). Returns (table_out [N, max_pages], lens_out [N], refs_out, moves
+    int32 [N, 2], n_moves [1]): pass moves and n_moves to sa_cache_copy for each layer's
+    caches. refs_out=refs counts in place."""
+    index = _cuda_index(page_table)
+    for t, name in ((page_table, "page_table"), (refs, "refs"), (src, "src")):
+        if not isinstance(t, torch.Tensor) or t.dim() != (2 if t is page_table else 1):
+            raise ValueError(f"{name} must be int32 " +
+                             ("[B, max_pages]" if name == "page_table" else "with one dimension"))
+    N, dev = src.shape[0], page_table.device
+    new = lambda *shape: _empty(shape, torch.int32, dev, stream)
+    table_out = new(N, page_table.shape[1]) if table_out is None else table_out
+    lens_out = new(N) if lens_out is None else lens_out
+    refs_out = new(refs.shape[0]) if refs_out is None else refs_out
+    moves = new(N, 2) if moves is None else moves
+    n_moves = new(1) if n_moves is None else n_moves
+    workspace = _pages_workspace(refs.shape[0], max(N, page_table.shape[0]), dev, stream, workspace)
+    _call("sa_pages_fork", _bind().fork, index, stream, page_table, seq_lens, refs, src, table_out,
+          lens_out, refs_out, moves, n_moves, workspace, dev_status)
+    return table_out, lens_out, refs_out, moves, n_moves
+
+
+def sa_pages_resize(page_table: torch.Tensor, refs: torch.Tensor, seq_lens: torch.Tensor,
+                    more: int = 0, *, more_lens: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Every sequence holds exactly the pages for seq_lens[b] + more tokens
+    (``more_lens`` int32 [B] in place of ``more``): missing ones are taken from the free
+    ones (refs 0), those behind are given back. Changes page_table and refs."""
+    index = _cuda_index(page_table)
+    if workspace is None:
+        for t, name in ((page_table, "page_table"), (refs, "refs")):
+            if not isinstance(t, torch.Tensor) or t.dim() < 1:
+                raise ValueError(f"{name} must be an int32 tensor")
+        workspace = _pages_workspace(refs.shape[0], page_table.shape[0], page_table.device, stream,
+                                     None)
+    _call("sa_pages_resize", _bind().resize, index, stream, page_table, refs, seq_lens, more,
+          more_lens, workspace, dev_status)
+
+
+def sa_pages_compact(page_table: Optional[torch.Tensor], refs: torch.Tensor, *,
+                     table_out: Optional[torch.Tensor] = None,
+                     refs_out: Optional[torch.Tensor] = None,
+                     moves: Optional[torch.Tensor] = None,
+                     n_moves: Optional[torch.Tensor] = None,
+                     n_used: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None, stream=None):
+    """The pages in use (refs > 0) move to the front of the pool. Returns (table_out,
+    refs_out, moves int32 [n, 2], n_moves [1], n_used [1]): the table and counts by the
+    new ids, the pairs (page, new id) for sa_cache_copy, how many pages are in use.
+    table_out=page_table and refs_out=refs work in place."""
+    index = _cuda_index(refs)
+    new = lambda *shape: _empty(shape, torch.int32, refs.device, stream)
+    if page_table is not None and table_out is None:
+        table_out = new(*page_table.shape)
+    refs_out = new(refs.shape[0]) if refs_out is None else refs_out
+    moves = new(max(1, refs.shape[0] // 2), 2) if moves is None else moves
+    n_moves = new(1) if n_moves is None else n_moves
+    n_used = new(1) if n_used is None else n_used
+    workspace = _pages_workspace(refs.shape[0], 1 if page_table is None else page_table.shape[0],
+                                 refs.device, stream, workspace)
+    _call("sa_pages_compact", _bind().compact, index, stream, refs, page_table, table_out,
+          refs_out, moves, n_moves, n_used, workspace, dev_status)
+    return table_out, refs_out, moves, n_moves, n_used
+
+
+def sa_cache_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, moves: torch.Tensor,
+                  n_moves: Optional[torch.Tensor] = None, *,
+                  k_sum: Optional[torch.Tensor] = None,
+                  dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Page moves[i][0] to page moves[i][1] (int32 [n, 2]) for i < n_moves (int32 [1], all
+    without): keys, values and, where given, key sums of one layer's caches."""
+    index = _cuda_index(k_cache)
+    _call("sa_cache_copy", _bind().copy, index, stream, k_cache, v_cache, moves, n_moves, k_sum,
+          dev_status)
 
 
 def check_dev_status(dev_status: torch.Tensor, what: str = "device status") -> None:

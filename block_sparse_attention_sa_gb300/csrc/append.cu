@@ -139,9 +139,40 @@ struct Angle {
   float4 c, s;
 };
 
-template <int D>
-__device__ __forceinline__ Angle angle_at(const AppendArgs& a, int t, int l) {
+// The axes of a lane's four pairs (kAxes), a byte each.
+__device__ __forceinline__ uint32_t lane_axes(const AppendArgs& a, int l) {
+  return reinterpret_cast<const uint32_t*>(a.axes.axis_of)[l];
+}
+
+// Of new token s of sequence b at place t. kAxes: a row of the tables for each pair,
+// where a lane's pairs share an axis (as all but a few lanes' do) one for the four.
+template <int D, bool kAxes>
+__device__ __forceinline__ Angle angle_at(const AppendArgs& a, int b, int s, int t, int l, uint32_t axes,
+                                          int* status) {
   Angle g{make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (kAxes) {
+    bool out = false;
+    if (axes == (axes & 0xffu) * 0x01010101u) {
+      if ((axes & 0xffu) == SA_ROPE_STAYS) return g;
+      const int64_t at = static_cast<int64_t>(axis_row(a.axes, b, s, axes & 0xff, t, &out)) * (D / 2) + 4 * l;
+      g.c = get(reinterpret_cast<const float4*>(a.cos + at));
+      g.s = get(reinterpret_cast<const float4*>(a.sin + at));
+    } else {
+      float c[4] = {1.f, 1.f, 1.f, 1.f}, si[4] = {};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int axis = axes >> (8 * i) & 0xff;
+        if (axis == SA_ROPE_STAYS) continue;
+        const int64_t at = static_cast<int64_t>(axis_row(a.axes, b, s, axis, t, &out)) * (D / 2) + 4 * l + i;
+        c[i] = get(a.cos + at);
+        si[i] = get(a.sin + at);
+      }
+      g.c = make_float4(c[0], c[1], c[2], c[3]);
+      g.s = make_float4(si[0], si[1], si[2], si[3]);
+    }
+    if (out) *status |= SA_DEV_CAPACITY;
+    return g;
+  }
   if (a.cos) {
     const int64_t at = static_cast<int64_t>(t) * (D / 2) + 4 * l;
     g.c = get(reinterpret_cast<const float4*>(a.cos + at));
@@ -151,8 +182,9 @@ __device__ __forceinline__ Angle angle_at(const AppendArgs& a, int t, int l) {
 }
 
 // Norm and rotation of a vector held by D / 8 lanes of a converged warp.
-template <int D, bool kHalf>
-__device__ __forceinline__ void turn(Vec& v, const AppendArgs& a, const float* gamma, const Angle& g) {
+template <int D, bool kHalf, bool kAxes>
+__device__ __forceinline__ void turn(Vec& v, const AppendArgs& a, const float* gamma, const Angle& g,
+                                     uint32_t axes) {
   if (a.norm) {
     float ss = 0.f;
 #pragma unroll
@@ -169,6 +201,8 @@ __device__ __forceinline__ void turn(Vec& v, const AppendArgs& a, const float* g
     for (int i = 0; i < 4; ++i) {
       float& p = v.x[kHalf ? i : 2 * i];
       float& q = v.x[kHalf ? 4 + i : 2 * i + 1];
+      // infinities beside a pair that stays are not its affair
+      if (kAxes && (axes >> (8 * i) & 0xffu) == SA_ROPE_STAYS) continue;
       const float p0 = p, q0 = q;
       p = fmaf(p0, c[i], -q0 * s[i]);
       q = fmaf(p0, s[i], q0 * c[i]);
@@ -177,13 +211,14 @@ __device__ __forceinline__ void turn(Vec& v, const AppendArgs& a, const float* g
 }
 
 // How many of the new tokens of sequence b have a place: in its page table, and
-// in the rotation tables where there are some.
+// in the rotation tables where there are some (with axes any position has a row).
+template <bool kAxes>
 __device__ __forceinline__ int tokens_of(const AppendArgs& a, int b, int* base, int* status) {
   bool bad;
   *base = clamp_len(get(a.pm.seq_lens + b), a.pm, &bad);
   int n = a.new_lens ? min(max(get(a.new_lens + b), 0), a.S) : a.S;
   int room = a.pm.max_pages * kBlock - *base;
-  if (a.cos) room = min(room, max(0, a.rope_rows - *base));
+  if (!kAxes && a.cos) room = min(room, max(0, a.rope_rows - *base));
   if (bad) *status |= SA_DEV_BAD_CACHE;
   if (n > room) {
     n = room;
@@ -203,7 +238,7 @@ __device__ __forceinline__ int page_of(const AppendArgs& a, int b, int t, int* s
 // A key-value unit: the tokens of this call in page place `pu` (counted from
 // the first one touched) of sequence b, one head; kShare lane groups take
 // every kShare-th token. Returns with the lanes' sums of what they stored.
-template <int D, bool kFp8, bool kHalf, int kShare>
+template <int D, bool kFp8, bool kHalf, bool kAxes, int kShare>
 __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int pu, int h, int grp,
                                                int l, bool there, int* page, int* slot0,
                                                float* sum, int* status) {
@@ -226,7 +261,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
     cv = scale_of(a.v_scale, h);
   }
   int base = 0;
-  const int n = there ? tokens_of(a, b, &base, status) : 0;
+  const int n = there ? tokens_of<kAxes>(a, b, &base, status) : 0;
   // tokens [s0, s1) of the page
   const int64_t edge = (static_cast<int64_t>(base / kBlock) + pu) * kBlock - base;
   const int s0 = edge > 0 ? static_cast<int>(min(edge, static_cast<int64_t>(n))) : 0;
@@ -240,6 +275,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
   // where the next one is read and stored
   int left = (s1 - s0 - grp + kShare - 1) / kShare;
   int t = base + s0 + grp;
+  const uint32_t axes = kAxes ? lane_axes(a, l) : 0u;
   k += (s0 + grp) * a.ks[1];
   v += (s0 + grp) * a.vs[1];
   const int64_t k_step = kShare * a.ks[1], v_step = kShare * a.vs[1];
@@ -261,7 +297,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
         kw[u] = load8<D, kHalf>(k, l);
         vw[u] = load8<D, false>(v, l);
       }
-      g[u] = angle_at<D>(a, t + u * kShare, l);
+      g[u] = angle_at<D, kAxes>(a, b, t - base + u * kShare, t + u * kShare, l, axes, status);
       k += k_step;
       v += v_step;
     }
@@ -269,7 +305,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
     for (int u = 0; u < kTokens; ++u) {
       const bool on = u < left;
       Vec y = unpack(on ? kw[u] : make_uint4(0u, 0u, 0u, 0u));
-      turn<D, kHalf>(y, a, gk, g[u]);
+      turn<D, kHalf, kAxes>(y, a, gk, g[u], axes);
       if (!on) continue;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += y.x[i];
@@ -290,7 +326,7 @@ __device__ __forceinline__ void key_value_unit(const AppendArgs& a, int b, int p
 }
 
 // kWhole: a CTA takes one key-value unit, else each of its lane groups one.
-template <int D, bool kFp8, bool kHalf, bool kWhole>
+template <int D, bool kFp8, bool kHalf, bool kAxes, bool kWhole>
 __global__ void __launch_bounds__(D, (kWhole ? 7 : 4) * 128 / D) append_kernel(AppendArgs a, int units, int page_units,
                                                           int kv_ctas, int per_log2) {
   constexpr int L = D / 8;
@@ -305,11 +341,11 @@ __global__ void __launch_bounds__(D, (kWhole ? 7 : 4) * 128 / D) append_kernel(A
     const int pu = there ? bp - b * static_cast<unsigned>(page_units) : 0;
     int page, slot0;
     float sum[8];
-    key_value_unit<D, kFp8, kHalf, kWhole ? kGroups : 1>(a, b, pu, h, kWhole ? grp : 0, l, there,
+    key_value_unit<D, kFp8, kHalf, kAxes, kWhole ? kGroups : 1>(a, b, pu, h, kWhole ? grp : 0, l, there,
                                                          &page, &slot0, sum, &status);
     if (there && a.lens_out && pu == 0 && h == 0 && l == 0 && (!kWhole || grp == 0)) {
       int base;
-      const int n = tokens_of(a, b, &base, &status);
+      const int n = tokens_of<kAxes>(a, b, &base, &status);
       a.lens_out[b] = base + n;
     }
     if (kWhole && a.k_sum) {
@@ -364,13 +400,14 @@ __global__ void __launch_bounds__(D, (kWhole ? 7 : 4) * 128 / D) append_kernel(A
     for (int i = 0; i < 8; ++i) gq[i] = 1.f;
     if (a.gamma_q) load8f<D, kHalf>(a.gamma_q, l, gq);
     int base = 0, none = 0;             // the key-value CTAs report what is wrong
-    bool on = there && s < tokens_of(a, b, &base, &none);
+    bool on = there && s < tokens_of<kAxes>(a, b, &base, &none);
     const int t = base + (on ? s : 0);
     if (!__any_sync(0xffffffffu, on)) return;
     // the queries and their angles are on their way while the page is looked up
     if (!early) load(0, on);
     Angle g = {};
-    if (on) g = angle_at<D>(a, t, l);
+    const uint32_t axes = kAxes ? lane_axes(a, l) : 0u;
+    if (on) g = angle_at<D, kAxes>(a, b, s, t, l, axes, &none);
     on = on && page_of(a, b, t, &none) >= 0;
     for (int h0 = 0; h0 < a.H; h0 += kQueryHeads * per) {
       if (h0 > 0) load(h0, on);
@@ -379,7 +416,7 @@ __global__ void __launch_bounds__(D, (kWhole ? 7 : 4) * 128 / D) append_kernel(A
         if (h0 + u * per >= a.H) break;
         const int h = h0 + u * per + hg;
         Vec y = unpack(w[u]);
-        turn<D, kHalf>(y, a, gq, g);
+        turn<D, kHalf, kAxes>(y, a, gq, g, axes);
         if (on && h < a.H) store8<D, kHalf>(out + h * a.os[2], l, pack(y));
       }
     }
@@ -387,7 +424,7 @@ __global__ void __launch_bounds__(D, (kWhole ? 7 : 4) * 128 / D) append_kernel(A
   if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
-template <int D, bool kFp8, bool kHalf>
+template <int D, bool kFp8, bool kHalf, bool kAxes>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   // the pages S tokens can touch, wherever the first of them lies
   const int64_t page_units = (static_cast<int64_t>(a.S) + kBlock - 2) / kBlock + 1;
@@ -404,16 +441,22 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
   const int64_t at_once = kGroups >> per_log2;
   const int64_t grid = kv + (a.q ? (tokens + at_once - 1) / at_once : 0);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const auto kernel = whole ? append_kernel<D, kFp8, kHalf, true> : append_kernel<D, kFp8, kHalf, false>;
+  const auto kernel = whole ? append_kernel<D, kFp8, kHalf, kAxes, true>
+                            : append_kernel<D, kFp8, kHalf, kAxes, false>;
   kernel<<<static_cast<unsigned>(grid), D, 0, st>>>(
       a, static_cast<int>(units), static_cast<int>(page_units), static_cast<int>(kv), per_log2);
   return cudaGetLastError();
 }
 
+template <int D, bool kFp8, bool kHalf>
+cudaError_t launch_axes(const AppendArgs& a, cudaStream_t st) {
+  return a.axes.n_axes > 0 ? launch<D, kFp8, kHalf, true>(a, st) : launch<D, kFp8, kHalf, false>(a, st);
+}
+
 template <int D>
 cudaError_t launch_d(const AppendArgs& a, bool fp8, bool half, cudaStream_t st) {
-  if (fp8) return half ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
-  return half ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+  if (fp8) return half ? launch_axes<D, true, true>(a, st) : launch_axes<D, true, false>(a, st);
+  return half ? launch_axes<D, false, true>(a, st) : launch_axes<D, false, false>(a, st);
 }
 
 }  // namespace

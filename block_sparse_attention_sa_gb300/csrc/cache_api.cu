@@ -115,6 +115,28 @@ sa_status encode_cache(CUtensorMap* m, const void* base, const sa_cache_params* 
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_INVALID_ARG;
 }
 
+// A pool of n_pages and a table of `rows` sequences, `stride` entries apart.
+sa_status check_pages(int64_t n_pages, int64_t max_pages, int64_t rows, int64_t stride) {
+  if (n_pages < 1 || max_pages < 1 || rows < 1) return SA_ERR_INVALID_ARG;
+  if (rows > 1 && stride < max_pages) return SA_ERR_INVALID_ARG;
+  if (n_pages >= (1 << 25) || max_pages >= (1 << 25) || rows > 65535) return SA_ERR_UNSUPPORTED;
+  return SA_OK;
+}
+
+sa_status check_pages_ws(int n_pages, int rows, const void* ws, size_t bytes) {
+  if (!ws || !aligned(ws, 256)) return SA_ERR_INVALID_ARG;
+  return bytes < pages_ws_bytes(n_pages, rows) ? SA_ERR_CAPACITY : SA_OK;
+}
+
+int64_t table_entries(int64_t max_pages, int64_t rows, int64_t stride) {
+  return (rows - 1) * stride + max_pages;
+}
+
+bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(m) * 4 && y < x + static_cast<uintptr_t>(n) * 4;
+}
+
 sa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
 
 }  // namespace
@@ -149,15 +171,17 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
   copy3(p->vc_stride, cs);
 }
 
-sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v, const void* q,
-                          void* q_out, const float* gamma_q, const float* gamma_k,
-                          const float* rope_cos, const float* rope_sin, void* k_cache,
-                          void* v_cache, const float* k_scale, const float* v_scale, float* k_sum,
-                          const int32_t* page_table, const int32_t* seq_lens,
-                          const int32_t* new_lens, int32_t* lens_out, int32_t* dev_status,
-                          void* stream) {
+static sa_status append(const sa_cache_params* p, const void* k, const void* v, const void* q,
+                        void* q_out, const float* gamma_q, const float* gamma_k,
+                        const float* rope_cos, const float* rope_sin, const sa_rope_axes* axes,
+                        void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
+                        float* k_sum, const int32_t* page_table, const int32_t* seq_lens,
+                        const int32_t* new_lens, int32_t* lens_out, int32_t* dev_status,
+                        void* stream) {
   sa_status s = check_cache(p);
   if (s != SA_OK) return s;
+  if (axes && ((s = check_axes(axes, p->B, p->S, p->D)) != SA_OK)) return s;
+  if (axes && (!rope_cos || !rope_sin)) return SA_ERR_INVALID_ARG;
   if (!k || !v || (q == nullptr) != (q_out == nullptr)) return SA_ERR_INVALID_ARG;
   if ((s = check_pool(p, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)) != SA_OK)
     return s;
@@ -213,9 +237,36 @@ sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v
   a.rope_rows = p->rope_rows;
   a.eps = p->eps;
   a.norm = p->qk_norm;
+  if (axes) a.axes = *axes;
   return from_cuda(launch_append(a, p->D, p->cache_format == SA_CACHE_FP8,
                                  p->rope_layout == SA_ROPE_HALF,
                                  static_cast<cudaStream_t>(stream)));
+}
+
+sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v, const void* q,
+                          void* q_out, const float* gamma_q, const float* gamma_k,
+                          const float* rope_cos, const float* rope_sin, void* k_cache,
+                          void* v_cache, const float* k_scale, const float* v_scale, float* k_sum,
+                          const int32_t* page_table, const int32_t* seq_lens,
+                          const int32_t* new_lens, int32_t* lens_out, int32_t* dev_status,
+                          void* stream) {
+  return append(p, k, v, q, q_out, gamma_q, gamma_k, rope_cos, rope_sin, nullptr, k_cache, v_cache,
+                k_scale, v_scale, k_sum, page_table, seq_lens, new_lens, lens_out, dev_status,
+                stream);
+}
+
+sa_status sa_cache_append_axes(const sa_cache_params* p, const void* k, const void* v,
+                               const void* q, void* q_out, const float* gamma_q,
+                               const float* gamma_k, const float* rope_cos,
+                               const float* rope_sin, const sa_rope_axes* axes, void* k_cache,
+                               void* v_cache, const float* k_scale, const float* v_scale,
+                               float* k_sum, const int32_t* page_table, const int32_t* seq_lens,
+                               const int32_t* new_lens, int32_t* lens_out, int32_t* dev_status,
+                               void* stream) {
+  if (!axes) return SA_ERR_INVALID_ARG;
+  return append(p, k, v, q, q_out, gamma_q, gamma_k, rope_cos, rope_sin, axes, k_cache, v_cache,
+                k_scale, v_scale, k_sum, page_table, seq_lens, new_lens, lens_out, dev_status,
+                stream);
 }
 
 int64_t sa_route_pages_max_nnz(const sa_cache_params* p) {
@@ -260,31 +311,42 @@ sa_status sa_route_pages(const sa_cache_params* p, const void* q, const float* k
 
 size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p) {
   if (check_cache(p) != SA_OK || p->S != 1) return 0;
-  return decode_ws_bytes(p->H, p->H_kv, p->D);
+  return decode_ws_bytes(p->H / p->H_kv, p->D);
 }
 
-sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_cache,
-                         const void* v_cache, const float* k_scale, const float* v_scale,
-                         const int32_t* page_table, const int32_t* seq_lens,
-                         const int32_t* row_ptr, const int32_t* col_idx, int64_t col_cap,
-                         void* o, float* lse, void* workspace, size_t ws_bytes,
-                         int32_t* dev_status, void* stream) {
+size_t sa_attn_tree_workspace_bytes(const sa_cache_params* p) {
+  if (check_cache(p) != SA_OK || p->S > SA_TREE_MAX) return 0;
+  return decode_ws_bytes(p->S * (p->H / p->H_kv), p->D);
+}
+
+// Attention over the cache: of one new token, or (tree) of a few.
+static sa_status attend(const sa_cache_params* p, const void* q, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale,
+                        const int32_t* page_table, const int32_t* seq_lens,
+                        const int32_t* new_lens, const int32_t* parents, int64_t parent_stride,
+                        const int32_t* row_ptr, const int32_t* col_idx, int64_t col_cap, void* o,
+                        float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                        void* stream, bool tree) {
   sa_status s = check_cache(p);
   if (s != SA_OK) return s;
-  if (p->S != 1) return SA_ERR_UNSUPPORTED;
-  // the pages of all units are counted in 31 bits
-  if (static_cast<int64_t>(p->B) * p->H_kv * decode_row_tiles(p->H, p->H_kv) >
-      INT32_MAX / static_cast<int64_t>(p->max_pages))
+  if (p->S > (tree ? SA_TREE_MAX : 1)) return SA_ERR_UNSUPPORTED;
+  // the pages of all units are counted in 31 bits; with a tree a row of the route may
+  // list the two that hold new tokens besides
+  const int rows = p->S * (p->H / p->H_kv);
+  if (static_cast<int64_t>(p->B) * p->H_kv * decode_row_tiles(rows) >
+      INT32_MAX / (static_cast<int64_t>(p->max_pages) + (tree ? 2 : 0)))
     return SA_ERR_UNSUPPORTED;
   if (col_cap < 0) return SA_ERR_INVALID_ARG;
   if (!q || !o || !workspace || (row_ptr == nullptr) != (col_idx == nullptr))
+    return SA_ERR_INVALID_ARG;
+  if (parents && p->B > 1 && (parent_stride < 0 || (parent_stride > 0 && parent_stride < p->S)))
     return SA_ERR_INVALID_ARG;
   if ((s = check_pool(p, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)) != SA_OK)
     return s;
   if ((s = check_tokens(p, q, p->q_stride, p->H)) != SA_OK) return s;
   if ((s = check_tokens(p, o, p->o_stride, p->H)) != SA_OK) return s;
   if (!aligned(workspace, 256)) return SA_ERR_INVALID_ARG;
-  if (ws_bytes < sa_attn_decode_workspace_bytes(p)) return SA_ERR_CAPACITY;
+  if (ws_bytes < decode_ws_bytes(rows, p->D)) return SA_ERR_CAPACITY;
   if (o == q) return SA_ERR_INVALID_ARG;       // read by CTAs that others' outputs would meet
   DecodeArgs a{};
   a.pm = page_map(p, page_table, seq_lens);
@@ -304,9 +366,13 @@ sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_
   a.lse = lse;
   a.dev_status = dev_status;
   a.B = p->B;
+  a.S = p->S;
   a.H = p->H;
   a.Hkv = p->H_kv;
   a.D = p->D;
+  a.new_lens = new_lens;
+  a.parents = parents;
+  a.parent_stride = p->B > 1 ? parent_stride : 0;
   const double scale = p->softmax_scale > 0.f ? static_cast<double>(p->softmax_scale)
                                               : 1.0 / std::sqrt(static_cast<double>(p->D));
   a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
@@ -314,8 +380,196 @@ sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_
   CUtensorMap kmap, vmap;
   if ((s = encode_cache(&kmap, k_cache, p, p->kc_stride)) != SA_OK) return s;
   if ((s = encode_cache(&vmap, v_cache, p, p->vc_stride)) != SA_OK) return s;
-  return from_cuda(launch_decode(a, kmap, vmap, p->cache_format == SA_CACHE_FP8,
-                                 static_cast<cudaStream_t>(stream)));
+  const bool fp8 = p->cache_format == SA_CACHE_FP8;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return from_cuda(tree ? launch_tree(a, kmap, vmap, fp8, st) : launch_decode(a, kmap, vmap, fp8, st));
+}
+
+sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_cache,
+                         const void* v_cache, const float* k_scale, const float* v_scale,
+                         const int32_t* page_table, const int32_t* seq_lens,
+                         const int32_t* row_ptr, const int32_t* col_idx, int64_t col_cap,
+                         void* o, float* lse, void* workspace, size_t ws_bytes,
+                         int32_t* dev_status, void* stream) {
+  return attend(p, q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, nullptr, nullptr,
+                0, row_ptr, col_idx, col_cap, o, lse, workspace, ws_bytes, dev_status, stream,
+                false);
+}
+
+sa_status sa_attn_tree(const sa_cache_params* p, const void* q, const void* k_cache,
+                       const void* v_cache, const float* k_scale, const float* v_scale,
+                       const int32_t* page_table, const int32_t* seq_lens,
+                       const int32_t* new_lens, const int32_t* parents, int64_t parent_stride,
+                       const int32_t* row_ptr, const int32_t* col_idx, int64_t col_cap, void* o,
+                       float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                       void* stream) {
+  return attend(p, q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, new_lens, parents,
+                parent_stride, row_ptr, col_idx, col_cap, o, lse, workspace, ws_bytes, dev_status,
+                stream, true);
+}
+
+sa_status sa_cache_accept(const sa_cache_params* p, void* k_cache, void* v_cache,
+                          const float* k_scale, float* k_sum, const int32_t* page_table,
+                          const int32_t* seq_lens, const int32_t* path, int64_t path_stride,
+                          const int32_t* path_lens, int32_t* lens_out, int32_t* dev_status,
+                          void* stream) {
+  sa_status s = check_cache(p);
+  if (s != SA_OK) return s;
+  if (p->S > SA_TREE_MAX) return SA_ERR_UNSUPPORTED;
+  if ((s = check_pool(p, k_cache, v_cache, k_scale, nullptr, page_table, seq_lens)) != SA_OK)
+    return s;
+  if (!path || !path_lens || !aligned(k_sum, 16)) return SA_ERR_INVALID_ARG;
+  if (p->B > 1 && path_stride < p->S) return SA_ERR_INVALID_ARG;
+  // written by some CTAs while others still read those
+  if (lens_out && (lens_overlap(lens_out, seq_lens, p->B) || lens_overlap(lens_out, path_lens, p->B)))
+    return SA_ERR_INVALID_ARG;
+  AcceptArgs a{};
+  a.pm = page_map(p, page_table, seq_lens);
+  a.kc = static_cast<char*>(k_cache);
+  a.vc = static_cast<char*>(v_cache);
+  const int64_t elt = p->cache_format == SA_CACHE_FP8 ? 1 : 2;
+  for (int i = 0; i < 3; ++i) {
+    a.kcs[i] = p->kc_stride[i] * elt;
+    a.vcs[i] = p->vc_stride[i] * elt;
+  }
+  a.k_scale = k_scale;
+  a.k_sum = k_sum;
+  a.path = path;
+  a.path_stride = p->B > 1 ? path_stride : 0;
+  a.path_lens = path_lens;
+  a.lens_out = lens_out;
+  a.dev_status = dev_status;
+  a.B = p->B;
+  a.S = p->S;
+  a.Hkv = p->H_kv;
+  return from_cuda(launch_accept(a, p->D, elt == 1, static_cast<cudaStream_t>(stream)));
+}
+
+sa_status sa_cache_copy(const sa_cache_params* p, void* k_cache, void* v_cache, float* k_sum,
+                        const int32_t* moves, int64_t move_cap, const int32_t* n_moves,
+                        int32_t* dev_status, void* stream) {
+  sa_status s = check_cache(p);
+  if (s != SA_OK) return s;
+  // no table or lengths here: the moves stand in for them in the check of the pool
+  if ((s = check_pool(p, k_cache, v_cache, nullptr, nullptr, moves, moves)) != SA_OK) return s;
+  if (move_cap < 1 || !aligned(k_sum, 16)) return SA_ERR_INVALID_ARG;
+  if (move_cap > INT32_MAX) return SA_ERR_UNSUPPORTED;
+  CopyArgs a{};
+  a.kc = static_cast<char*>(k_cache);
+  a.vc = static_cast<char*>(v_cache);
+  const int64_t elt = p->cache_format == SA_CACHE_FP8 ? 1 : 2;
+  for (int i = 0; i < 3; ++i) {
+    a.kcs[i] = p->kc_stride[i] * elt;
+    a.vcs[i] = p->vc_stride[i] * elt;
+  }
+  a.k_sum = k_sum;
+  a.moves = moves;
+  a.n_moves = n_moves;
+  a.move_cap = move_cap;
+  a.dev_status = dev_status;
+  a.n_pages = p->n_pages;
+  a.Hkv = p->H_kv;
+  a.D = p->D;
+  a.row_bytes = static_cast<int>(p->D * elt);
+  return from_cuda(launch_copy(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sa_pages_workspace_bytes(int32_t n_pages, int32_t rows) {
+  return check_pages(n_pages, 1, rows, 1) == SA_OK ? pages_ws_bytes(n_pages, rows) : 0;
+}
+
+sa_status sa_pages_fork(int32_t n_pages, int32_t max_pages, int32_t B, int32_t N,
+                        const int32_t* page_table, int64_t table_stride,
+                        const int32_t* seq_lens, const int32_t* refs, const int32_t* src,
+                        int32_t* table_out, int64_t out_stride, int32_t* lens_out,
+                        int32_t* refs_out, int32_t* moves, int32_t* n_moves, void* workspace,
+                        size_t ws_bytes, int32_t* dev_status, void* stream) {
+  sa_status s = check_pages(n_pages, max_pages, B, table_stride);
+  if (s != SA_OK || (s = check_pages(n_pages, max_pages, N, out_stride)) != SA_OK) return s;
+  if (!page_table || !seq_lens || !refs || !src || !table_out || !lens_out || !refs_out || !moves ||
+      !n_moves)
+    return SA_ERR_INVALID_ARG;
+  if ((s = check_pages_ws(n_pages, std::max(B, N), workspace, ws_bytes)) != SA_OK) return s;
+  const int64_t in = table_entries(max_pages, B, table_stride), out = table_entries(max_pages, N, out_stride);
+  if (overlap(table_out, out, page_table, in) || overlap(lens_out, N, seq_lens, B) ||
+      (refs_out != refs && overlap(refs_out, n_pages, refs, n_pages)))
+    return SA_ERR_INVALID_ARG;
+  PagesArgs a{};
+  a.table = page_table;
+  a.stride = table_stride;
+  a.table_out = table_out;
+  a.out_stride = out_stride;
+  a.lens = seq_lens;
+  a.refs = refs;
+  a.refs_out = refs_out;
+  a.src = src;
+  a.lens_out = lens_out;
+  a.moves = moves;
+  a.n_moves = n_moves;
+  a.ws = static_cast<int32_t*>(workspace);
+  a.dev_status = dev_status;
+  a.n_pages = n_pages;
+  a.max_pages = max_pages;
+  a.B = B;
+  a.N = N;
+  return from_cuda(launch_pages_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+sa_status sa_pages_resize(int32_t n_pages, int32_t max_pages, int32_t B, int32_t* page_table,
+                          int64_t table_stride, int32_t* refs, const int32_t* seq_lens,
+                          const int32_t* more_lens, int32_t more, void* workspace,
+                          size_t ws_bytes, int32_t* dev_status, void* stream) {
+  sa_status s = check_pages(n_pages, max_pages, B, table_stride);
+  if (s != SA_OK) return s;
+  if (!page_table || !seq_lens || !refs) return SA_ERR_INVALID_ARG;
+  if ((s = check_pages_ws(n_pages, B, workspace, ws_bytes)) != SA_OK) return s;
+  PagesArgs a{};
+  a.table = a.table_out = page_table;
+  a.stride = a.out_stride = table_stride;
+  a.lens = seq_lens;
+  a.more_lens = more_lens;
+  a.more = more;
+  a.refs = a.refs_out = refs;
+  a.ws = static_cast<int32_t*>(workspace);
+  a.dev_status = dev_status;
+  a.n_pages = n_pages;
+  a.max_pages = max_pages;
+  a.B = B;
+  return from_cuda(launch_pages_resize(a, static_cast<cudaStream_t>(stream)));
+}
+
+sa_status sa_pages_compact(int32_t n_pages, int32_t max_pages, int32_t B,
+                           const int32_t* page_table, int64_t table_stride, const int32_t* refs,
+                           int32_t* table_out, int64_t out_stride, int32_t* refs_out,
+                           int32_t* moves, int32_t* n_moves, int32_t* n_used, void* workspace,
+                           size_t ws_bytes, int32_t* dev_status, void* stream) {
+  sa_status s = B == 0 ? check_pages(n_pages, 1, 1, 1) : check_pages(n_pages, max_pages, B, table_stride);
+  if (s != SA_OK) return s;
+  if (B > 0 && (s = check_pages(n_pages, max_pages, B, out_stride)) != SA_OK) return s;
+  if ((B > 0) != (page_table != nullptr) || (B > 0) != (table_out != nullptr)) return SA_ERR_INVALID_ARG;
+  if (!refs || !refs_out || !moves || !n_moves || !n_used) return SA_ERR_INVALID_ARG;
+  if ((s = check_pages_ws(n_pages, std::max(B, 1), workspace, ws_bytes)) != SA_OK) return s;
+  if (B > 0 && !(table_out == page_table && (B == 1 || out_stride == table_stride)) &&
+      overlap(table_out, table_entries(max_pages, B, out_stride), page_table,
+              table_entries(max_pages, B, table_stride)))
+    return SA_ERR_INVALID_ARG;
+  if (refs_out != refs && overlap(refs_out, n_pages, refs, n_pages)) return SA_ERR_INVALID_ARG;
+  PagesArgs a{};
+  a.table = page_table;
+  a.stride = table_stride;
+  a.table_out = table_out;
+  a.out_stride = out_stride;
+  a.refs = refs;
+  a.refs_out = refs_out;
+  a.moves = moves;
+  a.n_moves = n_moves;
+  a.n_used = n_used;
+  a.ws = static_cast<int32_t*>(workspace);
+  a.dev_status = dev_status;
+  a.n_pages = n_pages;
+  a.max_pages = max_pages;
+  a.B = B;
+  return from_cuda(launch_pages_compact(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -36,11 +36,12 @@ struct AppendArgs {
   int B, S, H, Hkv, rope_rows;
   float eps;
   int norm;
+  sa_rope_axes axes;         // n_axes = 0: rows of the tables by place
 };
 
 struct DecodeArgs {
   PageMap pm;
-  const uint16_t* q;         // bf16 bits, [B, 1, H, D]
+  const uint16_t* q;         // bf16 bits, [B, S, H, D]
   const void* kc;
   const void* vc;
   int64_t qs[3], os[3], kcs[3], vcs[3];
@@ -52,9 +53,13 @@ struct DecodeArgs {
   uint16_t* o;
   float* lse;
   int32_t* dev_status;
-  int B, H, Hkv, D;
+  int B, S, H, Hkv, D;       // S: new tokens per sequence (1 but with a tree)
   float scale_log2;          // softmax_scale * log2(e)
   char* ws;
+  // a tree's; pm.seq_lens are then the lengths before the new tokens
+  const int32_t* new_lens;   // [B] or nullptr (S each)
+  const int32_t* parents;    // [B][parent_stride] or nullptr (each continues the last)
+  int64_t parent_stride;
 };
 
 struct RoutePagesArgs {
@@ -71,10 +76,66 @@ struct RoutePagesArgs {
 };
 
 cudaError_t launch_append(const AppendArgs& a, int D, bool fp8, bool half, cudaStream_t st);
-size_t decode_ws_bytes(int H, int Hkv, int D);
-int decode_row_tiles(int H, int Hkv);   // CTAs' worth of query heads on a key-value head
+// rows: query heads (of all new tokens of a sequence) on a key-value head
+size_t decode_ws_bytes(int rows, int D);
+int decode_row_tiles(int rows);         // CTAs' worth of them
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           bool fp8, cudaStream_t st);
+cudaError_t launch_tree(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        bool fp8, cudaStream_t st);
+
+struct AcceptArgs {
+  PageMap pm;
+  char* kc;
+  char* vc;
+  int64_t kcs[3], vcs[3];    // byte strides of page, head, token
+  const float* k_scale;
+  float* k_sum;
+  const int32_t* path;       // [B][path_stride]
+  const int32_t* path_lens;
+  int64_t path_stride;
+  int32_t* lens_out;
+  int32_t* dev_status;
+  int B, S, Hkv;
+};
+
+struct CopyArgs {
+  char* kc;
+  char* vc;
+  int64_t kcs[3], vcs[3];    // byte strides of page, head, token
+  float* k_sum;
+  const int32_t* moves;      // [move_cap][2]
+  const int32_t* n_moves;    // or nullptr (move_cap)
+  int64_t move_cap;
+  int32_t* dev_status;
+  int n_pages, Hkv, D, row_bytes;
+};
+
+// Tables and reference counts of a pool (sa_pages_*).
+struct PagesArgs {
+  const int32_t* table;      // [B][stride]
+  int64_t stride, out_stride;
+  int32_t* table_out;
+  const int32_t* lens;
+  const int32_t* more_lens;  // resize
+  const int32_t* refs;
+  int32_t* refs_out;
+  const int32_t* src;        // fork: [N]
+  int32_t* lens_out;
+  int32_t* moves;
+  int32_t* n_moves;
+  int32_t* n_used;           // compact
+  int32_t* ws;
+  int32_t* dev_status;
+  int n_pages, max_pages, B, N, more;
+};
+
+cudaError_t launch_accept(const AcceptArgs& a, int D, bool fp8, cudaStream_t st);
+cudaError_t launch_copy(const CopyArgs& a, cudaStream_t st);
+size_t pages_ws_bytes(int n_pages, int rows);
+cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t st);
+cudaError_t launch_pages_resize(const PagesArgs& a, cudaStream_t st);
+cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t st);
 size_t route_pages_ws_bytes(int64_t rows, int max_pages);
 cudaError_t launch_route_pages(const RoutePagesArgs& a, cudaStream_t st);
 

@@ -207,7 +207,10 @@ __global__ void __launch_bounds__(128) pool_kernel(RouteArgs a) {
 // sa_route would compute from the outputs, and Q and K are not read again.
 // Same grid and thread layout as pool_kernel; plain loads (the outputs may
 // overwrite the inputs in place).
-template <int D>
+//
+// kAxes (sa_qk_prologue_axes): a pair's row of the tables is the token's position on
+// the pair's axis; the tables hold positions, not tokens, and stay in L2.
+template <int D, bool kAxes>
 __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs pa) {
   constexpr int kLanes = D / 8;       // threads of one head vector
   constexpr int kChunk = 64;          // tokens whose rotary rows are staged at once
@@ -247,6 +250,11 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
 #pragma unroll
   for (int u = 0; u < 8; ++u) s[u] = c[u] = 0.f;
 
+  int stays = 0;                          // which of the thread's pairs are not turned
+  if (kAxes)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) stays |= (pa.axes.axis_of[d / 2 + v] == SA_ROPE_STAYS) << v;
+
   const int64_t off = b * st[0] + h * st[2] + d;
   for (int c0 = 0; c0 < n; c0 += kChunk) {
     const int nc = min(kChunk, n - c0);
@@ -258,9 +266,31 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
                           static_cast<size_t>(t0 + c0) * kRow4;
       const float4* sn4 = reinterpret_cast<const float4*>(pa.sin) +
                           static_cast<size_t>(t0 + c0) * kRow4;
-      for (int e = threadIdx.x; e < nc * kRow4; e += 128) {
-        reinterpret_cast<float4*>(&tab[0][0][0])[e] = cs4[e];
-        reinterpret_cast<float4*>(&tab[1][0][0])[e] = sn4[e];
+      if (kAxes) {
+        bool out = false;
+        for (int e = threadIdx.x; e < nc * kRow4; e += 128) {
+          const int t = e / kRow4, pair = e % kRow4 * 4;
+          float co[4], si[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int axis = pa.axes.axis_of[pair + v];
+            co[v] = 1.f;
+            si[v] = 0.f;
+            if (axis == SA_ROPE_STAYS) continue;
+            const int64_t at = static_cast<int64_t>(axis_row(pa.axes, b, t0 + c0 + t, axis, t0 + c0 + t, &out)) *
+                               (D / 2) + pair + v;
+            co[v] = pa.cos[at];
+            si[v] = pa.sin[at];
+          }
+          reinterpret_cast<float4*>(&tab[0][0][0])[e] = make_float4(co[0], co[1], co[2], co[3]);
+          reinterpret_cast<float4*>(&tab[1][0][0])[e] = make_float4(si[0], si[1], si[2], si[3]);
+        }
+        if (out && a.dev_status) atomicOr(a.dev_status, SA_DEV_CAPACITY);
+      } else {
+        for (int e = threadIdx.x; e < nc * kRow4; e += 128) {
+          reinterpret_cast<float4*>(&tab[0][0][0])[e] = cs4[e];
+          reinterpret_cast<float4*>(&tab[1][0][0])[e] = sn4[e];
+        }
       }
       __syncthreads();
     }
@@ -290,7 +320,7 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
         for (int v = 0; v < 8; ++v) ss = fmaf(x[v], x[v], ss);
 #pragma unroll
         for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = rsqrtf(ss * inv_d + pa.eps);
+        const float r = kAxes && !pa.norm ? 1.f : rsqrtf(ss * inv_d + pa.eps);
         float cv[4] = {1.f, 1.f, 1.f, 1.f}, sv[4] = {0.f, 0.f, 0.f, 0.f};
         if (rope && t + u < nc) {
           const float4 c4 = *reinterpret_cast<const float4*>(&tab[0][t + u][d / 2]);
@@ -304,8 +334,12 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
         for (int v = 0; v < 4; ++v) {
           const float y0 = x[2 * v] * r * g[2 * v];
           const float y1 = x[2 * v + 1] * r * g[2 * v + 1];
-          const float o0 = fmaf(y0, cv[v], -y1 * sv[v]);
-          const float o1 = fmaf(y0, sv[v], y1 * cv[v]);
+          float o0 = fmaf(y0, cv[v], -y1 * sv[v]);
+          float o1 = fmaf(y0, sv[v], y1 * cv[v]);
+          if (kAxes && (stays >> v & 1)) {      // infinities beside it are not its affair
+            o0 = y0;
+            o1 = y1;
+          }
           const __nv_bfloat162 hb = __floats2bfloat162_rn(o0, o1);
           packed[v] = *reinterpret_cast<const uint32_t*>(&hb);
           yr[2 * v] = bf16_to_f32(static_cast<uint16_t>(packed[v] & 0xffffu));
@@ -822,8 +856,10 @@ cudaError_t launch_pool_d(const RouteArgs& a, const PrologueArgs* pa, cudaStream
       cudaMemsetAsync(a.ws + a.L.kmax, 0, sizeof(int) * static_cast<size_t>(a.B) * a.H, st);
   if (e != cudaSuccess) return e;
   dim3 grid(a.Nb, (a.H * D + 1023) / 1024, 2 * a.B);
-  if (pa)
-    prologue_kernel<D><<<grid, 128, 0, st>>>(a, *pa);
+  if (pa && pa->axes.n_axes > 0)
+    prologue_kernel<D, true><<<grid, 128, 0, st>>>(a, *pa);
+  else if (pa)
+    prologue_kernel<D, false><<<grid, 128, 0, st>>>(a, *pa);
   else
     pool_kernel<D><<<grid, 128, 0, st>>>(a);
   return cudaGetLastError();

@@ -311,6 +311,19 @@ HostPipe* host_pipe(int dev) {
 }
 
 }  // namespace
+// Axes that the kernels can index: every pair's axis is one of them, and the positions'
+// strides go forward.
+sa_status check_axes(const sa_rope_axes* x, int B, int S, int D) {
+  if (!x || x->n_axes < 1 || x->n_axes > 8 || x->rows < 1) return SA_ERR_INVALID_ARG;
+  for (int i = 0; i < D / 2; ++i)
+    if (x->axis_of[i] >= x->n_axes && x->axis_of[i] != SA_ROPE_STAYS) return SA_ERR_INVALID_ARG;
+  if (!x->positions) return SA_OK;
+  if ((reinterpret_cast<uintptr_t>(x->positions) & 3u) != 0) return SA_ERR_INVALID_ARG;
+  // one sequence's or one token's positions may serve all (a stride of 0)
+  if ((B > 1 && x->pos_stride[0] < 0) || (S > 1 && x->pos_stride[1] < 0)) return SA_ERR_INVALID_ARG;
+  return SA_OK;
+}
+
 }  // namespace sa
 
 using namespace sa;
@@ -468,6 +481,38 @@ sa_status sa_qk_prologue(const sa_params* p, const void* q_in, const void* k_in,
   pa.eps = eps;
   pa.q_out = static_cast<uint16_t*>(q_out);
   pa.k_out = static_cast<uint16_t*>(k_out);
+  return from_cuda(launch_pool(a, &pa, static_cast<cudaStream_t>(stream)));
+}
+
+sa_status sa_qk_prologue_axes(const sa_params* p, const void* q_in, const void* k_in,
+                              int32_t qk_norm, const float* gamma_q, const float* gamma_k,
+                              float eps, const float* rope_cos, const float* rope_sin,
+                              const sa_rope_axes* axes, void* q_out, void* k_out,
+                              void* workspace, size_t ws_bytes, int32_t* dev_status,
+                              void* stream) {
+  sa_status s = check_params(p);
+  if (s != SA_OK) return s;
+  if ((s = check_axes(axes, p->B, p->S, p->D)) != SA_OK) return s;
+  if (!q_in || !k_in || !q_out || !k_out || !rope_cos || !rope_sin) return SA_ERR_INVALID_ARG;
+  if (!aligned16(q_in) || !aligned16(k_in) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(gamma_q) || !aligned16(gamma_k) || !aligned16(rope_cos) || !aligned16(rope_sin))
+    return SA_ERR_INVALID_ARG;
+  if (qk_norm != 0 && qk_norm != 1) return SA_ERR_INVALID_ARG;
+  if (!qk_norm && (gamma_q || gamma_k)) return SA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return SA_ERR_INVALID_ARG;
+  RouteArgs a;
+  s = route_args(p, q_in, k_in, nullptr, nullptr, 0, workspace, ws_bytes, dev_status, &a);
+  if (s != SA_OK) return s;
+  PrologueArgs pa{};
+  pa.gamma_q = gamma_q;
+  pa.gamma_k = gamma_k;
+  pa.cos = rope_cos;
+  pa.sin = rope_sin;
+  pa.eps = eps;
+  pa.q_out = static_cast<uint16_t*>(q_out);
+  pa.k_out = static_cast<uint16_t*>(k_out);
+  pa.norm = qk_norm;
+  pa.axes = *axes;
   return from_cuda(launch_pool(a, &pa, static_cast<cudaStream_t>(stream)));
 }
 
@@ -649,7 +694,7 @@ sa_status sa_forward_host(const sa_params* p, const void* q_host, const void* k_
 
 sa_status sa_dev_status_decode(int32_t d) {
   if (d & SA_DEV_TIMEOUT) return SA_ERR_TIMEOUT;
-  if (d & (SA_DEV_BAD_ROUTE | SA_DEV_BAD_CACHE)) return SA_ERR_INVALID_ARG;
+  if (d & (SA_DEV_BAD_ROUTE | SA_DEV_BAD_CACHE | SA_DEV_BAD_TREE)) return SA_ERR_INVALID_ARG;
   if (d & SA_DEV_CAPACITY) return SA_ERR_CAPACITY;
   if (d & SA_DEV_RANGE) return SA_ERR_UNSUPPORTED;
   return SA_OK;

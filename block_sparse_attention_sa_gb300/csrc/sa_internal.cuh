@@ -72,7 +72,22 @@ struct PrologueArgs {
   float eps;
   uint16_t* q_out;         // bf16 bits, strides of q (may equal q)
   uint16_t* k_out;         // strides of k (may equal k)
+  int norm;                // with axes: whether the norm is applied (else it always is)
+  sa_rope_axes axes;       // n_axes = 0: none
 };
+
+sa_status check_axes(const sa_rope_axes* axes, int B, int S, int D);
+
+#ifdef __CUDACC__
+// The row of the rotation tables for a token's position on an axis; *out: it had none.
+__device__ __forceinline__ int axis_row(const sa_rope_axes& x, int b, int s, int axis, int place,
+                                        bool* out) {
+  const int p = x.positions ? x.positions[b * x.pos_stride[0] + s * x.pos_stride[1] + axis] : place;
+  const int row = min(max(p, 0), x.rows - 1);
+  *out |= row != p;
+  return row;
+}
+#endif
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);   // pool + select
 // pa == nullptr: pool q, k; else the prologue writes q_out, k_out and pools them

@@ -60,9 +60,13 @@ enum {
                                attended)                                      */
   SA_DEV_RANGE = 1 << 3,    /* a V value does not fit fp16 (|v| > 65504); the
                                P.V product runs in fp16, see sa_attn_sparse    */
-  SA_DEV_BAD_CACHE = 1 << 4 /* a paged-cache call met a sequence length or a
+  SA_DEV_BAD_CACHE = 1 << 4,/* a paged-cache call met a sequence length or a
                                page id outside its range (see sa_cache_params
                                for what is then done)                         */
+  SA_DEV_BAD_TREE = 1 << 5  /* a new token's parent that does not come before
+                               it (sa_attn_tree), a path that does not ascend
+                               (sa_cache_accept) or a source row that does not
+                               exist (sa_pages_fork); see there               */
 };
 
 /* Arithmetic of the attention's score product Q.K^T (sa_attn_*). */
@@ -238,6 +242,39 @@ sa_status sa_qk_prologue(const sa_params* p, const void* q_in, const void* k_in,
                          const float* rope_cos, const float* rope_sin, void* q_out,
                          void* k_out, void* workspace, size_t ws_bytes,
                          int32_t* dev_status, void* stream);
+
+/* A pair that sa_rope_axes leaves as it is. */
+#define SA_ROPE_STAYS 255
+
+/* Rotary positions with several axes (time, height, width): pair i of a head
+ * vector is turned by row `position on axis axis_of[i]` of the rotation tables,
+ * column i. A pair of SA_ROPE_STAYS is not turned, whatever it holds. */
+typedef struct sa_rope_axes {
+  const int32_t* positions; /* device int32 [B][S][n_axes], the axes contiguous,
+                               or NULL: a token's place in its sequence, on
+                               every axis                                      */
+  int64_t pos_stride[2];    /* elements between two sequences, two tokens     */
+  int32_t n_axes;           /* 1 to 8                                          */
+  int32_t rows;             /* rows of the rotation tables, >= 1. A position
+                               outside [0, rows) counts as the nearest one
+                               inside and raises SA_DEV_CAPACITY               */
+  uint8_t axis_of[64];      /* of pair i < D/2: an axis, or SA_ROPE_STAYS      */
+} sa_rope_axes;
+
+/*
+ * sa_qk_prologue_axes -- sa_qk_prologue with positions on several axes: token t
+ * of sequence b turns pair i by rope_cos, rope_sin[positions[b][t][axis_of[i]]][i].
+ * The tables hold every position once, not every token. qk_norm = 0 leaves the
+ * norm out (the gammas are then NULL); rope_cos and rope_sin (fp32
+ * [axes->rows][D/2]) are given. Else, the block means that sa_route_pooled routes
+ * from among it, as sa_qk_prologue.
+ */
+sa_status sa_qk_prologue_axes(const sa_params* p, const void* q_in, const void* k_in,
+                              int32_t qk_norm, const float* gamma_q, const float* gamma_k,
+                              float eps, const float* rope_cos, const float* rope_sin,
+                              const sa_rope_axes* axes, void* q_out, void* k_out,
+                              void* workspace, size_t ws_bytes, int32_t* dev_status,
+                              void* stream);
 
 /*
  * sa_route_pooled -- sa_route from the block means that sa_qk_prologue left
@@ -482,7 +519,7 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * k_sum of the page (where given) gains y before it is rounded; a page's first
  * slot starts its sum anew.
  * Taking tokens back (a guess that was rejected) is setting the length back, but
- * k_sum has gained their keys: before more is appended, the sums of the page that
+ * k_sum has gained their keys (sa_cache_accept puts that right): before more is appended, the sums of the page that
  * the sequence then ends in (page_table[b][n / 64], where n % 64 > 0), [H_kv, D]
  * floats, have to be put back as they were at that length. Those of the pages
  * behind it start anew.
@@ -515,6 +552,24 @@ sa_status sa_cache_append(const sa_cache_params* p, const void* k, const void* v
                           const float* v_scale, float* k_sum, const int32_t* page_table,
                           const int32_t* seq_lens, const int32_t* new_lens, int32_t* lens_out,
                           int32_t* dev_status, void* stream);
+
+/*
+ * sa_cache_append_axes -- sa_cache_append with positions on several axes: a token
+ * turns pair i by rope_cos, rope_sin[positions[b][s][axis_of[i]]][i] (fp32
+ * [axes->rows][D/2], both given) and is still stored behind its sequence's tokens.
+ * So the positions of an image's tokens, or of drafted tokens that lie side by side
+ * in a tree, need not follow their slots. No token is left out for its position:
+ * lens_out is seq_lens[b] + n_b, at most 64 max_pages. p->rope_rows is not read.
+ * positions need only hold the tokens that new_lens counts.
+ */
+sa_status sa_cache_append_axes(const sa_cache_params* p, const void* k, const void* v,
+                               const void* q, void* q_out, const float* gamma_q,
+                               const float* gamma_k, const float* rope_cos,
+                               const float* rope_sin, const sa_rope_axes* axes, void* k_cache,
+                               void* v_cache, const float* k_scale, const float* v_scale,
+                               float* k_sum, const int32_t* page_table, const int32_t* seq_lens,
+                               const int32_t* new_lens, int32_t* lens_out, int32_t* dev_status,
+                               void* stream);
 
 /* Most entries sa_route_pages can list, B*H_kv*min(max_pages, max(page_budget,
  * ceil(P/64) + 1)) (0 on bad params). */
@@ -596,6 +651,183 @@ sa_status sa_attn_decode(const sa_cache_params* p, const void* q, const void* k_
                          const int32_t* row_ptr, const int32_t* col_idx, int64_t col_cap,
                          void* o, float* lse, void* workspace, size_t ws_bytes,
                          int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted tokens: a few new tokens of each sequence, appended with sa_cache_append
+ * or sa_cache_append_axes, attended all at once, and those of the path that turned
+ * out right kept. The calls take the lengths from before the append (seq_lens) and
+ * the new tokens' numbers (new_lens), as sa_cache_append does.
+ * ---------------------------------------------------------------------- */
+
+/* Most new tokens of a sequence. */
+#define SA_TREE_MAX 64
+
+/* Bytes of device workspace sa_attn_tree needs (0 on bad params). */
+size_t sa_attn_tree_workspace_bytes(const sa_cache_params* p);
+
+/*
+ * sa_attn_tree -- attention of the new tokens of each sequence, a tree (or
+ * several) of drafted ones, over its cached keys: new token s < n_b of sequence b
+ * (n_b = new_lens[b], S where new_lens is NULL), which lies at position
+ * seq_lens[b] + s, sees the tokens u < seq_lens[b] and those new ones that it
+ * continues: itself, parents[b][s], that one's parent, and so on to one whose
+ * parent is -1. Else as sa_attn_decode, for head h of g = h / (H / H_kv):
+ *   l_u = softmax_scale * q_sh . k_u,  a_u = exp(l_u - max l) / sum exp(.),
+ *   o_sh = sum_u a_u v_u,              lse_sh = max l + log sum exp(l - max l)
+ * With a route (row_ptr, col_idx) only tokens in the pages listed for row
+ * b*H_kv + g, and in all pages that hold new tokens, listed or not. What a token
+ * does not see has no effect on it, infinities and NaN included.
+ * A token without a place (position >= 64 max_pages, SA_DEV_CAPACITY) is left
+ * out; rows of o and lse of tokens that are left out or not counted by n_b stay
+ * as they were. Tokens whose every page has a bad id get o = 0, lse = -inf.
+ *
+ * Precision: as sa_attn_decode.
+ *
+ * q          device bf16 [B, S, H, D], rotated as the cached keys are; S at most
+ *            SA_TREE_MAX.
+ * seq_lens   lengths before the new tokens.
+ * parents    device int32: token s of sequence b has parents[b*parent_stride + s]
+ *            in [-1, s) (0: one tree for all), or NULL: each continues the one
+ *            before it. A parent outside that range counts as -1 and raises
+ *            SA_DEV_BAD_TREE.
+ * row_ptr,   as sa_attn_decode; entries from seq_lens[b] / 64 on are passed over
+ * col_idx    (those pages are attended anyway).
+ * o          device bf16 [B, S, H, D] (o_stride); no overlap with q.
+ * lse        device fp32 [B, H, S] (natural log), or NULL.
+ * workspace  device scratch of sa_attn_tree_workspace_bytes(p) bytes, 256-byte
+ *            aligned; its contents on entry do not matter.
+ * Errors: as sa_attn_decode; S above SA_TREE_MAX: SA_ERR_UNSUPPORTED.
+ */
+sa_status sa_attn_tree(const sa_cache_params* p, const void* q, const void* k_cache,
+                       const void* v_cache, const float* k_scale, const float* v_scale,
+                       const int32_t* page_table, const int32_t* seq_lens,
+                       const int32_t* new_lens, const int32_t* parents, int64_t parent_stride,
+                       const int32_t* row_ptr, const int32_t* col_idx, int64_t col_cap, void* o,
+                       float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                       void* stream);
+
+/*
+ * sa_cache_accept -- the new tokens of the path that turned out right move
+ * together: token path[b][i] of sequence b, i < m_b = path_lens[b], from position
+ * seq_lens[b] + path[b][i] to seq_lens[b] + i, keys and values. The sequence then
+ * ends at seq_lens[b] + m_b; what lies behind that is stale.
+ * k_sum (where given) of the pages from seq_lens[b] / 64 to the one that holds the
+ * new last token becomes the sum of their keys as they are stored (code * k_scale)
+ * up to the new length: with m_b = 0 this takes all new tokens back.
+ * A path has to ascend, path[b][i-1] < path[b][i] < SA_TREE_MAX, and to lie in
+ * the page table; it counts as far as it does, and SA_DEV_BAD_TREE is raised
+ * where it does not. A token whose old or new page has a bad id is not moved
+ * (SA_DEV_BAD_CACHE) but counted.
+ * The pages that new tokens lie in must belong to one sequence alone.
+ *
+ * path       device int32: path[b*path_stride + i], i < p->S (at most
+ *            SA_TREE_MAX).
+ * path_lens  device int32 [B] in [0, S] (clamped into it).
+ * lens_out   device int32 [B], or NULL: the new lengths; no overlap with
+ *            seq_lens or path_lens.
+ * k_scale    as sa_cache_append (read for k_sum only).
+ * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED before launch; SA_ERR_CUDA.
+ */
+sa_status sa_cache_accept(const sa_cache_params* p, void* k_cache, void* v_cache,
+                          const float* k_scale, float* k_sum, const int32_t* page_table,
+                          const int32_t* seq_lens, const int32_t* path, int64_t path_stride,
+                          const int32_t* path_lens, int32_t* lens_out, int32_t* dev_status,
+                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of the pool: who holds them. A page table and an array of reference
+ * counts serve the caches of all layers; these calls change only those and name
+ * the pages whose contents have to be copied, which sa_cache_copy does a layer at a
+ * time.
+ *   refs        int32 [n_pages]: how many places hold the page; 0: it is free.
+ *               A caller may hold pages of its own (a shared prompt) by counting
+ *               them in.
+ *   page_table  int32 [B][table_stride]: -1 where a sequence has no page. An entry
+ *               outside [-1, n_pages) counts as -1 and raises SA_DEV_BAD_CACHE.
+ * A page that is not full belongs to one sequence; full ones may be shared, as
+ * nothing is appended to them. Free pages are taken in ascending order of their ids,
+ * as they are free when the call begins. The workspace serves any of the three.
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of device workspace the sa_pages_* calls need for a pool of n_pages and
+ * tables of at most `rows` sequences (0 on bad sizes). */
+size_t sa_pages_workspace_bytes(int32_t n_pages, int32_t rows);
+
+/*
+ * sa_pages_fork -- a new table whose sequence i continues sequence src[i] of the
+ * old one (src[i] = -1: an empty one), for beams, several answers to one prompt,
+ * reordering and dropping sequences. The first i that continues a sequence takes
+ * over its row; every other one shares the full pages, gets a free page in place of
+ * one that is not full (its copy), and none behind that. The old table is given up:
+ *   refs_out = refs - (places in the old table) + (places in the new one).
+ * Where no page is free (SA_DEV_CAPACITY) a sequence keeps its full pages and their
+ * tokens only. src[i] outside [-1, B) counts as -1 and raises SA_DEV_BAD_TREE;
+ * a seq_lens[b] outside [0, 64 max_pages] counts as the nearest (SA_DEV_BAD_CACHE).
+ *
+ * page_table, seq_lens, refs   the old state; not modified (but refs_out may be refs).
+ * src         device int32 [N].
+ * table_out   device int32 [N][out_stride], max_pages entries a row; no overlap
+ *             with page_table.
+ * lens_out    device int32 [N]; no overlap with seq_lens.
+ * refs_out    device int32 [n_pages]: refs itself, or no overlap with it.
+ * moves       device int32 [N][2]: (page, its copy), n_moves[0] of them, in the
+ *             order of i.
+ * n_moves     device int32 [1].
+ * workspace   device scratch of sa_pages_workspace_bytes(n_pages, max(B, N))
+ *             bytes, 256-byte aligned.
+ * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED (B or N above 65,535, n_pages or
+ * max_pages from 2^25 on) / SA_ERR_CAPACITY before launch; SA_ERR_CUDA.
+ */
+sa_status sa_pages_fork(int32_t n_pages, int32_t max_pages, int32_t B, int32_t N,
+                        const int32_t* page_table, int64_t table_stride,
+                        const int32_t* seq_lens, const int32_t* refs, const int32_t* src,
+                        int32_t* table_out, int64_t out_stride, int32_t* lens_out,
+                        int32_t* refs_out, int32_t* moves, int32_t* n_moves, void* workspace,
+                        size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * sa_pages_resize -- every sequence holds exactly the pages for seq_lens[b] +
+ * more_lens[b] tokens (+ more where more_lens is NULL), in place: places before that
+ * without a page get a free one, row by row, pages behind it are given back. Where no
+ * page is free, or beyond max_pages, SA_DEV_CAPACITY is raised and places stay empty.
+ * seq_lens = 0 with more = 0 frees a sequence. The wanted length counts as at
+ * least 0 (SA_DEV_BAD_CACHE where it is below).
+ */
+sa_status sa_pages_resize(int32_t n_pages, int32_t max_pages, int32_t B, int32_t* page_table,
+                          int64_t table_stride, int32_t* refs, const int32_t* seq_lens,
+                          const int32_t* more_lens, int32_t more, void* workspace,
+                          size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * sa_pages_compact -- the pages in use move to the front of the pool: with n_used
+ * pages in use (refs > 0), the k-th of those at or behind n_used takes the place of
+ * the k-th free one before it. Afterwards pages [0, n_used) are in use, so the pool
+ * behind them can be given back or a checkpoint written without holes.
+ *
+ * table_out   device int32 [B][out_stride]: page_table with the new ids; page_table
+ *             itself (with the same stride), or no overlap.
+ * refs_out    refs itself, or no overlap.
+ * moves       device int32 [n_pages / 2][2] (at least one): (page, its new id),
+ *             ascending, n_moves[0] of them. new ids and old ones are distinct.
+ * n_used      device int32 [1].
+ * B may be 0 (page_table, table_out NULL): refs alone.
+ */
+sa_status sa_pages_compact(int32_t n_pages, int32_t max_pages, int32_t B,
+                           const int32_t* page_table, int64_t table_stride, const int32_t* refs,
+                           int32_t* table_out, int64_t out_stride, int32_t* refs_out,
+                           int32_t* moves, int32_t* n_moves, int32_t* n_used, void* workspace,
+                           size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * sa_cache_copy -- the keys, values and key sums (k_sum, where given) of page
+ * moves[i][0] to page moves[i][1], i < n_moves[0] (at most move_cap; all of them
+ * where n_moves is NULL). No page may be written twice or both read and written. A
+ * pair with an id outside [0, n_pages) is left out (SA_DEV_BAD_CACHE). p: H_kv, D,
+ * n_pages, cache_format and the caches' strides are read.
+ */
+sa_status sa_cache_copy(const sa_cache_params* p, void* k_cache, void* v_cache, float* k_sum,
+                        const int32_t* moves, int64_t move_cap, const int32_t* n_moves,
+                        int32_t* dev_status, void* stream);
 
 /* Decodes *dev_status bits into the most severe sa_status (SA_OK if 0). */
 sa_status sa_dev_status_decode(int32_t dev_status);
