@@ -316,7 +316,7 @@ size_t sa_attn_decode_workspace_bytes(const sa_cache_params* p) {
 
 size_t sa_attn_tree_workspace_bytes(const sa_cache_params* p) {
   if (check_cache(p) != SA_OK || p->S > SA_TREE_MAX) return 0;
-  return decode_ws_bytes(p->S * (p->H / p->H_kv), p->D);
+  return tree_ws_bytes(p->S * (p->H / p->H_kv), p->D);
 }
 
 // Attention over the cache: of one new token, or (tree) of a few.
@@ -346,7 +346,7 @@ static sa_status attend(const sa_cache_params* p, const void* q, const void* k_c
   if ((s = check_tokens(p, q, p->q_stride, p->H)) != SA_OK) return s;
   if ((s = check_tokens(p, o, p->o_stride, p->H)) != SA_OK) return s;
   if (!aligned(workspace, 256)) return SA_ERR_INVALID_ARG;
-  if (ws_bytes < decode_ws_bytes(rows, p->D)) return SA_ERR_CAPACITY;
+  if (ws_bytes < (tree ? tree_ws_bytes(rows, p->D) : decode_ws_bytes(rows, p->D))) return SA_ERR_CAPACITY;
   if (o == q) return SA_ERR_INVALID_ARG;       // read by CTAs that others' outputs would meet
   DecodeArgs a{};
   a.pm = page_map(p, page_table, seq_lens);

@@ -81,8 +81,12 @@ size_t decode_ws_bytes(int rows, int D);
 int decode_row_tiles(int rows);         // CTAs' worth of them
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           bool fp8, cudaStream_t st);
+size_t tree_ws_bytes(int rows, int D);
 cudaError_t launch_tree(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         bool fp8, cudaStream_t st);
+size_t tree_tile_ws_bytes(int rows, int D);
+cudaError_t launch_tree_tile(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                             bool fp8, cudaStream_t st);
 
 struct AcceptArgs {
   PageMap pm;

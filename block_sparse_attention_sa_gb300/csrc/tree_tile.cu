@@ -1,0 +1,988 @@
+// tree_tile.cu -- attention of a tree of new tokens over the paged cache where more than
+// 64 rows (pairs of a new token and a query head) share a key-value head: tcgen05.
+//   l_u = scale q.k_u,  a = softmax(l),  o = sum a_u v_u,  lse = log sum exp l
+//
+// Tiles. A CTA holds 128 rows (tcgen05 M = 128) and walks a run of pages, two (128 keys)
+// a step. The list of all (sequence, key-value head) units' steps is cut into equal runs,
+// as decode_kernel.cuh cuts its pages; grid (runs, row tiles), so that the tiles of one
+// unit walk the same pages side by side and all but the first find them in L2. A unit
+// that is cut leaves partial results, which tile_join_kernel adds in order.
+//
+// Pipeline, as in attn.cu: TMEM holds three S buffers and one O accumulator. S(j) = Q K(j)^T
+// goes to buffer j % 3; the softmax turns it into P over the same columns; O += P V(j).
+// K is K-major as the page lies (rows of d), and so is V as an MN-major operand (rows of
+// keys): no transpose, no repacking. The MMA warp issues QK(j+2) before it waits for P(j).
+// P as two terms of 16 bits, high and low, each 64 columns: both fit the buffer that S
+// leaves. Bf16 terms are cut, not rounded, and 2^-24 of the weight is added to what is
+// left, so that both are positive and an infinite value stays one; weights to 2^-16.
+// Over a cache in e4m3 the terms are fp16 of 2^11 p (weights to 2^-21 of themselves or
+// 2^-36 of the largest), against codes turned into fp16, exact, by a warpgroup of its own
+// on their way from TMA's stages to the MMA's.
+//
+// Softmax. Two warpgroups take the steps in turn, one thread a row. The running maximum
+// passes from step to step through shared memory and moves only when a step's exceeds it
+// by more than 2^4.
+//
+// Steps that hold new tokens, the last page or a page that is not there are masked bit by
+// bit (the ancestors of a row's token, shifted to the page); their warpgroup also takes
+// out of V in shared memory, before it hands over P, the rows that do not count and what
+// is no finite number among the new tokens' values: a weight of 0 would not silence
+// those. Rows that see such a value get it added in the epilogue.
+//
+// Warps: 0-3 softmax of even steps, 4-7 of odd ones, 8 producer, 9 MMA, 10 and 11 the
+// queries (rows gathered by token and head, for e4m3 scaled by a power of two), 12-15
+// conversion (e4m3). Every wait is bounded (SA_DEV_TIMEOUT).
+#include "decode_kernel.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int kSBuf = 3;
+constexpr int kInfo = 16;            // steps whose pages are remembered
+constexpr int kProducer = 8, kMma = 9, kQuery = 10, kConvert = 12;
+constexpr int kColO = 384;           // S[b] at columns [128 b, 128 b + 128)
+constexpr float kRaise = 4.f;        // the maximum moves when exceeded by this power of two
+constexpr float kTileShift = 11.f;   // e4m3: P is held as 2^11 p, at most 2^15
+
+// A unit's piece of a run, for the roles; steps < 0: no more.
+struct Head {
+  int b, g, dest, steps, pages, base, fresh, special;
+};
+
+// The pages of a step: their ids, how many tokens of each count, and the new token in the
+// first slot (-64: none before the second page's end).
+struct StepInfo {
+  int page[2], live[2], first[2];
+  int masked;
+};
+
+template <int D, bool kFp8>
+struct Tile {
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  // softmax and other warpgroups' registers (setmaxnreg): 2*128*216 + 128*64 <= 384*168,
+  // 2*128*192 + 2*128*64 = 512*128
+  static constexpr int kSoftRegs = kFp8 ? 192 : 216, kRegs = 64;
+  static constexpr int kRegion = BM * 128;              // 128 bytes of each of 128 rows
+  static constexpr int kQBytes = BM * D * 2;
+  static constexpr int kTile = BN * D * 2;              // K or V of a step, 16 bits an element
+  static constexpr int kStages = D == 64 ? 8 : (kFp8 ? 4 : 5);
+  static constexpr int kRow = D * (kFp8 ? 1 : 2);       // a token of the cache
+  static constexpr int kBox = kRow < 128 ? kRow : 128;
+  static constexpr int kRaw = kFp8 ? BN * D : 0;        // K or V of a step as it is stored
+  static constexpr int kRawStages = kFp8 ? 3 : 0;
+  static constexpr int kPageBytes = kBlock * kRow;
+  static constexpr int oQ = 0, oTiles = oQ + kQBytes, oRaw = oTiles + kStages * kTile;
+  static constexpr int oBar = oRaw + kRawStages * kRaw;
+  // barriers
+  static constexpr int bHeadFull = 0, bHeadEmpty = 2, bQFull = 4, bQEmpty = 5, bFull = 6;
+  static constexpr int bEmpty = bFull + kStages, bSFull = bEmpty + kStages, bPFull = bSFull + kSBuf;
+  static constexpr int bPvDone = bPFull + kSBuf, bTileDone = bPvDone + 2, bOFree = bTileDone + 1;
+  static constexpr int bFin = bOFree + 1, bInfo = bFin + 1, bRawFull = bInfo + kInfo;
+  static constexpr int bRawEmpty = bRawFull + kRawStages, kBars = bRawEmpty + kRawStages;
+  static constexpr int oMisc = oBar + kBars * 8;        // tmem base, abort flag, odd values [2]
+  static constexpr int oHead = oMisc + 16;
+  static constexpr int oInfo = oHead + 2 * static_cast<int>(sizeof(Head));
+  static constexpr int oSeen = (oInfo + kInfo * static_cast<int>(sizeof(StepInfo)) + 7) & ~7;   // [2][64]
+  static constexpr int oFactor = oSeen + 2 * 64 * 8;    // [2][128]
+  static constexpr int oXch = oFactor + 2 * BM * 4;     // [2][2][128] of (m, l, stop)
+  static constexpr int oHand = oXch + 2 * 2 * BM * 12;  // [2][128]
+  static constexpr int kBytes = oHand + 2 * BM * 8 + 1024;
+  static_assert(kBytes <= 227 * 1024, "the tile does not fit shared memory");
+  static_assert(oMisc % 8 == 0 && oHand % 8 == 0 && oXch % 4 == 0, "alignment");
+};
+
+struct TileCut {
+  int unit, first, last, pad;
+};
+
+// The MN-major operand of 16 keys of a page of V in the 128-byte swizzle: rows of 128
+// bytes (64 d), 8-row atoms of 1,024 bytes along the keys, the next 64 d 8 KB on.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(8192 >> 4) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
+         static_cast<uint64_t>(2) << 61;
+}
+
+__device__ __forceinline__ bool elected() {
+  uint32_t pred = 0;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(pred));
+  return pred != 0;
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// p = 2^((s - m) f) for 32 logits as two terms, pairs of keys in a word (e4m3: of 2^11 p);
+// returns the sum of the p. Subtracting before scaling, the largest key has weight 1
+// however coarse fp32 is at its logit's size.
+template <bool kFp8>
+__device__ __forceinline__ float weigh32(const uint32_t* v, float m, float f, uint32_t* hi, uint32_t* lo) {
+  const uint64_t nm = f2_pack(-m, -m), ff = f2_pack(f, f), shift = f2_pack(kTileShift, kTileShift);
+  const uint64_t minus = f2_pack(-1.f, -1.f), tiny = f2_pack(0x1p-24f, 0x1p-24f);
+  uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+  for (int u = 0; u < 32; u += 2) {
+    const uint64_t d = f2_add(f2_pack(__uint_as_float(v[u]), __uint_as_float(v[u + 1])), nm);
+    const uint64_t y = kFp8 ? f2_fma(d, ff, shift) : f2_mul(d, ff);
+    float y0, y1;
+    f2_unpack(y, y0, y1);
+    const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+    const uint64_t p = f2_pack(p0, p1);
+    acc[(u >> 1) & 1] = f2_add(acc[(u >> 1) & 1], p);
+    float r0, r1;
+    if (kFp8) {
+      const uint32_t h = pack_half(p0, p1);
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      hi[u >> 1] = h;
+      f2_unpack(f2_fma(f2_pack(b.x, b.y), minus, p), r0, r1);
+      lo[u >> 1] = pack_half(r0, r1);
+    } else {
+      const uint32_t h = top_bf16(p0, p1);
+      hi[u >> 1] = h;
+      f2_unpack(f2_fma(p, tiny, f2_fma(f2_pack(lo_f32(h), hi_f32(h)), minus, p)), r0, r1);
+      lo[u >> 1] = pack_bf16(r0, r1);
+    }
+  }
+  float a, b;
+  f2_unpack(f2_add(acc[0], acc[1]), a, b);
+  return a + b;
+}
+
+__device__ __forceinline__ float max32(const uint32_t* v) {
+  float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      m[c] = fmax3(m[c], __uint_as_float(v[i + 2 * c]), __uint_as_float(v[i + 2 * c + 1]));
+  return fmaxf(m[0], m[1]);
+}
+
+__device__ __forceinline__ void keep32(uint32_t* v, uint32_t bits) {
+#pragma unroll
+  for (int u = 0; u < 32; ++u)
+    if (!(bits >> u & 1)) v[u] = __float_as_uint(-INFINITY);
+}
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(Tile<D, kFp8>::kThreads, 1)
+tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const DecodeArgs a, float* partial, TileCut* cuts) {
+  using L = Tile<D, kFp8>;
+  constexpr unsigned full = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.H / a.Hkv, rt = blockIdx.y, run_id = blockIdx.x, runs = gridDim.x;
+  const bool routed = a.row_ptr != nullptr;
+  const int n_groups = routed ? a.B * a.Hkv : a.B, per_group = routed ? 1 : a.Hkv;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::oMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  volatile int* odd_seen = reinterpret_cast<volatile int*>(misc + 2);
+  const AbortSignal abort{abort_flag, nullptr};
+  const volatile int never_flag = 0;
+  const AbortSignal drain{&never_flag, nullptr};
+  volatile Head* heads = reinterpret_cast<volatile Head*>(smem + L::oHead);
+  volatile StepInfo* infos = reinterpret_cast<volatile StepInfo*>(smem + L::oInfo);
+  volatile uint64_t* seen_sets = reinterpret_cast<volatile uint64_t*>(smem + L::oSeen);
+  volatile float* factors = reinterpret_cast<volatile float*>(smem + L::oFactor);
+  auto bar = [&](int i) { return sbase + L::oBar + 8u * static_cast<uint32_t>(i); };
+  auto fail = [&]() {
+    *abort_flag = 1;
+    if (a.dev_status) atomicOr(a.dev_status, SA_DEV_TIMEOUT);
+  };
+  int status = 0;
+
+  let_next_launch();
+  if (tid == 0) {
+    for (int i = 0; i < L::kBars; ++i) {
+      uint32_t n = 1;
+      if (i >= L::bHeadEmpty && i < L::bHeadEmpty + 2) n = 1 + 8 + 2;     // MMA, softmax, queries
+      if (i == L::bQFull) n = 2;
+      if (i >= L::bPFull && i < L::bPFull + kSBuf) n = 128;
+      if (i == L::bOFree) n = 256;
+      if (kFp8 && i >= L::bFull && i < L::bFull + L::kStages) n = 4;       // the converting warps
+      if (kFp8 && i >= L::bRawEmpty) n = 4;
+      mbar_init(bar(i), n);
+    }
+    *abort_flag = 0;
+    odd_seen[0] = odd_seen[1] = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (tid < 256) reinterpret_cast<uint64_t*>(smem + L::oHand)[tid] = 0xffffffff00000000ull;
+  if (warp == kMma) {
+    tmem_alloc(sbase + L::oMisc, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  // this CTA's run of the list of steps of the sequences that have rows in this tile
+  const Run run = plan_run<L::kThreads>(n_groups, per_group, [&](int i, int* from) {
+    const int pages = group_pages<true>(a, i, from, &status);
+    int base, none;
+    const int fresh = new_tokens(a, routed ? i / a.Hkv : i, &base, &none);
+    return static_cast<int64_t>(fresh) * G > rt * BM ? (pages + 1) / 2 : 0;
+  });
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const int total_steps = run.hi - run.lo;
+
+  if (warp == kProducer) {
+    regs_dec<L::kRegs>();
+    // ---------------------------------------------------------- producer --
+    int left = total_steps, group = run.group, off = run.off, cnt = run.count;
+    int it = 0, item = 0, gstep = 0;
+    TileCut cut{-1, 0, 0, 0};
+    bool ok = true;
+    while (left > 0 && ok && group < n_groups) {
+      int from;
+      const int pages = group_pages<true>(a, group, &from, &status);
+      if (off >= cnt * per_group) {
+        off = 0;
+        if (++group < n_groups) {
+          int base, none;
+          const int fresh = new_tokens(a, routed ? group / a.Hkv : group, &base, &none);
+          cnt = static_cast<int64_t>(fresh) * G > rt * BM
+                    ? (group_pages<true>(a, group, &from, &status) + 1) / 2 : 0;
+        }
+        continue;
+      }
+      const int sub = off < cnt ? 0 : off / cnt, s0 = off - sub * cnt, take = min(left, cnt - s0);
+      const int b = routed ? group / a.Hkv : group, g = routed ? group - b * a.Hkv : sub;
+      int base;
+      const int fresh = new_tokens(a, b, &base, &status);
+      const int n = base + fresh, nb = (n + kBlock - 1) / kBlock, own = base / kBlock;
+      const int entries = pages - (nb - own);
+      const int dest = take == cnt ? -1 : (s0 == 0 ? 1 : 0);
+      const int p0 = 2 * s0, n_pages = min(2 * take, pages - p0);
+      const int x = it & 1;
+      if (it >= 2 && !mbar_wait_warp(bar(L::bHeadEmpty + x), ((it >> 1) - 1) & 1, abort)) {
+        if (lane == 0) fail();
+        break;
+      }
+      if (lane == 0) {
+        volatile Head* h = heads + x;
+        h->b = b;
+        h->g = g;
+        h->dest = dest;
+        h->steps = take;
+        h->pages = n_pages;
+        h->base = base;
+        h->fresh = fresh;
+        h->special = routed ? p0 + n_pages > entries : p0 + n_pages > own;
+        odd_seen[x] = 0;
+        mbar_arrive(bar(L::bHeadFull + x));
+      }
+      __syncwarp();
+      if (dest == 1)
+        cut = TileCut{b * a.Hkv + g, run_id, run_of(run.T, runs, run.hi - left + cnt - 1), 0};
+      // one item of the ring: K (which = 0) or V of step j of the piece
+      auto load = [&](int which, int j) -> bool {
+        constexpr int NS = kFp8 ? L::kRawStages : L::kStages;
+        const int st = item % NS, e = kFp8 ? L::bRawEmpty : L::bEmpty, f = kFp8 ? L::bRawFull : L::bFull;
+        if (item >= NS && !mbar_wait_warp(bar(e + st), (item / NS - 1) & 1, abort)) return false;
+        if (lane == 0) {
+          volatile StepInfo* in = infos + (gstep + j) % kInfo;
+          const int n0 = in->live[0] > 0, n1 = in->live[1] > 0;
+          const uint32_t to = bar(f + st);
+          const uint32_t dst = sbase + (kFp8 ? L::oRaw + st * L::kRaw : L::oTiles + st * L::kTile);
+          if (n0 + n1 > 0)
+            mbar_arrive_expect_tx(to, (n0 + n1) * L::kPageBytes);
+          else
+            mbar_arrive(to);
+          for (int kh = 0; kh < 2; ++kh) {
+            if (in->live[kh] <= 0) continue;
+            constexpr int kBoxes = L::kRow / L::kBox, kElts = L::kBox / (kFp8 ? 1 : 2);
+            for (int dh = 0; dh < kBoxes; ++dh) {
+              // K: all rows of a slice of d follow each other; V: a page's slices do
+              const uint32_t at = kFp8 ? dst + kh * L::kPageBytes
+                                       : dst + (which ? kh * L::kPageBytes + dh * 8192
+                                                      : dh * L::kRegion + kh * 8192);
+              tma_load_4d(at, which ? &vmap : &kmap, to, dh * kElts, 0, g, in->page[kh]);
+            }
+          }
+        }
+        __syncwarp();
+        ++item;
+        return true;
+      };
+      int pg = 0, lv = 0, fs = 0;         // the batch's pages, a lane each
+      for (int j = 0; j < take + 2 && ok; ++j) {
+        if (j < take) {
+          const int q = 2 * j % 32;
+          if (q == 0) {                   // the next 32 pages are looked up
+            const int at = 2 * j + lane;
+            pg = -1;
+            lv = 0;
+            fs = -kBlock;
+            if (at < n_pages) {
+              int p = p0 + at;
+              if (routed && p >= entries) {
+                p += own - entries;
+              } else if (routed) {
+                const int c = from + p;
+                const bool there = from >= 0 && c < a.col_cap;
+                const int prev = there && p > 0 ? get(a.col_idx + c - 1) : -1;
+                p = there ? get(a.col_idx + c) : -1;
+                if (p < 0 || p >= nb || p <= prev) {
+                  status |= SA_DEV_BAD_ROUTE;
+                  p = -1;
+                }
+                if (p >= own) p = -1;
+              }
+              if (p >= 0) {
+                pg = get(a.pm.table + b * a.pm.table_stride + p);
+                lv = min(kBlock, n - p * kBlock);
+                fs = max(p * kBlock - base, -kBlock);
+                if (pg < 0 || pg >= a.pm.n_pages) {
+                  status |= SA_DEV_BAD_CACHE;
+                  lv = 0;
+                }
+              }
+            }
+          }
+          const int pg0 = __shfl_sync(full, pg, q), pg1 = __shfl_sync(full, pg, q + 1);
+          const int lv0 = __shfl_sync(full, lv, q), lv1 = __shfl_sync(full, lv, q + 1);
+          const int fs0 = __shfl_sync(full, fs, q), fs1 = __shfl_sync(full, fs, q + 1);
+          if (lane == 0) {
+            volatile StepInfo* in = infos + (gstep + j) % kInfo;
+            in->page[0] = pg0;
+            in->page[1] = pg1;
+            in->live[0] = lv0;
+            in->live[1] = lv1;
+            in->first[0] = fs0;
+            in->first[1] = fs1;
+            const bool two = 2 * j + 1 < n_pages;
+            in->masked = lv0 < kBlock || fs0 > -kBlock || (two && (lv1 < kBlock || fs1 > -kBlock));
+            mbar_arrive(bar(L::bInfo + (gstep + j) % kInfo));
+          }
+          __syncwarp();
+          ok = load(0, j);
+        }
+        if (ok && j >= 2) ok = load(1, j - 2);
+      }
+      if (!ok) {
+        if (lane == 0) fail();
+        break;
+      }
+      gstep += take;
+      off += take;
+      left -= take;
+      ++it;
+    }
+    // no more units
+    const int x = it & 1;
+    if (it >= 2 && !mbar_wait_warp(bar(L::bHeadEmpty + x), ((it >> 1) - 1) & 1, abort)) {
+      if (lane == 0) fail();
+    } else if (lane == 0) {
+      heads[x].steps = -1;
+      mbar_arrive(bar(L::bHeadFull + x));
+    }
+    if (lane == 0) {
+      cuts[static_cast<int64_t>(rt) * runs + run_id] = cut;
+      // no copy may be in flight when the CTA ends
+      constexpr int NS = kFp8 ? L::kRawStages : L::kStages;
+      for (int s = 0; s < NS && s < item; ++s) {
+        const int last = (item - 1 - s) / NS;       // the fills of stage s before its last one
+        mbar_wait(bar((kFp8 ? L::bRawFull : L::bFull) + s), last & 1, drain);
+      }
+    }
+  } else if (warp == kMma) {
+    regs_dec<L::kRegs>();
+    // --------------------------------------------------------------- MMA --
+    constexpr int kType = kFp8 ? 0 : 1;
+    constexpr uint32_t kIdQK128 = idesc_f16(BM, 128, kType), kIdQK64 = idesc_f16(BM, 64, kType);
+    constexpr uint32_t kIdPV = idesc_f16(BM, D, kType) | (1u << 16);      // B is MN-major
+    constexpr int kKS = D / 16;
+    uint64_t qd[kKS];
+#pragma unroll
+    for (int k = 0; k < kKS; ++k)
+      qd[k] = sdesc_kmajor_sw128(sbase + L::oQ + (k >> 2) * L::kRegion + (k & 3) * 32);
+    const uint32_t o_tmem = tmem + kColO;
+    int c = 0, gs0 = 0;
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      const int x = it & 1;
+      if (!mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort)) {
+        if (lane == 0) fail();
+        break;
+      }
+      const int n = heads[x].steps, n_pages = heads[x].pages;
+      if (n < 0) break;
+      if (!mbar_wait_warp(bar(L::bQFull), it & 1, abort)) {
+        if (lane == 0) fail();
+        break;
+      }
+      tc_fence_after();
+      auto issue_qk = [&](int j) -> bool {
+        const int st = c % L::kStages;
+        if (!mbar_wait_warp(bar(L::bFull + st), (c / L::kStages) & 1, abort)) return false;
+        tc_fence_after();
+        const int b = (gs0 + j) % kSBuf;
+        const uint32_t idesc = 2 * j + 1 < n_pages ? kIdQK128 : kIdQK64;
+        const uint64_t kb = sdesc_kmajor_sw128(sbase + L::oTiles + st * L::kTile);
+#pragma unroll
+        for (int h = 0; h < kKS / 4; ++h) {
+          const uint64_t k0 = kb + static_cast<uint64_t>((h * L::kRegion) >> 4);
+          umma_ss_x4_elect(tmem + b * 128, qd[4 * h], qd[4 * h + 1], qd[4 * h + 2], qd[4 * h + 3], k0, k0 + 2,
+                           k0 + 4, k0 + 6, idesc, h > 0);
+        }
+        umma_commit_elect(bar(L::bSFull + b));
+        umma_commit_elect(bar(L::bEmpty + st));
+        if (j == n - 1) umma_commit_elect(bar(L::bQEmpty));
+        ++c;
+        return true;
+      };
+      for (int j = 0; j < 2 && j < n && ok; ++j) ok = issue_qk(j);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 2 < n && !issue_qk(j + 2)) {
+          ok = false;
+          break;
+        }
+        // the last piece's epilogue has read O
+        if (j == 0 && it >= 1 && !mbar_wait_warp(bar(L::bOFree), (it - 1) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        const int gsj = gs0 + j, b = gsj % kSBuf, st = c % L::kStages;
+        bool unused = false;
+        if (!mbar_wait2_warp(bar(L::bPFull + b), (gsj / kSBuf) & 1, bar(L::bFull + st), (c / L::kStages) & 1,
+                             false, 0u, 0u, &unused, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t pa = tmem + b * 128;
+        const uint64_t vb = sdesc_mn_sw128(sbase + L::oTiles + st * L::kTile);
+        const int halves = 2 * j + 1 < n_pages ? 2 : 1;
+        for (int kh = 0; kh < halves; ++kh) {
+          const uint64_t v0 = vb + static_cast<uint64_t>(kh * (kBlock * D * 2 >> 4));
+          // 16 keys are 2 KB of rows
+          umma_ts_x4_elect(o_tmem, pa + 32 * kh, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, j > 0 || kh > 0);
+          umma_ts_x4_elect(o_tmem, pa + 64 + 32 * kh, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, 1u);
+        }
+        umma_commit_elect(bar(L::bEmpty + st));
+        umma_commit_elect(bar(L::bPvDone + (gsj & 1)));
+        ++c;
+      }
+      gs0 += n;
+      if (!ok) {
+        if (lane == 0) fail();
+        break;
+      }
+      umma_commit_elect(bar(L::bTileDone));
+      if (elected()) mbar_arrive(bar(L::bHeadEmpty + x));
+    }
+    umma_commit_elect(bar(L::bFin));
+    mbar_wait_warp(bar(L::bFin), 0, drain);
+  } else if (warp == kQuery || warp == kQuery + 1) {
+    regs_dec<L::kRegs>();
+    // ----------------------------------------------------------- queries --
+    constexpr int kLanes = D / 8, kRowsOnce = 64 / kLanes, kBatch = 4;    // lanes of a row
+    const int t64 = tid - kQuery * 32, sub = t64 % kLanes, r0 = t64 / kLanes;
+    for (int it = 0;; ++it) {
+      const int x = it & 1;
+      if (!mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort)) {
+        if (lane == 0) fail();
+        break;
+      }
+      if (heads[x].steps < 0) break;
+      const int b = heads[x].b, g = heads[x].g, rows = heads[x].fresh * G;
+      const float scale = a.scale_log2 * (kFp8 && a.k_scale ? get(a.k_scale + g) : 1.f);
+      if (it >= 1 && !mbar_wait_warp(bar(L::bQEmpty), (it - 1) & 1, abort)) {
+        if (lane == 0) fail();
+        break;
+      }
+      if (warp == kQuery && heads[x].special) {
+        uint64_t set[2];
+        ancestors(a, b, heads[x].fresh, lane, set, &status);
+        seen_sets[x * 64 + lane] = set[0];
+        seen_sets[x * 64 + 32 + lane] = set[1];
+      }
+      for (int rb = 0; rb < BM; rb += kRowsOnce * kBatch) {
+        uint4 w[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int row = rt * BM + rb + u * kRowsOnce + r0;
+          w[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (row < rows) {
+            const int tok = row / G;
+            w[u] = *reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + tok * a.qs[1] + (g * G + row - tok * G) * a.qs[2] + 8 * sub);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int r = rb + u * kRowsOnce + r0;
+          if (kFp8) {
+            // in fp16, a row scaled by a power of two so that its largest element is in
+            // [2^14, 2^15): bits are lost only below 2^-39 of it
+            uint32_t* e = &w[u].x;
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_f32(e[i])), fabsf(hi_f32(e[i]))));
+#pragma unroll
+            for (int s = kLanes / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, s));
+            const int ex = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
+            const float up1 = ldexpf(1.f, ex / 2), up2 = ldexpf(1.f, ex - ex / 2);
+            float f = scale * ldexpf(1.f, -(ex / 2)) * ldexpf(1.f, -(ex - ex / 2));
+            if (f == 0.f) f = 0x1p-149f;
+            if (sub == 0) factors[x * BM + r] = f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = pack_half(lo_f32(e[i]) * up1 * up2, hi_f32(e[i]) * up1 * up2);
+          } else if (sub == 0) {
+            factors[x * BM + r] = scale;
+          }
+          *reinterpret_cast<uint4*>(smem + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4)) = w[u];
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(L::bQFull));
+        mbar_arrive(bar(L::bHeadEmpty + x));
+      }
+    }
+  } else if (kFp8 && warp >= kConvert) {
+    regs_dec<L::kRegs>();
+    // -------------------------------------------------------- conversion --
+    // A thread turns a row (one token's codes) into fp16: as read, so written, without
+    // bank conflicts, as the rows' pieces are swizzled alike.
+    const int r = tid - kConvert * 32, kh = r >> 6, row = r & 63;
+    const int items = 2 * total_steps;
+    // the items' order: K(0), K(1), then K(j + 2), V(j) of each piece
+    constexpr int NR = kFp8 ? L::kRawStages : 1;
+    int n = 0, it = 0, done = 0;                // the piece's steps, its items so far
+    for (int c = 0; c < items; ++c) {
+      if (done == 2 * n) {
+        const int x = it & 1;
+        if (!mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort)) {
+          if (lane == 0) fail();
+          break;
+        }
+        n = heads[x].steps;
+        if (n < 0) break;
+        done = 0;
+        ++it;
+      }
+      // of the first min(2, n) items, and then every second one while there are K left, K
+      const int ks = min(2, n), rest = done - ks;
+      const bool is_v = rest >= 0 && (rest >= 2 * (n - ks) || (rest & 1));
+      const int rs = c % NR, st = c % L::kStages;
+      if (!mbar_wait_warp(bar(L::bRawFull + rs), (c / NR) & 1, abort) ||
+          (c >= L::kStages && !mbar_wait_warp(bar(L::bEmpty + st), (c / L::kStages - 1) & 1, abort))) {
+        if (lane == 0) fail();
+        break;
+      }
+      const uint8_t* src = smem + L::oRaw + rs * L::kRaw + kh * L::kPageBytes;
+      uint8_t* dst = smem + L::oTiles + st * L::kTile;
+      constexpr int kPieces = D / 16;           // of a row of codes
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const uint32_t at = D == 64 ? row * 64 + ((p ^ ((row >> 1) & 3)) << 4) : row * 128 + ((p ^ (row & 7)) << 4);
+        const uint4 w = *reinterpret_cast<const uint4*>(src + at);
+        const uint2 h0 = e4m3x4_half4(w.x), h1 = e4m3x4_half4(w.y), h2 = e4m3x4_half4(w.z), h3 = e4m3x4_half4(w.w);
+        const int dh = p >> 2, c0 = (p & 3) * 2;
+        uint8_t* to = dst + (is_v ? kh * (kBlock * D * 2) + dh * 8192 : dh * L::kRegion + kh * 8192) + row * 128;
+        *reinterpret_cast<uint4*>(to + ((c0 ^ (row & 7)) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+        *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(L::bFull + st));
+        mbar_arrive(bar(L::bRawEmpty + rs));
+      }
+      ++done;
+    }
+  } else {
+    regs_inc<L::kSoftRegs>();
+    // ----------------------------------------------------------- softmax --
+    const int sm = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t pair_bar = 1 + quarter;
+    float* xm = reinterpret_cast<float*>(smem + L::oXch);
+    float* xl = xm + 4 * BM;
+    int* xs = reinterpret_cast<int*>(xl + 4 * BM);
+    volatile uint64_t* hand = reinterpret_cast<volatile uint64_t*>(smem + L::oHand);
+    volatile uint64_t* hand_mine = hand + sm * BM + r;
+    const volatile uint64_t* hand_theirs = hand + (sm ^ 1) * BM + r;
+    int xc = 0;
+    auto pair_xchg = [&](float m, float l, bool stop, float& m_o, float& l_o) -> bool {
+      const int sl = xc & 1;
+      ++xc;
+      const int mine = (sl * 2 + sm) * BM + r, theirs = (sl * 2 + (sm ^ 1)) * BM + r;
+      xm[mine] = m;
+      xl[mine] = l;
+      xs[mine] = stop ? 1 : 0;
+      named_bar_sync(pair_bar, 64);
+      m_o = xm[theirs];
+      l_o = xl[theirs];
+      return stop || xs[theirs] != 0;
+    };
+    auto wait_handoff = [&](int g_prev, uint64_t& hv) -> bool {
+      hv = *hand_theirs;
+      if (__all_sync(full, static_cast<int>(hv >> 32) >= g_prev)) return true;
+      unsigned long long t0 = 0;
+      if (lane == 0) t0 = globaltimer();
+      for (uint32_t i = 1;; ++i) {
+        hv = *hand_theirs;
+        if (__all_sync(full, static_cast<int>(hv >> 32) >= g_prev)) return true;
+        if ((i & 63u) == 0u) {
+          int give_up = 0;
+          if (lane == 0) give_up = abort.raised() || (globaltimer() - t0 > kWaitTimeoutNs);
+          if (__shfl_sync(full, give_up, 0)) return false;
+        }
+      }
+    };
+    int gs = 0;
+    for (int it = 0;; ++it) {
+      const int x = it & 1;
+      bool stop = !mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort);
+      if (stop && lane == 0) fail();
+      float u0, u1;
+      if (pair_xchg(0.f, 0.f, stop, u0, u1)) break;
+      const int n = heads[x].steps;
+      if (n < 0) break;
+      const int b = heads[x].b, g = heads[x].g, dest = heads[x].dest, n_pages = heads[x].pages;
+      const int n_rows = heads[x].fresh * G, row = rt * BM + r;
+      const bool special = heads[x].special != 0;
+      stop = !mbar_wait_warp(bar(L::bQFull), it & 1, abort);    // the rows' factors are there
+      if (stop && lane == 0) fail();
+      const float f = factors[x * BM + r];
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = (gs ^ sm) & 1; j < n && !stop; j += 2) {
+        const int gg = gs + j, sb = gg % kSBuf;
+        const uint32_t s_col = sb * 128;
+        const bool two = 2 * j + 1 < n_pages;
+        volatile StepInfo* in = infos + gg % kInfo;
+        if (!mbar_wait_warp(bar(L::bInfo + gg % kInfo), (gg / kInfo) & 1, abort)) {
+          stop = true;
+          break;
+        }
+        const bool masked = in->masked != 0;
+        if (masked) {
+          // V's rows that do not count, and among the new tokens what is no finite number
+          const int k_before = min(j + 3, n), c = 2 * gs + k_before + j, st = c % L::kStages;
+          if (!mbar_wait_warp(bar(L::bFull + st), (c / L::kStages) & 1, abort)) {
+            stop = true;
+            break;
+          }
+          const int kh = r >> 6, key = r & 63;
+          if (kh == 0 || two) {
+            const int lv = in->live[kh], fs = in->first[kh];
+            uint8_t* v = smem + L::oTiles + st * L::kTile + kh * (kBlock * D * 2) + key * 128;
+            if (key >= lv) {
+#pragma unroll
+              for (int p = 0; p < D / 8; ++p)
+                *reinterpret_cast<uint4*>(v + (p >> 3) * 8192 + (((p & 7) ^ (key & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (fs + key >= 0) {
+              constexpr uint32_t kOdd = kFp8 ? 0x7c00u : 0x7f80u;
+              bool odd = false;
+#pragma unroll
+              for (int p = 0; p < D / 8; ++p) {
+                uint4* at = reinterpret_cast<uint4*>(v + (p >> 3) * 8192 + (((p & 7) ^ (key & 7)) << 4));
+                uint4 w = *at;
+                uint32_t* e = &w.x;
+                bool here = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if ((e[i] & kOdd) == kOdd) {
+                    e[i] &= 0xffff0000u;
+                    here = true;
+                  }
+                  if ((e[i] >> 16 & kOdd) == kOdd) {
+                    e[i] &= 0xffffu;
+                    here = true;
+                  }
+                }
+                if (here) *at = w;
+                odd |= here;
+              }
+              if (odd) odd_seen[x] = 1;
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        if (!mbar_wait_warp(bar(L::bSFull + sb), (gg / kSBuf) & 1, abort)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[128];
+        float mx0, mx1, mx2 = -INFINITY, mx3 = -INFINITY;
+        tmem_ld32_max(lane_base + s_col, sr, mx0);
+        tmem_ld32_max(lane_base + s_col + 32, sr + 32, mx1);
+        if (two) {
+          tmem_ld32_max(lane_base + s_col + 64, sr + 64, mx2);
+          tmem_ld32_max(lane_base + s_col + 96, sr + 96, mx3);
+        }
+        tmem_wait_ld();
+        reg_fence32(sr);
+        reg_fence32(sr + 32);
+        reg_fence_f(mx0);
+        reg_fence_f(mx1);
+        if (two) {
+          reg_fence32(sr + 64);
+          reg_fence32(sr + 96);
+          reg_fence_f(mx2);
+          reg_fence_f(mx3);
+        }
+        if (masked) {
+          uint64_t keep[2];
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            const int lv = in->live[kh], fs = in->first[kh];
+            keep[kh] = lv >= kBlock ? ~0ull : (1ull << lv) - 1;
+            if (fs > -kBlock) keep[kh] &= slots_seen(seen_sets[x * 64 + min(row / G, 63)], fs);
+          }
+          keep32(sr, static_cast<uint32_t>(keep[0]));
+          keep32(sr + 32, static_cast<uint32_t>(keep[0] >> 32));
+          mx0 = max32(sr);
+          mx1 = max32(sr + 32);
+          if (two) {
+            keep32(sr + 64, static_cast<uint32_t>(keep[1]));
+            keep32(sr + 96, static_cast<uint32_t>(keep[1] >> 32));
+            mx2 = max32(sr + 64);
+            mx3 = max32(sr + 96);
+          }
+        }
+        const float bmax = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        float m_prev = -INFINITY;
+        if (j > 0) {
+          uint64_t hv;
+          if (!wait_handoff(gg - 1, hv)) {
+            stop = true;
+            break;
+          }
+          m_prev = __uint_as_float(static_cast<uint32_t>(hv));
+        }
+        float m_new = m_prev;
+        if (m_prev == -INFINITY || (bmax - m_prev) * f > kRaise) m_new = fmaxf(bmax, m_prev);
+        *hand_mine = (static_cast<uint64_t>(static_cast<uint32_t>(gg)) << 32) | __float_as_uint(m_new);
+        const bool raised = m_new != m_prev && m_prev != -INFINITY;
+        if (__any_sync(full, raised)) {
+          if (!mbar_wait_warp(bar(L::bPvDone + ((gg - 1) & 1)), ((gg - 1) >> 1) & 1, abort)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const float alpha = raised ? fast_exp2((m_prev - m_new) * f) : 1.f;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + kColO + 32 * cc, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+            tmem_st32(lane_base + kColO + 32 * cc, o);
+          }
+        }
+        const float m_use = m_new == -INFINITY ? 0.f : m_new;
+        float rs;
+        {
+          uint32_t hi[32], lo[32];
+          rs = weigh32<kFp8>(sr, m_use, f, hi, lo);
+          rs += weigh32<kFp8>(sr + 32, m_use, f, hi + 16, lo + 16);
+          tmem_st32(lane_base + s_col, hi);
+          tmem_st32(lane_base + s_col + 64, lo);
+        }
+        if (two) {
+          uint32_t hi[32], lo[32];
+          rs += weigh32<kFp8>(sr + 64, m_use, f, hi, lo);
+          rs += weigh32<kFp8>(sr + 96, m_use, f, hi + 16, lo + 16);
+          tmem_st32(lane_base + s_col + 32, hi);
+          tmem_st32(lane_base + s_col + 96, lo);
+        }
+        l_run = (m_run == -INFINITY ? l_run : l_run * fast_exp2((m_run - m_use) * f)) + rs;
+        m_run = m_new;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(L::bPFull + sb));
+      }
+      if (stop && lane == 0) fail();
+      gs += n;
+      // -------------------------------------------------------- epilogue --
+      if (!stop) {
+        stop = !mbar_wait_warp(bar(L::bTileDone), it & 1, abort);
+        if (stop && lane == 0) fail();
+      }
+      float m_oth, l_oth;
+      if (pair_xchg(m_run, l_run, stop, m_oth, l_oth)) break;
+      tc_fence_after();
+      const float m_tot = fmaxf(m_run, m_oth);
+      // a set without a maximum has a sum of 0, or NaN if only NaN was there
+      const float l_tot = (m_run == -INFINITY ? l_run : l_run * fast_exp2((m_run - m_tot) * f)) +
+                          (m_oth == -INFINITY ? l_oth : l_oth * fast_exp2((m_oth - m_tot) * f));
+      const bool row_ok = row < n_rows;
+      const int tok = row / G, h = g * G + row - tok * G, c0 = sm * (D / 2);
+      const float inv = l_tot == 0.f ? 0.f : (kFp8 && a.v_scale ? get(a.v_scale + g) : 1.f) / l_tot;
+      const uint64_t odd_of = special && row_ok && odd_seen[x] ? seen_sets[x * 64 + tok] : 0ull;
+      float* part = partial + ((static_cast<int64_t>(rt) * runs + run_id) * 2 + max(dest, 0)) * (BM * (D + 2));
+#pragma unroll 1
+      for (int cc = 0; cc < D / 64; ++cc) {
+        uint32_t ov[32];
+        tmem_ld32(lane_base + kColO + c0 + 32 * cc, ov);
+        tmem_wait_ld();
+        reg_fence32(ov);
+        if (!row_ok) continue;
+        // values that were taken out and that this row sees
+        for (uint64_t left = odd_of; left; left &= left - 1) {
+          const int t = heads[x].base + __ffsll(left) - 1;
+          const int page = get(a.pm.table + b * a.pm.table_stride + t / kBlock);
+          if (page < 0 || page >= a.pm.n_pages) continue;
+          const int64_t at = page * a.vcs[0] + g * a.vcs[1] + t % kBlock * a.vcs[2] + c0 + 32 * cc;
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            float v;
+            if (kFp8) {
+              const uint8_t code = static_cast<const uint8_t*>(a.vc)[at + u];
+              v = (code & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : 0.f;
+            } else {
+              const uint16_t w = static_cast<const uint16_t*>(a.vc)[at + u];
+              v = (w & 0x7f80u) == 0x7f80u ? __uint_as_float(static_cast<uint32_t>(w) << 16) : 0.f;
+            }
+            ov[u] = __float_as_uint(__uint_as_float(ov[u]) + v);
+          }
+        }
+        if (dest < 0) {
+          uint16_t* out = a.o + b * a.os[0] + tok * a.os[1] + h * a.os[2] + c0 + 32 * cc;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            float y[8];
+            // a row without weight may face an O that was never written
+#pragma unroll
+            for (int u = 0; u < 8; ++u) y[u] = l_tot == 0.f ? 0.f : __uint_as_float(ov[8 * v + u]) * inv;
+            *reinterpret_cast<uint4*>(out + 8 * v) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                                pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+          }
+        } else {
+          float* out = part + r * D + c0 + 32 * cc;
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            *reinterpret_cast<float4*>(out + 4 * v) =
+                l_tot == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                             : make_float4(__uint_as_float(ov[4 * v]), __uint_as_float(ov[4 * v + 1]),
+                                           __uint_as_float(ov[4 * v + 2]), __uint_as_float(ov[4 * v + 3]));
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(L::bOFree));
+      if (row_ok && sm == 0) {
+        const float m2 = m_tot * f;
+        if (dest >= 0)
+          *reinterpret_cast<float2*>(part + BM * D + 2 * r) = make_float2(m_tot == -INFINITY ? -INFINITY : m2, l_tot);
+        else if (a.lse)
+          a.lse[(static_cast<int64_t>(b) * a.H + h) * a.S + tok] =
+              l_tot == 0.f ? -INFINITY
+                           : (m2 + log2f(kFp8 ? l_tot * 0x1p-11f : l_tot)) * 0.69314718055994530942f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::bHeadEmpty + x));
+    }
+  }
+  if (status && a.dev_status) atomicOr(a.dev_status, status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMma) tmem_dealloc(tmem, 512);
+}
+
+// grid (row tiles * runs, 16), 256 threads: a warp adds the partials of one row of the unit
+// that is cut behind a run's end, in the order of the runs.
+template <int D>
+__global__ void __launch_bounds__(256)
+tile_join_kernel(DecodeArgs a, int runs, float unit, const float* partial, const TileCut* cuts) {
+  wait_for_first();
+  const int4 whole = *reinterpret_cast<const int4*>(cuts + blockIdx.x);
+  const int rt = blockIdx.x / runs, bg = whole.x, first = whole.y, last = whole.z;
+  if (bg < 0 || bg >= a.B * a.Hkv || first < 0 || last <= first || last >= runs) return;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), row = rt * BM + r;
+  const int G = a.H / a.Hkv, b = bg / a.Hkv, g = bg - b * a.Hkv;
+  int base, none = 0;
+  if (row >= new_tokens(a, b, &base, &none) * G) return;
+  constexpr int V = D / 32;
+  float o[V] = {}, m = -INFINITY, l = 0.f;
+  auto piece = [&](int i) {
+    return partial + ((static_cast<int64_t>(rt) * runs + i) * 2 + (i == first ? 1 : 0)) * (BM * (D + 2));
+  };
+  constexpr int kOnce = 4;
+  for (int i0 = first; i0 <= last; i0 += kOnce) {
+    float2 ml[kOnce];
+    float v[kOnce][V];
+#pragma unroll
+    for (int u = 0; u < kOnce; ++u) {
+      const float* p = piece(min(i0 + u, last));
+      ml[u] = *reinterpret_cast<const float2*>(p + BM * D + 2 * r);
+#pragma unroll
+      for (int x = 0; x < V; ++x) v[u][x] = p[r * D + V * lane + x];
+    }
+#pragma unroll
+    for (int u = 0; u < kOnce; ++u) {
+      if (i0 + u > last) break;
+      if (ml[u].x == -INFINITY) {            // nothing counted there (a sum of 0, or NaN)
+        l += ml[u].y;
+        continue;
+      }
+      const float now = fmaxf(m, ml[u].x), c0 = m == -INFINITY ? 0.f : ex2(m - now), c1 = ex2(ml[u].x - now);
+      l = (m == -INFINITY ? l : l * c0) + ml[u].y * c1;
+      m = now;
+#pragma unroll
+      for (int x = 0; x < V; ++x) o[x] = o[x] * c0 + v[u][x] * c1;
+    }
+  }
+  const int tok = row / G, h = g * G + row - tok * G;
+  const float inv = l == 0.f ? 0.f : (a.v_scale ? a.v_scale[g] : 1.f) / l;
+  uint16_t* out = a.o + b * a.os[0] + tok * a.os[1] + h * a.os[2] + V * lane;
+  if (V == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[V - 2] * inv, o[V - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(o[0] * inv, o[1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[(static_cast<int64_t>(b) * a.H + h) * a.S + tok] =
+        l == 0.f ? -INFINITY : (m + log2f(l * unit)) * 0.69314718055994530942f;
+}
+
+int tile_runs(int rows) {
+  const int RT = (rows + BM - 1) / BM;
+  return RT < kSms ? kSms / RT : 1;
+}
+
+template <int D, bool kFp8>
+cudaError_t launch_tile(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t st) {
+  using L = Tile<D, kFp8>;
+  const int rows = a.S * (a.H / a.Hkv), RT = (rows + BM - 1) / BM, runs = tile_runs(rows);
+  TileCut* cuts = reinterpret_cast<TileCut*>(a.ws);
+  float* partial = reinterpret_cast<float*>(a.ws + ((static_cast<size_t>(RT) * runs * sizeof(TileCut) + 255) & ~static_cast<size_t>(255)));
+  const auto kernel = tree_tile_kernel<D, kFp8>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3(static_cast<unsigned>(runs), static_cast<unsigned>(RT)), L::kThreads, L::kBytes, st>>>(kmap, vmap, a, partial, cuts);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_close(tile_join_kernel<D>, dim3(static_cast<unsigned>(RT * runs), BM / 8), 256, 0, st, a, runs,
+                      kFp8 ? 0x1p-11f : 1.f, partial, cuts);
+}
+
+}  // namespace
+
+size_t tree_tile_ws_bytes(int rows, int D) {
+  const size_t n = static_cast<size_t>((rows + BM - 1) / BM) * tile_runs(rows);
+  return ((n * sizeof(TileCut) + 255) & ~static_cast<size_t>(255)) + n * 2 * BM * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_tree_tile(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, bool fp8,
+                             cudaStream_t st) {
+  if (a.D == 64) return fp8 ? launch_tile<64, true>(a, kmap, vmap, st) : launch_tile<64, false>(a, kmap, vmap, st);
+  return fp8 ? launch_tile<128, true>(a, kmap, vmap, st) : launch_tile<128, false>(a, kmap, vmap, st);
+}
+
+}  // namespace sa
