@@ -15,13 +15,13 @@
 // P as two terms of 16 bits, high and low, each 64 columns: both fit the buffer that S
 // leaves. Bf16 terms are cut, not rounded, and 2^-24 of the weight is added to what is
 // left, so that both are positive and an infinite value stays one; weights to 2^-16.
-// Over a cache in e4m3 the terms are fp16 of 2^11 p (weights to 2^-21 of themselves or
-// 2^-36 of the largest), against codes turned into fp16, exact, by a warpgroup of its own
+// Over a cache in e4m3 the terms are fp16 of 2^5 p (weights to 2^-21 of themselves or
+// 2^-30 of the largest), against codes turned into fp16, exact, by a warpgroup of its own
 // on their way from TMA's stages to the MMA's.
 //
 // Softmax. Two warpgroups take the steps in turn, one thread a row. The running maximum
 // passes from step to step through shared memory and moves only when a step's exceeds it
-// by more than 2^4.
+// by more than 2^14 (e4m3: 2^10).
 //
 // Steps that hold new tokens, the last page or a page that is not there are masked bit by
 // bit (the ancestors of a row's token, shifted to the page); their warpgroup also takes
@@ -42,8 +42,7 @@ constexpr int kSBuf = 3;
 constexpr int kInfo = 16;            // steps whose pages are remembered
 constexpr int kProducer = 8, kMma = 9, kQuery = 10, kConvert = 12;
 constexpr int kColO = 384;           // S[b] at columns [128 b, 128 b + 128)
-constexpr float kRaise = 4.f;        // the maximum moves when exceeded by this power of two
-constexpr float kTileShift = 11.f;   // e4m3: P is held as 2^11 p, at most 2^15
+constexpr float kTileShift = 5.f;    // e4m3: P is held as 2^5 p
 
 // A unit's piece of a run, for the roles; steps < 0: no more.
 struct Head {
@@ -60,13 +59,13 @@ struct StepInfo {
 template <int D, bool kFp8>
 struct Tile {
   static constexpr int kThreads = kFp8 ? 512 : 384;
-  // softmax and other warpgroups' registers (setmaxnreg): 2*128*216 + 128*64 <= 384*168,
-  // 2*128*192 + 2*128*64 = 512*128
-  static constexpr int kSoftRegs = kFp8 ? 192 : 216, kRegs = 64;
+  // The running maximum moves when it is exceeded by this power of two (each move rescales
+  // O): fp16 holds 2^5 2^10, bf16 any.
+  static constexpr float kRaise = kFp8 ? 10.f : 14.f;
   static constexpr int kRegion = BM * 128;              // 128 bytes of each of 128 rows
   static constexpr int kQBytes = BM * D * 2;
   static constexpr int kTile = BN * D * 2;              // K or V of a step, 16 bits an element
-  static constexpr int kStages = D == 64 ? 8 : (kFp8 ? 4 : 5);
+  static constexpr int kStages = kFp8 && D == 128 ? 4 : 5;
   static constexpr int kRow = D * (kFp8 ? 1 : 2);       // a token of the cache
   static constexpr int kBox = kRow < 128 ? kRow : 128;
   static constexpr int kRaw = kFp8 ? BN * D : 0;        // K or V of a step as it is stored
@@ -104,32 +103,34 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
          static_cast<uint64_t>(2) << 61;
 }
 
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
+
+// 16 bytes to shared memory, zeros without a source.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
 __device__ __forceinline__ bool elected() {
   uint32_t pred = 0;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(pred));
   return pred != 0;
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// p = 2^((s - m) f) for 32 logits as two terms, pairs of keys in a word (e4m3: of 2^11 p);
+// p = 2^((s - m) f) for 32 logits as two terms, pairs of keys in a word (e4m3: of 2^5 p);
 // returns the sum of the p. Subtracting before scaling, the largest key has weight 1
 // however coarse fp32 is at its logit's size.
 template <bool kFp8>
 __device__ __forceinline__ float weigh32(const uint32_t* v, float m, float f, uint32_t* hi, uint32_t* lo) {
-  const uint64_t nm = f2_pack(-m, -m), ff = f2_pack(f, f), shift = f2_pack(kTileShift, kTileShift);
-  const uint64_t minus = f2_pack(-1.f, -1.f), tiny = f2_pack(0x1p-24f, 0x1p-24f);
+  const uint64_t nm = f2_pack(-m, -m), ff = f2_pack(f, f);
+  const uint64_t add = kFp8 ? f2_pack(kTileShift, kTileShift) : 0ull;
+  const uint64_t minus = f2_pack(-1.f, -1.f), more = f2_pack(1.f + 0x1p-23f, 1.f + 0x1p-23f);
   uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
   for (int u = 0; u < 32; u += 2) {
     const uint64_t d = f2_add(f2_pack(__uint_as_float(v[u]), __uint_as_float(v[u + 1])), nm);
-    const uint64_t y = kFp8 ? f2_fma(d, ff, shift) : f2_mul(d, ff);
     float y0, y1;
-    f2_unpack(y, y0, y1);
+    f2_unpack(f2_fma(d, ff, add), y0, y1);
     const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
     const uint64_t p = f2_pack(p0, p1);
     acc[(u >> 1) & 1] = f2_add(acc[(u >> 1) & 1], p);
@@ -141,15 +142,43 @@ __device__ __forceinline__ float weigh32(const uint32_t* v, float m, float f, ui
       f2_unpack(f2_fma(f2_pack(b.x, b.y), minus, p), r0, r1);
       lo[u >> 1] = pack_half(r0, r1);
     } else {
-      const uint32_t h = top_bf16(p0, p1);
-      hi[u >> 1] = h;
-      f2_unpack(f2_fma(p, tiny, f2_fma(f2_pack(lo_f32(h), hi_f32(h)), minus, p)), r0, r1);
+      hi[u >> 1] = top_bf16(p0, p1);
+      // less what the high term holds, and 2^-23 of the weight more
+      const float n0 = __uint_as_float((__float_as_uint(p0) & 0xffff0000u) | 0x80000000u);
+      const float n1 = __uint_as_float((__float_as_uint(p1) & 0xffff0000u) | 0x80000000u);
+      f2_unpack(f2_fma(p, more, f2_pack(n0, n1)), r0, r1);
       lo[u >> 1] = pack_bf16(r0, r1);
     }
   }
   float a, b;
   f2_unpack(f2_add(acc[0], acc[1]), a, b);
   return a + b;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+
+// O += P V of 64 keys, one term of P: 16 keys are 8 of its columns (32 keys each 32 columns
+// of the buffer: the high term's 16, the low one's) and 2 KB of V.
+__device__ __forceinline__ void pv_elect(uint32_t o_tmem, uint32_t p_tmem, uint64_t v0, uint64_t v1, uint64_t v2,
+                                         uint64_t v3, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "setp.eq.b32 t, %7, %7;\n\t"
+      "add.u32 a1, %1, 8;\n\t"
+      "add.u32 a2, %1, 32;\n\t"
+      "add.u32 a3, %1, 40;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %6, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %3, %6, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %4, %6, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], %5, %6, t;\n\t}"
+      ::"r"(o_tmem), "r"(p_tmem), "l"(v0), "l"(v1), "l"(v2), "l"(v3), "r"(idesc), "r"(accumulate) : "memory");
 }
 
 __device__ __forceinline__ float max32(const uint32_t* v) {
@@ -198,7 +227,6 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (a.dev_status) atomicOr(a.dev_status, SA_DEV_TIMEOUT);
   };
   int status = 0;
-
   let_next_launch();
   if (tid == 0) {
     for (int i = 0; i < L::kBars; ++i) {
@@ -236,7 +264,6 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const int total_steps = run.hi - run.lo;
 
   if (warp == kProducer) {
-    regs_dec<L::kRegs>();
     // ---------------------------------------------------------- producer --
     int left = total_steps, group = run.group, off = run.off, cnt = run.count;
     int it = 0, item = 0, gstep = 0;
@@ -287,8 +314,12 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       // one item of the ring: K (which = 0) or V of step j of the piece
       auto load = [&](int which, int j) -> bool {
         constexpr int NS = kFp8 ? L::kRawStages : L::kStages;
-        const int st = item % NS, e = kFp8 ? L::bRawEmpty : L::bEmpty, f = kFp8 ? L::bRawFull : L::bFull;
-        if (item >= NS && !mbar_wait_warp(bar(e + st), (item / NS - 1) & 1, abort)) return false;
+        const int st = item % NS, f = kFp8 ? L::bRawFull : L::bFull;
+        if (kFp8) {
+          if (item >= NS && !mbar_wait_warp(bar(L::bRawEmpty + st), (item / NS - 1) & 1, abort)) return false;
+        } else {
+          if (item >= NS && !mbar_wait_warp(bar(L::bEmpty + st), (item / NS - 1) & 1, abort)) return false;
+        }
         if (lane == 0) {
           volatile StepInfo* in = infos + (gstep + j) % kInfo;
           const int n0 = in->live[0] > 0, n1 = in->live[1] > 0;
@@ -396,8 +427,10 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
     }
   } else if (warp == kMma) {
-    regs_dec<L::kRegs>();
     // --------------------------------------------------------------- MMA --
+    // One warp feeds the tensor pipe, which holds only a few products ahead: what the warp
+    // does between them is the pipe's pause. So one look at the barriers a step where all
+    // is there, one election for the products of half a step, two commits a step.
     constexpr int kType = kFp8 ? 0 : 1;
     constexpr uint32_t kIdQK128 = idesc_f16(BM, 128, kType), kIdQK64 = idesc_f16(BM, 64, kType);
     constexpr uint32_t kIdPV = idesc_f16(BM, D, kType) | (1u << 16);      // B is MN-major
@@ -466,8 +499,8 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         for (int kh = 0; kh < halves; ++kh) {
           const uint64_t v0 = vb + static_cast<uint64_t>(kh * (kBlock * D * 2 >> 4));
           // 16 keys are 2 KB of rows
-          umma_ts_x4_elect(o_tmem, pa + 32 * kh, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, j > 0 || kh > 0);
-          umma_ts_x4_elect(o_tmem, pa + 64 + 32 * kh, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, 1u);
+          pv_elect(o_tmem, pa + 64 * kh, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, j > 0 || kh > 0);
+          pv_elect(o_tmem, pa + 64 * kh + 16, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, 1u);
         }
         umma_commit_elect(bar(L::bEmpty + st));
         umma_commit_elect(bar(L::bPvDone + (gsj & 1)));
@@ -484,9 +517,8 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     umma_commit_elect(bar(L::bFin));
     mbar_wait_warp(bar(L::bFin), 0, drain);
   } else if (warp == kQuery || warp == kQuery + 1) {
-    regs_dec<L::kRegs>();
     // ----------------------------------------------------------- queries --
-    constexpr int kLanes = D / 8, kRowsOnce = 64 / kLanes, kBatch = 4;    // lanes of a row
+    constexpr int kLanes = D / 8, kRowsOnce = 64 / kLanes;    // lanes of a row
     const int t64 = tid - kQuery * 32, sub = t64 % kLanes, r0 = t64 / kLanes;
     for (int it = 0;; ++it) {
       const int x = it & 1;
@@ -501,46 +533,53 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (lane == 0) fail();
         break;
       }
+      // all rows on their way at once, straight to where the MMA reads them
+      int tok = (rt * BM + r0) / G, head = rt * BM + r0 - tok * G;
+      const int d_tok = kRowsOnce / G, d_head = kRowsOnce - d_tok * G;
+#pragma unroll 4
+      for (int r = r0; r < BM; r += kRowsOnce) {
+        const bool there = rt * BM + r < rows;
+        const uint16_t* src = a.q + b * a.qs[0] + (there ? tok * a.qs[1] + (g * G + head) * a.qs[2] : 0) + 8 * sub;
+        copy_16(sbase + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4), src, there);
+        if (!kFp8 && sub == 0) factors[x * BM + r] = scale;
+        tok += d_tok;
+        head += d_head;
+        if (head >= G) {
+          head -= G;
+          ++tok;
+        }
+      }
       if (warp == kQuery && heads[x].special) {
         uint64_t set[2];
         ancestors(a, b, heads[x].fresh, lane, set, &status);
         seen_sets[x * 64 + lane] = set[0];
         seen_sets[x * 64 + 32 + lane] = set[1];
       }
-      for (int rb = 0; rb < BM; rb += kRowsOnce * kBatch) {
-        uint4 w[kBatch];
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (kFp8) {
+        // in fp16, a row scaled by a power of two so that its largest element is in
+        // [2^14, 2^15): bits are lost only below 2^-39 of it
+#pragma unroll 2
+        for (int r = r0; r < BM; r += kRowsOnce) {
+          uint4* at = reinterpret_cast<uint4*>(smem + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4));
+          uint4 w = *at;
+          uint32_t* e = &w.x;
+          float top = 0.f;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int row = rt * BM + rb + u * kRowsOnce + r0;
-          w[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (row < rows) {
-            const int tok = row / G;
-            w[u] = *reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + tok * a.qs[1] + (g * G + row - tok * G) * a.qs[2] + 8 * sub);
-          }
-        }
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_f32(e[i])), fabsf(hi_f32(e[i]))));
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int r = rb + u * kRowsOnce + r0;
-          if (kFp8) {
-            // in fp16, a row scaled by a power of two so that its largest element is in
-            // [2^14, 2^15): bits are lost only below 2^-39 of it
-            uint32_t* e = &w[u].x;
-            float top = 0.f;
+          for (int s = kLanes / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, s));
+          // its exponent, of a subnormal one by its first bit
+          const uint32_t bits = __float_as_uint(top);
+          const int ex = top > 0.f && top < INFINITY
+                             ? 14 - (bits >= 0x00800000u ? static_cast<int>(bits >> 23) - 127 : -118 - __clz(bits)) : 0;
+          const float up1 = power_of_two(ex / 2), up2 = power_of_two(ex - ex / 2);
+          float f = scale * power_of_two(-(ex / 2)) * power_of_two(-(ex - ex / 2));
+          if (f == 0.f) f = 0x1p-149f;
+          if (sub == 0) factors[x * BM + r] = f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_f32(e[i])), fabsf(hi_f32(e[i]))));
-#pragma unroll
-            for (int s = kLanes / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, s));
-            const int ex = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
-            const float up1 = ldexpf(1.f, ex / 2), up2 = ldexpf(1.f, ex - ex / 2);
-            float f = scale * ldexpf(1.f, -(ex / 2)) * ldexpf(1.f, -(ex - ex / 2));
-            if (f == 0.f) f = 0x1p-149f;
-            if (sub == 0) factors[x * BM + r] = f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = pack_half(lo_f32(e[i]) * up1 * up2, hi_f32(e[i]) * up1 * up2);
-          } else if (sub == 0) {
-            factors[x * BM + r] = scale;
-          }
-          *reinterpret_cast<uint4*>(smem + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4)) = w[u];
+          for (int i = 0; i < 4; ++i) e[i] = pack_half(lo_f32(e[i]) * up1 * up2, hi_f32(e[i]) * up1 * up2);
+          *at = w;
         }
       }
       fence_proxy_async_smem();
@@ -551,7 +590,6 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
     }
   } else if (kFp8 && warp >= kConvert) {
-    regs_dec<L::kRegs>();
     // -------------------------------------------------------- conversion --
     // A thread turns a row (one token's codes) into fp16: as read, so written, without
     // bank conflicts, as the rows' pieces are swizzled alike.
@@ -584,7 +622,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const uint8_t* src = smem + L::oRaw + rs * L::kRaw + kh * L::kPageBytes;
       uint8_t* dst = smem + L::oTiles + st * L::kTile;
       constexpr int kPieces = D / 16;           // of a row of codes
-#pragma unroll
+#pragma unroll 4
       for (int p = 0; p < kPieces; ++p) {
         const uint32_t at = D == 64 ? row * 64 + ((p ^ ((row >> 1) & 3)) << 4) : row * 128 + ((p ^ (row & 7)) << 4);
         const uint4 w = *reinterpret_cast<const uint4*>(src + at);
@@ -603,7 +641,6 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       ++done;
     }
   } else {
-    regs_inc<L::kSoftRegs>();
     // ----------------------------------------------------------- softmax --
     const int sm = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -716,45 +753,40 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           break;
         }
         tc_fence_after();
-        uint32_t sr[128];
-        float mx0, mx1, mx2 = -INFINITY, mx3 = -INFINITY;
-        tmem_ld32_max(lane_base + s_col, sr, mx0);
-        tmem_ld32_max(lane_base + s_col + 32, sr + 32, mx1);
-        if (two) {
-          tmem_ld32_max(lane_base + s_col + 64, sr + 64, mx2);
-          tmem_ld32_max(lane_base + s_col + 96, sr + 96, mx3);
-        }
-        tmem_wait_ld();
-        reg_fence32(sr);
-        reg_fence32(sr + 32);
-        reg_fence_f(mx0);
-        reg_fence_f(mx1);
-        if (two) {
-          reg_fence32(sr + 64);
-          reg_fence32(sr + 96);
-          reg_fence_f(mx2);
-          reg_fence_f(mx3);
-        }
-        if (masked) {
-          uint64_t keep[2];
-#pragma unroll
-          for (int kh = 0; kh < 2; ++kh) {
-            const int lv = in->live[kh], fs = in->first[kh];
-            keep[kh] = lv >= kBlock ? ~0ull : (1ull << lv) - 1;
-            if (fs > -kBlock) keep[kh] &= slots_seen(seen_sets[x * 64 + min(row / G, 63)], fs);
+        // the step's maximum, 64 keys at a time (masked: by bits, and written back so)
+        const uint32_t s_addr = lane_base + s_col;
+        const int groups = two ? 4 : 2;
+        float bmax = -INFINITY;
+        if (!masked) {
+#pragma unroll 1
+          for (int c = 0; c < groups; c += 2) {
+            uint32_t sr[64];
+            float mx0, mx1;
+            tmem_ld32_max(s_addr + 32 * c, sr, mx0);
+            tmem_ld32_max(s_addr + 32 * c + 32, sr + 32, mx1);
+            tmem_wait_ld();
+            reg_fence64(sr);
+            reg_fence_f(mx0);
+            reg_fence_f(mx1);
+            bmax = fmax3(bmax, mx0, mx1);
           }
-          keep32(sr, static_cast<uint32_t>(keep[0]));
-          keep32(sr + 32, static_cast<uint32_t>(keep[0] >> 32));
-          mx0 = max32(sr);
-          mx1 = max32(sr + 32);
-          if (two) {
-            keep32(sr + 64, static_cast<uint32_t>(keep[1]));
-            keep32(sr + 96, static_cast<uint32_t>(keep[1] >> 32));
-            mx2 = max32(sr + 64);
-            mx3 = max32(sr + 96);
+        } else {
+          const uint64_t set = special ? seen_sets[x * 64 + min(row / G, 63)] : 0ull;
+#pragma unroll 1
+          for (int c = 0; c < groups; ++c) {
+            const int lv = in->live[c >> 1], fs = in->first[c >> 1];
+            uint64_t keep = lv >= kBlock ? ~0ull : (1ull << lv) - 1;
+            if (fs > -kBlock) keep &= slots_seen(set, fs);
+            uint32_t sr[32];
+            tmem_ld32(s_addr + 32 * c, sr);
+            tmem_wait_ld();
+            reg_fence32(sr);
+            keep32(sr, static_cast<uint32_t>(keep >> (32 * (c & 1))));
+            bmax = fmaxf(bmax, max32(sr));
+            tmem_st32(s_addr + 32 * c, sr);
           }
+          tmem_wait_st();
         }
-        const float bmax = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
         float m_prev = -INFINITY;
         if (j > 0) {
           uint64_t hv;
@@ -765,7 +797,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           m_prev = __uint_as_float(static_cast<uint32_t>(hv));
         }
         float m_new = m_prev;
-        if (m_prev == -INFINITY || (bmax - m_prev) * f > kRaise) m_new = fmaxf(bmax, m_prev);
+        if (m_prev == -INFINITY || (bmax - m_prev) * f > L::kRaise) m_new = fmaxf(bmax, m_prev);
         *hand_mine = (static_cast<uint64_t>(static_cast<uint32_t>(gg)) << 32) | __float_as_uint(m_new);
         const bool raised = m_new != m_prev && m_prev != -INFINITY;
         if (__any_sync(full, raised)) {
@@ -786,23 +818,22 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tmem_st32(lane_base + kColO + 32 * cc, o);
           }
         }
+        // P over S, 32 keys at a time: a loop of few instructions, as a step's worth of them
+        // unrolled would leave the other warps waiting for theirs
         const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        float rs;
-        {
-          uint32_t hi[32], lo[32];
-          rs = weigh32<kFp8>(sr, m_use, f, hi, lo);
-          rs += weigh32<kFp8>(sr + 32, m_use, f, hi + 16, lo + 16);
-          tmem_st32(lane_base + s_col, hi);
-          tmem_st32(lane_base + s_col + 64, lo);
+        float rs = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < groups; ++c) {
+          uint32_t sr[32], hi[16], lo[16];
+          tmem_ld32(s_addr + 32 * c, sr);
+          tmem_wait_ld();
+          reg_fence32(sr);
+          rs += weigh32<kFp8>(sr, m_use, f, hi, lo);
+          tmem_st16(s_addr + 32 * c, hi);
+          tmem_st16(s_addr + 32 * c + 16, lo);
         }
-        if (two) {
-          uint32_t hi[32], lo[32];
-          rs += weigh32<kFp8>(sr + 64, m_use, f, hi, lo);
-          rs += weigh32<kFp8>(sr + 96, m_use, f, hi + 16, lo + 16);
-          tmem_st32(lane_base + s_col + 32, hi);
-          tmem_st32(lane_base + s_col + 96, lo);
-        }
-        l_run = (m_run == -INFINITY ? l_run : l_run * fast_exp2((m_run - m_use) * f)) + rs;
+        if (m_run != -INFINITY && m_run != m_new) l_run *= fast_exp2((m_run - m_new) * f);
+        l_run += rs;
         m_run = m_new;
         tmem_wait_st();
         tc_fence_before();
@@ -820,8 +851,8 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       tc_fence_after();
       const float m_tot = fmaxf(m_run, m_oth);
       // a set without a maximum has a sum of 0, or NaN if only NaN was there
-      const float l_tot = (m_run == -INFINITY ? l_run : l_run * fast_exp2((m_run - m_tot) * f)) +
-                          (m_oth == -INFINITY ? l_oth : l_oth * fast_exp2((m_oth - m_tot) * f));
+      const float l_tot = (m_run == -INFINITY || m_run == m_tot ? l_run : l_run * fast_exp2((m_run - m_tot) * f)) +
+                          (m_oth == -INFINITY || m_oth == m_tot ? l_oth : l_oth * fast_exp2((m_oth - m_tot) * f));
       const bool row_ok = row < n_rows;
       const int tok = row / G, h = g * G + row - tok * G, c0 = sm * (D / 2);
       const float inv = l_tot == 0.f ? 0.f : (kFp8 && a.v_scale ? get(a.v_scale + g) : 1.f) / l_tot;
@@ -883,7 +914,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         else if (a.lse)
           a.lse[(static_cast<int64_t>(b) * a.H + h) * a.S + tok] =
               l_tot == 0.f ? -INFINITY
-                           : (m2 + log2f(kFp8 ? l_tot * 0x1p-11f : l_tot)) * 0.69314718055994530942f;
+                           : (m2 + log2f(kFp8 ? l_tot * 0x1p-5f : l_tot)) * 0.69314718055994530942f;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::bHeadEmpty + x));
@@ -969,7 +1000,7 @@ cudaError_t launch_tile(const DecodeArgs& a, const CUtensorMap& kmap, const CUte
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_close(tile_join_kernel<D>, dim3(static_cast<unsigned>(RT * runs), BM / 8), 256, 0, st, a, runs,
-                      kFp8 ? 0x1p-11f : 1.f, partial, cuts);
+                      kFp8 ? 0x1p-5f : 1.f, partial, cuts);
 }
 
 }  // namespace
