@@ -11,7 +11,7 @@
 // Pipeline, as in attn.cu: TMEM holds three S buffers and one O accumulator. S(j) = Q K(j)^T
 // goes to buffer j % 3; the softmax turns it into P over the same columns; O += P V(j).
 // K is K-major as the page lies (rows of d), and so is V as an MN-major operand (rows of
-// keys): no transpose, no repacking. The MMA warp issues QK(j+2) before it waits for P(j).
+// keys): no transpose, no repacking. S runs up to two steps ahead of P.
 // P as two terms of 16 bits, high and low, each 64 columns: both fit the buffer that S
 // leaves. Bf16 terms are cut, not rounded, and 2^-24 of the weight is added to what is
 // left, so that both are positive and an infinite value stays one; weights to 2^-16.
@@ -29,9 +29,10 @@
 // is no finite number among the new tokens' values: a weight of 0 would not silence
 // those. Rows that see such a value get it added in the epilogue.
 //
-// Warps: 0-3 softmax of even steps, 4-7 of odd ones, 8 producer, 9 MMA, 10 and 11 the
-// queries (rows gathered by token and head, for e4m3 scaled by a power of two), 12-15
-// conversion (e4m3). Every wait is bounded (SA_DEV_TIMEOUT).
+// Warps: 0-3 softmax of even steps, 4-7 of odd ones, 8 pages and loads of K, 9
+// and 10 the products, 11 the queries (rows gathered by token and head, for e4m3 scaled by a
+// power of two) and loads of V, 12-15 conversion (e4m3). Every wait is bounded
+// (SA_DEV_TIMEOUT).
 #include "decode_kernel.cuh"
 
 namespace sa {
@@ -40,7 +41,7 @@ namespace {
 constexpr int BM = 128, BN = 128;
 constexpr int kSBuf = 3;
 constexpr int kInfo = 16;            // steps whose pages are remembered
-constexpr int kProducer = 8, kMma = 9, kQuery = 10, kConvert = 12;
+constexpr int kProducer = 8, kScore = 9, kMma = 10, kValue = 11, kConvert = 12;
 constexpr int kColO = 384;           // S[b] at columns [128 b, 128 b + 128)
 constexpr float kTileShift = 5.f;    // e4m3: P is held as 2^5 p
 
@@ -65,20 +66,20 @@ struct Tile {
   static constexpr int kRegion = BM * 128;              // 128 bytes of each of 128 rows
   static constexpr int kQBytes = BM * D * 2;
   static constexpr int kTile = BN * D * 2;              // K or V of a step, 16 bits an element
-  static constexpr int kStages = kFp8 && D == 128 ? 4 : 5;
+  // Stages of K and of V (steps; D = 64 has room for more), and of what is still in e4m3.
+  static constexpr int kK = D == 64 ? 3 : 2, kV = D == 64 || !kFp8 ? 3 : 2;
   static constexpr int kRow = D * (kFp8 ? 1 : 2);       // a token of the cache
-  static constexpr int kBox = kRow < 128 ? kRow : 128;
-  static constexpr int kRaw = kFp8 ? BN * D : 0;        // K or V of a step as it is stored
-  static constexpr int kRawStages = kFp8 ? 3 : 0;
   static constexpr int kPageBytes = kBlock * kRow;
-  static constexpr int oQ = 0, oTiles = oQ + kQBytes, oRaw = oTiles + kStages * kTile;
-  static constexpr int oBar = oRaw + kRawStages * kRaw;
+  static constexpr int kRaw = kFp8 ? 3 : 0;             // pages of codes of K and as many of V
+  static constexpr int oQ = 0, oK = oQ + kQBytes, oV = oK + kK * kTile, oRaw = oV + kV * kTile;
+  static constexpr int oBar = oRaw + 2 * kRaw * kPageBytes;
   // barriers
-  static constexpr int bHeadFull = 0, bHeadEmpty = 2, bQFull = 4, bQEmpty = 5, bFull = 6;
-  static constexpr int bEmpty = bFull + kStages, bSFull = bEmpty + kStages, bPFull = bSFull + kSBuf;
-  static constexpr int bPvDone = bPFull + kSBuf, bTileDone = bPvDone + 2, bOFree = bTileDone + 1;
-  static constexpr int bFin = bOFree + 1, bInfo = bFin + 1, bRawFull = bInfo + kInfo;
-  static constexpr int bRawEmpty = bRawFull + kRawStages, kBars = bRawEmpty + kRawStages;
+  static constexpr int bHeadFull = 0, bHeadEmpty = 2, bQFull = 4, bQEmpty = 5, bKFull = 6;
+  static constexpr int bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV;
+  static constexpr int bSFull = bVEmpty + kV, bPFull = bSFull + kSBuf, bPvDone = bPFull + kSBuf;
+  static constexpr int bTileDone = bPvDone + 2, bOFree = bTileDone + 1, bPvIssued = bOFree + 1;
+  static constexpr int bFin = bPvIssued + kSBuf, bInfo = bFin + 2, bRawFull = bInfo + kInfo;
+  static constexpr int bRawEmpty = bRawFull + 2 * kRaw, kBars = bRawEmpty + 2 * kRaw;
   static constexpr int oMisc = oBar + kBars * 8;        // tmem base, abort flag, odd values [2]
   static constexpr int oHead = oMisc + 16;
   static constexpr int oInfo = oHead + 2 * static_cast<int>(sizeof(Head));
@@ -106,6 +107,15 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
 
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+  return w;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, uint4 w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+
 // 16 bytes to shared memory, zeros without a source.
 __device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -115,6 +125,29 @@ __device__ __forceinline__ bool elected() {
   uint32_t pred = 0;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(pred));
   return pred != 0;
+}
+
+// Both pages (-1: none) of a step's K or V in bf16 into a tile, by one lane: all rows of a
+// slice of 64 d follow each other in K, a page's slices in V.
+template <int D, bool kValues>
+__device__ __forceinline__ void load_tile(const CUtensorMap* map, uint32_t f, uint32_t dst, int pa, int pb, int g) {
+  constexpr uint32_t kSlice = kValues ? kBlock * 128 : BM * 128, kNext = kValues ? kBlock * D * 2 : kBlock * 128;
+  if (elected()) {
+    const int bytes = ((pa >= 0) + (pb >= 0)) * (kBlock * D * 2);
+    if (bytes > 0)
+      mbar_arrive_expect_tx(f, bytes);
+    else
+      mbar_arrive(f);
+    if (pa >= 0) {
+      tma_load_4d(dst, map, f, 0, 0, g, pa);
+      if (D == 128) tma_load_4d(dst + kSlice, map, f, 64, 0, g, pa);
+    }
+    if (pb >= 0) {
+      tma_load_4d(dst + kNext, map, f, 0, 0, g, pb);
+      if (D == 128) tma_load_4d(dst + kNext + kSlice, map, f, 64, 0, g, pb);
+    }
+  }
+  __syncwarp();
 }
 
 // p = 2^((s - m) f) for 32 logits as two terms, pairs of keys in a word (e4m3: of 2^5 p);
@@ -231,12 +264,11 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   if (tid == 0) {
     for (int i = 0; i < L::kBars; ++i) {
       uint32_t n = 1;
-      if (i >= L::bHeadEmpty && i < L::bHeadEmpty + 2) n = 1 + 8 + 2;     // MMA, softmax, queries
-      if (i == L::bQFull) n = 2;
+      if (i >= L::bHeadEmpty && i < L::bHeadEmpty + 2) n = 2 + 8 + 1;     // products, softmax, queries and V
       if (i >= L::bPFull && i < L::bPFull + kSBuf) n = 128;
       if (i == L::bOFree) n = 256;
-      if (kFp8 && i >= L::bFull && i < L::bFull + L::kStages) n = 4;       // the converting warps
-      if (kFp8 && i >= L::bRawEmpty) n = 4;
+      if (kFp8 && ((i >= L::bKFull && i < L::bKEmpty) || (i >= L::bVFull && i < L::bVEmpty) || i >= L::bRawEmpty))
+        n = 2;                               // converting warps
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -263,10 +295,58 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const uint32_t tmem = misc[0];
   const int total_steps = run.hi - run.lo;
 
+  // K's or V's pages (-1: none) of the next step into its ring: tiles of bf16, or pages of
+  // codes that have yet to be turned into fp16. Addresses and pages are in registers: read
+  // from shared memory box by box they took 1,500 cycles a tile, and the kernel's pace.
+  auto load_step = [&](bool values, int& st, int& ph, int& filled, int pa, int pb, int g) -> bool {
+    if (!kFp8) {
+      const int n = values ? L::kV : L::kK;
+      if (!mbar_wait_warp(bar((values ? L::bVEmpty : L::bKEmpty) + st), ph, abort)) return false;
+      if (values)
+        load_tile<D, true>(&vmap, bar(L::bVFull + st), sbase + L::oV + st * L::kTile, pa, pb, g);
+      else
+        load_tile<D, false>(&kmap, bar(L::bKFull + st), sbase + L::oK + st * L::kTile, pa, pb, g);
+      ++filled;
+      if (++st == n) {
+        st = 0;
+        ph ^= 1;
+      }
+      return true;
+    }
+    for (int kh = 0; kFp8 && kh < 2; ++kh) {
+      const int at = (values ? L::kRaw : 0) + st, page = kh ? pb : pa;
+      if (!mbar_wait_warp(bar(L::bRawEmpty + at), ph, abort)) return false;
+      if (elected()) {
+        const uint32_t f = bar(L::bRawFull + at);
+        if (page >= 0) {
+          mbar_arrive_expect_tx(f, L::kPageBytes);
+          tma_load_4d(sbase + L::oRaw + at * L::kPageBytes, values ? &vmap : &kmap, f, 0, 0, g, page);
+        } else {
+          mbar_arrive(f);
+        }
+      }
+      __syncwarp();
+      ++filled;
+      if (++st == (kFp8 ? L::kRaw : 1)) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    return true;
+  };
+  // no copy may be in flight when the CTA ends
+  auto drain_loads = [&](bool values, int filled) {
+    const int n = kFp8 ? L::kRaw : (values ? L::kV : L::kK);
+    const int f = kFp8 ? L::bRawFull + (values ? L::kRaw : 0) : (values ? L::bVFull : L::bKFull);
+    for (int s = 0; s < n && s < filled; ++s)       // the fills of stage s before its last one
+      mbar_wait(bar(f + s), (filled - 1 - s) / n & 1, drain);
+  };
+
   if (warp == kProducer) {
     // ---------------------------------------------------------- producer --
     int left = total_steps, group = run.group, off = run.off, cnt = run.count;
-    int it = 0, item = 0, gstep = 0;
+    int it = 0, gstep = 0;
+    int k_st = 0, k_ph = 1, filled = 0;   // the next stage of K (e4m3: page of codes)
     TileCut cut{-1, 0, 0, 0};
     bool ok = true;
     while (left > 0 && ok && group < n_groups) {
@@ -311,43 +391,12 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       __syncwarp();
       if (dest == 1)
         cut = TileCut{b * a.Hkv + g, run_id, run_of(run.T, runs, run.hi - left + cnt - 1), 0};
-      // one item of the ring: K (which = 0) or V of step j of the piece
-      auto load = [&](int which, int j) -> bool {
-        constexpr int NS = kFp8 ? L::kRawStages : L::kStages;
-        const int st = item % NS, f = kFp8 ? L::bRawFull : L::bFull;
-        if (kFp8) {
-          if (item >= NS && !mbar_wait_warp(bar(L::bRawEmpty + st), (item / NS - 1) & 1, abort)) return false;
-        } else {
-          if (item >= NS && !mbar_wait_warp(bar(L::bEmpty + st), (item / NS - 1) & 1, abort)) return false;
-        }
-        if (lane == 0) {
-          volatile StepInfo* in = infos + (gstep + j) % kInfo;
-          const int n0 = in->live[0] > 0, n1 = in->live[1] > 0;
-          const uint32_t to = bar(f + st);
-          const uint32_t dst = sbase + (kFp8 ? L::oRaw + st * L::kRaw : L::oTiles + st * L::kTile);
-          if (n0 + n1 > 0)
-            mbar_arrive_expect_tx(to, (n0 + n1) * L::kPageBytes);
-          else
-            mbar_arrive(to);
-          for (int kh = 0; kh < 2; ++kh) {
-            if (in->live[kh] <= 0) continue;
-            constexpr int kBoxes = L::kRow / L::kBox, kElts = L::kBox / (kFp8 ? 1 : 2);
-            for (int dh = 0; dh < kBoxes; ++dh) {
-              // K: all rows of a slice of d follow each other; V: a page's slices do
-              const uint32_t at = kFp8 ? dst + kh * L::kPageBytes
-                                       : dst + (which ? kh * L::kPageBytes + dh * 8192
-                                                      : dh * L::kRegion + kh * 8192);
-              tma_load_4d(at, which ? &vmap : &kmap, to, dh * kElts, 0, g, in->page[kh]);
-            }
-          }
-        }
-        __syncwarp();
-        ++item;
-        return true;
-      };
-      int pg = 0, lv = 0, fs = 0;         // the batch's pages, a lane each
-      for (int j = 0; j < take + 2 && ok; ++j) {
-        if (j < take) {
+      // Loads of a step's two pages. (Addresses and pages in registers: this warp's own
+      // pace, with its pages read from shared memory 1,500 cycles a tile, was the kernel's.)
+      int pg = 0, lv = 0, fs = 0;         // 32 pages that were looked up, a lane each
+      for (int j = 0; j < take && ok; ++j) {
+        int ka, kb;
+        {
           const int q = 2 * j % 32;
           if (q == 0) {                   // the next 32 pages are looked up
             const int at = 2 * j + lane;
@@ -378,27 +427,27 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                   lv = 0;
                 }
               }
+              if (lv <= 0) pg = -1;
             }
           }
-          const int pg0 = __shfl_sync(full, pg, q), pg1 = __shfl_sync(full, pg, q + 1);
+          ka = __shfl_sync(full, pg, q);
+          kb = __shfl_sync(full, pg, q + 1);
           const int lv0 = __shfl_sync(full, lv, q), lv1 = __shfl_sync(full, lv, q + 1);
           const int fs0 = __shfl_sync(full, fs, q), fs1 = __shfl_sync(full, fs, q + 1);
           if (lane == 0) {
             volatile StepInfo* in = infos + (gstep + j) % kInfo;
-            in->page[0] = pg0;
-            in->page[1] = pg1;
+            in->page[0] = ka;
+            in->page[1] = kb;
             in->live[0] = lv0;
             in->live[1] = lv1;
             in->first[0] = fs0;
             in->first[1] = fs1;
-            const bool two = 2 * j + 1 < n_pages;
-            in->masked = lv0 < kBlock || fs0 > -kBlock || (two && (lv1 < kBlock || fs1 > -kBlock));
+            in->masked = lv0 < kBlock || fs0 > -kBlock || (2 * j + 1 < n_pages && (lv1 < kBlock || fs1 > -kBlock));
             mbar_arrive(bar(L::bInfo + (gstep + j) % kInfo));
           }
           __syncwarp();
-          ok = load(0, j);
         }
-        if (ok && j >= 2) ok = load(1, j - 2);
+        ok = load_step(false, k_st, k_ph, filled, ka, kb, g);
       }
       if (!ok) {
         if (lane == 0) fail();
@@ -419,137 +468,147 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     }
     if (lane == 0) {
       cuts[static_cast<int64_t>(rt) * runs + run_id] = cut;
-      // no copy may be in flight when the CTA ends
-      constexpr int NS = kFp8 ? L::kRawStages : L::kStages;
-      for (int s = 0; s < NS && s < item; ++s) {
-        const int last = (item - 1 - s) / NS;       // the fills of stage s before its last one
-        mbar_wait(bar((kFp8 ? L::bRawFull : L::bFull) + s), last & 1, drain);
-      }
+      drain_loads(false, filled);
     }
-  } else if (warp == kMma) {
-    // --------------------------------------------------------------- MMA --
-    // One warp feeds the tensor pipe, which holds only a few products ahead: what the warp
-    // does between them is the pipe's pause. So one look at the barriers a step where all
-    // is there, one election for the products of half a step, two commits a step.
-    constexpr int kType = kFp8 ? 0 : 1;
-    constexpr uint32_t kIdQK128 = idesc_f16(BM, 128, kType), kIdQK64 = idesc_f16(BM, 64, kType);
-    constexpr uint32_t kIdPV = idesc_f16(BM, D, kType) | (1u << 16);      // B is MN-major
+  } else if (warp == kScore) {
+    // ------------------------------------------------------------ Q K^T --
+    // Two warps feed the tensor pipe, one the scores, one the outputs. It takes products a
+    // few ahead of the one it works on, and a warp's waits, commits and 50 cycles a product
+    // (of 64) add up to 2,200 cycles a step of 1,536. S of step g takes the buffer of step
+    // g - 3 once that one's PV is issued; the fences order the two warps' products.
+    constexpr uint32_t kIdQK128 = idesc_f16(BM, 128, kFp8 ? 0 : 1), kIdQK64 = idesc_f16(BM, 64, kFp8 ? 0 : 1);
     constexpr int kKS = D / 16;
     uint64_t qd[kKS];
 #pragma unroll
     for (int k = 0; k < kKS; ++k)
       qd[k] = sdesc_kmajor_sw128(sbase + L::oQ + (k >> 2) * L::kRegion + (k & 3) * 32);
-    const uint32_t o_tmem = tmem + kColO;
-    int c = 0, gs0 = 0;
+    const uint64_t kd = sdesc_kmajor_sw128(sbase + L::oK);
+    int g = 0, sb = 0, sb_ph = 1, st = 0, ph = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int x = it & 1;
-      if (!mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort)) {
-        if (lane == 0) fail();
-        break;
-      }
+      ok = mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort);
+      if (!ok) break;
       const int n = heads[x].steps, n_pages = heads[x].pages;
       if (n < 0) break;
-      if (!mbar_wait_warp(bar(L::bQFull), it & 1, abort)) {
-        if (lane == 0) fail();
-        break;
-      }
-      tc_fence_after();
-      auto issue_qk = [&](int j) -> bool {
-        const int st = c % L::kStages;
-        if (!mbar_wait_warp(bar(L::bFull + st), (c / L::kStages) & 1, abort)) return false;
+      ok = mbar_wait_warp(bar(L::bQFull), it & 1, abort);
+      for (int j = 0; j < n && ok; ++j) {
+        ok = mbar_wait_warp(bar(L::bKFull + st), ph, abort) &&
+             (g < kSBuf || mbar_wait_warp(bar(L::bPvIssued + sb), sb_ph, abort));
+        if (!ok) break;
         tc_fence_after();
-        const int b = (gs0 + j) % kSBuf;
         const uint32_t idesc = 2 * j + 1 < n_pages ? kIdQK128 : kIdQK64;
-        const uint64_t kb = sdesc_kmajor_sw128(sbase + L::oTiles + st * L::kTile);
+        const uint64_t kb = kd + static_cast<uint64_t>(st * (L::kTile >> 4));
 #pragma unroll
         for (int h = 0; h < kKS / 4; ++h) {
           const uint64_t k0 = kb + static_cast<uint64_t>((h * L::kRegion) >> 4);
-          umma_ss_x4_elect(tmem + b * 128, qd[4 * h], qd[4 * h + 1], qd[4 * h + 2], qd[4 * h + 3], k0, k0 + 2,
+          umma_ss_x4_elect(tmem + sb * 128, qd[4 * h], qd[4 * h + 1], qd[4 * h + 2], qd[4 * h + 3], k0, k0 + 2,
                            k0 + 4, k0 + 6, idesc, h > 0);
         }
-        umma_commit_elect(bar(L::bSFull + b));
-        umma_commit_elect(bar(L::bEmpty + st));
+        umma_commit_elect(bar(L::bSFull + sb));
+        umma_commit_elect(bar(L::bKEmpty + st));
         if (j == n - 1) umma_commit_elect(bar(L::bQEmpty));
-        ++c;
-        return true;
-      };
-      for (int j = 0; j < 2 && j < n && ok; ++j) ok = issue_qk(j);
+        ++g;
+        if (++st == L::kK) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (++sb == kSBuf) {
+          sb = 0;
+          sb_ph ^= 1;
+        }
+      }
+      if (ok && elected()) mbar_arrive(bar(L::bHeadEmpty + x));
+    }
+    if (!ok && lane == 0) fail();
+    umma_commit_elect(bar(L::bFin));
+    mbar_wait_warp(bar(L::bFin), 0, drain);
+  } else if (warp == kMma) {
+    // --------------------------------------------------------------- P V --
+    constexpr uint32_t kIdPV = idesc_f16(BM, D, kFp8 ? 0 : 1) | (1u << 16);      // B is MN-major
+    const uint64_t vd = sdesc_mn_sw128(sbase + L::oV);
+    const uint32_t o_tmem = tmem + kColO;
+    int g = 0, sb = 0, sb_ph = 0, st = 0, ph = 0;
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      const int x = it & 1;
+      ok = mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort);
+      if (!ok) break;
+      const int n = heads[x].steps, n_pages = heads[x].pages;
+      if (n < 0) break;
+      // the last piece's epilogue has read O
+      ok = it == 0 || mbar_wait_warp(bar(L::bOFree), (it - 1) & 1, abort);
       for (int j = 0; j < n && ok; ++j) {
-        if (j + 2 < n && !issue_qk(j + 2)) {
-          ok = false;
-          break;
-        }
-        // the last piece's epilogue has read O
-        if (j == 0 && it >= 1 && !mbar_wait_warp(bar(L::bOFree), (it - 1) & 1, abort)) {
-          ok = false;
-          break;
-        }
-        const int gsj = gs0 + j, b = gsj % kSBuf, st = c % L::kStages;
         bool unused = false;
-        if (!mbar_wait2_warp(bar(L::bPFull + b), (gsj / kSBuf) & 1, bar(L::bFull + st), (c / L::kStages) & 1,
-                             false, 0u, 0u, &unused, abort)) {
-          ok = false;
-          break;
-        }
+        ok = mbar_wait2_warp(bar(L::bPFull + sb), sb_ph, bar(L::bVFull + st), ph, false, 0u, 0u, &unused, abort);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t pa = tmem + b * 128;
-        const uint64_t vb = sdesc_mn_sw128(sbase + L::oTiles + st * L::kTile);
-        const int halves = 2 * j + 1 < n_pages ? 2 : 1;
-        for (int kh = 0; kh < halves; ++kh) {
-          const uint64_t v0 = vb + static_cast<uint64_t>(kh * (kBlock * D * 2 >> 4));
-          // 16 keys are 2 KB of rows
-          pv_elect(o_tmem, pa + 64 * kh, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, j > 0 || kh > 0);
-          pv_elect(o_tmem, pa + 64 * kh + 16, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, 1u);
+        const uint32_t pa = tmem + sb * 128;
+        const uint64_t v0 = vd + static_cast<uint64_t>(st * (L::kTile >> 4));
+        // 16 keys are 2 KB of rows
+        pv_elect(o_tmem, pa, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, j > 0);
+        pv_elect(o_tmem, pa + 16, v0, v0 + 128, v0 + 256, v0 + 384, kIdPV, 1u);
+        if (2 * j + 1 < n_pages) {
+          const uint64_t v1 = v0 + (kBlock * D * 2 >> 4);
+          pv_elect(o_tmem, pa + 64, v1, v1 + 128, v1 + 256, v1 + 384, kIdPV, 1u);
+          pv_elect(o_tmem, pa + 80, v1, v1 + 128, v1 + 256, v1 + 384, kIdPV, 1u);
         }
-        umma_commit_elect(bar(L::bEmpty + st));
-        umma_commit_elect(bar(L::bPvDone + (gsj & 1)));
-        ++c;
+        tc_fence_before();
+        if (elected()) mbar_arrive(bar(L::bPvIssued + sb));
+        umma_commit_elect(bar(L::bVEmpty + st));
+        umma_commit_elect(bar(L::bPvDone + (g & 1)));
+        ++g;
+        if (++st == L::kV) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (++sb == kSBuf) {
+          sb = 0;
+          sb_ph ^= 1;
+        }
       }
-      gs0 += n;
-      if (!ok) {
-        if (lane == 0) fail();
-        break;
-      }
+      if (!ok) break;
       umma_commit_elect(bar(L::bTileDone));
       if (elected()) mbar_arrive(bar(L::bHeadEmpty + x));
     }
-    umma_commit_elect(bar(L::bFin));
-    mbar_wait_warp(bar(L::bFin), 0, drain);
-  } else if (warp == kQuery || warp == kQuery + 1) {
-    // ----------------------------------------------------------- queries --
-    constexpr int kLanes = D / 8, kRowsOnce = 64 / kLanes;    // lanes of a row
-    const int t64 = tid - kQuery * 32, sub = t64 % kLanes, r0 = t64 / kLanes;
-    for (int it = 0;; ++it) {
+    if (!ok && lane == 0) fail();
+    umma_commit_elect(bar(L::bFin + 1));
+    mbar_wait_warp(bar(L::bFin + 1), 0, drain);
+  } else if (warp == kValue) {
+    // ---------------------------------------- queries, then loads of V --
+    constexpr int kLanes = D / 8, kRowsOnce = 32 / kLanes;    // lanes of a row
+    const int sub = lane % kLanes, r0 = lane / kLanes;
+    int st = 0, ph = 1, gv = 0, filled = 0;
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
       const int x = it & 1;
-      if (!mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort)) {
-        if (lane == 0) fail();
-        break;
-      }
-      if (heads[x].steps < 0) break;
-      const int b = heads[x].b, g = heads[x].g, rows = heads[x].fresh * G;
+      ok = mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort);
+      if (!ok) break;
+      const int n = heads[x].steps, b = heads[x].b, g = heads[x].g, rows = heads[x].fresh * G;
+      if (n < 0) break;
       const float scale = a.scale_log2 * (kFp8 && a.k_scale ? get(a.k_scale + g) : 1.f);
-      if (it >= 1 && !mbar_wait_warp(bar(L::bQEmpty), (it - 1) & 1, abort)) {
-        if (lane == 0) fail();
-        break;
-      }
+      ok = it == 0 || mbar_wait_warp(bar(L::bQEmpty), (it - 1) & 1, abort);
+      if (!ok) break;
       // all rows on their way at once, straight to where the MMA reads them
-      int tok = (rt * BM + r0) / G, head = rt * BM + r0 - tok * G;
-      const int d_tok = kRowsOnce / G, d_head = kRowsOnce - d_tok * G;
+      const int first = rt * BM + r0, d_tok = kRowsOnce / G, d_head = kRowsOnce - d_tok * G;
+      const int64_t step = d_tok * a.qs[1] + d_head * a.qs[2], wrap = a.qs[1] - G * a.qs[2];
+      int head = first % G, left = rows - first;       // rows from this one on
+      const uint16_t* src = a.q + b * a.qs[0] + first / G * a.qs[1] + (g * G + head) * a.qs[2] + 8 * sub;
+      uint32_t dst = sbase + L::oQ + (sub >> 3) * L::kRegion + r0 * 128;
 #pragma unroll 4
       for (int r = r0; r < BM; r += kRowsOnce) {
-        const bool there = rt * BM + r < rows;
-        const uint16_t* src = a.q + b * a.qs[0] + (there ? tok * a.qs[1] + (g * G + head) * a.qs[2] : 0) + 8 * sub;
-        copy_16(sbase + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4), src, there);
+        copy_16(dst + (((sub & 7) ^ (r & 7)) << 4), left > 0 ? src : a.q, left > 0);
         if (!kFp8 && sub == 0) factors[x * BM + r] = scale;
-        tok += d_tok;
+        src += step;
         head += d_head;
         if (head >= G) {
           head -= G;
-          ++tok;
+          src += wrap;
         }
+        dst += kRowsOnce * 128;
+        left -= kRowsOnce;
       }
-      if (warp == kQuery && heads[x].special) {
+      if (heads[x].special) {
         uint64_t set[2];
         ancestors(a, b, heads[x].fresh, lane, set, &status);
         seen_sets[x * 64 + lane] = set[0];
@@ -559,87 +618,78 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (kFp8) {
         // in fp16, a row scaled by a power of two so that its largest element is in
         // [2^14, 2^15): bits are lost only below 2^-39 of it
-#pragma unroll 2
+#pragma unroll 4
         for (int r = r0; r < BM; r += kRowsOnce) {
-          uint4* at = reinterpret_cast<uint4*>(smem + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4));
-          uint4 w = *at;
+          const uint32_t at = sbase + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4);
+          uint4 w = load_shared(at);
           uint32_t* e = &w.x;
           float top = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_f32(e[i])), fabsf(hi_f32(e[i]))));
 #pragma unroll
           for (int s = kLanes / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, s));
-          // its exponent, of a subnormal one by its first bit
-          const uint32_t bits = __float_as_uint(top);
-          const int ex = top > 0.f && top < INFINITY
-                             ? 14 - (bits >= 0x00800000u ? static_cast<int>(bits >> 23) - 127 : -118 - __clz(bits)) : 0;
-          const float up1 = power_of_two(ex / 2), up2 = power_of_two(ex - ex / 2);
+          // its exponent; beyond 2^127 a row next to the least floats is scaled by that
+          const int ex = top < INFINITY ? min(141 - static_cast<int>(__float_as_uint(top) >> 23), 127) : 0;
+          const float up = power_of_two(ex);
           float f = scale * power_of_two(-(ex / 2)) * power_of_two(-(ex - ex / 2));
           if (f == 0.f) f = 0x1p-149f;
           if (sub == 0) factors[x * BM + r] = f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = pack_half(lo_f32(e[i]) * up1 * up2, hi_f32(e[i]) * up1 * up2);
-          *at = w;
+          for (int i = 0; i < 4; ++i) e[i] = pack_half(lo_f32(e[i]) * up, hi_f32(e[i]) * up);
+          store_shared(at, w);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(L::bQFull));
-        mbar_arrive(bar(L::bHeadEmpty + x));
+      if (lane == 0) mbar_arrive(bar(L::bQFull));
+      for (int j = 0; j < n && ok; ++j, ++gv) {
+        const volatile StepInfo* in = infos + gv % kInfo;
+        ok = mbar_wait_warp(bar(L::bInfo + gv % kInfo), (gv / kInfo) & 1, abort);
+        if (ok) ok = load_step(true, st, ph, filled, in->page[0], in->page[1], g);
       }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(bar(L::bHeadEmpty + x));
     }
+    if (!ok && lane == 0) fail();
+    if (lane == 0) drain_loads(true, filled);
   } else if (kFp8 && warp >= kConvert) {
     // -------------------------------------------------------- conversion --
-    // A thread turns a row (one token's codes) into fp16: as read, so written, without
-    // bank conflicts, as the rows' pieces are swizzled alike.
-    const int r = tid - kConvert * 32, kh = r >> 6, row = r & 63;
-    const int items = 2 * total_steps;
-    // the items' order: K(0), K(1), then K(j + 2), V(j) of each piece
-    constexpr int NR = kFp8 ? L::kRawStages : 1;
-    int n = 0, it = 0, done = 0;                // the piece's steps, its items so far
-    for (int c = 0; c < items; ++c) {
-      if (done == 2 * n) {
-        const int x = it & 1;
-        if (!mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort)) {
-          if (lane == 0) fail();
-          break;
+    // Two warps turn K into fp16, two V: a thread two rows (tokens) of each. As read, so
+    // written, without bank conflicts, as the rows' pieces are swizzled alike.
+    const bool values = warp >= kConvert + 2;
+    const int row = tid & 63, raw0 = values ? L::kRaw : 0;
+    constexpr int NR = kFp8 ? L::kRaw : 1;
+    bool ok = true;
+    for (int g = 0; g < total_steps && ok; ++g) {
+      const int st = values ? g % L::kV : g % L::kK, round = values ? g / L::kV : g / L::kK;
+      ok = mbar_wait_warp(bar((values ? L::bVEmpty : L::bKEmpty) + st), (round & 1) ^ 1, abort);
+      for (int kh = 0; kh < 2 && ok; ++kh) {
+        const int c = 2 * g + kh, rs = raw0 + c % NR;
+        ok = mbar_wait_warp(bar(L::bRawFull + rs), (c / NR) & 1, abort);
+        const uint32_t src = sbase + L::oRaw + rs * L::kPageBytes;
+        const uint32_t dst = sbase + (values ? L::oV + st * L::kTile + kh * (kBlock * D * 2)
+                                             : L::oK + st * L::kTile + kh * 8192) + row * 128;
+        const uint32_t slice = values ? 8192 : L::kRegion;
+        constexpr int kPieces = D / 16;           // of a row of codes
+        uint4 w[kPieces];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+          w[p] = load_shared(src + (D == 64 ? row * 64 + ((p ^ ((row >> 1) & 3)) << 4) : row * 128 + ((p ^ (row & 7)) << 4)));
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+          const uint2 h0 = e4m3x4_half4(w[p].x), h1 = e4m3x4_half4(w[p].y), h2 = e4m3x4_half4(w[p].z), h3 = e4m3x4_half4(w[p].w);
+          const uint32_t c0 = (p & 3) * 2, to = dst + (p >> 2) * slice;
+          store_shared(to + ((c0 ^ (row & 7)) << 4), make_uint4(h0.x, h0.y, h1.x, h1.y));
+          store_shared(to + (((c0 + 1) ^ (row & 7)) << 4), make_uint4(h2.x, h2.y, h3.x, h3.y));
         }
-        n = heads[x].steps;
-        if (n < 0) break;
-        done = 0;
-        ++it;
-      }
-      // of the first min(2, n) items, and then every second one while there are K left, K
-      const int ks = min(2, n), rest = done - ks;
-      const bool is_v = rest >= 0 && (rest >= 2 * (n - ks) || (rest & 1));
-      const int rs = c % NR, st = c % L::kStages;
-      if (!mbar_wait_warp(bar(L::bRawFull + rs), (c / NR) & 1, abort) ||
-          (c >= L::kStages && !mbar_wait_warp(bar(L::bEmpty + st), (c / L::kStages - 1) & 1, abort))) {
-        if (lane == 0) fail();
-        break;
-      }
-      const uint8_t* src = smem + L::oRaw + rs * L::kRaw + kh * L::kPageBytes;
-      uint8_t* dst = smem + L::oTiles + st * L::kTile;
-      constexpr int kPieces = D / 16;           // of a row of codes
-#pragma unroll 4
-      for (int p = 0; p < kPieces; ++p) {
-        const uint32_t at = D == 64 ? row * 64 + ((p ^ ((row >> 1) & 3)) << 4) : row * 128 + ((p ^ (row & 7)) << 4);
-        const uint4 w = *reinterpret_cast<const uint4*>(src + at);
-        const uint2 h0 = e4m3x4_half4(w.x), h1 = e4m3x4_half4(w.y), h2 = e4m3x4_half4(w.z), h3 = e4m3x4_half4(w.w);
-        const int dh = p >> 2, c0 = (p & 3) * 2;
-        uint8_t* to = dst + (is_v ? kh * (kBlock * D * 2) + dh * 8192 : dh * L::kRegion + kh * 8192) + row * 128;
-        *reinterpret_cast<uint4*>(to + ((c0 ^ (row & 7)) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-        *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bRawEmpty + rs));
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(L::bFull + st));
-        mbar_arrive(bar(L::bRawEmpty + rs));
-      }
-      ++done;
+      if (ok && lane == 0) mbar_arrive(bar((values ? L::bVFull : L::bKFull) + st));
     }
+    if (!ok && lane == 0) fail();
   } else {
     // ----------------------------------------------------------- softmax --
     const int sm = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
@@ -707,26 +757,26 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         const bool masked = in->masked != 0;
         if (masked) {
           // V's rows that do not count, and among the new tokens what is no finite number
-          const int k_before = min(j + 3, n), c = 2 * gs + k_before + j, st = c % L::kStages;
-          if (!mbar_wait_warp(bar(L::bFull + st), (c / L::kStages) & 1, abort)) {
+          const int st = gg % L::kV;
+          if (!mbar_wait_warp(bar(L::bVFull + st), (gg / L::kV) & 1, abort)) {
             stop = true;
             break;
           }
           const int kh = r >> 6, key = r & 63;
           if (kh == 0 || two) {
             const int lv = in->live[kh], fs = in->first[kh];
-            uint8_t* v = smem + L::oTiles + st * L::kTile + kh * (kBlock * D * 2) + key * 128;
+            const uint32_t v = sbase + L::oV + st * L::kTile + kh * (kBlock * D * 2) + key * 128;
             if (key >= lv) {
-#pragma unroll
+#pragma unroll 4
               for (int p = 0; p < D / 8; ++p)
-                *reinterpret_cast<uint4*>(v + (p >> 3) * 8192 + (((p & 7) ^ (key & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                store_shared(v + (p >> 3) * 8192 + (((p & 7) ^ (key & 7)) << 4), make_uint4(0u, 0u, 0u, 0u));
             } else if (fs + key >= 0) {
               constexpr uint32_t kOdd = kFp8 ? 0x7c00u : 0x7f80u;
               bool odd = false;
-#pragma unroll
+#pragma unroll 4
               for (int p = 0; p < D / 8; ++p) {
-                uint4* at = reinterpret_cast<uint4*>(v + (p >> 3) * 8192 + (((p & 7) ^ (key & 7)) << 4));
-                uint4 w = *at;
+                const uint32_t at = v + (p >> 3) * 8192 + (((p & 7) ^ (key & 7)) << 4);
+                uint4 w = load_shared(at);
                 uint32_t* e = &w.x;
                 bool here = false;
 #pragma unroll
@@ -740,7 +790,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                     here = true;
                   }
                 }
-                if (here) *at = w;
+                if (here) store_shared(at, w);
                 odd |= here;
               }
               if (odd) odd_seen[x] = 1;
