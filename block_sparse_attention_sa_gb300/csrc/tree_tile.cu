@@ -74,7 +74,7 @@ struct Tile {
   static constexpr int oQ = 0, oK = oQ + kQBytes, oV = oK + kK * kTile, oRaw = oV + kV * kTile;
   static constexpr int oBar = oRaw + 2 * kRaw * kPageBytes;
   // barriers
-  static constexpr int bHeadFull = 0, bHeadEmpty = 2, bQFull = 4, bQEmpty = 5, bKFull = 6;
+  static constexpr int bHeadFull = 0, bHeadEmpty = 2, bQFull = 4, bQEmpty = 5, bQRaw = 6, bKFull = 7;
   static constexpr int bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV;
   static constexpr int bSFull = bVEmpty + kV, bPFull = bSFull + kSBuf, bPvDone = bPFull + kSBuf;
   static constexpr int bTileDone = bPvDone + 2, bOFree = bTileDone + 1, bPvIssued = bOFree + 1;
@@ -267,6 +267,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (i >= L::bHeadEmpty && i < L::bHeadEmpty + 2) n = 2 + 8 + 1;     // products, softmax, queries and V
       if (i >= L::bPFull && i < L::bPFull + kSBuf) n = 128;
       if (i == L::bOFree) n = 256;
+      if (kFp8 && i == L::bQFull) n = 4;     // converting warps
       if (kFp8 && ((i >= L::bKFull && i < L::bKEmpty) || (i >= L::bVFull && i < L::bVEmpty) || i >= L::bRawEmpty))
         n = 2;                               // converting warps
       mbar_init(bar(i), n);
@@ -586,7 +587,6 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (!ok) break;
       const int n = heads[x].steps, b = heads[x].b, g = heads[x].g, rows = heads[x].fresh * G;
       if (n < 0) break;
-      const float scale = a.scale_log2 * (kFp8 && a.k_scale ? get(a.k_scale + g) : 1.f);
       ok = it == 0 || mbar_wait_warp(bar(L::bQEmpty), (it - 1) & 1, abort);
       if (!ok) break;
       // all rows on their way at once, straight to where the MMA reads them
@@ -598,7 +598,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 #pragma unroll 4
       for (int r = r0; r < BM; r += kRowsOnce) {
         copy_16(dst + (((sub & 7) ^ (r & 7)) << 4), left > 0 ? src : a.q, left > 0);
-        if (!kFp8 && sub == 0) factors[x * BM + r] = scale;
+        if (!kFp8 && sub == 0) factors[x * BM + r] = a.scale_log2;
         src += step;
         head += d_head;
         if (head >= G) {
@@ -615,33 +615,9 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         seen_sets[x * 64 + 32 + lane] = set[1];
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (kFp8) {
-        // in fp16, a row scaled by a power of two so that its largest element is in
-        // [2^14, 2^15): bits are lost only below 2^-39 of it
-#pragma unroll 4
-        for (int r = r0; r < BM; r += kRowsOnce) {
-          const uint32_t at = sbase + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4);
-          uint4 w = load_shared(at);
-          uint32_t* e = &w.x;
-          float top = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_f32(e[i])), fabsf(hi_f32(e[i]))));
-#pragma unroll
-          for (int s = kLanes / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, s));
-          // its exponent; beyond 2^127 a row next to the least floats is scaled by that
-          const int ex = top < INFINITY ? min(141 - static_cast<int>(__float_as_uint(top) >> 23), 127) : 0;
-          const float up = power_of_two(ex);
-          float f = scale * power_of_two(-(ex / 2)) * power_of_two(-(ex - ex / 2));
-          if (f == 0.f) f = 0x1p-149f;
-          if (sub == 0) factors[x * BM + r] = f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = pack_half(lo_f32(e[i]) * up, hi_f32(e[i]) * up);
-          store_shared(at, w);
-        }
-      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::bQFull));
+      if (lane == 0) mbar_arrive(bar(kFp8 ? L::bQRaw : L::bQFull));
       for (int j = 0; j < n && ok; ++j, ++gv) {
         const volatile StepInfo* in = infos + gv % kInfo;
         ok = mbar_wait_warp(bar(L::bInfo + gv % kInfo), (gv / kInfo) & 1, abort);
@@ -660,7 +636,47 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int row = tid & 63, raw0 = values ? L::kRaw : 0;
     constexpr int NR = kFp8 ? L::kRaw : 1;
     bool ok = true;
+    int it = 0, last = 0;                       // the next piece, and where the last one ends
     for (int g = 0; g < total_steps && ok; ++g) {
+      if (g == last) {
+        // a piece begins: its queries
+        const int x = it & 1;
+        ok = mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort);
+        if (!ok || heads[x].steps < 0) break;
+        last += heads[x].steps;
+        const float scale = a.scale_log2 * (a.k_scale ? get(a.k_scale + heads[x].g) : 1.f);
+        ok = mbar_wait_warp(bar(L::bQRaw), it & 1, abort);
+        if (!ok) break;
+        constexpr int kLanes = D / 8, kRowsOnce = 32 / kLanes;
+        const int sub = lane % kLanes, r0 = (warp - kConvert) * 32 + lane / kLanes;
+        // in fp16, a row scaled by a power of two so that its largest element is in
+        // [2^14, 2^15): bits are lost only below 2^-39 of it
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kRowsOnce) {
+          const int r = r0 + i;
+          const uint32_t at = sbase + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4);
+          uint4 w = load_shared(at);
+          uint32_t* e = &w.x;
+          float top = 0.f;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) top = fmaxf(top, fmaxf(fabsf(lo_f32(e[y])), fabsf(hi_f32(e[y]))));
+#pragma unroll
+          for (int s = kLanes / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, s));
+          // its exponent; beyond 2^127 a row next to the least floats is scaled by that
+          const int ex = top < INFINITY ? min(141 - static_cast<int>(__float_as_uint(top) >> 23), 127) : 0;
+          const float up = power_of_two(ex);
+          float f = scale * power_of_two(-(ex / 2)) * power_of_two(-(ex - ex / 2));
+          if (f == 0.f) f = 0x1p-149f;
+          if (sub == 0) factors[x * BM + r] = f;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) e[y] = pack_half(lo_f32(e[y]) * up, hi_f32(e[y]) * up);
+          store_shared(at, w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bQFull));
+        ++it;
+      }
       const int st = values ? g % L::kV : g % L::kK, round = values ? g / L::kV : g / L::kK;
       ok = mbar_wait_warp(bar((values ? L::bVEmpty : L::bKEmpty) + st), (round & 1) ^ 1, abort);
       for (int kh = 0; kh < 2 && ok; ++kh) {
@@ -946,10 +962,11 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                                                                 pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
           }
         } else {
-          float* out = part + r * D + c0 + 32 * cc;
+          // four columns of all rows follow each other: lanes are rows
+          float4* out = reinterpret_cast<float4*>(part) + (c0 / 4 + 8 * cc) * BM + r;
 #pragma unroll
           for (int v = 0; v < 8; ++v)
-            *reinterpret_cast<float4*>(out + 4 * v) =
+            out[v * BM] =
                 l_tot == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                              : make_float4(__uint_as_float(ov[4 * v]), __uint_as_float(ov[4 * v + 1]),
                                            __uint_as_float(ov[4 * v + 2]), __uint_as_float(ov[4 * v + 3]));
@@ -977,8 +994,8 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
-// grid (row tiles * runs, 16), 256 threads: a warp adds the partials of one row of the unit
-// that is cut behind a run's end, in the order of the runs.
+// grid (row tiles * runs, D / 8), 256 threads: adds the partials of the unit that is cut
+// behind a run's end, in the order of the runs; a thread has four columns of a row.
 template <int D>
 __global__ void __launch_bounds__(256)
 tile_join_kernel(DecodeArgs a, int runs, float unit, const float* partial, const TileCut* cuts) {
@@ -986,25 +1003,23 @@ tile_join_kernel(DecodeArgs a, int runs, float unit, const float* partial, const
   const int4 whole = *reinterpret_cast<const int4*>(cuts + blockIdx.x);
   const int rt = blockIdx.x / runs, bg = whole.x, first = whole.y, last = whole.z;
   if (bg < 0 || bg >= a.B * a.Hkv || first < 0 || last <= first || last >= runs) return;
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), row = rt * BM + r;
+  const int r = threadIdx.x % BM, c4 = blockIdx.y * 2 + threadIdx.x / BM, row = rt * BM + r;
   const int G = a.H / a.Hkv, b = bg / a.Hkv, g = bg - b * a.Hkv;
   int base, none = 0;
   if (row >= new_tokens(a, b, &base, &none) * G) return;
-  constexpr int V = D / 32;
-  float o[V] = {}, m = -INFINITY, l = 0.f;
+  float o[4] = {}, m = -INFINITY, l = 0.f;
   auto piece = [&](int i) {
     return partial + ((static_cast<int64_t>(rt) * runs + i) * 2 + (i == first ? 1 : 0)) * (BM * (D + 2));
   };
   constexpr int kOnce = 4;
   for (int i0 = first; i0 <= last; i0 += kOnce) {
     float2 ml[kOnce];
-    float v[kOnce][V];
+    float4 v[kOnce];
 #pragma unroll
     for (int u = 0; u < kOnce; ++u) {
       const float* p = piece(min(i0 + u, last));
       ml[u] = *reinterpret_cast<const float2*>(p + BM * D + 2 * r);
-#pragma unroll
-      for (int x = 0; x < V; ++x) v[u][x] = p[r * D + V * lane + x];
+      v[u] = reinterpret_cast<const float4*>(p)[c4 * BM + r];
     }
 #pragma unroll
     for (int u = 0; u < kOnce; ++u) {
@@ -1016,18 +1031,17 @@ tile_join_kernel(DecodeArgs a, int runs, float unit, const float* partial, const
       const float now = fmaxf(m, ml[u].x), c0 = m == -INFINITY ? 0.f : ex2(m - now), c1 = ex2(ml[u].x - now);
       l = (m == -INFINITY ? l : l * c0) + ml[u].y * c1;
       m = now;
-#pragma unroll
-      for (int x = 0; x < V; ++x) o[x] = o[x] * c0 + v[u][x] * c1;
+      o[0] = o[0] * c0 + v[u].x * c1;
+      o[1] = o[1] * c0 + v[u].y * c1;
+      o[2] = o[2] * c0 + v[u].z * c1;
+      o[3] = o[3] * c0 + v[u].w * c1;
     }
   }
   const int tok = row / G, h = g * G + row - tok * G;
   const float inv = l == 0.f ? 0.f : (a.v_scale ? a.v_scale[g] : 1.f) / l;
-  uint16_t* out = a.o + b * a.os[0] + tok * a.os[1] + h * a.os[2] + V * lane;
-  if (V == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[V - 2] * inv, o[V - 1] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16(o[0] * inv, o[1] * inv);
-  if (lane == 0 && a.lse)
+  *reinterpret_cast<uint2*>(a.o + b * a.os[0] + tok * a.os[1] + h * a.os[2] + 4 * c4) =
+      make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+  if (c4 == 0 && a.lse)
     a.lse[(static_cast<int64_t>(b) * a.H + h) * a.S + tok] =
         l == 0.f ? -INFINITY : (m + log2f(l * unit)) * 0.69314718055994530942f;
 }
@@ -1049,7 +1063,7 @@ cudaError_t launch_tile(const DecodeArgs& a, const CUtensorMap& kmap, const CUte
   kernel<<<dim3(static_cast<unsigned>(runs), static_cast<unsigned>(RT)), L::kThreads, L::kBytes, st>>>(kmap, vmap, a, partial, cuts);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_close(tile_join_kernel<D>, dim3(static_cast<unsigned>(RT * runs), BM / 8), 256, 0, st, a, runs,
+  return launch_close(tile_join_kernel<D>, dim3(static_cast<unsigned>(RT * runs), D / 8), 256, 0, st, a, runs,
                       kFp8 ? 0x1p-5f : 1.f, partial, cuts);
 }
 
