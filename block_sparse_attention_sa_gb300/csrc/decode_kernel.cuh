@@ -601,8 +601,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int k = 0; k < D / 16; ++k)
         if (k % S::kKeyWarps == kw) q_frag[32 * k] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
     };
-    // The ancestors of the tokens of this warp's rows. Those of the first unit are on
-    // their way with its queries, those of another wait for a page that needs them.
+    // The ancestors of the tokens of this warp's rows. Those of the first unit are made
+    // while its first page is on its way, those of another once a page needs them.
     bool seen_ready = false;
     auto load_seen = [&](int b, int rt) {
       int base, none = 0;
@@ -624,8 +624,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const int sub = run.off < run.count ? 0 : run.off / run.count;
       const int b = routed ? run.group / a.Hkv : run.group;
       load_queries(b, routed ? run.group - b * a.Hkv : sub / RT, routed ? sub : sub % RT);
-      if (kTree) load_seen(b, routed ? sub : sub % RT);
       ok = meet();
+      if (kTree) load_seen(b, routed ? sub : sub % RT);
     }
     int s = 0;
     uint32_t ph = 0;
@@ -1169,12 +1169,11 @@ template <int D, bool kFp8, bool kTree>
 cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      cudaStream_t st) {
   const int rows = a.S * (a.H / a.Hkv);
-  switch (row_groups(rows)) {
-    case 1: return rows <= 8 ? launch<D, kFp8, 1, true, kTree>(a, kmap, vmap, st)
-                             : launch<D, kFp8, 1, false, kTree>(a, kmap, vmap, st);
-    case 2: return launch<D, kFp8, 2, false, kTree>(a, kmap, vmap, st);
-    default: return launch<D, kFp8, 4, false, kTree>(a, kmap, vmap, st);
-  }
+  if (rows <= 8) return launch<D, kFp8, 1, true, kTree>(a, kmap, vmap, st);
+  if (rows <= 16) return launch<D, kFp8, 1, false, kTree>(a, kmap, vmap, st);
+  // a tree has no more rows here
+  if (kTree || rows <= 32) return launch<D, kFp8, 2, false, kTree>(a, kmap, vmap, st);
+  return launch<D, kFp8, kTree ? 2 : 4, false, kTree>(a, kmap, vmap, st);
 }
 
 }  // namespace

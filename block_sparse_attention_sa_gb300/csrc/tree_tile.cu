@@ -1,5 +1,5 @@
 // tree_tile.cu -- attention of a tree of new tokens over the paged cache where more than
-// 64 rows (pairs of a new token and a query head) share a key-value head: tcgen05.
+// 16 rows (pairs of a new token and a query head) share a key-value head: tcgen05.
 //   l_u = scale q.k_u,  a = softmax(l),  o = sum a_u v_u,  lse = log sum exp l
 //
 // Tiles. A CTA holds 128 rows (tcgen05 M = 128) and walks a run of pages, two (128 keys)
@@ -300,37 +300,36 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   // codes that have yet to be turned into fp16. Addresses and pages are in registers: read
   // from shared memory box by box they took 1,500 cycles a tile, and the kernel's pace.
   auto load_step = [&](bool values, int& st, int& ph, int& filled, int pa, int pb, int g) -> bool {
-    if (!kFp8) {
-      const int n = values ? L::kV : L::kK;
+    if constexpr (!kFp8) {
       if (!mbar_wait_warp(bar((values ? L::bVEmpty : L::bKEmpty) + st), ph, abort)) return false;
       if (values)
         load_tile<D, true>(&vmap, bar(L::bVFull + st), sbase + L::oV + st * L::kTile, pa, pb, g);
       else
         load_tile<D, false>(&kmap, bar(L::bKFull + st), sbase + L::oK + st * L::kTile, pa, pb, g);
       ++filled;
-      if (++st == n) {
+      if (++st == (values ? L::kV : L::kK)) {
         st = 0;
         ph ^= 1;
       }
-      return true;
-    }
-    for (int kh = 0; kFp8 && kh < 2; ++kh) {
-      const int at = (values ? L::kRaw : 0) + st, page = kh ? pb : pa;
-      if (!mbar_wait_warp(bar(L::bRawEmpty + at), ph, abort)) return false;
-      if (elected()) {
-        const uint32_t f = bar(L::bRawFull + at);
-        if (page >= 0) {
-          mbar_arrive_expect_tx(f, L::kPageBytes);
-          tma_load_4d(sbase + L::oRaw + at * L::kPageBytes, values ? &vmap : &kmap, f, 0, 0, g, page);
-        } else {
-          mbar_arrive(f);
+    } else {
+      for (int kh = 0; kh < 2; ++kh) {
+        const int at = (values ? L::kRaw : 0) + st, page = kh ? pb : pa;
+        if (!mbar_wait_warp(bar(L::bRawEmpty + at), ph, abort)) return false;
+        if (elected()) {
+          const uint32_t f = bar(L::bRawFull + at);
+          if (page >= 0) {
+            mbar_arrive_expect_tx(f, L::kPageBytes);
+            tma_load_4d(sbase + L::oRaw + at * L::kPageBytes, values ? &vmap : &kmap, f, 0, 0, g, page);
+          } else {
+            mbar_arrive(f);
+          }
         }
-      }
-      __syncwarp();
-      ++filled;
-      if (++st == (kFp8 ? L::kRaw : 1)) {
-        st = 0;
-        ph ^= 1;
+        __syncwarp();
+        ++filled;
+        if (++st == L::kRaw) {
+          st = 0;
+          ph ^= 1;
+        }
       }
     }
     return true;

@@ -216,6 +216,19 @@ def test_many_sequences(sa, H, Hkv):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S,G", [(16, 1), (17, 1), (5, 5), (4, 8), (11, 3), (1, 32), (3, 43), (2, 64), (64, 2)])
+def test_rows_next_to_the_tiles_sizes(sa, S, G, D, fmt):
+    """16 to 129 rows on a key-value head, tables small and large."""
+    lens = [(71 * i) % 400 for i in range(12)]
+    for max_pages in (None, 40):
+        c = Case(lens, S, 3 * G, 3, D, fmt, seed=S, max_pages=max_pages)
+        o, lse = c.run(sa)
+        assert int(c.st.item()) == 0
+        c.check(o, lse)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
 @pytest.mark.parametrize("layout", ["page_token", "gapped"])
 @pytest.mark.parametrize("H", [6, 48])
 def test_cache_layouts(sa, layout, fmt, H):
