@@ -57,6 +57,12 @@ __device__ __forceinline__ uint64_t sub2_rn(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint64_t mul2_rn(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // two_sum on both lanes of a pair (the same operations, lane by lane)
 __device__ __forceinline__ void two_sum2(uint64_t& s, uint64_t& e, uint64_t b) {
   const uint64_t a = s;
@@ -207,10 +213,7 @@ __global__ void __launch_bounds__(128) pool_kernel(RouteArgs a) {
 // sa_route would compute from the outputs, and Q and K are not read again.
 // Same grid and thread layout as pool_kernel; plain loads (the outputs may
 // overwrite the inputs in place).
-//
-// kAxes (sa_qk_prologue_axes): a pair's row of the tables is the token's position on
-// the pair's axis; the tables hold positions, not tokens, and stay in L2.
-template <int D, bool kAxes>
+template <int D>
 __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs pa) {
   constexpr int kLanes = D / 8;       // threads of one head vector
   constexpr int kChunk = 64;          // tokens whose rotary rows are staged at once
@@ -250,11 +253,6 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
 #pragma unroll
   for (int u = 0; u < 8; ++u) s[u] = c[u] = 0.f;
 
-  int stays = 0;                          // which of the thread's pairs are not turned
-  if (kAxes)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) stays |= (pa.axes.axis_of[d / 2 + v] == SA_ROPE_STAYS) << v;
-
   const int64_t off = b * st[0] + h * st[2] + d;
   for (int c0 = 0; c0 < n; c0 += kChunk) {
     const int nc = min(kChunk, n - c0);
@@ -266,31 +264,9 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
                           static_cast<size_t>(t0 + c0) * kRow4;
       const float4* sn4 = reinterpret_cast<const float4*>(pa.sin) +
                           static_cast<size_t>(t0 + c0) * kRow4;
-      if (kAxes) {
-        bool out = false;
-        for (int e = threadIdx.x; e < nc * kRow4; e += 128) {
-          const int t = e / kRow4, pair = e % kRow4 * 4;
-          float co[4], si[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int axis = pa.axes.axis_of[pair + v];
-            co[v] = 1.f;
-            si[v] = 0.f;
-            if (axis == SA_ROPE_STAYS) continue;
-            const int64_t at = static_cast<int64_t>(axis_row(pa.axes, b, t0 + c0 + t, axis, t0 + c0 + t, &out)) *
-                               (D / 2) + pair + v;
-            co[v] = pa.cos[at];
-            si[v] = pa.sin[at];
-          }
-          reinterpret_cast<float4*>(&tab[0][0][0])[e] = make_float4(co[0], co[1], co[2], co[3]);
-          reinterpret_cast<float4*>(&tab[1][0][0])[e] = make_float4(si[0], si[1], si[2], si[3]);
-        }
-        if (out && a.dev_status) atomicOr(a.dev_status, SA_DEV_CAPACITY);
-      } else {
-        for (int e = threadIdx.x; e < nc * kRow4; e += 128) {
-          reinterpret_cast<float4*>(&tab[0][0][0])[e] = cs4[e];
-          reinterpret_cast<float4*>(&tab[1][0][0])[e] = sn4[e];
-        }
+      for (int e = threadIdx.x; e < nc * kRow4; e += 128) {
+        reinterpret_cast<float4*>(&tab[0][0][0])[e] = cs4[e];
+        reinterpret_cast<float4*>(&tab[1][0][0])[e] = sn4[e];
       }
       __syncthreads();
     }
@@ -320,7 +296,7 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
         for (int v = 0; v < 8; ++v) ss = fmaf(x[v], x[v], ss);
 #pragma unroll
         for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = kAxes && !pa.norm ? 1.f : rsqrtf(ss * inv_d + pa.eps);
+        const float r = rsqrtf(ss * inv_d + pa.eps);
         float cv[4] = {1.f, 1.f, 1.f, 1.f}, sv[4] = {0.f, 0.f, 0.f, 0.f};
         if (rope && t + u < nc) {
           const float4 c4 = *reinterpret_cast<const float4*>(&tab[0][t + u][d / 2]);
@@ -334,12 +310,8 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
         for (int v = 0; v < 4; ++v) {
           const float y0 = x[2 * v] * r * g[2 * v];
           const float y1 = x[2 * v + 1] * r * g[2 * v + 1];
-          float o0 = fmaf(y0, cv[v], -y1 * sv[v]);
-          float o1 = fmaf(y0, sv[v], y1 * cv[v]);
-          if (kAxes && (stays >> v & 1)) {      // infinities beside it are not its affair
-            o0 = y0;
-            o1 = y1;
-          }
+          const float o0 = fmaf(y0, cv[v], -y1 * sv[v]);
+          const float o1 = fmaf(y0, sv[v], y1 * cv[v]);
           const __nv_bfloat162 hb = __floats2bfloat162_rn(o0, o1);
           packed[v] = *reinterpret_cast<const uint32_t*>(&hb);
           yr[2 * v] = bf16_to_f32(static_cast<uint16_t>(packed[v] & 0xffffu));
@@ -357,6 +329,150 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
     }
   }
   store_pooled<D>(a, which, b, h, d, i, nrow, n, s, c, active);
+}
+
+// ------------------------------------------------- prologue with axes ---
+// The prologue where a pair's row of the tables is the token's position on the pair's
+// axis (sa_qk_prologue_axes). The tables hold positions, not tokens, and stay in L2; a
+// chunk of 64 tokens' angles is gathered into shared memory once for 8 heads. A thread has 8 consecutive d of a head, so its four pairs' axes never change and its
+// positions and angles are two rounds of independent loads.
+//
+// Every byte of q and k is read and written once: 38,247 tokens, 56 heads of 128, 2.19 GB.
+// Paired fp32 instructions for the norm and the sums keep the issue slots below the
+// memory's time (scalar, with the tables gathered for q and k apart: 574 us).
+template <int D>
+__global__ void __launch_bounds__(128, 6) prologue_axes_kernel(RouteArgs a, PrologueArgs pa) {
+  constexpr int kLanes = D / 8, kT = 4;   // threads of a head vector; tokens in flight
+  __shared__ __align__(16) float4 tab[2][kBlock][kLanes];      // [cos, sin][token][four pairs]
+  const int i = blockIdx.x, which = blockIdx.z & 1, b = blockIdx.z >> 1, tid = threadIdx.x, lane8 = tid % kLanes;
+  const int blk = which ? kBlock : a.qblk, nrow = which ? a.Nb : a.Nq;
+  if (i >= nrow) return;                  // uniform over the CTA
+  const int e0 = (blockIdx.y * 128 + tid) * 8, d = e0 % D;
+  const bool active = e0 < a.H * D;
+  const int h = active ? e0 / D : 0;
+  int axis[4];
+  int stays = 0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    axis[v] = pa.axes.axis_of[4 * lane8 + v];
+    stays |= (axis[v] == SA_ROPE_STAYS) << v;
+  }
+  const bool one_axis = axis[0] == axis[1] && axis[0] == axis[2] && axis[0] == axis[3];
+  const int64_t step = which ? a.ks[1] : a.qs[1];
+  const int64_t at0 = b * (which ? a.ks[0] : a.qs[0]) + h * (which ? a.ks[2] : a.qs[2]) + d + static_cast<int64_t>(i) * blk * step;
+  const uint16_t* X = (which ? a.k : a.q) + at0;
+  uint16_t* Y = (which ? pa.k_out : pa.q_out) + at0;
+  const float* gamma = which ? pa.gamma_k : pa.gamma_q;
+  uint64_t g2[4], s2[4], c2[4];           // weights; running sums, two d in a pair
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    g2[v] = f2_pack(1.f, 1.f);
+    s2[v] = c2[v] = 0ull;
+  }
+  if (active && gamma) {
+    const float4 g0 = reinterpret_cast<const float4*>(gamma + d)[0];
+    const float4 g1 = reinterpret_cast<const float4*>(gamma + d)[1];
+    g2[0] = f2_pack(g0.x, g0.y);
+    g2[1] = f2_pack(g0.z, g0.w);
+    g2[2] = f2_pack(g1.x, g1.y);
+    g2[3] = f2_pack(g1.z, g1.w);
+  }
+  const int total = min(blk, a.S - i * blk);
+  bool out = false;
+  for (int c0 = 0; c0 < total; c0 += kBlock) {       // 64-token chunks of the block
+    const int t0 = i * blk + c0, n = min(kBlock, a.S - t0);
+    uint4 buf[kT];
+    auto load = [&](int t) {
+#pragma unroll
+      for (int u = 0; u < kT; ++u) {
+        buf[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (active && t + u < n) buf[u] = *reinterpret_cast<const uint4*>(X + u * step);
+      }
+      X += kT * step;
+    };
+    load(0);
+    __syncthreads();                      // the last chunk's angles are read
+    constexpr int kRows = 128 / kLanes;   // tokens at a time
+#pragma unroll 4
+    for (int t = tid / kLanes; t < n; t += kRows) {
+      float4 co = make_float4(1.f, 1.f, 1.f, 1.f), si = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (one_axis) {
+        if (!(stays & 1)) {
+          const int64_t at = static_cast<int64_t>(axis_row(pa.axes, b, t0 + t, axis[0], t0 + t, &out)) * (D / 2) + 4 * lane8;
+          co = __ldg(reinterpret_cast<const float4*>(pa.cos + at));
+          si = __ldg(reinterpret_cast<const float4*>(pa.sin + at));
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (stays >> v & 1) continue;
+          const int64_t at = static_cast<int64_t>(axis_row(pa.axes, b, t0 + t, axis[v], t0 + t, &out)) * (D / 2) + 4 * lane8 + v;
+          (&co.x)[v] = __ldg(pa.cos + at);
+          (&si.x)[v] = __ldg(pa.sin + at);
+        }
+      }
+      tab[0][t][lane8] = co;
+      tab[1][t][lane8] = si;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int t = 0; t < n; t += kT) {
+      uint4 now[kT];
+#pragma unroll
+      for (int u = 0; u < kT; ++u) now[u] = buf[u];
+      if (t + kT < n) load(t + kT);       // on their way while these are turned
+#pragma unroll
+      for (int u = 0; u < kT; ++u) {
+        const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+        uint64_t x[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          x[v] = (static_cast<uint64_t>(w[v] & 0xffff0000u) << 32) | (w[v] << 16);
+        if (pa.norm) {
+          uint64_t ss2 = f2_fma(x[0], x[0], 0ull);
+#pragma unroll
+          for (int v = 1; v < 4; ++v) ss2 = f2_fma(x[v], x[v], ss2);
+          float lo, hi;
+          f2_unpack(ss2, lo, hi);
+          float ss = lo + hi;
+#pragma unroll
+          for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float r = rsqrtf(ss * (1.f / D) + pa.eps);
+          const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) x[v] = mul2_rn(mul2_rn(x[v], r2), g2[v]);
+        }
+        if (active && t + u < n) {
+          const float4 co = tab[0][t + u][lane8], si = tab[1][t + u][lane8];
+          const float cs[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
+          uint32_t packed[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            float y0, y1;
+            f2_unpack(x[v], y0, y1);
+            float o0 = fmaf(y0, cs[v], -y1 * sn[v]), o1 = fmaf(y0, sn[v], y1 * cs[v]);
+            if (stays >> v & 1) {         // infinities beside it are not its affair
+              o0 = y0;
+              o1 = y1;
+            }
+            const __nv_bfloat162 hb = __floats2bfloat162_rn(o0, o1);
+            packed[v] = *reinterpret_cast<const uint32_t*>(&hb);
+            two_sum2(s2[v], c2[v], (static_cast<uint64_t>(packed[v] & 0xffff0000u) << 32) | (packed[v] << 16));
+          }
+          *reinterpret_cast<uint4*>(Y) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        }
+        Y += step;
+      }
+    }
+  }
+  float s[8], c[8];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    f2_unpack(s2[v], s[2 * v], s[2 * v + 1]);
+    f2_unpack(c2[v], c[2 * v], c[2 * v + 1]);
+  }
+  store_pooled<D>(a, which, b, h, d, i, nrow, total, s, c, active);
+  if (out && a.dev_status) atomicOr(a.dev_status, SA_DEV_CAPACITY);
 }
 
 // --------------------------------------------------------------- score ---
@@ -857,9 +973,9 @@ cudaError_t launch_pool_d(const RouteArgs& a, const PrologueArgs* pa, cudaStream
   if (e != cudaSuccess) return e;
   dim3 grid(a.Nb, (a.H * D + 1023) / 1024, 2 * a.B);
   if (pa && pa->axes.n_axes > 0)
-    prologue_kernel<D, true><<<grid, 128, 0, st>>>(a, *pa);
+    prologue_axes_kernel<D><<<grid, 128, 0, st>>>(a, *pa);
   else if (pa)
-    prologue_kernel<D, false><<<grid, 128, 0, st>>>(a, *pa);
+    prologue_kernel<D><<<grid, 128, 0, st>>>(a, *pa);
   else
     pool_kernel<D><<<grid, 128, 0, st>>>(a);
   return cudaGetLastError();
