@@ -337,17 +337,21 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
 // chunk of 64 tokens' angles is gathered into shared memory once for 8 heads. A thread has 8 consecutive d of a head, so its four pairs' axes never change and its
 // positions and angles are two rounds of independent loads.
 //
-// Every byte of q and k is read and written once: 38,247 tokens, 56 heads of 128, 2.19 GB.
-// Paired fp32 instructions for the norm and the sums keep the issue slots below the
-// memory's time (scalar, with the tables gathered for q and k apart: 574 us).
-template <int D>
-__global__ void __launch_bounds__(128, 6) prologue_axes_kernel(RouteArgs a, PrologueArgs pa) {
-  constexpr int kLanes = D / 8, kT = 4;   // threads of a head vector; tokens in flight
+// Every byte of q and k is read and written once: 38,247 tokens, 56 heads of 128, 2.19 GB
+// in 421 us, 5.2 TB/s (373 us without the norm, whose sums across lanes are what the
+// memory's time does not cover). All heads of a block of tokens run side by side, so that
+// whole tokens are read (a head group's blocks side by side: 440 us); eight tokens are on
+// their way in a thread, four CTAs an SM (four and six: 430 us), and a group of tokens has
+// no conditions in it, so that their chains overlap (470 us with them).
+template <int D, bool kNorm, bool kStay>
+__global__ void __launch_bounds__(128, 4) prologue_axes_kernel(RouteArgs a, PrologueArgs pa, int parts) {
+  constexpr int kLanes = D / 8, kT = 8;   // threads of a head vector; tokens in flight
   __shared__ __align__(16) float4 tab[2][kBlock][kLanes];      // [cos, sin][token][four pairs]
-  const int i = blockIdx.x, which = blockIdx.z & 1, b = blockIdx.z >> 1, tid = threadIdx.x, lane8 = tid % kLanes;
+  const int part = blockIdx.x % parts, i = blockIdx.x / parts, which = blockIdx.z & 1, b = blockIdx.z >> 1;
+  const int tid = threadIdx.x, lane8 = tid % kLanes;
   const int blk = which ? kBlock : a.qblk, nrow = which ? a.Nb : a.Nq;
   if (i >= nrow) return;                  // uniform over the CTA
-  const int e0 = (blockIdx.y * 128 + tid) * 8, d = e0 % D;
+  const int e0 = (part * 128 + tid) * 8, d = e0 % D;
   const bool active = e0 < a.H * D;
   const int h = active ? e0 / D : 0;
   int axis[4];
@@ -382,12 +386,11 @@ __global__ void __launch_bounds__(128, 6) prologue_axes_kernel(RouteArgs a, Prol
   for (int c0 = 0; c0 < total; c0 += kBlock) {       // 64-token chunks of the block
     const int t0 = i * blk + c0, n = min(kBlock, a.S - t0);
     uint4 buf[kT];
+    // threads beyond the heads read head 0's and keep nothing of it
     auto load = [&](int t) {
 #pragma unroll
-      for (int u = 0; u < kT; ++u) {
-        buf[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (active && t + u < n) buf[u] = *reinterpret_cast<const uint4*>(X + u * step);
-      }
+      for (int u = 0; u < kT; ++u)
+        if (t + u < n) buf[u] = *reinterpret_cast<const uint4*>(X + u * step);
       X += kT * step;
     };
     load(0);
@@ -415,54 +418,61 @@ __global__ void __launch_bounds__(128, 6) prologue_axes_kernel(RouteArgs a, Prol
       tab[1][t][lane8] = si;
     }
     __syncthreads();
+    // a token: norm (its sum of squares across the head's lanes), rotation, sums
+    auto turn = [&](const uint4& in, int t) {
+      const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+      uint64_t x[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) x[v] = (static_cast<uint64_t>(w[v] & 0xffff0000u) << 32) | (w[v] << 16);
+      if (kNorm) {
+        uint64_t ss2 = f2_fma(x[0], x[0], 0ull);
+#pragma unroll
+        for (int v = 1; v < 4; ++v) ss2 = f2_fma(x[v], x[v], ss2);
+        float lo, hi;
+        f2_unpack(ss2, lo, hi);
+        float ss = lo + hi;
+#pragma unroll
+        for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.f / D) + pa.eps);
+        const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] = mul2_rn(mul2_rn(x[v], r2), g2[v]);
+      }
+      const float4 co = tab[0][t][lane8], si = tab[1][t][lane8];
+      const float cs[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
+      uint32_t packed[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float y0, y1;
+        f2_unpack(x[v], y0, y1);
+        float o0 = fmaf(y0, cs[v], -y1 * sn[v]), o1 = fmaf(y0, sn[v], y1 * cs[v]);
+        if (kStay && (stays >> v & 1)) {  // infinities beside it are not its affair
+          o0 = y0;
+          o1 = y1;
+        }
+        const __nv_bfloat162 hb = __floats2bfloat162_rn(o0, o1);
+        packed[v] = *reinterpret_cast<const uint32_t*>(&hb);
+        two_sum2(s2[v], c2[v], (static_cast<uint64_t>(packed[v] & 0xffff0000u) << 32) | (packed[v] << 16));
+      }
+      if (active) *reinterpret_cast<uint4*>(Y) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+      Y += step;
+    };
+    int t = 0;
 #pragma unroll 1
-    for (int t = 0; t < n; t += kT) {
+    for (; t + kT <= n; t += kT) {        // no conditions: the tokens' chains overlap
       uint4 now[kT];
 #pragma unroll
       for (int u = 0; u < kT; ++u) now[u] = buf[u];
-      if (t + kT < n) load(t + kT);       // on their way while these are turned
+      load(t + kT);                       // on their way while these are turned
 #pragma unroll
-      for (int u = 0; u < kT; ++u) {
-        const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
-        uint64_t x[4];
+      for (int u = 0; u < kT; ++u) turn(now[u], t + u);
+    }
+    for (int u = 0; t + u < n; ++u) {     // the last block's last few
+      uint4 in = buf[0];
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          x[v] = (static_cast<uint64_t>(w[v] & 0xffff0000u) << 32) | (w[v] << 16);
-        if (pa.norm) {
-          uint64_t ss2 = f2_fma(x[0], x[0], 0ull);
-#pragma unroll
-          for (int v = 1; v < 4; ++v) ss2 = f2_fma(x[v], x[v], ss2);
-          float lo, hi;
-          f2_unpack(ss2, lo, hi);
-          float ss = lo + hi;
-#pragma unroll
-          for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * (1.f / D) + pa.eps);
-          const uint64_t r2 = f2_pack(r, r);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) x[v] = mul2_rn(mul2_rn(x[v], r2), g2[v]);
-        }
-        if (active && t + u < n) {
-          const float4 co = tab[0][t + u][lane8], si = tab[1][t + u][lane8];
-          const float cs[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
-          uint32_t packed[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            float y0, y1;
-            f2_unpack(x[v], y0, y1);
-            float o0 = fmaf(y0, cs[v], -y1 * sn[v]), o1 = fmaf(y0, sn[v], y1 * cs[v]);
-            if (stays >> v & 1) {         // infinities beside it are not its affair
-              o0 = y0;
-              o1 = y1;
-            }
-            const __nv_bfloat162 hb = __floats2bfloat162_rn(o0, o1);
-            packed[v] = *reinterpret_cast<const uint32_t*>(&hb);
-            two_sum2(s2[v], c2[v], (static_cast<uint64_t>(packed[v] & 0xffff0000u) << 32) | (packed[v] << 16));
-          }
-          *reinterpret_cast<uint4*>(Y) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-        }
-        Y += step;
-      }
+      for (int v = 1; v < kT; ++v)
+        if (u == v) in = buf[v];
+      turn(in, t + u);
     }
   }
   float s[8], c[8];
@@ -972,8 +982,13 @@ cudaError_t launch_pool_d(const RouteArgs& a, const PrologueArgs* pa, cudaStream
       cudaMemsetAsync(a.ws + a.L.kmax, 0, sizeof(int) * static_cast<size_t>(a.B) * a.H, st);
   if (e != cudaSuccess) return e;
   dim3 grid(a.Nb, (a.H * D + 1023) / 1024, 2 * a.B);
-  if (pa && pa->axes.n_axes > 0)
-    prologue_axes_kernel<D><<<grid, 128, 0, st>>>(a, *pa);
+  if (pa && pa->axes.n_axes > 0) {
+    bool stays = false;
+    for (int v = 0; v < D / 2; ++v) stays |= pa->axes.axis_of[v] == SA_ROPE_STAYS;
+    const auto kernel = pa->norm ? (stays ? prologue_axes_kernel<D, true, true> : prologue_axes_kernel<D, true, false>)
+                                 : (stays ? prologue_axes_kernel<D, false, true> : prologue_axes_kernel<D, false, false>);
+    kernel<<<dim3(grid.x * grid.y, 1, grid.z), 128, 0, st>>>(a, *pa, static_cast<int>(grid.y));
+  }
   else if (pa)
     prologue_kernel<D><<<grid, 128, 0, st>>>(a, *pa);
   else
