@@ -855,18 +855,19 @@ def sa_pages_fork(page_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.
     int32 [N, 2], n_moves [1]): pass moves and n_moves to sa_cache_copy for each layer's
     caches. refs_out=refs counts in place."""
     index = _cuda_index(page_table)
-    for t, name in ((page_table, "page_table"), (refs, "refs"), (src, "src")):
-        if not isinstance(t, torch.Tensor) or t.dim() != (2 if t is page_table else 1):
-            raise ValueError(f"{name} must be int32 " +
-                             ("[B, max_pages]" if name == "page_table" else "with one dimension"))
-    N, dev = src.shape[0], page_table.device
-    new = lambda *shape: _empty(shape, torch.int32, dev, stream)
-    table_out = new(N, page_table.shape[1]) if table_out is None else table_out
-    lens_out = new(N) if lens_out is None else lens_out
-    refs_out = new(refs.shape[0]) if refs_out is None else refs_out
-    moves = new(N, 2) if moves is None else moves
-    n_moves = new(1) if n_moves is None else n_moves
-    workspace = _pages_workspace(refs.shape[0], max(N, page_table.shape[0]), dev, stream, workspace)
+    if any(t is None for t in (table_out, lens_out, refs_out, moves, n_moves, workspace)):
+        for t, name, dim in ((page_table, "page_table", 2), (refs, "refs", 1), (src, "src", 1)):
+            if not isinstance(t, torch.Tensor) or t.dim() != dim:
+                raise ValueError(f"{name} must be int32 with {dim} dimension(s)")
+        N, dev = src.shape[0], page_table.device
+        new = lambda *shape: _empty(shape, torch.int32, dev, stream)
+        table_out = new(N, page_table.shape[1]) if table_out is None else table_out
+        lens_out = new(N) if lens_out is None else lens_out
+        refs_out = new(refs.shape[0]) if refs_out is None else refs_out
+        moves = new(N, 2) if moves is None else moves
+        n_moves = new(1) if n_moves is None else n_moves
+        workspace = _pages_workspace(refs.shape[0], max(N, page_table.shape[0]), dev, stream,
+                                     workspace)
     _call("sa_pages_fork", _bind().fork, index, stream, page_table, seq_lens, refs, src, table_out,
           lens_out, refs_out, moves, n_moves, workspace, dev_status)
     return table_out, lens_out, refs_out, moves, n_moves
@@ -903,15 +904,19 @@ def sa_pages_compact(page_table: Optional[torch.Tensor], refs: torch.Tensor, *,
     new ids, the pairs (page, new id) for sa_cache_copy, how many pages are in use.
     table_out=page_table and refs_out=refs work in place."""
     index = _cuda_index(refs)
-    new = lambda *shape: _empty(shape, torch.int32, refs.device, stream)
-    if page_table is not None and table_out is None:
-        table_out = new(*page_table.shape)
-    refs_out = new(refs.shape[0]) if refs_out is None else refs_out
-    moves = new(max(1, refs.shape[0] // 2), 2) if moves is None else moves
-    n_moves = new(1) if n_moves is None else n_moves
-    n_used = new(1) if n_used is None else n_used
-    workspace = _pages_workspace(refs.shape[0], 1 if page_table is None else page_table.shape[0],
-                                 refs.device, stream, workspace)
+    if any(t is None for t in (table_out, refs_out, moves, n_moves, n_used, workspace)):
+        new = lambda *shape: _empty(shape, torch.int32, refs.device, stream)
+        rows = 1
+        if page_table is not None:
+            if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+                raise ValueError("page_table must be int32 [B, max_pages]")
+            table_out = new(*page_table.shape) if table_out is None else table_out
+            rows = page_table.shape[0]
+        refs_out = new(refs.shape[0]) if refs_out is None else refs_out
+        moves = new(max(1, refs.shape[0] // 2), 2) if moves is None else moves
+        n_moves = new(1) if n_moves is None else n_moves
+        n_used = new(1) if n_used is None else n_used
+        workspace = _pages_workspace(refs.shape[0], rows, refs.device, stream, workspace)
     _call("sa_pages_compact", _bind().compact, index, stream, refs, page_table, table_out,
           refs_out, moves, n_moves, n_used, workspace, dev_status)
     return table_out, refs_out, moves, n_moves, n_used

@@ -119,7 +119,7 @@ sa_status encode_cache(CUtensorMap* m, const void* base, const sa_cache_params* 
 sa_status check_pages(int64_t n_pages, int64_t max_pages, int64_t rows, int64_t stride) {
   if (n_pages < 1 || max_pages < 1 || rows < 1) return SA_ERR_INVALID_ARG;
   if (rows > 1 && stride < max_pages) return SA_ERR_INVALID_ARG;
-  if (n_pages >= (1 << 25) || max_pages >= (1 << 25) || rows > 65535) return SA_ERR_UNSUPPORTED;
+  if (n_pages >= (1 << 25) || max_pages >= (1 << 25) || rows > 16384) return SA_ERR_UNSUPPORTED;
   return SA_OK;
 }
 

@@ -14,6 +14,7 @@
 namespace sa {
 namespace {
 
+constexpr int kMostRows = 16384;    // sequences of a table (check_pages)
 constexpr int kCtas = 8;            // the largest cluster that every part runs
 constexpr int kThreads = 1024;
 constexpr int kWarps = kCtas * kThreads / 32;
@@ -137,38 +138,44 @@ __device__ __forceinline__ void report(const PagesArgs& a, int status) {
 
 // ---------------------------------------------------------------- fork --
 
+// Every CTA counts for itself, in shared memory, who continues whom: two meetings of the
+// cluster less than with counts in global memory (8.2 us a call, four beams).
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_fork_kernel(PagesArgs a) {
+  let_next_launch();
+  wait_for_first();
   __shared__ Counts counts;
+  extern __shared__ int32_t of_old[];   // [B] the first that continues it, [B] how many do
+  int32_t *first = of_old, *takers = first + a.B;
   const int t = cta_rank() * kThreads + threadIdx.x, warp = t >> 5, lane = t & 31;
-  // the first that continues an old sequence, how many do; which copy a new one gets
-  int32_t *first = a.ws, *takers = first + a.B, *copy = takers + a.B, *list = copy + a.N;
+  int32_t *copy = a.ws, *list = copy + a.N;   // which copy a new sequence gets; the copies' pages
   int status = 0;
-  for (int b = t; b < a.B; b += kCtas * kThreads) {
+  for (int b = threadIdx.x; b < a.B; b += kThreads) {
     first[b] = a.N;
     takers[b] = 0;
   }
   if (a.refs_out != a.refs)
     for (int p = t; p < a.n_pages; p += kCtas * kThreads) a.refs_out[p] = a.refs[p];
-  cluster_sync();
-  for (int i = t; i < a.N; i += kCtas * kThreads) {
+  const Part rows = part_of(a.N, warp), pages = part_of(a.n_pages, warp);
+  const int free_pages = count_free(a, pages, lane);
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.N; i += kThreads) {
     const int s = source_of(a, i, &status);
     if (s < 0) continue;
     atomicMin(first + s, i);
     atomicAdd(takers + s, 1);
   }
-  cluster_sync();
+  __syncthreads();
   // the new sequences that need a copy, in order, and the free pages
-  const Part rows = part_of(a.N, warp), pages = part_of(a.n_pages, warp);
   auto needs_copy = [&](int i) {
     if (i >= rows.hi) return false;
     const int s = source_of(a, i, &status);
-    if (s < 0 || fresh(first + s) == i) return false;
+    if (s < 0 || first[s] == i) return false;
     const int n = length_of(a, s, &status);
     return n % kBlock > 0 && page_at(a, a.table[s * a.stride + n / kBlock], &status) >= 0;
   };
   int need = 0;
   for (int i = rows.lo; i < rows.hi; i += 32) need += __popc(__ballot_sync(kFull, needs_copy(i + lane)));
-  const Sums sum = sums_of(counts, warp, lane, need, count_free(a, pages, lane));
+  const Sums sum = sums_of(counts, warp, lane, need, free_pages);
   list_free(a, pages, lane, sum.before.y, min(sum.all.x, sum.all.y), list);
   int k = sum.before.x;
   for (int i = rows.lo; i < rows.hi; i += 32) {
@@ -181,10 +188,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
   cluster_sync();
   // new rows
   for (int i = warp; i < a.N; i += kWarps) {
-    const int s = source_of(a, i, &status);
+    const int c = fresh(copy + i), s = source_of(a, i, &status);
     const int n = s < 0 ? 0 : length_of(a, s, &status), whole = n / kBlock;
-    const bool again = s >= 0 && fresh(first + s) != i;
-    const int c = fresh(copy + i);
+    const bool again = s >= 0 && first[s] != i;
     int page = -1, end = n;
     if (c >= 0) {
       if (c < sum.all.y) {
@@ -200,6 +206,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
       }
     }
     if (lane == 0) a.lens_out[i] = end;
+#pragma unroll 4
     for (int j = lane; j < a.max_pages; j += 32) {
       int e = s < 0 ? -1 : page_at(a, a.table[s * a.stride + j], &status);
       if (again && j >= whole) e = j == whole ? page : -1;
@@ -208,8 +215,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
   }
   // the old rows' places, less those that were taken over
   for (int b = warp; b < a.B; b += kWarps) {
-    const int n = fresh(takers + b), whole = length_of(a, b, &status) / kBlock;
+    const int n = takers[b];
     if (n == 1) continue;
+    const int whole = length_of(a, b, &status) / kBlock;
+#pragma unroll 4
     for (int j = lane; j < a.max_pages; j += 32) {
       const int e = page_at(a, a.table[b * a.stride + j], &status);
       const int more = n == 0 ? -1 : (j < whole ? n - 1 : 0);
@@ -222,6 +231,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
 // -------------------------------------------------------------- resize --
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_resize_kernel(PagesArgs a) {
+  let_next_launch();
+  wait_for_first();
   __shared__ Counts counts;
   const int t = cta_rank() * kThreads + threadIdx.x, warp = t >> 5, lane = t & 31;
   int status = 0;
@@ -281,10 +292,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
 // ------------------------------------------------------------- compact --
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_compact_kernel(PagesArgs a) {
+  let_next_launch();
+  wait_for_first();
   __shared__ Counts counts;
   const int t = cta_rank() * kThreads + threadIdx.x, warp = t >> 5, lane = t & 31;
-  // a page's id afterwards; the free pages before n_used, ascending; the pages from
-  // n_used on, descending; how many those are
+  // a page's id afterwards (of one from n_used on, which is found by its place among those:
+  // -1 - that, from the end); the free pages before n_used, ascending; the pages from n_used
+  // on, descending; how many those are
   int32_t *now = a.ws, *hole = now + a.n_pages, *late = hole + a.n_pages, *n_late = late + a.n_pages;
   int status = 0;
   const Part pages = part_of(a.n_pages, warp);
@@ -297,6 +311,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
   const Sums sum = sums_of(counts, warp, lane, n, 0);
   const int used = sum.all.x;
   int before = sum.before.x;          // pages in use before the warp's next 32
+#pragma unroll 4
   for (int i = pages.lo; i < pages.hi; i += 32) {
     const int p = i + lane;
     const bool in = p < pages.hi;
@@ -304,9 +319,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
     const unsigned m = __ballot_sync(kFull, r > 0);
     const int rank = before + below(m, lane);
     if (in) {
-      now[p] = p;
+      const bool moves = p >= used && r > 0;
+      now[p] = moves ? -1 - (used - 1 - rank) : p;
       if (p < used && r <= 0) hole[p - rank] = p;
-      if (p >= used && r > 0) late[used - 1 - rank] = p;
+      if (moves) late[used - 1 - rank] = p;
       if (p == used) n_late[0] = used - rank;
       if (a.refs_out != a.refs) a.refs_out[p] = r;
     }
@@ -319,7 +335,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
     const int from = fresh(late + moved - 1 - k), to = fresh(hole + k);
     a.moves[2 * k] = from;
     a.moves[2 * k + 1] = to;
-    now[from] = to;
     a.refs_out[to] = a.refs[from];
     a.refs_out[from] = 0;
   }
@@ -327,31 +342,41 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
     a.n_moves[0] = moved;
     a.n_used[0] = used;
   }
-  cluster_sync();
   for (int b = warp; b < a.B; b += kWarps)
+#pragma unroll 4
     for (int j = lane; j < a.max_pages; j += 32) {
       const int e = page_at(a, a.table[b * a.stride + j], &status);
-      a.table_out[b * a.out_stride + j] = e < 0 ? -1 : fresh(now + e);
+      int to = e < 0 ? -1 : fresh(now + e);
+      if (e >= 0 && to < 0) to = fresh(hole + moved + to);       // hole[moved - 1 - place]
+      a.table_out[b * a.out_stride + j] = to;
     }
   report(a, status);
 }
 
-template <class K>
-cudaError_t launch(K kernel, const PagesArgs& a, cudaStream_t st) {
-  kernel<<<kCtas, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+// Launched while the kernel before still runs where that allows it (these do, and
+// sa_cache_copy's): the steps of a fork come one behind the other, 8 of 152 SMs busy.
+cudaError_t launch(void (*kernel)(PagesArgs), const PagesArgs& a, size_t smem, cudaStream_t st) {
+  return launch_close(kernel, dim3(kCtas), kThreads, smem, st, a);
 }
 
 }  // namespace
 
 size_t pages_ws_bytes(int n_pages, int rows) {
-  // fork: first, takers, copy, and a list as long as the rows; resize: a list of pages;
+  // fork: a copy's number for each row and a list as long; resize: a list of pages;
   // compact: three
-  return (4 * static_cast<size_t>(rows) + 3 * static_cast<size_t>(n_pages) + 64) * sizeof(int32_t);
+  return (2 * static_cast<size_t>(rows) + 3 * static_cast<size_t>(n_pages) + 64) * sizeof(int32_t);
 }
 
-cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t st) { return launch(pages_fork_kernel, a, st); }
-cudaError_t launch_pages_resize(const PagesArgs& a, cudaStream_t st) { return launch(pages_resize_kernel, a, st); }
-cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t st) { return launch(pages_compact_kernel, a, st); }
+cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t st) {
+  static_assert(2 * kMostRows * sizeof(int32_t) + sizeof(Counts) <= 227 * 1024, "counts do not fit shared memory");
+  const size_t smem = 2 * static_cast<size_t>(a.B) * sizeof(int32_t);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch(pages_fork_kernel, a, smem, st);
+}
+cudaError_t launch_pages_resize(const PagesArgs& a, cudaStream_t st) { return launch(pages_resize_kernel, a, 0, st); }
+cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t st) { return launch(pages_compact_kernel, a, 0, st); }
 
 }  // namespace sa

@@ -775,7 +775,7 @@ size_t sa_pages_workspace_bytes(int32_t n_pages, int32_t rows);
  * n_moves     device int32 [1].
  * workspace   device scratch of sa_pages_workspace_bytes(n_pages, max(B, N))
  *             bytes, 256-byte aligned.
- * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED (B or N above 65,535, n_pages or
+ * Errors: SA_ERR_INVALID_ARG / SA_ERR_UNSUPPORTED (B or N above 16,384, n_pages or
  * max_pages from 2^25 on) / SA_ERR_CAPACITY before launch; SA_ERR_CUDA.
  */
 sa_status sa_pages_fork(int32_t n_pages, int32_t max_pages, int32_t B, int32_t N,

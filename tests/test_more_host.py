@@ -103,8 +103,8 @@ def test_pages_refusals(sa):
     L = sa.load_library()
     n = L.sa_pages_workspace_bytes(100, 7)
     assert n > 0 and L.sa_pages_workspace_bytes(0, 7) == 0 and L.sa_pages_workspace_bytes(100, 0) == 0
-    assert L.sa_pages_workspace_bytes(1 << 25, 1) == 0 and L.sa_pages_workspace_bytes(5, 65536) == 0
-    assert n >= 4 * (4 * 7 + 100)
+    assert L.sa_pages_workspace_bytes(1 << 25, 1) == 0 and L.sa_pages_workspace_bytes(5, 16385) == 0
+    assert n >= 4 * (2 * 7 + 3 * 100)
 
     def fork(**kw):
         a = dict(n_pages=100, max_pages=5, B=7, N=6, table=A, stride=5, lens=A, refs=A, src=A, out=P(FAR), out_stride=5,
@@ -119,7 +119,7 @@ def test_pages_refusals(sa):
                dict(refs_out=P(4100))):
         assert fork(**kw) == INVALID, kw
     assert fork(n=n - 1) == CAPACITY
-    assert fork(N=65536) == UNSUPPORTED and fork(n_pages=1 << 25) == UNSUPPORTED
+    assert fork(N=16385) == UNSUPPORTED and fork(n_pages=1 << 25) == UNSUPPORTED
 
     def resize(**kw):
         a = dict(n_pages=100, max_pages=5, B=7, table=A, stride=5, refs=A, lens=A, more_lens=None, more=1, ws=A, n=n)
