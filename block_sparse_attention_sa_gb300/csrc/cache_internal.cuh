@@ -148,6 +148,7 @@ cudaError_t launch_route_pages(const RoutePagesArgs& a, cudaStream_t st);
 // its end, so that launch and set-up overlap. Not so from call to call: blocks
 // of a next call that sit waiting on an SM take the place of a run of this one
 // (e4m3 decoding of 3 x 112,640 tokens: 115 us so, 150 us with every launch close).
+// But for the calls of pages.cu, which take eight SMs, and the copy of pages behind them.
 __device__ __forceinline__ void let_next_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

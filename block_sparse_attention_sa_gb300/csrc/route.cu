@@ -334,11 +334,12 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
 // ------------------------------------------------- prologue with axes ---
 // The prologue where a pair's row of the tables is the token's position on the pair's
 // axis (sa_qk_prologue_axes). The tables hold positions, not tokens, and stay in L2; a
-// chunk of 64 tokens' angles is gathered into shared memory once for 8 heads. A thread has 8 consecutive d of a head, so its four pairs' axes never change and its
-// positions and angles are two rounds of independent loads.
+// chunk of 64 tokens' angles is gathered into shared memory once for 8 heads. A thread has
+// 8 consecutive d of a head, so its four pairs' axes never change and its positions and
+// angles are two rounds of independent loads.
 //
 // Every byte of q and k is read and written once: 38,247 tokens, 56 heads of 128, 2.19 GB
-// in 421 us, 5.2 TB/s (373 us without the norm, whose sums across lanes are what the
+// in 416 us, 5.3 TB/s (372 us without the norm, whose sums across lanes are what the
 // memory's time does not cover). All heads of a block of tokens run side by side, so that
 // whole tokens are read (a head group's blocks side by side: 440 us); eight tokens are on
 // their way in a thread, four CTAs an SM (four and six: 430 us), and a group of tokens has

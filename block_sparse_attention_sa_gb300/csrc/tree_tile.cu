@@ -150,6 +150,14 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, uint32_t f, ui
   __syncwarp();
 }
 
+// a b + c with subnormal numbers as they are: the factor of a row of small queries may be
+// one, and a masked logit of -inf times 0 would be NaN.
+__device__ __forceinline__ uint64_t fma2_subnormal(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // p = 2^((s - m) f) for 32 logits as two terms, pairs of keys in a word (e4m3: of 2^5 p);
 // returns the sum of the p. Subtracting before scaling, the largest key has weight 1
 // however coarse fp32 is at its logit's size.
@@ -163,7 +171,7 @@ __device__ __forceinline__ float weigh32(const uint32_t* v, float m, float f, ui
   for (int u = 0; u < 32; u += 2) {
     const uint64_t d = f2_add(f2_pack(__uint_as_float(v[u]), __uint_as_float(v[u + 1])), nm);
     float y0, y1;
-    f2_unpack(f2_fma(d, ff, add), y0, y1);
+    f2_unpack(fma2_subnormal(d, ff, add), y0, y1);
     const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
     const uint64_t p = f2_pack(p0, p1);
     acc[(u >> 1) & 1] = f2_add(acc[(u >> 1) & 1], p);

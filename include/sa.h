@@ -681,7 +681,11 @@ size_t sa_attn_tree_workspace_bytes(const sa_cache_params* p);
  * out; rows of o and lse of tokens that are left out or not counted by n_b stay
  * as they were. Tokens whose every page has a bad id get o = 0, lse = -inf.
  *
- * Precision: as sa_attn_decode.
+ * Precision: as sa_attn_decode; where more than 16 rows (new tokens times H / H_kv)
+ * share a key-value head, P.V takes P to 2^-16 of itself, as two bf16 terms (with
+ * SA_CACHE_FP8 to 2^-21 of itself or 2^-30 of the largest, as two fp16 terms), and
+ * with SA_CACHE_FP8 q is taken in fp16 scaled by a power of two for each row, exact but
+ * for bits below 2^-39 of its largest element.
  *
  * q          device bf16 [B, S, H, D], rotated as the cached keys are; S at most
  *            SA_TREE_MAX.

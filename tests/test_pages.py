@@ -240,6 +240,44 @@ def test_captured_and_replayed(sa):
             assert bool((kc[b] == kc[a, 0, 0, 0]).all()) and bool((vc[b] == kc[a, 0, 0, 0]).all())
 
 
+def test_calls_behind_each_other_and_on_two_streams(sa):
+    """Each call sees what the ones before it on its stream have written, without a wait of
+    the host, while another stream does the same with another pool."""
+    pools = [Pool(24, 6, seed=40 + i, free=80) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in pools]
+    rng = np.random.default_rng(1)
+    srcs = [[rng.integers(-1, 24, 24).astype(np.int32) for _ in range(6)] for _ in pools]
+    state = [[dev(p.table), dev(p.lens), dev(p.refs)] for p in pools]
+    src = [[dev(s) for s in x] for x in srcs]
+    kc = [torch.zeros((p.n_pages, 1, PAGE, 64), dtype=torch.bfloat16, device="cuda") for p in pools]
+    big = torch.ones(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    for step in range(6):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                table, lens, refs = state[i]
+                late = (big * 0).sum().int() + src[i][step]        # ready only when that is done
+                table, lens, refs, moves, n = sa.sa_pages_fork(table, lens, refs, late)
+                sa.sa_pages_resize(table, refs, lens, 1)
+                sa.sa_cache_copy(kc[i], kc[i].clone(), moves, n)
+                lens = lens.clamp(max=6 * PAGE - 1) + 1
+                sa.sa_pages_resize(table, refs, lens)
+                table, refs, moves, n, used = sa.sa_pages_compact(table, refs)
+                state[i] = [table, lens, refs]
+    torch.cuda.synchronize()
+    for p, x, (table, lens, refs) in zip(pools, srcs, state):
+        t, l, r = p.table, p.lens, p.refs
+        for s in x:
+            t, l, r, _, _ = fork_ref(t, l, r, s)
+            l = np.array(l)
+            t, r, _ = resize_ref(t, r, l + 1)
+            l = np.minimum(l, 6 * PAGE - 1) + 1
+            t, r, _ = resize_ref(t, r, l)
+            t, r, *_ = compact_ref(t, r)
+        assert np.array_equal(table.cpu().numpy(), t) and lens.tolist() == l.tolist()
+        assert refs.tolist() == list(r)
+
+
 def test_refusals(sa):
     pool = Pool(5, 4, seed=1)
     t, n, r, src = dev(pool.table), dev(pool.lens), dev(pool.refs), dev([0, 1, 2])

@@ -438,6 +438,63 @@ def test_repeats_captured_and_on_other_streams(sa, H, fmt):
     assert torch.equal(o3, fresh)
 
 
+@pytest.mark.parametrize("H,fmt", [(4, "bf16"), (4, "fp8"), (40, "bf16"), (40, "fp8")])
+def test_queries_that_are_no_numbers_stay_in_their_rows(sa, H, fmt):
+    """NaN and infinities in one token's queries are its own affair, and so is their size."""
+    c = Case([500, 70], 9, H, 2, 128, fmt, seed=21)
+    o, lse = c.run(sa)
+    o, lse = o.clone(), lse.clone()
+    c.q[0, 3, 0, 5] = float("nan")
+    c.q[0, 5, H - 1] = float("inf")
+    c.q[1, 8, H // 2, ::2] = 3e38
+    c.q[1, 0, 1] = 0.0
+    c.q[1, 1, 1] = 1e-38
+    o2, lse2 = c.run(sa)
+    same = torch.ones((2, 9, H), dtype=torch.bool, device="cuda")
+    for b, s, h in ((0, 3, 0), (0, 5, H - 1), (1, 8, H // 2), (1, 0, 1), (1, 1, 1)):
+        same[b, s, h] = False
+    assert torch.equal(o[same], o2[same])
+    assert torch.equal(lse.transpose(1, 2)[same], lse2.transpose(1, 2)[same])
+    assert bool(o2[0, 3, 0].isnan().all())
+    # queries of 0: the mean of the values that are seen, lse = log of their number
+    seen = [70 + 1, 70 + 1 + (1 if c.parents[1, 1] == 0 else 0)]
+    for s in (0, 1):
+        n = seen[s]
+        off = n * 2.0 ** -24 + 2.0 ** -22 * (math.log(n) + 2)
+        assert abs(float(lse2[1, 1, s]) - math.log(n)) <= off
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("H", [4, 40])
+def test_the_smallest_scales(sa, H, fmt):
+    """A subnormal scale makes every weight one, of what a token sees."""
+    c = Case([500, 70], 9, H, 2, 128, fmt, seed=22, scale=1e-40)
+    o, lse = c.run(sa)
+    c.check(o, lse)
+
+
+def test_calls_side_by_side(sa):
+    """Calls on two streams at once, each with its own workspace, as one by one."""
+    cases = [Case([4000, 900], 6, H, 2, 128, fmt, seed=30 + i)
+             for i, (H, fmt) in enumerate([(4, "bf16"), (40, "fp8"), (40, "bf16"), (12, "fp8")])]
+    alone = [tuple(x.clone() for x in c.run(sa)) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [dict(q=c.q.cuda(), table=dev(c.table), lens=dev(c.lens), up=dev(c.parents),
+                 kw={} if c.ks is None else dict(k_scale=c.ks.cuda(), v_scale=c.vs.cuda()))
+            for c in cases]
+    torch.cuda.synchronize()
+    outs = [[] for _ in cases]
+    for _ in range(5):
+        for i, (c, a, st) in enumerate(zip(cases, args, streams)):
+            with torch.cuda.stream(st):
+                outs[i].append(sa.sa_attn_tree(a["q"], c.kc, c.vc, a["table"], a["lens"],
+                                               parents=a["up"], **a["kw"]))
+    torch.cuda.synchronize()
+    for (o, lse), got in zip(alone, outs):
+        for o2, l2 in got:
+            assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
 def test_one_token_is_a_decoding_step(sa):
     """With one new token the tree is sa_attn_decode over the length with it."""
     c = Case([300, 0, 64, 1000], 1, 8, 2, 128, "bf16", seed=3)
