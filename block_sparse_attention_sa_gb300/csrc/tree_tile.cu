@@ -269,24 +269,23 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   };
   int status = 0;
   let_next_launch();
+  for (int i = tid; i < L::kBars; i += L::kThreads) {      // one by one they take 1,000 cycles
+    uint32_t n = 1;
+    if (i >= L::bHeadEmpty && i < L::bHeadEmpty + 2) n = 2 + 8 + 1;     // products, softmax, queries and V
+    if (i >= L::bPFull && i < L::bPFull + kSBuf) n = 128;
+    if (i == L::bOFree) n = 256;
+    if (kFp8 && i == L::bQFull) n = 4;     // converting warps
+    if (kFp8 && ((i >= L::bKFull && i < L::bKEmpty) || (i >= L::bVFull && i < L::bVEmpty) || i >= L::bRawEmpty))
+      n = 2;                               // converting warps
+    mbar_init(bar(i), n);
+    fence_barrier_init();
+  }
   if (tid == 0) {
-    for (int i = 0; i < L::kBars; ++i) {
-      uint32_t n = 1;
-      if (i >= L::bHeadEmpty && i < L::bHeadEmpty + 2) n = 2 + 8 + 1;     // products, softmax, queries and V
-      if (i >= L::bPFull && i < L::bPFull + kSBuf) n = 128;
-      if (i == L::bOFree) n = 256;
-      if (kFp8 && i == L::bQFull) n = 4;     // converting warps
-      if (kFp8 && ((i >= L::bKFull && i < L::bKEmpty) || (i >= L::bVFull && i < L::bVEmpty) || i >= L::bRawEmpty))
-        n = 2;                               // converting warps
-      mbar_init(bar(i), n);
-    }
     *abort_flag = 0;
     odd_seen[0] = odd_seen[1] = 0;
-    fence_barrier_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
-  if (tid < 256) reinterpret_cast<uint64_t*>(smem + L::oHand)[tid] = 0xffffffff00000000ull;
   if (warp == kMma) {
     tmem_alloc(sbase + L::oMisc, 512);
     tmem_relinquish();
@@ -658,26 +657,40 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         const int sub = lane % kLanes, r0 = (warp - kConvert) * 32 + lane / kLanes;
         // in fp16, a row scaled by a power of two so that its largest element is in
         // [2^14, 2^15): bits are lost only below 2^-39 of it
-#pragma unroll 4
-        for (int i = 0; i < 32; i += kRowsOnce) {
-          const int r = r0 + i;
-          const uint32_t at = sbase + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4);
-          uint4 w = load_shared(at);
-          uint32_t* e = &w.x;
-          float top = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 4 * kRowsOnce) {      // four at once
+          uint4 w[4];
+          float top[4];
+          auto at = [&](int u) {
+            const int r = r0 + i + u * kRowsOnce;
+            return sbase + L::oQ + (sub >> 3) * L::kRegion + r * 128 + (((sub & 7) ^ (r & 7)) << 4);
+          };
 #pragma unroll
-          for (int y = 0; y < 4; ++y) top = fmaxf(top, fmaxf(fabsf(lo_f32(e[y])), fabsf(hi_f32(e[y]))));
+          for (int u = 0; u < 4; ++u) w[u] = load_shared(at(u));
 #pragma unroll
-          for (int s = kLanes / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, s));
-          // its exponent; beyond 2^127 a row next to the least floats is scaled by that
-          const int ex = top < INFINITY ? min(141 - static_cast<int>(__float_as_uint(top) >> 23), 127) : 0;
-          const float up = power_of_two(ex);
-          float f = scale * power_of_two(-(ex / 2)) * power_of_two(-(ex - ex / 2));
-          if (f == 0.f) f = 0x1p-149f;
-          if (sub == 0) factors[x * BM + r] = f;
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t* e = &w[u].x;
+            top[u] = 0.f;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) e[y] = pack_half(lo_f32(e[y]) * up, hi_f32(e[y]) * up);
-          store_shared(at, w);
+            for (int y = 0; y < 4; ++y) top[u] = fmaxf(top[u], fmaxf(fabsf(lo_f32(e[y])), fabsf(hi_f32(e[y]))));
+          }
+#pragma unroll
+          for (int s = kLanes / 2; s >= 1; s >>= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(full, top[u], s));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            // its exponent; beyond 2^127 a row next to the least floats is scaled by that
+            const int ex = top[u] < INFINITY ? min(141 - static_cast<int>(__float_as_uint(top[u]) >> 23), 127) : 0;
+            const float up = power_of_two(ex);
+            float f = scale * power_of_two(-(ex / 2)) * power_of_two(-(ex - ex / 2));
+            if (f == 0.f) f = 0x1p-149f;
+            if (sub == 0) factors[x * BM + r0 + i + u * kRowsOnce] = f;
+            uint32_t* e = &w[u].x;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) e[y] = pack_half(lo_f32(e[y]) * up, hi_f32(e[y]) * up);
+            store_shared(at(u), w[u]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
