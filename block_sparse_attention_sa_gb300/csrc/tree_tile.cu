@@ -286,6 +286,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
+  if (tid < 256) reinterpret_cast<uint64_t*>(smem + L::oHand)[tid] = 0xffffffff00000000ull;
   if (warp == kMma) {
     tmem_alloc(sbase + L::oMisc, 512);
     tmem_relinquish();
@@ -560,10 +561,11 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           pv_elect(o_tmem, pa + 64, v1, v1 + 128, v1 + 256, v1 + 384, kIdPV, 1u);
           pv_elect(o_tmem, pa + 80, v1, v1 + 128, v1 + 256, v1 + 384, kIdPV, 1u);
         }
-        tc_fence_before();
-        if (elected()) mbar_arrive(bar(L::bPvIssued + sb));
         umma_commit_elect(bar(L::bVEmpty + st));
         umma_commit_elect(bar(L::bPvDone + (g & 1)));
+        // behind the commits: S(g + 3) is there only after PV(g) has been told done
+        tc_fence_before();
+        if (elected()) mbar_arrive(bar(L::bPvIssued + sb));
         ++g;
         if (++st == L::kV) {
           st = 0;
@@ -791,10 +793,17 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           break;
         }
         const bool masked = in->masked != 0;
+        if (!mbar_wait_warp(bar(L::bSFull + sb), (gg / kSBuf) & 1, abort)) {
+          stop = true;
+          break;
+        }
         if (masked) {
           // V's rows that do not count, and among the new tokens what is no finite number
+          // (a barrier tells a phase from the next only: the stage's last use, of step gg - 2
+          // or before, has to be over, and for that one, as S(gg) is there, step gg - 4's is)
           const int st = gg % L::kV;
-          if (!mbar_wait_warp(bar(L::bVFull + st), (gg / L::kV) & 1, abort)) {
+          if ((gg >= 2 && !mbar_wait_warp(bar(L::bPvDone + (gg & 1)), ((gg - 2) >> 1) & 1, abort)) ||
+              !mbar_wait_warp(bar(L::bVFull + st), (gg / L::kV) & 1, abort)) {
             stop = true;
             break;
           }
@@ -833,10 +842,6 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
           }
           fence_proxy_async_smem();
-        }
-        if (!mbar_wait_warp(bar(L::bSFull + sb), (gg / kSBuf) & 1, abort)) {
-          stop = true;
-          break;
         }
         tc_fence_after();
         // the step's maximum, 64 keys at a time (masked: by bits, and written back so)

@@ -281,6 +281,24 @@ def test_bad_routes_are_reported_and_left_out(sa, H):
     c.check(o, lse, [[], [], [2, 3]])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("base", [100, 600, 1400])
+def test_runs_of_many_steps_that_end_in_new_tokens(sa, base, fmt, D):
+    """Runs that hold the ends of units behind other steps, what lies behind the last tokens
+    being no number, with the cache in L2 and not; every time the same."""
+    c = Case([base, base + 60, base + 1, base, base - 37], 64, 48, 2, D, fmt, seed=base)
+    o, lse = c.run(sa)
+    c.check(o, lse)
+    o, lse = o.clone(), lse.clone()
+    large = torch.zeros(1 << 26, device="cuda")
+    for i in range(12):
+        if i % 2:
+            large.add_(1)
+        o2, lse2 = c.run(sa)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("H", [4, 48])
 def test_bad_lengths_pages_and_parents(sa, H):
     c = Case([100, 200, 70, 300], 6, H, 2, 64, "bf16", seed=4, max_pages=5, garbage=False)
