@@ -33,7 +33,7 @@
 // unit: 197 us for 1.08 GB, 5.5 TB/s, the memory. 64 new tokens behind 3 x 112,640, 448
 // rows: 600 us in bf16, 1,030 TFLOP/s: the tensor pipe, which does half as much again for the
 // second term of P; a step's products take 1,536 cycles, a step 1,700 to 1,800, at the clock
-// that the power leaves (1.5 to 1.8 GHz). In e4m3 681 us: shared memory, through which each
+// that the power leaves (1.5 to 1.8 GHz). In e4m3 678 us: shared memory, through which each
 // key and value goes three times more (2,048 cycles a step at 128 bytes a cycle). With one warp for all products
 // 705 us, with 32 keys of the softmax unrolled to 128 774 us: a step's code then does not
 // fit the instruction cache. 777 tokens, 64 new ones: 18.6 us, the chain lengths, page,
@@ -650,8 +650,9 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // -------------------------------------------------------- conversion --
     // Two warps turn K into fp16, two V: a thread two rows (tokens) of each. As read, so
     // written, without bank conflicts, as the rows' pieces are swizzled alike. A page's codes
-    // are in registers, and their stage is given back, before the wait for the tile's place
-    // (3 x 64 new tokens behind 112,640: 681 us; waiting first 713).
+    // are read before the wait for the tile's place (3 x 64 new tokens behind 112,640: 678 us;
+    // waiting first 713). Their stage is given back only behind the stores, which need the
+    // loads' results: an arrival may pass loads that are still under way.
     const bool values = warp >= kConvert + 2;
     const int row = tid & 63, raw0 = values ? L::kRaw : 0;
     constexpr int NR = kFp8 ? L::kRaw : 1;
@@ -727,8 +728,6 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           w[p] = load_shared(src + (D == 64 ? row * 64 + ((p ^ ((row >> 1) & 3)) << 4) : row * 128 + ((p ^ (row & 7)) << 4)));
         if (kh == 0 && ok) ok = mbar_wait_warp(bar((values ? L::bVEmpty : L::bKEmpty) + st), (round & 1) ^ 1, abort);
         if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::bRawEmpty + rs));
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
           const uint2 h0 = e4m3x4_half4(w[p].x), h1 = e4m3x4_half4(w[p].y), h2 = e4m3x4_half4(w[p].z), h3 = e4m3x4_half4(w[p].w);
@@ -736,6 +735,8 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           store_shared(to + ((c0 ^ (row & 7)) << 4), make_uint4(h0.x, h0.y, h1.x, h1.y));
           store_shared(to + (((c0 + 1) ^ (row & 7)) << 4), make_uint4(h2.x, h2.y, h3.x, h3.y));
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bRawEmpty + rs));
       }
       fence_proxy_async_smem();
       __syncwarp();

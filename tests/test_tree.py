@@ -491,6 +491,31 @@ def test_the_smallest_scales(sa, H, fmt):
     c.check(o, lse)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens,H,Hkv,S", [([2617] * 8, 56, 1, 64), ([4164, 23, 1, 361, 1803, 1019, 4693], 40, 1, 48),
+                                          ([1782, 2178, 323, 39, 69, 37], 56, 8, 64)])
+def test_the_same_every_time(sa, lens, H, Hkv, S, fmt, D):
+    """Some hundred calls with the cache in L2 and not: loads that come early or late."""
+    c = Case(lens, S, H, Hkv, D, fmt, seed=7)
+    args = [c.q.cuda(), c.kc, c.vc, dev(c.table), dev(c.lens)]
+    kw = {} if c.ks is None else dict(k_scale=c.ks.cuda(), v_scale=c.vs.cuda())
+    p = sa.make_cache_params(args[3], q=args[0], k_cache=c.kc, v_cache=c.vc)
+    kw.update(parents=dev(c.parents),
+              workspace=torch.empty(sa.sa_attn_tree_workspace_bytes(p), dtype=torch.uint8, device="cuda"))
+    large = torch.zeros(1 << 26, device="cuda")
+    o, lse = sa.sa_attn_tree(*args, **kw)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(300):
+        if i % 2:
+            large.add_(1)
+        o2, lse2 = sa.sa_attn_tree(*args, **kw)
+        differ += (o2 != o).any().long() + (lse2 != lse).any().long()
+    assert int(differ.item()) == 0
+    if fmt == "bf16" and D == 64 and Hkv == 8:
+        c.check(o, lse)
+
+
 def test_calls_side_by_side(sa):
     """Calls on two streams at once, each with its own workspace, as one by one."""
     cases = [Case([4000, 900], 6, H, 2, 128, fmt, seed=30 + i)
