@@ -488,7 +488,7 @@ typedef struct sa_cache_params {
   int32_t rope_layout;      /* sa_cache_append: SA_ROPE_*                      */
   int32_t rope_rows;        /* sa_cache_append: rows of the rotation tables    */
   float eps;                /* sa_cache_append: >= 0, added to the mean square */
-  float softmax_scale;      /* sa_attn_decode: 0 => 1/sqrt(D)                  */
+  float softmax_scale;      /* sa_attn_decode, _tree: 0 => 1/sqrt(D)           */
   int64_t table_stride;     /* elements between two sequences of page_table    */
   int64_t q_stride[3];      /* element strides of b, s, h of the new tokens'   */
   int64_t k_stride[3];      /* q, k, v and of o (sa_cache_append: of q_out),   */
@@ -519,7 +519,8 @@ void sa_cache_params_init(sa_cache_params* p, int32_t B, int32_t H, int32_t H_kv
  * k_sum of the page (where given) gains y before it is rounded; a page's first
  * slot starts its sum anew.
  * Taking tokens back (a guess that was rejected) is setting the length back, but
- * k_sum has gained their keys (sa_cache_accept puts that right): before more is appended, the sums of the page that
+ * k_sum has gained their keys. sa_cache_accept puts that right for drafted tokens;
+ * without it, before more is appended, the sums of the page that
  * the sequence then ends in (page_table[b][n / 64], where n % 64 > 0), [H_kv, D]
  * floats, have to be put back as they were at that length. Those of the pages
  * behind it start anew.
