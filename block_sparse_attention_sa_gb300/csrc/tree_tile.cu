@@ -30,19 +30,19 @@
 // those. Rows that see such a value get it added in the epilogue.
 //
 // Bounds. 32 sequences of 16 new tokens behind 8,192, 56/8 heads of 128 in bf16, 112 rows a
-// unit: 197 us for 1.08 GB, 5.5 TB/s, the memory. 64 new tokens behind 3 x 112,640, 448
-// rows: 593 us in bf16, 1,050 TFLOP/s: the tensor pipe (82% busy), which does half as much
+// unit: 195 us for 1.08 GB, 5.5 TB/s, the memory. 64 new tokens behind 3 x 112,640, 448
+// rows: 597 us in bf16, 1,040 TFLOP/s: the tensor pipe (82% busy), which does half as much
 // again for the second term of P; a step's products take 1,536 cycles, a step 1,700 to
-// 1,800, at the clock that the power leaves (1.5 to 1.8 GHz). In e4m3 676 us, pipe 60%
+// 1,800, at the clock that the power leaves (1.5 to 1.8 GHz). In e4m3 647 us, pipe 60%
 // busy: there is room for two steps' keys and values in 16 bits, and the way of each from
 // its codes' arrival to the product (wait, read, convert, write, told) is 2,000 cycles.
 // With one warp for all products bf16 took 705 us, with 32 keys of the softmax unrolled to
 // 128 774 us: a step's code then does not fit the instruction cache. 777 tokens, 64 new
-// ones: 18.3 us, the chain lengths, page, queries, scores, weights, output, partial, join.
+// ones: 17.5 us, the chain lengths, page, queries, scores, weights, output, partial, join.
 //
 // Warps: 0-3 softmax of even steps, 4-7 of odd ones, 8 pages and loads of K, 9
 // and 10 the products, 11 the queries (rows gathered by token and head, for e4m3 scaled by a
-// power of two) and loads of V, 12-15 conversion (e4m3). Every wait is bounded
+// power of two; the first by warps 0-7) and loads of V, 12-15 conversion (e4m3). Every wait is bounded
 // (SA_DEV_TIMEOUT).
 #include "decode_kernel.cuh"
 
@@ -90,7 +90,7 @@ struct Tile {
   static constexpr int bSFull = bVEmpty + kV, bPFull = bSFull + kSBuf, bPvDone = bPFull + kSBuf;
   static constexpr int bTileDone = bPvDone + 2, bOFree = bTileDone + 1, bPvIssued = bOFree + 1;
   static constexpr int bFin = bPvIssued + kSBuf, bInfo = bFin + 2, bRawFull = bInfo + kInfo;
-  static constexpr int bRawEmpty = bRawFull + 2 * kRaw, kBars = bRawEmpty + 2 * kRaw;
+  static constexpr int bRawEmpty = bRawFull + 2 * kRaw, bQFirst = bRawEmpty + 2 * kRaw, kBars = bQFirst + 1;
   static constexpr int oMisc = oBar + kBars * 8;        // tmem base, abort flag, odd values [2]
   static constexpr int oHead = oMisc + 16;
   static constexpr int oInfo = oHead + 2 * static_cast<int>(sizeof(Head));
@@ -286,8 +286,9 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (i >= L::bPFull && i < L::bPFull + kSBuf) n = 128;
     if (i == L::bOFree) n = 256;
     if (kFp8 && i == L::bQFull) n = 4;     // converting warps
-    if (kFp8 && ((i >= L::bKFull && i < L::bKEmpty) || (i >= L::bVFull && i < L::bVEmpty) || i >= L::bRawEmpty))
+    if (kFp8 && ((i >= L::bKFull && i < L::bKEmpty) || (i >= L::bVFull && i < L::bVEmpty) || (i >= L::bRawEmpty && i < L::bQFirst)))
       n = 2;                               // converting warps
+    if (i == L::bQFirst) n = 8;            // softmax warps
     mbar_init(bar(i), n);
     fence_barrier_init();
   }
@@ -359,6 +360,51 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int f = kFp8 ? L::bRawFull + (values ? L::kRaw : 0) : (values ? L::bVFull : L::bKFull);
     for (int s = 0; s < n && s < filled; ++s)       // the fills of stage s before its last one
       mbar_wait(bar(f + s), (filled - 1 - s) / n & 1, drain);
+  };
+
+  // A piece's queries, all rows on their way at once, straight to where the MMA reads them,
+  // by `threads` threads of which this is the t-th: those of the first piece by the softmax
+  // warps, which have nothing else to do (64 new tokens behind 777: 17.5 us, by one warp
+  // 18.3), later ones by the warp that loads V, while the piece before is still at work.
+  auto load_queries = [&](int x, int t, int threads) {
+    constexpr int kLanes = D / 8;                     // threads of a row
+    const int once = threads / kLanes, sub = t % kLanes, r0 = t / kLanes;
+    const int b = heads[x].b, g = heads[x].g, rows = heads[x].fresh * G;
+    const int first = rt * BM + r0, d_tok = once / G, d_head = once - d_tok * G;
+    const int64_t step = d_tok * a.qs[1] + d_head * a.qs[2], wrap = a.qs[1] - G * a.qs[2];
+    int head = first % G, left = rows - first;        // rows from this one on
+    const uint16_t* src = a.q + b * a.qs[0] + first / G * a.qs[1] + (g * G + head) * a.qs[2] + 8 * sub;
+    uint32_t dst = sbase + L::oQ + (sub >> 3) * L::kRegion + r0 * 128;
+#pragma unroll 4
+    for (int r = r0; r < BM; r += once) {
+      copy_16(dst + (((sub & 7) ^ (r & 7)) << 4), left > 0 ? src : a.q, left > 0);
+      if (!kFp8 && sub == 0) factors[x * BM + r] = a.scale_log2;
+      src += step;
+      head += d_head;
+      if (head >= G) {
+        head -= G;
+        src += wrap;
+      }
+      dst += once * 128;
+      left -= once;
+    }
+  };
+  // e4m3: QFull is told by the converting warps, for every piece
+  auto queries_there = [&](int it) {
+    if (kFp8) return mbar_wait_warp(bar(L::bQFull), it & 1, abort);
+    return it == 0 ? mbar_wait_warp(bar(L::bQFirst), 0, abort) : mbar_wait_warp(bar(L::bQFull), (it - 1) & 1, abort);
+  };
+  auto load_ancestors = [&](int x) {
+    uint64_t set[2];
+    ancestors(a, heads[x].b, heads[x].fresh, lane, set, &status);
+    seen_sets[x * 64 + lane] = set[0];
+    seen_sets[x * 64 + 32 + lane] = set[1];
+  };
+  auto finish_queries = [&](int i) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(i));
   };
 
   if (warp == kProducer) {
@@ -510,7 +556,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (!ok) break;
       const int n = heads[x].steps, n_pages = heads[x].pages;
       if (n < 0) break;
-      ok = mbar_wait_warp(bar(L::bQFull), it & 1, abort);
+      ok = queries_there(it);
       for (int j = 0; j < n && ok; ++j) {
         ok = mbar_wait_warp(bar(L::bKFull + st), ph, abort) &&
              (g < kSBuf || mbar_wait_warp(bar(L::bPvIssued + sb), sb_ph, abort));
@@ -596,47 +642,21 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     mbar_wait_warp(bar(L::bFin + 1), 0, drain);
   } else if (warp == kValue) {
     // ---------------------------------------- queries, then loads of V --
-    constexpr int kLanes = D / 8, kRowsOnce = 32 / kLanes;    // lanes of a row
-    const int sub = lane % kLanes, r0 = lane / kLanes;
     int st = 0, ph = 1, gv = 0, filled = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int x = it & 1;
       ok = mbar_wait_warp(bar(L::bHeadFull + x), (it >> 1) & 1, abort);
       if (!ok) break;
-      const int n = heads[x].steps, b = heads[x].b, g = heads[x].g, rows = heads[x].fresh * G;
+      const int n = heads[x].steps, g = heads[x].g;
       if (n < 0) break;
       ok = it == 0 || mbar_wait_warp(bar(L::bQEmpty), (it - 1) & 1, abort);
       if (!ok) break;
-      // all rows on their way at once, straight to where the MMA reads them
-      const int first = rt * BM + r0, d_tok = kRowsOnce / G, d_head = kRowsOnce - d_tok * G;
-      const int64_t step = d_tok * a.qs[1] + d_head * a.qs[2], wrap = a.qs[1] - G * a.qs[2];
-      int head = first % G, left = rows - first;       // rows from this one on
-      const uint16_t* src = a.q + b * a.qs[0] + first / G * a.qs[1] + (g * G + head) * a.qs[2] + 8 * sub;
-      uint32_t dst = sbase + L::oQ + (sub >> 3) * L::kRegion + r0 * 128;
-#pragma unroll 4
-      for (int r = r0; r < BM; r += kRowsOnce) {
-        copy_16(dst + (((sub & 7) ^ (r & 7)) << 4), left > 0 ? src : a.q, left > 0);
-        if (!kFp8 && sub == 0) factors[x * BM + r] = a.scale_log2;
-        src += step;
-        head += d_head;
-        if (head >= G) {
-          head -= G;
-          src += wrap;
-        }
-        dst += kRowsOnce * 128;
-        left -= kRowsOnce;
+      if (it > 0) {
+        load_queries(x, lane, 32);
+        if (heads[x].special) load_ancestors(x);
+        finish_queries(kFp8 ? L::bQRaw : L::bQFull);
       }
-      if (heads[x].special) {
-        uint64_t set[2];
-        ancestors(a, b, heads[x].fresh, lane, set, &status);
-        seen_sets[x * 64 + lane] = set[0];
-        seen_sets[x * 64 + 32 + lane] = set[1];
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kFp8 ? L::bQRaw : L::bQFull));
       for (int j = 0; j < n && ok; ++j, ++gv) {
         const volatile StepInfo* in = infos + gv % kInfo;
         ok = mbar_wait_warp(bar(L::bInfo + gv % kInfo), (gv / kInfo) & 1, abort);
@@ -668,7 +688,7 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (!ok || heads[x].steps < 0) break;
         last += heads[x].steps;
         const float scale = a.scale_log2 * (a.k_scale ? get(a.k_scale + heads[x].g) : 1.f);
-        ok = mbar_wait_warp(bar(L::bQRaw), it & 1, abort);
+        ok = it == 0 ? mbar_wait_warp(bar(L::bQFirst), 0, abort) : mbar_wait_warp(bar(L::bQRaw), (it - 1) & 1, abort);
         if (!ok) break;
         constexpr int kLanes = D / 8, kRowsOnce = 32 / kLanes;
         const int sub = lane % kLanes, r0 = (warp - kConvert) * 32 + lane / kLanes;
@@ -796,7 +816,12 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const int b = heads[x].b, g = heads[x].g, dest = heads[x].dest, n_pages = heads[x].pages;
       const int n_rows = heads[x].fresh * G, row = rt * BM + r;
       const bool special = heads[x].special != 0;
-      stop = !mbar_wait_warp(bar(L::bQFull), it & 1, abort);    // the rows' factors are there
+      if (it == 0) {
+        load_queries(x, tid, 256);
+        if (warp == 0 && special) load_ancestors(x);
+        finish_queries(L::bQFirst);
+      }
+      stop = !queries_there(it);                        // and the rows' factors
       if (stop && lane == 0) fail();
       const float f = factors[x * BM + r];
       float m_run = -INFINITY, l_run = 0.f;
