@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(128, 4) prologue_axes_kernel(RouteArgs a, Prol
   const bool one_axis = axis[0] == axis[1] && axis[0] == axis[2] && axis[0] == axis[3];
   const int64_t step = which ? a.ks[1] : a.qs[1];
   const int64_t at0 = b * (which ? a.ks[0] : a.qs[0]) + h * (which ? a.ks[2] : a.qs[2]) + d + static_cast<int64_t>(i) * blk * step;
-  const uint16_t* X = (which ? a.k : a.q) + at0;
+  const uint16_t* X0 = (which ? a.k : a.q) + at0;
   uint16_t* Y = (which ? pa.k_out : pa.q_out) + at0;
   const float* gamma = which ? pa.gamma_k : pa.gamma_q;
   uint64_t g2[4], s2[4], c2[4];           // weights; running sums, two d in a pair
@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(128, 4) prologue_axes_kernel(RouteArgs a, Prol
   bool out = false;
   for (int c0 = 0; c0 < total; c0 += kBlock) {       // 64-token chunks of the block
     const int t0 = i * blk + c0, n = min(kBlock, a.S - t0);
+    const uint16_t* X = X0 + c0 * step;   // the next tokens to load; ends a chunk kT tokens ahead
     uint4 buf[kT];
     // threads beyond the heads read head 0's and keep nothing of it
     auto load = [&](int t) {
