@@ -36,6 +36,16 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The cluster's CTAs are placed together, but need not have begun together, and the shared
+// memory of one may be touched only once it runs. So each says first of all that it does, and
+// sums_of waits for all to have said so: behind the loads and the counting, where they long have.
+__device__ __forceinline__ void cluster_begun() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_begun() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // What other CTAs of this launch have written: from L2, past this SM's L1.
 __device__ __forceinline__ int fresh(const int32_t* p) { return __ldcg(p); }
 
@@ -44,11 +54,12 @@ struct Counts {
 };
 
 // The sums of two counts over the warps before this one (first) and over all (second).
-// Meets the cluster once.
+// Meets the cluster once, behind cluster_begun().
 struct Sums {
   int2 before, all;
 };
 __device__ __forceinline__ Sums sums_of(Counts& c, int warp, int lane, int x, int y) {
+  cluster_wait_begun();
   if (lane < kCtas) {
     uint32_t to;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&c.of[warp])), "r"(lane));
@@ -146,6 +157,7 @@ __device__ __forceinline__ void report(const PagesArgs& a, int status) {
 // Every CTA counts for itself, in shared memory, who continues whom: two meetings of the
 // cluster less than with counts in global memory (8.2 us a call, four beams).
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_fork_kernel(PagesArgs a) {
+  cluster_begun();
   let_next_launch();
   wait_for_first();
   __shared__ Counts counts;
@@ -236,6 +248,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
 // -------------------------------------------------------------- resize --
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_resize_kernel(PagesArgs a) {
+  cluster_begun();
   let_next_launch();
   wait_for_first();
   __shared__ Counts counts;
@@ -297,6 +310,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_
 // ------------------------------------------------------------- compact --
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) pages_compact_kernel(PagesArgs a) {
+  cluster_begun();
   let_next_launch();
   wait_for_first();
   __shared__ Counts counts;
