@@ -387,10 +387,13 @@ size_t pages_ws_bytes(int n_pages, int rows) {
 }
 
 cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t st) {
-  static_assert(2 * kMostRows * sizeof(int32_t) + sizeof(Counts) <= 227 * 1024, "counts do not fit shared memory");
+  // for the most rows, whatever this call has: the limit is the kernel's, for all threads of
+  // the host, and a smaller one could come between another's and its launch
+  constexpr int kMostSmem = 2 * kMostRows * sizeof(int32_t);
+  static_assert(kMostSmem + sizeof(Counts) <= 227 * 1024, "counts do not fit shared memory");
   const size_t smem = 2 * static_cast<size_t>(a.B) * sizeof(int32_t);
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
   }
   return launch(pages_fork_kernel, a, smem, st);
