@@ -743,7 +743,9 @@ sa_status sa_cache_accept(const sa_cache_params* p, void* k_cache, void* v_cache
  * Pages of the pool: who holds them. A page table and an array of reference
  * counts serve the caches of all layers; these calls change only those and name
  * the pages whose contents have to be copied, which sa_cache_copy does a layer at a
- * time.
+ * time. A new table stands for what it says once that is done in every layer, with the
+ * key sums where pages are routed: before the next sa_pages_fork or sa_pages_compact,
+ * and before tokens are appended or attended.
  *   refs        int32 [n_pages]: how many places hold the page; 0: it is free.
  *               A caller may hold pages of its own (a shared prompt) by counting
  *               them in.
