@@ -390,6 +390,20 @@ def sa_qk_prologue(q: torch.Tensor, k: torch.Tensor, gamma_q: Optional[torch.Ten
     for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k"), (cos, "cos"), (sin, "sin")):
         if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous fp32 tensor")
+    # the kernels read and write q's shape of each
+    for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")):
+        if (t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[3] != q.shape[3]
+                or any(a < b for a, b in zip(t.shape, q.shape))):
+            raise ValueError(f"{name} must be bf16 with q's shape [B, S, H, D]")
+    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        if t is not None and t.numel() < q.shape[3]:
+            raise ValueError(f"{name} must have D elements")
+    for t, name in ((cos, "cos"), (sin, "sin")):
+        if t is not None and not by_axes and t.numel() < q.shape[1] * (q.shape[3] // 2):
+            raise ValueError(f"{name} must be [S, D/2]")
+    _require_cuda(q_out, k_out, workspace, dev_status)
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.numel() < 1):
+        raise ValueError("dev_status must be an int32 tensor")
     p = make_params(q, k, q_block=q_block)
     ws = _workspace(sa_route_workspace_bytes(p), q.device, workspace)
     if by_axes:
