@@ -696,7 +696,8 @@ size_t sa_attn_tree_workspace_bytes(const sa_cache_params* p);
  *            before it. A parent outside that range counts as -1 and raises
  *            SA_DEV_BAD_TREE.
  * row_ptr,   as sa_attn_decode; entries from seq_lens[b] / 64 on are passed over
- * col_idx    (those pages are attended anyway).
+ * col_idx    (those pages are attended anyway). sa_route_pages makes one for all
+ *            tokens of a sequence from one token's queries and seq_lens.
  * o          device bf16 [B, S, H, D] (o_stride); no overlap with q.
  * lse        device fp32 [B, H, S] (natural log), or NULL.
  * workspace  device scratch of sa_attn_tree_workspace_bytes(p) bytes, 256-byte
