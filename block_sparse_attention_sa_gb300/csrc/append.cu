@@ -21,6 +21,12 @@
 // bf16, 1.43 GB in 217 us, 6.6 TB/s. 5 x up to 2,047 tokens, 16/16 heads of 64,
 // e4m3, 62 MB in 16.7 us, 3.7 TB/s: instructions bound it, 61% of the issue slots
 // while its CTAs run. One token 3.5 us, 128 tokens 4.1 us: launch and the chain of loads.
+//
+// With axes (kAxes) a token's angle is two dependent loads, position and row, made in every
+// round of two tokens and again for every key-value head, and the chain bounds long calls:
+// 56/8 heads of 128 in bf16, 8,192 tokens 134 us (56 by place), 38,247 tokens 584 us (224). Where
+// a border lies inside a lane's four pairs its angles are loaded one by one: 8,192 tokens 138 us
+// with 22, 21 and 21 pairs, 150 us with axes that alternate pair by pair.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

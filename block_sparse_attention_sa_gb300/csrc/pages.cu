@@ -10,7 +10,7 @@
 // without a list of free pages that would have to be kept in step with refs.
 //
 // Bound by the chain of dependent steps. In a graph, four sequences of 777 tokens (256 of
-// up to 2,048): fork 6.0 us (7.5), resize 3.4 (4.2); compact 4.0 us for a pool of 128
+// up to 2,048): fork 6.2 us (7.6), resize 3.3 (4.3); compact 4.1 us for a pool of 128
 // pages, 7.2 for one of 6,144. Fork, resize and the copy called one by one on an idle GPU:
 // 12 us (22), 20.5 (31) with every launch behind the end of the one before.
 #include "cache_internal.cuh"

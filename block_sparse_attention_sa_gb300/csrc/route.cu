@@ -339,8 +339,10 @@ __global__ void __launch_bounds__(128) prologue_kernel(RouteArgs a, PrologueArgs
 // angles are two rounds of independent loads.
 //
 // Every byte of q and k is read and written once: 38,247 tokens, 56 heads of 128, 2.19 GB
-// in 416 us, 5.3 TB/s (372 us without the norm, whose sums across lanes are what the
-// memory's time does not cover). All heads of a block of tokens run side by side, so that
+// in 415 us, 5.3 TB/s, 404 us with query blocks of 128 (372 us without the norm, whose sums
+// across lanes are what the memory's time does not cover). That is with the axes' borders at
+// multiples of four pairs, where a thread's four pairs share a row of the tables; 22, 21 and
+// 21 pairs take 450 us, axes that alternate pair by pair 440: a position and two angles a pair. All heads of a block of tokens run side by side, so that
 // whole tokens are read (a head group's blocks side by side: 440 us); eight tokens are on
 // their way in a thread, four CTAs an SM (four and six: 430 us), and a group of tokens has
 // no conditions in it, so that their chains overlap (470 us with them).

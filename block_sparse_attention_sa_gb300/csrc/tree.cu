@@ -7,12 +7,22 @@
 namespace sa {
 
 // Whether tcgen05 takes a tree, 128 rows (pairs of a new token and a query head) of a
-// key-value head at a time, or decode_kernel, whose products are those of 16 rows. 64
-// sequences of 3,000 tokens, 8 heads of 128 in bf16: 16 rows 162 us with the latter and 152
-// with the former, 17 rows 191 and 154, 64 rows 394 and 156; of 6,000 in e4m3: 16 rows 188
-// and 269, 33 rows 605 and 275 (heads of 64: 32 rows 199 and 232, 33 rows 359 and 234). Up
-// to 32 rows decode_kernel starts sooner (777 tokens, 32/8 heads, 8 new ones: 17 us and
-// 19), which decides where a run is a page or two, as far as the table's size tells.
+// key-value head at a time, or decode_kernel, whose products are those of 16 rows. In us,
+// decode_kernel and tiles (L2 flushed before each call):
+//   rows a key-value head              8         16        17        32        33 and more
+//   64 x 3,000, 8 heads of 128, bf16   154 146   162 150   191 150   207 152   64 rows: 394 156
+//     heads of 64                       97  97   105 100   123 100   141 100
+//   64 x 6,000, 8 heads of 128, e4m3   160 263   188 263   287 269   303 269   605 275
+//     heads of 64                      103 233   128 233   181 238   199 237   359 234
+//   8 x 1,500, 8 heads of 128, bf16     28  31    33  31    35  31    41  31
+//   3 x 38,247, 2 heads of 128, bf16    42  48    42  46    46  48    48  45
+//   1 x 777, 8 heads of 128, bf16       16  19    17  19    17  19    17  19
+//     e4m3                              16  21    17  21    17  22    19  21
+// Up to 16 rows decode_kernel, which reads a page once: it loses 5 to 8% in large batches in
+// bf16 from 12 rows on and wins elsewhere, in e4m3 by 20 to 45%. Above 32 tiles. Between, a
+// product of 32 rows costs decode_kernel more than the tiles' start, but for e4m3 with heads
+// of 64, where turning codes into fp16 bounds the tiles, and where a run is a page or two, as
+// far as the table's size tells.
 static bool in_tiles(int rows, int D, bool fp8, int64_t pages) {
   if (rows <= 16) return false;
   return rows > 32 || !((fp8 && D == 64) || pages <= 2 * kSms);

@@ -31,11 +31,12 @@
 //
 // Bounds. 32 sequences of 16 new tokens behind 8,192, 56/8 heads of 128 in bf16, 112 rows a
 // unit: 195 us for 1.08 GB, 5.5 TB/s, the memory. 64 new tokens behind 3 x 112,640, 448
-// rows: 597 us in bf16, 1,040 TFLOP/s: the tensor pipe (82% busy), which does half as much
-// again for the second term of P; a step's products take 1,536 cycles, a step 1,700 to
-// 1,800, at the clock that the power leaves (1.5 to 1.8 GHz). In e4m3 647 us, pipe 60%
-// busy: there is room for two steps' keys and values in 16 bits, and the way of each from
-// its codes' arrival to the product (wait, read, convert, write, told) is 2,000 cycles.
+// rows: 580 to 597 us in bf16, 1,040 to 1,070 TFLOP/s: the tensor pipe (82% busy), which
+// does half as much again for the second term of P; a step's products take 1,536 cycles, a
+// step 1,700 to 1,800, at the clock that the power leaves (1.5 to 1.8 GHz). In e4m3 640 to
+// 650 us with pauses between the calls, 687 to 695 back to back at the power limit, pipe 60%
+// busy: there is room for two steps' keys and values in 16 bits, and the way of each from its
+// codes' arrival to the product (wait, read, convert, write, told) is 2,000 cycles.
 // With one warp for all products bf16 took 705 us, with 32 keys of the softmax unrolled to
 // 128 774 us: a step's code then does not fit the instruction cache. 777 tokens, 64 new
 // ones: 17.5 us, the chain lengths, page, queries, scores, weights, output, partial, join.
@@ -671,8 +672,9 @@ tree_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // -------------------------------------------------------- conversion --
     // Two warps turn K into fp16, two V: a thread two rows (tokens) of each. As read, so
     // written, without bank conflicts, as the rows' pieces are swizzled alike. A page's codes
-    // are read before the wait for the tile's place (3 x 64 new tokens behind 112,640: 676 us;
-    // waiting first 713; both pages' codes at once 756; all four warps for K, then V 810).
+    // are read before the wait for the tile's place (when that was tried, 3 x 64 new tokens
+    // behind 112,640 took 676 us so; waiting first 713; both pages' codes at once 756; all four
+    // warps for K, then V 810).
     // Their stage is given back only behind the stores, which need the loads' results: an
     // arrival may pass loads that are still under way.
     const bool values = warp >= kConvert + 2;

@@ -686,7 +686,9 @@ size_t sa_attn_tree_workspace_bytes(const sa_cache_params* p);
  * share a key-value head, P.V takes P to 2^-16 of itself, as two bf16 terms (with
  * SA_CACHE_FP8 to 2^-21 of itself or 2^-30 of the largest, as two fp16 terms), and
  * with SA_CACHE_FP8 q is taken in fp16 scaled by a power of two for each row, exact but
- * for bits below 2^-39 of its largest element.
+ * for bits below 2^-39 of its largest element. Long sums in the tensor cores' fp32
+ * accumulators are cut, not rounded: over 112,640 tokens o comes out smaller, by about
+ * 1.2e-4 of itself (half a bf16 step is up to 39e-4).
  *
  * q          device bf16 [B, S, H, D], rotated as the cached keys are; S at most
  *            SA_TREE_MAX.
@@ -753,7 +755,7 @@ sa_status sa_cache_accept(const sa_cache_params* p, void* k_cache, void* v_cache
  *   page_table  int32 [B][table_stride]: -1 where a sequence has no page. An entry
  *               outside [-1, n_pages) counts as -1 and raises SA_DEV_BAD_CACHE.
  * A page that is not full belongs to one sequence; full ones may be shared, as
- * nothing is appended to them. Free pages are taken in ascending order of their ids,
+ * nothing is appended to them (so a sequence is not set back into a page that others hold). Free pages are taken in ascending order of their ids,
  * as they are free when the call begins. The workspace serves any of the three.
  * ---------------------------------------------------------------------- */
 
